@@ -1,0 +1,415 @@
+// AdamW over many tensors at once, the global gradient norm before it, and
+// the values of 8-bit states.  include/xp_train.h states the formulas.
+//
+// All three are elementwise or a sum: what bounds them is the memory they
+// move.  A group's tensors are cut into units once, at creation, and one
+// launch covers every tensor, so many small tensors cost no more launches
+// than one.
+#include <cuda_bf16.h>
+
+#include "xp_train_internal.h"
+
+namespace xp {
+namespace {
+
+// ---------------------------------------------------------------- vectors of kVec elements
+
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  uint4 q[2];
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 q[1];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load_vec(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Raw<T>) / 16); ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&f)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(r.q[i].x);
+    f[4 * i + 1] = __uint_as_float(r.q[i].y);
+    f[4 * i + 2] = __uint_as_float(r.q[i].z);
+    f[4 * i + 3] = __uint_as_float(r.q[i].w);
+  }
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&f)[kVec]) {
+  const unsigned w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store_vec(float* p, const float (&f)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[kVec]) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
+}
+__device__ __forceinline__ float one(const float* p) { return *p; }
+__device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float* p, float f) { *p = f; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
+
+// n of kVec elements at p (n < kVec at a tensor's end, and at any n where the
+// pointer allows no vector); the rest read as 0.
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, bool vec, float (&f)[kVec]) {
+  if (vec && n == kVec) {
+    widen(load_vec(p), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = i < n ? one(p + i) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int n, bool vec, const float (&f)[kVec]) {
+  if (vec && n == kVec) {
+    store_vec(p, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i < n) put(p + i, f[i]);
+  }
+}
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int n, bool vec) {
+  if (vec && n == kVec) return *reinterpret_cast<const uint2*>(p);
+  uint2 c = make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < n) (i < 4 ? c.x : c.y) |= (unsigned)p[i] << (8 * (i & 3));
+  return c;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, uint2 c) {
+  if (vec && n == kVec) {
+    *reinterpret_cast<uint2*>(p) = c;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < n) p[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+}
+// Whether kVec elements of T starting at a multiple of kVec may move at once.
+template <typename T>
+__device__ __forceinline__ bool vec_ok(const T* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+// ---------------------------------------------------------------- 8-bit states
+
+// The fp32 pattern's last 20 bits are cut: what is left is the exponent and 3
+// mantissa bits, a whole number that the block's exponent shifts into 7 or 8
+// bits.  Decoding and encoding are integer operations on it, exact, with no
+// division by the block's scale.
+template <bool SIGNED>
+constexpr int kShift = SIGNED ? 119 : 247;
+
+template <bool SIGNED>
+__device__ __forceinline__ void decode_codes(uint2 c, int e, float (&f)[kVec]) {
+  const int base = 8 * e - kShift<SIGNED>;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int b = (int)(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xffu);
+    const int mag = SIGNED ? (b & 127) : b;
+    unsigned bits = (unsigned)max(mag + base, 0) << 20;
+    bits = mag == 0 ? 0u : bits;
+    if (SIGNED) bits |= (unsigned)(b & 128) << 24;
+    f[i] = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(bits);
+  }
+}
+
+// exponent of the largest magnitude among a thread's elements
+__device__ __forceinline__ unsigned top_exponent(const float (&f)[kVec]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+  return top >> 23;
+}
+
+template <bool SIGNED>
+__device__ __forceinline__ unsigned encode_one(float x, unsigned noise, int e) {
+  const unsigned bits = __float_as_uint(x) & 0x7fffffffu;
+  int c = (int)((bits + noise) >> 20) - (8 * e - kShift<SIGNED>);
+  c = min(max(c, SIGNED ? 0 : 1), SIGNED ? 127 : 255);
+  c = bits == 0 ? 0 : c;
+  if (SIGNED && c > 0) c |= (int)(__float_as_uint(x) >> 24) & 128;
+  return (unsigned)c;
+}
+
+// A 32-bit mix of the step and the position: multiplications by odd constants
+// and shifts, each invertible, so that positions never collide within a key.
+__device__ __forceinline__ unsigned mix(unsigned x) {
+  x = (x ^ (x >> 16)) * 0xDDF15BA9u;
+  x = (x ^ (x >> 15)) * 0xE31B8755u;
+  return x ^ (x >> 16);
+}
+constexpr unsigned kPosLo = 0x8ED88009u, kPosHi = 0xB86D3E2Fu;
+__device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { return mix(seed * kPosLo + mix(step)); }
+
+// ---------------------------------------------------------------- the step
+
+// One unit per CTA, kVec elements per thread at a time.
+template <typename P, typename G, bool S8>
+__global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_constant__ StepParams prm) {
+  __shared__ float s_coef[2];
+  __shared__ unsigned s_step;
+  if (prm.report && prm.skip_nonfinite && prm.report->nonfinite) return;   // the same answer in every CTA
+  if (threadIdx.x == 0) {
+    volatile GroupState* st = prm.state;
+    const unsigned long long step = st->step;
+    const double p1 = st->power1, p2 = st->power2;
+    s_coef[0] = st->inv_bias1;
+    s_coef[1] = st->inv_sqrt_bias2;
+    s_step = (unsigned)(step + 1);
+    // the last CTA to have read the words writes the next step's
+    __threadfence();
+    if (atomicAdd(&prm.state->arrived_step, 1u) == gridDim.x - 1) {
+      const double n1 = p1 * prm.beta1_d, n2 = p2 * prm.beta2_d;
+      st->step = step + 1;
+      st->power1 = n1;
+      st->power2 = n2;
+      st->inv_bias1 = (float)(1.0 / (1.0 - n1));
+      st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
+      st->arrived_step = 0;
+    }
+  }
+  const GroupUnit u = prm.units[blockIdx.x];
+  const GroupTensor t = prm.tensors[u.tensor];
+  const float lr = prm.lr_dev ? *prm.lr_dev : prm.lr;
+  const float gscale = prm.report ? prm.report->scale : prm.grad_scale;
+  const float keep = 1.0f - lr * t.decay;
+  P* param = static_cast<P*>(t.param) + u.start;
+  const G* grad = static_cast<const G*>(t.grad) + u.start;
+  const bool vec = t.aligned && vec_ok(static_cast<const G*>(t.grad));
+  __syncthreads();
+  const float alpha = lr * s_coef[0], rs = s_coef[1];
+  const unsigned key = S8 ? step_key(prm.seed, s_step) : 0;
+
+  // every thread of a warp makes the same number of turns: 8-bit blocks
+  // share their exponent by shuffles
+  const unsigned turns = (u.n + kStepThreads * kVec - 1) / (kStepThreads * kVec);
+  for (unsigned turn = 0; turn < turns; ++turn) {
+    const unsigned at = (turn * kStepThreads + threadIdx.x) * kVec;
+    const int n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
+    float p[kVec], g[kVec], m[kVec], v[kVec];
+    load_some(grad + at, n, vec, g);
+    load_some(param + at, n, vec, p);
+    if constexpr (S8) {
+      const unsigned long long i = u.start + at;
+      const uint2 cm = load_codes(static_cast<const uint8_t*>(t.m) + i, n, vec);
+      const uint2 cv = load_codes(static_cast<const uint8_t*>(t.v) + i, n, vec);
+      const int em = n ? t.m_scale[i / XP_STATE8_BLOCK] : 0, ev = n ? t.v_scale[i / XP_STATE8_BLOCK] : 0;
+      decode_codes<true>(cm, em, m);
+      decode_codes<false>(cv, ev, v);
+    } else {
+      load_some(static_cast<const float*>(t.m) + u.start + at, n, vec, m);
+      load_some(static_cast<const float*>(t.v) + u.start + at, n, vec, v);
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float gi = g[i] * gscale;
+      m[i] = m[i] * prm.beta1 + gi * prm.one_minus_beta1;
+      v[i] = v[i] * prm.beta2 + gi * prm.one_minus_beta2 * gi;
+      const float d = __fsqrt_rn(v[i]) * rs + prm.eps;
+      p[i] = p[i] * keep - __fdiv_rn(m[i] * alpha, d);
+    }
+    store_some(param + at, n, vec, p);
+    if (t.copy) store_some(static_cast<__nv_bfloat16*>(t.copy) + u.start + at, n, vec, p);
+    if constexpr (S8) {
+      const unsigned long long i = u.start + at, pos = t.pos + i;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (k >= n) m[k] = v[k] = 0.f;
+      unsigned top = top_exponent(m) << 16 | top_exponent(v);
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
+      unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi + key;   // kVec positions share the high word
+      uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k, h += kPosLo) {
+        const unsigned r = mix(h);
+        const unsigned a = encode_one<true>(m[k], ((r >> 16) << 4) + 8u, em);
+        const unsigned b = encode_one<false>(v[k], ((r & 0xffffu) << 4) + 8u, ev);
+        (k < 4 ? cm.x : cm.y) |= a << (8 * (k & 3));
+        (k < 4 ? cv.x : cv.y) |= b << (8 * (k & 3));
+      }
+      store_codes(static_cast<uint8_t*>(t.m) + i, n, vec, cm);
+      store_codes(static_cast<uint8_t*>(t.v) + i, n, vec, cv);
+      if (n && (i & (XP_STATE8_BLOCK - 1)) == 0) {
+        t.m_scale[i / XP_STATE8_BLOCK] = (uint8_t)em;
+        t.v_scale[i / XP_STATE8_BLOCK] = (uint8_t)ev;
+      }
+    } else {
+      store_some(static_cast<float*>(t.m) + u.start + at, n, vec, m);
+      store_some(static_cast<float*>(t.v) + u.start + at, n, vec, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the norm
+
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Each CTA adds up its units' squares and leaves one fp64 sum; the CTA that
+// arrives last adds the sums up in their order, so the result does not depend
+// on which CTA that is.
+template <typename G>
+__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormParams prm) {
+  __shared__ double s_sum[kNormThreads / 32];
+  __shared__ bool s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double sum = 0.0;
+  for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) {
+    const GroupUnit u = prm.units[k];
+    const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
+    const bool vec = vec_ok(grad);
+    grad += u.start;
+    float acc[kVec] = {};
+    for (unsigned at = threadIdx.x * kVec; at < u.n; at += kNormThreads * kVec) {
+      float g[kVec];
+      load_some(grad + at, (int)min((unsigned)kVec, u.n - at), vec, g);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += g[i] * g[i];
+    }
+    sum += (double)(((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = warp_sum(lane < kNormThreads / 32 ? s_sum[lane] : 0.0);
+    if (lane == 0) {
+      prm.partial[blockIdx.x] = sum;
+      __threadfence();
+      s_last = atomicAdd(&prm.state->arrived_norm, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  sum = 0.0;
+  for (unsigned k = threadIdx.x; k < gridDim.x; k += kNormThreads) sum += __ldcg(prm.partial + k);
+  sum = warp_sum(sum);
+  __syncthreads();
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total = prm.accumulate ? prm.report->sumsq : 0.0;
+    for (int w = 0; w < kNormThreads / 32; ++w) total += s_sum[w];
+    const float norm = (float)((double)prm.grad_scale * sqrt(total));
+    float scale = prm.grad_scale;
+    if (prm.max_norm > 0.f && norm > prm.max_norm) scale *= prm.max_norm / norm;
+    prm.report->sumsq = total;
+    prm.report->norm = norm;
+    prm.report->scale = scale;
+    prm.report->nonfinite = isfinite(total) ? 0 : 1;
+    prm.state->arrived_norm = 0;
+  }
+}
+
+// ---------------------------------------------------------------- small ones
+
+__global__ void set_grads_kernel(const __grid_constant__ SetGradsParams prm) {
+  for (int i = threadIdx.x; i < prm.n; i += blockDim.x) prm.tensors[prm.first + i].grad = prm.grad[i];
+}
+
+__global__ void set_step_kernel(GroupState* s, unsigned long long step, double p1, double p2) {
+  s->step = step;
+  s->power1 = p1;
+  s->power2 = p2;
+  s->inv_bias1 = (float)(1.0 / (1.0 - p1));
+  s->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - p2));
+  s->arrived_step = 0;
+  s->arrived_norm = 0;
+}
+
+template <typename O>
+__global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_constant__ DecodeParams prm) {
+  const int which = blockIdx.y;
+  O* out = static_cast<O*>(prm.out[which]);
+  if (!out) return;
+  const unsigned long long at = ((unsigned long long)blockIdx.x * kStepThreads + threadIdx.x) * kVec;
+  if (at >= prm.count) return;
+  const int n = (int)min((unsigned long long)kVec, prm.count - at);
+  const uint8_t* code = prm.code[which];
+  const uint2 c = load_codes(code + at, n, (reinterpret_cast<uintptr_t>(code) & 7u) == 0);
+  const int e = prm.scale[which][at / XP_STATE8_BLOCK];
+  float f[kVec];
+  if (which == 0)
+    decode_codes<true>(c, e, f);
+  else
+    decode_codes<false>(c, e, f);
+  store_some(out + at, n, vec_ok(out), f);
+}
+
+template <typename P, typename G, bool S8>
+cudaError_t run_adamw(const StepParams& p, unsigned nunits, cudaStream_t st) {
+  adamw_kernel<P, G, S8><<<nunits, kStepThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const StepParams& p, unsigned nunits, int param_dtype, int grad_dtype, int state_dtype,
+                         cudaStream_t st) {
+  typedef __nv_bfloat16 H;
+  const bool s8 = state_dtype == XP_U8;
+  if (param_dtype == XP_F32) {
+    if (grad_dtype == XP_F32) return s8 ? run_adamw<float, float, true>(p, nunits, st) : run_adamw<float, float, false>(p, nunits, st);
+    return s8 ? run_adamw<float, H, true>(p, nunits, st) : run_adamw<float, H, false>(p, nunits, st);
+  }
+  if (grad_dtype == XP_F32) return s8 ? run_adamw<H, float, true>(p, nunits, st) : run_adamw<H, float, false>(p, nunits, st);
+  return s8 ? run_adamw<H, H, true>(p, nunits, st) : run_adamw<H, H, false>(p, nunits, st);
+}
+
+int norm_ctas(unsigned nunits) { return (int)(nunits < (unsigned)kNormMaxCtas ? nunits : (unsigned)kNormMaxCtas); }
+
+cudaError_t launch_grad_norm(const NormParams& p, int grad_dtype, cudaStream_t st) {
+  const int grid = norm_ctas(p.nunits) > 0 ? norm_ctas(p.nunits) : 1;
+  if (grad_dtype == XP_F32)
+    grad_norm_kernel<float><<<grid, kNormThreads, 0, st>>>(p);
+  else
+    grad_norm_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_set_grads(const SetGradsParams& p, cudaStream_t st) {
+  set_grads_kernel<<<1, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_set_step(GroupState* s, unsigned long long step, double p1, double p2, cudaStream_t st) {
+  set_step_kernel<<<1, 1, 0, st>>>(s, step, p1, p2);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode(const DecodeParams& p, int out_dtype, cudaStream_t st) {
+  const unsigned long long per = (unsigned long long)kStepThreads * kVec;
+  const dim3 grid((unsigned)((p.count + per - 1) / per), 2);
+  if (out_dtype == XP_F32)
+    decode_kernel<float><<<grid, kStepThreads, 0, st>>>(p);
+  else
+    decode_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace xp

@@ -1,0 +1,219 @@
+"""ctypes binding of the training operators of libxp.so (include/xp_train.h): same names, argument marshalling only.
+
+Tensors are torch tensors (or objects with the same `data_ptr()`, `shape`, `stride()` and `dtype`): their pointers,
+sizes, strides and types are read off, and shapes that do not belong together raise ValueError before the call.
+Streams, and the errors of the library itself (`XpError`), are as in `xp`.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import xp
+from .xp import XP_BF16, XP_F32, XP_OK, XP_U8, XpError, _stream  # noqa: F401
+
+XP_LAYERNORM_MAX_COLS = 131072
+XP_LAYERNORM_MAX_ROWS = 1 << 28
+XP_STATE8_BLOCK = 32
+XP_ADAMW_SKIP_NONFINITE = 1
+
+# every entry point include/xp_train.h declares
+EXPORTS = [
+    "xp_layernorm_forward", "xp_layernorm_workspace", "xp_layernorm_backward", "xp_group_create", "xp_group_destroy",
+    "xp_group_set_grads", "xp_group_set_step", "xp_group_get_step", "xp_grad_norm", "xp_adamw_step", "xp_state8_decode",
+]
+
+
+class xp_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("count", ctypes.c_size_t), ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class xp_group_config(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("seed", ctypes.c_uint32), ("step", ctypes.c_uint64)]
+
+
+class xp_grad_report(ctypes.Structure):
+    _fields_ = [("sumsq", ctypes.c_double), ("norm", ctypes.c_float), ("scale", ctypes.c_float),
+                ("nonfinite", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
+
+
+_lib = xp._lib
+_P, _I, _Z, _F, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint64
+for _name, _args in {
+    "xp_layernorm_forward": [_P, _Z, _P, _P, _P, _Z, _P, _P, _Z, _Z, _F, _I, _I, _P],
+    "xp_layernorm_workspace": [_Z, _Z, ctypes.POINTER(_Z)],
+    "xp_layernorm_backward": [_P, _Z, _P, _Z, _P, _P, _P, _P, _Z, _P, _P, _Z, _Z, _I, _I, _I, _P, _Z, _P],
+    "xp_group_create": [ctypes.POINTER(xp_group_config), _I, ctypes.POINTER(xp_tensor), ctypes.POINTER(_P)],
+    "xp_group_destroy": [_P],
+    "xp_group_set_grads": [_P, ctypes.POINTER(_P), _P],
+    "xp_group_set_step": [_P, _U64, _P],
+    "xp_group_get_step": [_P, ctypes.POINTER(_U64), _P],
+    "xp_grad_norm": [_P, _F, _F, _I, _P, _P],
+    "xp_adamw_step": [_P, _F, _P, _F, _P, _I, _P],
+    "xp_state8_decode": [_P, _P, _P, _P, _Z, _P, _P, _I, _P],
+}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = ctypes.c_int
+
+_DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
+_types = {}   # torch dtype -> xp_dtype, filled as types are met
+
+
+def _dtype(t) -> int:
+    d = t.dtype
+    found = _types.get(d)
+    if found is None:
+        if str(d) not in _DTYPES:
+            raise ValueError(f"no xp_dtype for {d}")
+        found = _types[d] = _DTYPES[str(d)]
+    return found
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(st: int, where: str):
+    if st != XP_OK:
+        xp._check(st, where)
+
+
+def _rows(t, shape, what):
+    """A matrix's row stride in elements; its columns lie side by side."""
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{what}'s columns are {col} elements apart")
+    return row
+
+
+def _vector(t, n, what, dtype=None):
+    if t is not None and (t.numel() != n or not t.is_contiguous() or (dtype is not None and _dtype(t) != dtype)):
+        raise ValueError(f"{what} is not {n} contiguous elements of its type")
+
+
+def xp_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y = layer norm of each row of x (rows x cols), with its statistics where mean and rstd are given."""
+    shape = x.shape
+    rows, cols = shape
+    dt = _dtype(x)
+    w = gamma if gamma is not None else beta
+    wdt = dt if w is None else _dtype(w)
+    xs, ys = _rows(x, shape, "x"), _rows(y, shape, "y")
+    if _dtype(y) != dt:
+        raise ValueError("x and y differ in type")
+    _vector(gamma, cols, "gamma", wdt)
+    _vector(beta, cols, "beta", wdt)
+    _vector(mean, rows, "mean", XP_F32)
+    _vector(rstd, rows, "rstd", XP_F32)
+    _check(_lib.xp_layernorm_forward(x.data_ptr(), xs, _p(gamma), _p(beta), y.data_ptr(), ys, _p(mean), _p(rstd), rows, cols,
+                                     eps, dt, wdt, _stream(stream)), "xp_layernorm_forward")
+
+
+def xp_layernorm_workspace(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.xp_layernorm_workspace(rows, cols, ctypes.byref(out)), "xp_layernorm_workspace")
+    return out.value
+
+
+def xp_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, accumulate: bool = False,
+                          stream=None) -> None:
+    """dx, and over the rows dgamma and dbeta, from dy and what the forward pass gave."""
+    shape = x.shape
+    rows, cols = shape
+    dt = _dtype(x)
+    wdt = dt if gamma is None else _dtype(gamma)
+    xs, dys, dxs = _rows(x, shape, "x"), _rows(dy, shape, "dy"), _rows(dx, shape, "dx")
+    if _dtype(dy) != dt or _dtype(dx) != dt:
+        raise ValueError("dy, x and dx differ in type")
+    _vector(gamma, cols, "gamma", wdt)
+    _vector(mean, rows, "mean", XP_F32)
+    _vector(rstd, rows, "rstd", XP_F32)
+    _vector(dgamma, cols, "dgamma", XP_F32)
+    _vector(dbeta, cols, "dbeta", XP_F32)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.xp_layernorm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _p(gamma), mean.data_ptr(), rstd.data_ptr(),
+                                      dx.data_ptr(), dxs, _p(dgamma), _p(dbeta), rows, cols, dt, wdt, 1 if accumulate else 0,
+                                      _p(workspace), nbytes, _stream(stream)), "xp_layernorm_backward")
+
+
+def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=None, copies=None, weight_decay=0.0,
+                    beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, seed: int = 0, step: int = 0) -> int:
+    """A group of tensors: lists of the same length.  params None: a group for xp_grad_norm alone.  States of
+    torch.uint8 are 8-bit codes and need scales; weight_decay is one number or a list.  The caller keeps the
+    tensors alive as long as the group."""
+    n = len(grads)
+    decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+    named = {"param": params, "m": m, "v": v, "m_scale": m_scales, "v_scale": v_scales, "copy": copies}
+    cfg = xp_group_config(beta1=beta1, beta2=beta2, eps=eps, seed=seed, step=step, grad_dtype=_dtype(grads[0]) if n else XP_F32,
+                          param_dtype=_dtype(params[0]) if params else XP_F32, state_dtype=_dtype(m[0]) if m else XP_F32)
+    if len(decay) != n or any(x is not None and len(x) != n for x in named.values()):
+        raise ValueError("the lists differ in length")
+    want = {"param": cfg.param_dtype, "grad": cfg.grad_dtype, "m": cfg.state_dtype, "v": cfg.state_dtype, "copy": XP_BF16,
+            "m_scale": XP_U8, "v_scale": XP_U8}
+    named["grad"] = grads
+    table = (xp_tensor * max(n, 1))()
+    for i in range(n):
+        count = grads[i].numel()
+        for name, tensors in named.items():
+            t = None if tensors is None else tensors[i]
+            if t is None:
+                continue
+            _vector(t, -(-count // XP_STATE8_BLOCK) if name.endswith("scale") else count, f"{name} {i}", want[name])
+            setattr(table[i], name, t.data_ptr())
+        table[i].count = count
+        table[i].weight_decay = decay[i]
+    out = ctypes.c_void_p()
+    _check(_lib.xp_group_create(ctypes.byref(cfg), n, table, ctypes.byref(out)), "xp_group_create")
+    return out.value
+
+
+def xp_group_destroy(group: int) -> None:
+    _check(_lib.xp_group_destroy(group), "xp_group_destroy")
+
+
+def xp_group_set_grads(group: int, grads, stream=None) -> None:
+    """Other gradient buffers, of the lengths and type the group was made with."""
+    ptrs = (ctypes.c_void_p * max(len(grads), 1))(*[t.data_ptr() for t in grads])
+    _check(_lib.xp_group_set_grads(group, ptrs, _stream(stream)), "xp_group_set_grads")
+
+
+def xp_group_set_step(group: int, step: int, stream=None) -> None:
+    _check(_lib.xp_group_set_step(group, step, _stream(stream)), "xp_group_set_step")
+
+
+def xp_group_get_step(group: int, stream=None) -> int:
+    out = ctypes.c_uint64()
+    _check(_lib.xp_group_get_step(group, ctypes.byref(out), _stream(stream)), "xp_group_get_step")
+    return out.value
+
+
+def xp_grad_norm(group: int, report, grad_scale: float = 1.0, max_norm: float = 0.0, accumulate: bool = False, stream=None) -> None:
+    """The norm of the group's gradients into `report`, 32 bytes of device memory laid out as xp_grad_report."""
+    _check(_lib.xp_grad_norm(group, grad_scale, max_norm, 1 if accumulate else 0, report.data_ptr(), _stream(stream)), "xp_grad_norm")
+
+
+def xp_adamw_step(group: int, lr: float, report=None, grad_scale: float = 1.0, skip_nonfinite: bool = False, lr_dev=None,
+                  stream=None) -> None:
+    """One AdamW step on the group's tensors, gradients scaled by the report's scale if there is one."""
+    _check(_lib.xp_adamw_step(group, lr, _p(lr_dev), grad_scale, _p(report), XP_ADAMW_SKIP_NONFINITE if skip_nonfinite else 0,
+                              _stream(stream)), "xp_adamw_step")
+
+
+def xp_state8_decode(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
+    """The values of 8-bit states, m's into m_out and v's into v_out (either may be None)."""
+    out = m_out if m_out is not None else v_out
+    if out is None:
+        return
+    count, dt = out.numel(), _dtype(out)
+    for name, code, scale, to in (("m", m, m_scale, m_out), ("v", v, v_scale, v_out)):
+        if to is not None:
+            _vector(to, count, name + "_out", dt)
+            _vector(code, count, name, XP_U8)
+            _vector(scale, -(-count // XP_STATE8_BLOCK), name + "_scale", XP_U8)
+    _check(_lib.xp_state8_decode(_p(m), _p(m_scale), _p(v), _p(v_scale), count, _p(m_out), _p(v_out), dt, _stream(stream)),
+           "xp_state8_decode")

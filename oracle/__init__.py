@@ -17,7 +17,9 @@ Entry points:
   return the result;
 * `ring_allreduce`: the ring as state machines; `ring_order_sum`: the plain
   definition of its result;
-* `fifo.explore`: every interleaving of a tiny system.
+* `fifo.explore`: every interleaving of a tiny system;
+* `train`: the training operators by their formulas (layer norm, gradient
+  norm, AdamW, 8-bit states).
 
 Pins (tests/test_oracle_*.py): byte identity of every copy path, exhaustive
 interleavings for N in {1, 2} with up to 4 slot-steps, planted protocol
@@ -26,6 +28,7 @@ arithmetic rounded to fp32, against int64 sums for int32, against the
 fp64 sum within the standard error bound, and the pages' printed sizes and
 ring-neighbour example (tests/golden/).
 """
+from . import train
 from .fifo import (CEFifo, CEProxy, CEReceiver, CESender, Deadlock, LL128Fifo, LL128LaneFifo, LL128LaneReceiver,
                    LL128LaneSender, LL128Receiver, LL128Sender, LLFifo, LLReceiver, LLSender, PostedChannel, PostedReceiver, PostedSender,
                    ProtocolViolation, SimpleFifo, SimpleReceiver, SimpleSender, System, ZeroCopyChannel,
@@ -45,5 +48,5 @@ __all__ = [
     "PostedChannel", "PostedSender", "PostedReceiver", "posted_transfer",
     "CEFifo", "CESender", "CEProxy", "CEReceiver", "ce_transfer",
     "LL128Fifo", "LL128Sender", "LL128Receiver", "ll128_flag", "ll128_transfer",
-    "LL128LaneFifo", "LL128LaneSender", "LL128LaneReceiver",
+    "LL128LaneFifo", "LL128LaneSender", "LL128LaneReceiver", "train",
 ]
