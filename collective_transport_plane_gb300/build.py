@@ -14,7 +14,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["xp_api.cu", "xp_p2p.cu", "xp_p2p_tma.cu", "xp_ll.cu", "xp_ll128.cu", "xp_ring.cu", "xp_ring_tma.cu",
            "xp_noalloc.cu", "xp_proxy.cu", "xp_train.cu", "xp_adamw.cu", "xp_layernorm.cu"]
-HEADERS = ["xp_internal.h", "xp_device.cuh", "xp_proxy.h", "xp_train_internal.h"]
+HEADERS = ["xp_internal.h", "xp_device.cuh", "xp_proxy.h", "xp_train_internal.h", "xp_train_device.cuh"]
 
 # --fmad=false and the default -ftz=false keep the ring's fp32 adds plain IEEE
 # round-to-nearest-even additions (the reductions must match the oracle bit

@@ -5,9 +5,7 @@
 // move.  A group's tensors are cut into units once, at creation, and one
 // launch covers every tensor, so many small tensors cost no more launches
 // than one.
-#include <cuda_bf16.h>
-
-#include "xp_train_internal.h"
+#include "xp_train_device.cuh"
 
 namespace xp {
 namespace {
@@ -162,32 +160,44 @@ __device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { ret
 
 // ---------------------------------------------------------------- the step
 
-// One unit per CTA, kVec elements per thread at a time.
+// One unit per CTA, kVec elements per thread at a time.  The last warp keeps
+// the books: it reads the words that live from step to step and, in the CTA
+// that is last to have read them, writes the next step's, while the others
+// work on the elements.
 template <typename P, typename G, bool S8>
-__global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_constant__ StepParams prm) {
+__global__ void __launch_bounds__(kStepThreads + 32) adamw_kernel(const __grid_constant__ StepParams prm) {
   __shared__ float s_coef[2];
   __shared__ unsigned s_step;
+  const GroupUnit u = prm.units[blockIdx.x];   // never written after the group's creation
+  wait_for_predecessors();
+  let_successor_start();
   if (prm.report && prm.skip_nonfinite && prm.report->nonfinite) return;   // the same answer in every CTA
-  if (threadIdx.x == 0) {
+  if (threadIdx.x >= kStepThreads) {
     volatile GroupState* st = prm.state;
-    const unsigned long long step = st->step;
-    const double p1 = st->power1, p2 = st->power2;
-    s_coef[0] = st->inv_bias1;
-    s_coef[1] = st->inv_sqrt_bias2;
-    s_step = (unsigned)(step + 1);
-    // the last CTA to have read the words writes the next step's
-    __threadfence();
-    if (atomicAdd(&prm.state->arrived_step, 1u) == gridDim.x - 1) {
-      const double n1 = p1 * prm.beta1_d, n2 = p2 * prm.beta2_d;
-      st->step = step + 1;
-      st->power1 = n1;
-      st->power2 = n2;
-      st->inv_bias1 = (float)(1.0 / (1.0 - n1));
-      st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
-      st->arrived_step = 0;
+    unsigned long long step = 0;
+    double p1 = 0, p2 = 0;
+    if (threadIdx.x == kStepThreads) {
+      step = st->step;
+      p1 = st->power1, p2 = st->power2;
+      s_coef[0] = st->inv_bias1;
+      s_coef[1] = st->inv_sqrt_bias2;
+      s_step = (unsigned)(step + 1);
     }
+    __syncthreads();
+    if (threadIdx.x == kStepThreads) {
+      __threadfence();
+      if (atomicAdd(&prm.state->arrived_step, 1u) == gridDim.x - 1) {
+        const double n1 = p1 * prm.beta1_d, n2 = p2 * prm.beta2_d;
+        st->step = step + 1;
+        st->power1 = n1;
+        st->power2 = n2;
+        st->inv_bias1 = (float)(1.0 / (1.0 - n1));
+        st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
+        st->arrived_step = 0;
+      }
+    }
+    return;
   }
-  const GroupUnit u = prm.units[blockIdx.x];
   const GroupTensor t = prm.tensors[u.tensor];
   const float lr = prm.lr_dev ? *prm.lr_dev : prm.lr;
   const float gscale = prm.report ? prm.report->scale : prm.grad_scale;
@@ -195,29 +205,38 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
   P* param = static_cast<P*>(t.param) + u.start;
   const G* grad = static_cast<const G*>(t.grad) + u.start;
   const bool vec = t.aligned && vec_ok(static_cast<const G*>(t.grad));
-  __syncthreads();
-  const float alpha = lr * s_coef[0], rs = s_coef[1];
-  const unsigned key = S8 ? step_key(prm.seed, s_step) : 0;
 
   // every thread of a warp makes the same number of turns: 8-bit blocks
   // share their exponent by shuffles
   const unsigned turns = (u.n + kStepThreads * kVec - 1) / (kStepThreads * kVec);
-  for (unsigned turn = 0; turn < turns; ++turn) {
-    const unsigned at = (turn * kStepThreads + threadIdx.x) * kVec;
-    const int n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
-    float p[kVec], g[kVec], m[kVec], v[kVec];
+  unsigned at = threadIdx.x * kVec;
+  int n = 0;
+  float p[kVec], g[kVec], m[kVec], v[kVec];
+  uint2 cm, cv;
+  int em = 0, ev = 0;
+  auto load = [&] {
+    n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
     load_some(grad + at, n, vec, g);
     load_some(param + at, n, vec, p);
     if constexpr (S8) {
       const unsigned long long i = u.start + at;
-      const uint2 cm = load_codes(static_cast<const uint8_t*>(t.m) + i, n, vec);
-      const uint2 cv = load_codes(static_cast<const uint8_t*>(t.v) + i, n, vec);
-      const int em = n ? t.m_scale[i / XP_STATE8_BLOCK] : 0, ev = n ? t.v_scale[i / XP_STATE8_BLOCK] : 0;
-      decode_codes<true>(cm, em, m);
-      decode_codes<false>(cv, ev, v);
+      cm = load_codes(static_cast<const uint8_t*>(t.m) + i, n, vec);
+      cv = load_codes(static_cast<const uint8_t*>(t.v) + i, n, vec);
+      em = n ? t.m_scale[i / XP_STATE8_BLOCK] : 0;
+      ev = n ? t.v_scale[i / XP_STATE8_BLOCK] : 0;
     } else {
       load_some(static_cast<const float*>(t.m) + u.start + at, n, vec, m);
       load_some(static_cast<const float*>(t.v) + u.start + at, n, vec, v);
+    }
+  };
+  load();
+  __syncthreads();
+  const float alpha = lr * s_coef[0], rs = s_coef[1];
+  const unsigned key = S8 ? step_key(prm.seed, s_step) : 0;
+  for (unsigned turn = 0; turn < turns;) {
+    if constexpr (S8) {
+      decode_codes<true>(cm, em, m);
+      decode_codes<false>(cv, ev, v);
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -237,9 +256,9 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
       unsigned top = top_exponent(m) << 16 | top_exponent(v);
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
+      em = (int)(top >> 16), ev = (int)(top & 0xffffu);
       unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi + key;   // kVec positions share the high word
-      uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+      cm = make_uint2(0, 0), cv = make_uint2(0, 0);
 #pragma unroll
       for (int k = 0; k < kVec; ++k, h += kPosLo) {
         const unsigned r = mix(h);
@@ -258,6 +277,9 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
       store_some(static_cast<float*>(t.m) + u.start + at, n, vec, m);
       store_some(static_cast<float*>(t.v) + u.start + at, n, vec, v);
     }
+    if (++turn == turns) break;
+    at += kStepThreads * kVec;
+    load();
   }
 }
 
@@ -277,6 +299,8 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
   __shared__ double s_sum[kNormThreads / 32];
   __shared__ bool s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_predecessors();
+  let_successor_start();
   double sum = 0.0;
   for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) {
     const GroupUnit u = prm.units[k];
@@ -329,10 +353,14 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
 // ---------------------------------------------------------------- small ones
 
 __global__ void set_grads_kernel(const __grid_constant__ SetGradsParams prm) {
+  wait_for_predecessors();
+  let_successor_start();
   for (int i = threadIdx.x; i < prm.n; i += blockDim.x) prm.tensors[prm.first + i].grad = prm.grad[i];
 }
 
 __global__ void set_step_kernel(GroupState* s, unsigned long long step, double p1, double p2) {
+  wait_for_predecessors();
+  let_successor_start();
   s->step = step;
   s->power1 = p1;
   s->power2 = p2;
@@ -344,6 +372,8 @@ __global__ void set_step_kernel(GroupState* s, unsigned long long step, double p
 
 template <typename O>
 __global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_constant__ DecodeParams prm) {
+  wait_for_predecessors();
+  let_successor_start();
   const int which = blockIdx.y;
   O* out = static_cast<O*>(prm.out[which]);
   if (!out) return;
@@ -363,8 +393,7 @@ __global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_const
 
 template <typename P, typename G, bool S8>
 cudaError_t run_adamw(const StepParams& p, unsigned nunits, cudaStream_t st) {
-  adamw_kernel<P, G, S8><<<nunits, kStepThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(adamw_kernel<P, G, S8>, dim3(nunits), kStepThreads + 32, 0, 1, st, p);
 }
 
 }  // namespace
@@ -381,35 +410,23 @@ cudaError_t launch_adamw(const StepParams& p, unsigned nunits, int param_dtype, 
   return s8 ? run_adamw<H, H, true>(p, nunits, st) : run_adamw<H, H, false>(p, nunits, st);
 }
 
-int norm_ctas(unsigned nunits) { return (int)(nunits < (unsigned)kNormMaxCtas ? nunits : (unsigned)kNormMaxCtas); }
-
 cudaError_t launch_grad_norm(const NormParams& p, int grad_dtype, cudaStream_t st) {
-  const int grid = norm_ctas(p.nunits) > 0 ? norm_ctas(p.nunits) : 1;
-  if (grad_dtype == XP_F32)
-    grad_norm_kernel<float><<<grid, kNormThreads, 0, st>>>(p);
-  else
-    grad_norm_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const unsigned grid = p.nunits < (unsigned)kNormMaxCtas ? p.nunits : (unsigned)kNormMaxCtas;
+  return launch_dependent(grad_dtype == XP_F32 ? grad_norm_kernel<float> : grad_norm_kernel<__nv_bfloat16>, dim3(grid), kNormThreads, 0, 1, st, p);
 }
 
 cudaError_t launch_set_grads(const SetGradsParams& p, cudaStream_t st) {
-  set_grads_kernel<<<1, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(set_grads_kernel, dim3(1), 256, 0, 1, st, p);
 }
 
 cudaError_t launch_set_step(GroupState* s, unsigned long long step, double p1, double p2, cudaStream_t st) {
-  set_step_kernel<<<1, 1, 0, st>>>(s, step, p1, p2);
-  return cudaGetLastError();
+  return launch_dependent(set_step_kernel, dim3(1), 1, 0, 1, st, s, step, p1, p2);
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int out_dtype, cudaStream_t st) {
   const unsigned long long per = (unsigned long long)kStepThreads * kVec;
   const dim3 grid((unsigned)((p.count + per - 1) / per), 2);
-  if (out_dtype == XP_F32)
-    decode_kernel<float><<<grid, kStepThreads, 0, st>>>(p);
-  else
-    decode_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(out_dtype == XP_F32 ? decode_kernel<float> : decode_kernel<__nv_bfloat16>, grid, kStepThreads, 0, 1, st, p);
 }
 
 }  // namespace xp

@@ -102,9 +102,9 @@ struct NormRowsParams {
   unsigned long long x_stride, dy_stride, out_stride;
   unsigned long long rows;
   unsigned cols;
-  unsigned slice;                        // columns of one CTA of a row's cluster
+  int threads;                           // of a row (of one CTA of its cluster)
   unsigned nparts;                       // backward: CTAs (per slice) that leave partial sums
-  int stages;                            // backward: rows in flight per group
+  int stages;                            // rows in flight per group
   float eps;
   int gamma_bf16;
   int accumulate;
@@ -116,7 +116,6 @@ cudaError_t launch_grad_norm(const NormParams& p, int grad_dtype, cudaStream_t s
 cudaError_t launch_set_grads(const SetGradsParams& p, cudaStream_t st);
 cudaError_t launch_set_step(GroupState* s, unsigned long long step, double beta1, double beta2, cudaStream_t st);
 cudaError_t launch_decode(const DecodeParams& p, int out_dtype, cudaStream_t st);
-int norm_ctas(unsigned nunits);
 
 cudaError_t launch_ln_forward(NormRowsParams& p, int dtype, cudaStream_t st);
 // Writes the number of partial rows to *nparts; workspace holds nparts * 2 * cols floats.
