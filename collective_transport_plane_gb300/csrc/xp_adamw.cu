@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kStepThreads + 32) adamw_kernel(const __grid_c
 
 // ---------------------------------------------------------------- the norm
 
-__device__ __forceinline__ double warp_sum(double x) {
+template <typename F>
+__device__ __forceinline__ F warp_sum(F x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -293,7 +294,8 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 // Each CTA adds up its units' squares and leaves one fp64 sum; the CTA that
 // arrives last adds the sums up in their order, so the result does not depend
-// on which CTA that is.
+// on which CTA that is.  fp32 up to a warp's sum, fp64 above: an SM does 2 fp64
+// additions per clock.
 template <typename G>
 __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormParams prm) {
   __shared__ double s_sum[kNormThreads / 32];
@@ -312,20 +314,18 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
       float g[kVec];
       load_some(grad + at, (int)min((unsigned)kVec, u.n - at), vec, g);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] += g[i] * g[i];
+      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(g[i], g[i], acc[i]);
     }
-    sum += (double)(((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+    const float w = warp_sum(((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+    if (lane == 0) sum += (double)w;
   }
-  sum = warp_sum(sum);
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
-  if (warp == 0) {
-    sum = warp_sum(lane < kNormThreads / 32 ? s_sum[lane] : 0.0);
-    if (lane == 0) {
-      prm.partial[blockIdx.x] = sum;
-      __threadfence();
-      s_last = atomicAdd(&prm.state->arrived_norm, 1u) == gridDim.x - 1;
-    }
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kNormThreads / 32; ++w) sum += s_sum[w];
+    prm.partial[blockIdx.x] = sum;
+    __threadfence();
+    s_last = atomicAdd(&prm.state->arrived_norm, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!s_last) return;

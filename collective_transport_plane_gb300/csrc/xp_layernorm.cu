@@ -5,9 +5,7 @@
 // operations on it: HBM bounds them.  A row belongs to a group of threads
 // that keeps it on chip between its sums and its output: a warp (short rows),
 // a part of a CTA or a whole one, or the CTAs of a thread-block cluster, each
-// with a slice of the row (long rows, and rows too few to fill the GPU).  A
-// grid of as many CTAs as the GPU holds walks over the rows; asynchronous
-// copies bring the next rows into shared memory while one is worked on.
+// with a slice of the row (long rows, and rows too few to fill the GPU).
 #include "xp_train_device.cuh"
 
 namespace xp {
@@ -26,95 +24,77 @@ __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float f) { *p = f; }
 __device__ __forceinline__ void put(bf16* p, float f) { *p = __float2bfloat16_rn(f); }
 
-// ---- units: the V elements a thread takes at once.  Rows that allow it move
-// in units of 16 bytes; others (lengths, strides or addresses that are no
-// multiple of 16 bytes) in units of 4 bytes, one fp32 or two bf16, read from
+// ---- units: the V elements a thread takes at once, as V / 2 pairs.  Rows that
+// allow it move in units of 16 bytes; others (lengths, strides or addresses
+// that are no multiple of 16 bytes) in units of two elements, read from
 // shared memory at any offset.
 template <typename T, int V>
 constexpr bool kWide = V * sizeof(T) == 16;
 
-template <typename T, int V>
-__device__ __forceinline__ void unpack16(uint4 q, float (&f)[V]) {
-  const unsigned w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      f[i] = __uint_as_float(w[i]);
-    } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ float lo_of(unsigned w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
+
+template <typename T, int P>
+__device__ __forceinline__ void unpack16(uint4 q, float2 (&f)[P]) {
+  if constexpr (sizeof(T) == 4) {
+    f[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    f[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+  } else {
+    f[0] = make_float2(lo_of(q.x), hi_of(q.x));
+    f[1] = make_float2(lo_of(q.y), hi_of(q.y));
+    f[2] = make_float2(lo_of(q.z), hi_of(q.z));
+    f[3] = make_float2(lo_of(q.w), hi_of(q.w));
   }
 }
-template <typename T, int V>
-__device__ __forceinline__ uint4 pack16(const float (&f)[V]) {
-  if constexpr (sizeof(T) == 4) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  } else {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    return *reinterpret_cast<uint4*>(h);
-  }
+__device__ __forceinline__ unsigned pack2(float2 f) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const unsigned*>(&h);
 }
 // The first n elements of a unit (wide units are whole or absent) to global
-// memory; p4: a 4-byte unit's address allows one store.
-template <typename T, int V>
-__device__ __forceinline__ void store_unit(T* p, int n, bool p4, const float (&f)[V]) {
-  if constexpr (kWide<T, V>) {
-    if (n > 0) *reinterpret_cast<uint4*>(p) = pack16<T, V>(f);
-  } else if constexpr (V == 2) {
-    if (n >= 2 && p4) {
-      *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0], f[1]);
-    } else {
-      if (n > 0) put(p, f[0]);
-      if (n > 1) put(p + 1, f[1]);
-    }
+// memory; p4: a pair of bf16 may go in one store.
+template <typename T, int P>
+__device__ __forceinline__ void store_unit(T* p, int n, bool p4, const float2 (&f)[P]) {
+  if constexpr (P == 4) {
+    if (n > 0) *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+  } else if constexpr (P == 2) {
+    if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  } else if (sizeof(T) == 2 && n >= 2 && p4) {
+    *reinterpret_cast<unsigned*>(p) = pack2(f[0]);
   } else {
-    if (n > 0) put(p, f[0]);
+    if (n > 0) put(p, f[0].x);
+    if (n > 1) put(p + 1, f[0].y);
   }
 }
-// gamma or beta: its own type, `none` where there is none
-template <int V>
-__device__ __forceinline__ void load_w(const void* w, int is_bf16, unsigned c, int n, float none, float (&f)[V]) {
+// A unit of gamma or beta; `none` where there is none.  No branches: the loads
+// of several units are in flight together.
+template <typename W, int P>
+__device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float none, float2 (&f)[P]) {
+  const W* p = static_cast<const W*>(w) + c;
+  const bool has = w && n > 0;
+  if constexpr (P == 1) {
+    f[0].x = has ? to_f(__ldg(p)) : none;
+    f[0].y = has && n > 1 ? to_f(__ldg(p + 1)) : none;
+  } else if constexpr (sizeof(W) == 4) {
+    const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = none;
-  if (!w || n <= 0) return;
-  if (is_bf16) {
-    const bf16* p = static_cast<const bf16*>(w) + c;
-    if constexpr (V == 8) {
-      if (n >= V) return unpack16<bf16, V>(__ldg(reinterpret_cast<const uint4*>(p)), f);
-    } else if constexpr (V == 4) {
-      if (n >= V) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-        f[0] = __uint_as_float(q.x << 16);
-        f[1] = __uint_as_float(q.x & 0xffff0000u);
-        f[2] = __uint_as_float(q.y << 16);
-        f[3] = __uint_as_float(q.y & 0xffff0000u);
-        return;
-      }
+    for (int i = 0; i < P / 2; ++i) {
+      const float4 q = has ? __ldg(reinterpret_cast<const float4*>(p) + i) : rest;
+      f[2 * i] = make_float2(q.x, q.y);
+      f[2 * i + 1] = make_float2(q.z, q.w);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) f[i] = __bfloat162float(p[i]);
   } else {
-    const float* p = static_cast<const float*>(w) + c;
-    if constexpr (V >= 4) {
-      if (n >= V) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
-          f[4 * i] = q.x;
-          f[4 * i + 1] = q.y;
-          f[4 * i + 2] = q.z;
-          f[4 * i + 3] = q.w;
-        }
-        return;
-      }
+    const unsigned rest = pack2(both(none));
+    uint4 q = make_uint4(rest, rest, rest, rest);
+    if constexpr (P == 4) {
+      q = has ? __ldg(reinterpret_cast<const uint4*>(p)) : q;
+    } else {
+      const uint2 h = has ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(rest, rest);
+      q.x = h.x, q.y = h.y;
     }
+    const unsigned words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) f[i] = __ldg(p + i);
+    for (int i = 0; i < P; ++i) f[i] = make_float2(lo_of(words[i]), hi_of(words[i]));
   }
 }
 
@@ -123,6 +103,15 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+// Two sums at once: lanes 0-15 end with x's, lanes 16-31 with y's.
+__device__ __forceinline__ float warp_sum_halves(float x, float y) {
+  const bool upper = threadIdx.x & 16;
+  float mine = upper ? y : x;
+  mine += __shfl_xor_sync(0xffffffffu, upper ? x : y, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  return mine;
 }
 __device__ __forceinline__ void group_bar(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
@@ -146,21 +135,43 @@ __device__ __forceinline__ void store_remote(const float2* p, unsigned rank, flo
 }
 
 // Shared words of the sums.  Two buffers in turn: a thread that reads one
-// meets the others at the next sum's barrier before it is written again.
-struct SumWords {
-  float2 warp[2][kMaxWarps];
+// meets the others at the next sum's barrier before it is written again.  A
+// group's warps have kWarpWords words or a multiple of it, 0 where there is
+// no warp.
+constexpr int kWarpWords = 8;
+struct alignas(16) SumWords {
+  float2 warp[2][kMaxWarps + kWarpWords];
   float2 cta[2][kMaxCluster8];
 };
+__device__ __forceinline__ void clear_words(SumWords& w) {   // before a barrier
+  float2* p = &w.warp[0][0];
+  for (int i = threadIdx.x; i < 2 * (kMaxWarps + kWarpWords); i += blockDim.x) p[i] = make_float2(0.f, 0.f);
+}
 
 // Both components summed over the row's threads, the same value in each; the
 // order of the additions is fixed.  In steps, so that several rows share a
 // barrier: each warp's sum, the group meets, the warps' sums added up; in a
-// cluster then the same among its CTAs, through their shared memory.
-template <int MODE>
-__device__ __forceinline__ float2 row_partial(float2 v, SumWords& w, int buf) {
-  v.x = warp_sum(v.x);
-  v.y = warp_sum(v.y);
-  if (MODE != kWarp && (threadIdx.x & 31) == 0) w.warp[buf][threadIdx.x >> 5] = v;
+// cluster then the same among its CTAs, through their shared memory.  (TWO:
+// else x alone.)
+__device__ __forceinline__ int words_span(int threads) { return ((threads >> 5) + kWarpWords - 1) & ~(kWarpWords - 1); }
+template <int MODE, bool TWO = true>
+__device__ __forceinline__ float2 row_partial(float2 v, SumWords& w, int buf, int group, int threads) {
+  if constexpr (MODE == kWarp) {
+    if constexpr (TWO) {
+      const float h = warp_sum_halves(v.x, v.y);
+      return make_float2(__shfl_sync(0xffffffffu, h, 0), __shfl_sync(0xffffffffu, h, 16));
+    }
+    return make_float2(warp_sum(v.x), 0.f);
+  }
+  const int lane = threadIdx.x & 31;
+  float* mine = reinterpret_cast<float*>(w.warp[buf] + group * words_span(threads) + (threadIdx.x >> 5) - group * (threads >> 5));
+  if constexpr (TWO) {
+    const float h = warp_sum_halves(v.x, v.y);
+    if ((lane & 15) == 0) mine[lane >> 4] = h;
+  } else {
+    v.x = warp_sum(v.x);
+    if (lane == 0) *mine = v.x;
+  }
   return v;
 }
 template <int MODE>
@@ -168,37 +179,42 @@ __device__ __forceinline__ void row_meet(int group, int threads) {
   if constexpr (MODE == kCluster) __syncthreads();
   if constexpr (MODE == kCta) group_bar(group, threads);
 }
-template <int MODE>
+template <int MODE, bool TWO = true>
 __device__ __forceinline__ float2 row_total(float2 v, const SumWords& w, int buf, int group, int threads) {
-  if constexpr (MODE != kWarp) {
-    const int lane = threadIdx.x & 31, nw = threads >> 5;
-    v = lane < nw ? w.warp[buf][group * nw + lane] : make_float2(0.f, 0.f);
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
+  if constexpr (MODE == kWarp) return v;
+  const int span = words_span(threads);
+  const float2* all = w.warp[buf] + group * span;
+  v = make_float2(0.f, 0.f);
+  for (int at = 0; at < span; at += kWarpWords) {
+#pragma unroll
+    for (int i = 0; i < kWarpWords; i += 2) {
+      const float4 q = *reinterpret_cast<const float4*>(all + at + i);
+      if constexpr (TWO)
+        v = __fadd2_rn(__fadd2_rn(v, make_float2(q.x, q.y)), make_float2(q.z, q.w));
+      else
+        v.x = (v.x + q.x) + q.z;
+    }
   }
   return v;
 }
 __device__ __forceinline__ void row_send(float2 v, SumWords& w, int buf) {
   if (threadIdx.x < cluster_size()) store_remote(&w.cta[buf][cluster_rank()], threadIdx.x, v);
 }
-__device__ __forceinline__ float2 row_join(const SumWords& w, int buf, unsigned n) {
+__device__ __forceinline__ float2 row_join(const SumWords& w, int buf) {
   float2 v = make_float2(0.f, 0.f);
-  for (unsigned r = 0; r < n; ++r) {
-    v.x += w.cta[buf][r].x;
-    v.y += w.cta[buf][r].y;
-  }
+  for (unsigned r = 0, n = cluster_size(); r < n; ++r) v = __fadd2_rn(v, w.cta[buf][r]);
   return v;
 }
-template <int MODE>
+template <int MODE, bool TWO>
 __device__ __forceinline__ float2 row_sum(float2 v, SumWords& w, int buf, int group, int threads) {
-  v = row_partial<MODE>(v, w, buf);
+  v = row_partial<MODE, TWO>(v, w, buf, group, threads);
   row_meet<MODE>(group, threads);
-  v = row_total<MODE>(v, w, buf, group, threads);
+  v = row_total<MODE, TWO>(v, w, buf, group, threads);
   if constexpr (MODE == kCluster) {
     row_send(v, w, buf);
     cluster_arrive();
     cluster_wait();
-    v = row_join(w, buf, cluster_size());
+    v = row_join(w, buf);
   }
   return v;
 }
@@ -233,67 +249,80 @@ __host__ __device__ constexpr unsigned row_bytes(unsigned threads, unsigned e) {
   return kWide<T, V> ? e * threads * (unsigned)sizeof(T) : (e * threads * (unsigned)sizeof(T) + 48u) & ~15u;
 }
 
-// One matrix's rows, as the threads of a group see them.  Past a row's end
-// they read zeros.
+// How the threads of a group bring a row of a matrix.  Past its end they read
+// zeros.
 //
 // Wide units: a thread copies the units it will use itself, unit k at slot
 // k * threads + thread, so nothing but its own copies has to have landed; it
 // clears the slots of units that the row does not have once.
 //
-// 4-byte units: the group copies the 16-byte pieces that cover the row, at
-// the row's own offset within them, and zeros behind them up to what a row at
-// the largest offset would touch; the group meets before it reads.  A first
-// piece that begins before the matrix does is copied element by element.
+// Pairs: the group copies the 16-byte pieces that cover the row, at the row's
+// own offset within them, and zeros behind them up to what a row at the
+// largest offset would touch; the group meets before it reads.  A first piece
+// that begins before the matrix does is copied element by element.
 template <typename T, int V>
-struct Rows {
-  const T* base;      // row 0, first column of this CTA's slice
-  u64 stride;
-  const T* lo;        // the matrix's first element
-  int cols;           // of the slice
-
-  __device__ __forceinline__ const T* row(u64 r) const { return base + r * stride; }
-
-  __device__ __forceinline__ void fetch_unit(const T* a, unsigned smem, int u) const {
-    if (u * V < cols) copy_async16(smem + u * 16, a + u * V);
-  }
-  __device__ __forceinline__ void fetch_pieces(u64 r, char* smem, int tid, int threads) const {
-    const char* a = reinterpret_cast<const char*>(row(r));
-    const int len = cols * (int)sizeof(T), off = (int)(reinterpret_cast<uintptr_t>(a) & 15u);
-    const char* first = a - off;
-    const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(lo) & ~(uintptr_t)15);   // of which 0 bytes are read
-    const int pieces = (len + 29) >> 4;
-    const unsigned to = (unsigned)__cvta_generic_to_shared(smem);
-    for (int j = tid; j < pieces; j += threads) {
-      const int here = min(max(off + len - 16 * j, 0), 16);   // bytes of this piece up to the row's end
-      if (j == 0 && first < reinterpret_cast<const char*>(lo)) {
-        for (int b = 0; b < 16; b += sizeof(T))
-          *reinterpret_cast<T*>(smem + b) = b >= off && b < here ? *reinterpret_cast<const T*>(first + b) : T(0.f);
-      } else {
-        copy_async16(to + 16 * j, here ? first + 16 * j : nothing, here);
-      }
+__device__ __forceinline__ void fetch_unit(const T* row, int cols, unsigned smem, int u) {
+  if (u * V < cols) copy_async16(smem + u * 16, row + u * V);
+}
+template <typename T>
+__device__ __forceinline__ void fetch_pieces(const T* row, int cols, const T* matrix, char* smem, int tid, int threads) {
+  const char* a = reinterpret_cast<const char*>(row);
+  const int len = cols * (int)sizeof(T), off = (int)(reinterpret_cast<uintptr_t>(a) & 15u);
+  const char* first = a - off;
+  const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(matrix) & ~(uintptr_t)15);   // of which 0 bytes are read
+  const int pieces = (len + 29) >> 4;
+  const unsigned to = (unsigned)__cvta_generic_to_shared(smem);
+  for (int j = tid; j < pieces; j += threads) {
+    const int here = min(max(off + len - 16 * j, 0), 16);   // bytes of this piece up to the row's end
+    if (j == 0 && first < reinterpret_cast<const char*>(matrix)) {
+      for (int b = 0; b < 16; b += sizeof(T))
+        *reinterpret_cast<T*>(smem + b) = b >= off && b < here ? *reinterpret_cast<const T*>(first + b) : T(0.f);
+    } else {
+      copy_async16(to + 16 * j, here ? first + 16 * j : nothing, here);
     }
   }
-  // Unit u of row r.
-  __device__ __forceinline__ void read(u64 r, const char* smem, int u, float (&f)[V]) const {
+}
+
+// Loads from shared memory by its 32-bit address.  (Volatile: they stay behind
+// the wait for the copies.)
+__device__ __forceinline__ uint4 load_shared16(unsigned a) {
+  uint4 q;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(a));
+  return q;
+}
+__device__ __forceinline__ unsigned load_shared4(unsigned a) {
+  unsigned w;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+  return w;
+}
+
+// A row in shared memory.
+template <typename T, int V>
+struct Landed {
+  unsigned at;
+  unsigned select;   // pairs of bf16: which halves of two words are a pair
+
+  __device__ __forceinline__ Landed(unsigned smem, const T* row) : at(smem), select(0) {
+    if constexpr (!kWide<T, V>) {
+      const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);
+      at = smem + (off & ~3u);
+      select = off & 2 ? 0x5432u : 0x3210u;
+    }
+  }
+  __device__ __forceinline__ void read(int u, float2 (&f)[V / 2]) const {
     if constexpr (kWide<T, V>) {
-      unpack16<T, V>(*reinterpret_cast<const uint4*>(smem + 16 * u), f);
+      unpack16<T, V / 2>(load_shared16(at + 16 * u), f);
+    } else if constexpr (sizeof(T) == 4) {
+      f[0] = make_float2(__uint_as_float(load_shared4(at + 8 * u)), __uint_as_float(load_shared4(at + 8 * u + 4)));
     } else {
-      const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(row(r)) & 15u);
-      const unsigned* w = reinterpret_cast<const unsigned*>(smem + (off & ~3u)) + u;
-      if constexpr (V == 1) {
-        f[0] = __uint_as_float(w[0]);
-      } else {
-        unsigned q = w[0];
-        if (off & 2) q = __byte_perm(q, w[1], 0x5432);
-        f[0] = __uint_as_float(q << 16);
-        f[1] = __uint_as_float(q & 0xffff0000u);
-      }
+      const unsigned q = __byte_perm(load_shared4(at + 4 * u), load_shared4(at + 4 * u + 4), select);
+      f[0] = make_float2(lo_of(q), hi_of(q));
     }
   }
 };
 
 // Clears what no copy will ever write: a thread's slots of units its rows do
-// not have, or (4-byte units) all of the group's `bytes`.
+// not have, or (pairs) all of the group's rows.
 template <typename T, int V, int NV>
 __device__ __forceinline__ void clear_slots(char* slot, unsigned row_len, int nrows, int cols, int tid, int threads) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -319,118 +348,117 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 
 // ---------------------------------------------------------------- forward
 
-// The row stays in registers between its sums: E elements per thread, its
-// unit k at column (k * threads + thread) * V.
-template <typename T, int V, int E, int MODE, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
+// One row per group, in registers from its load to its output: E elements per
+// thread, unit k at column (k * threads + thread) * V.  The CTAs are small and
+// many: eight of 128 threads are on an SM, so that one's sums are another's
+// loads, and the hardware hands the rows out.
+//   Measured at 16384 x 4096 bf16 (268 MB, a plain copy of it takes 42 us):
+//   32 elements per thread 43 us, 16 elements 49, 8 elements 75; one
+//   persistent CTA per SM with a warp per row and rows copied ahead 50.
+template <typename T, int V, int E, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
   __shared__ SumWords words;
-  constexpr int NV = E / V;
+  constexpr int NV = E / V, P = V / 2;
   constexpr bool WIDE = kWide<T, V>;
-  const int threads = MODE == kWarp ? 32 : prm.threads;
-  const int group = MODE == kCluster ? 0 : threadIdx.x / threads;
+  const int threads = MODE == kWarp ? 32 : blockDim.x;
+  const int group = MODE == kWarp ? threadIdx.x >> 5 : 0;
   const int tid = threadIdx.x - group * threads;
-  const int groups = MODE == kCluster ? 1 : blockDim.x / threads;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
+  const u64 row = MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + group : blockIdx.x / csize;
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
   const int cols = c0 < prm.cols ? (int)min((unsigned)E * threads, prm.cols - c0) : 0;   // a cluster's last CTA may have none
-  const int stages = prm.stages;
-  const unsigned len = row_bytes<T, V>(threads, E);
-  char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * stages * len;   // [group][stage]
-  const unsigned slot_s = (unsigned)__cvta_generic_to_shared(slot);
-  const Rows<T, V> x = {static_cast<const T*>(prm.x) + c0, prm.x_stride, static_cast<const T*>(prm.x), cols};
-  const u64 step = (u64)(gridDim.x / csize) * groups;
-  const u64 first = (u64)(blockIdx.x / csize) * groups + group;
+  const T* x = static_cast<const T*>(prm.x) + row * prm.x_stride + c0;
   if (MODE == kCluster) cluster_arrive();   // its end: every CTA of the cluster runs
-  clear_slots<T, V, NV>(slot, len, stages, cols, tid, threads);
-  if constexpr (!WIDE) group_sync<MODE>(group, threads);
+  if constexpr (MODE != kWarp) clear_words(words);
   wait_for_predecessors();
   let_successor_start();
+  if (MODE == kWarp && row >= prm.rows) return;
 
-  auto fetch = [&](u64 row, int stage) {
-    if (row < prm.rows) {
-      if constexpr (WIDE) {
+  float2 f[NV][P];
+  if constexpr (WIDE) {
+    const uint4* a = reinterpret_cast<const uint4*>(x);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) x.fetch_unit(x.row(row), slot_s + stage * len, k * threads + tid);
-      } else {
-        x.fetch_pieces(row, slot + stage * len, tid, threads);
-      }
+    for (int k = 0; k < NV; ++k) {
+      const int u = k * threads + tid;
+      unpack16<T, P>(u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0), f[k]);
     }
+    if constexpr (MODE != kWarp) __syncthreads();   // the words are clear
+  } else {
+    const unsigned len = row_bytes<T, V>(threads, E);
+    char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * len;
+    clear_slots<T, V, NV>(slot, len, 1, cols, tid, threads);
+    if constexpr (MODE == kWarp) __syncwarp(); else __syncthreads();
+    fetch_pieces(x, cols, static_cast<const T*>(prm.x), slot, tid, threads);
     commit();
-  };
-  for (int s = 0; s < stages; ++s) fetch(first + s * step, s);
-  float g[E], b[E];
+    wait_groups(0);
+    if constexpr (MODE == kWarp) __syncwarp(); else __syncthreads();
+    const Landed<T, V> here((unsigned)__cvta_generic_to_shared(slot), x);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) here.read(k * threads + tid, f[k]);
+  }
+  float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * threads + tid) * V;
-    float w[V];
-    load_w<V>(prm.gamma, prm.gamma_bf16, c0 + c, cols - c, 1.f, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) g[k * V + i] = w[i];
-    load_w<V>(prm.beta, prm.gamma_bf16, c0 + c, cols - c, 0.f, w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) b[k * V + i] = w[i];
+    for (int i = 0; i < P; ++i) sum = __fadd2_rn(sum, f[k][i]);
   }
   if (MODE == kCluster) cluster_wait();
   const float inv = 1.0f / (float)prm.cols;
-  int stage = 0;
-  for (u64 row = first; row < prm.rows; row += step) {
-    wait_groups(stages - 1);
-    if constexpr (!WIDE) group_sync<MODE>(group, threads);   // the others' copies have landed too
-    float f[NV][V];
-    float sum = 0.f;
+  const float mean = row_sum<MODE, false>(make_float2(sum.x + sum.y, 0.f), words, 0, 0, threads).x * inv;
+  float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      x.read(row, slot + stage * len, k * threads + tid, f[k]);
+  for (int k = 0; k < NV; ++k) {
+    const int n = cols - (k * threads + tid) * V;   // wide units are whole or absent
+    const float2 m = make_float2(n > 0 ? -mean : 0.f, (WIDE ? n > 0 : n > 1) ? -mean : 0.f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += f[k][i];
+    for (int i = 0; i < P; ++i) {
+      f[k][i] = __fadd2_rn(f[k][i], m);
+      sq = __ffma2_rn(f[k][i], f[k][i], sq);
     }
-    const float mean = row_sum<MODE>(make_float2(sum, 0.f), words, 0, group, threads).x * inv;
-    // the row has been read: by this thread (wide units), or by the whole group (that met in the sum)
-    if (!WIDE && MODE == kWarp) __syncwarp();
-    fetch(row + (u64)stages * step, stage);
-    if (++stage == stages) stage = 0;
-    float sq = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int n = cols - (k * threads + tid) * V;   // wide units are whole or absent
-      const float m = n > 0 ? mean : 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        f[k][i] -= WIDE || i < n ? m : 0.f;
-        sq = fmaf(f[k][i], f[k][i], sq);
-      }
-    }
-    const float var = row_sum<MODE>(make_float2(sq, 0.f), words, 1, group, threads).x * inv;
-    const float rstd = 1.0f / sqrtf(var + prm.eps);
-    if (tid == 0 && c0 == 0) {
-      if (prm.mean) prm.mean[row] = mean;
-      if (prm.rstd) prm.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(prm.out) + row * prm.out_stride + c0;
-    const bool p4 = (reinterpret_cast<uintptr_t>(y) & 3u) == 0;
+  }
+  const float var = row_sum<MODE, false>(make_float2(sq.x + sq.y, 0.f), words, 1, 0, threads).x * inv;
+  const float rstd = 1.0f / sqrtf(var + prm.eps);
+  if (tid == 0 && c0 == 0) {
+    if (prm.mean) prm.mean[row] = mean;
+    if (prm.rstd) prm.rstd[row] = rstd;
+  }
+  T* y = static_cast<T*>(prm.out) + row * prm.out_stride + c0;
+  const bool p4 = (reinterpret_cast<uintptr_t>(y) & 3u) == 0;
+  auto output = [&](auto w) {
+    typedef decltype(w) W;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * threads + tid) * V;
+      float2 g[P], b[P];
+      load_w<W, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
+      load_w<W, P>(prm.beta, c0 + c, cols - c, 0.f, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[k][i] = fmaf(f[k][i] * rstd, g[k * V + i], b[k * V + i]);
-      store_unit<T, V>(y + c, cols - c, p4, f[k]);
+      for (int i = 0; i < P; ++i) f[k][i] = __ffma2_rn(__fmul2_rn(f[k][i], both(rstd)), g[i], b[i]);
+      store_unit<T, P>(y + c, cols - c, p4, f[k]);
     }
-  }
+  };
+  if (prm.gamma_bf16)
+    output(bf16());
+  else
+    output(float());
 }
 
 // ---------------------------------------------------------------- backward
 
-// Each group walks over its rows, R at a time, and keeps its columns' sums of
-// dgamma and dbeta in registers.  A row is read twice from shared memory,
-// for its sums and for dx: with d = x - mean and a = dy * gamma,
+// Each group walks over the rows, R at a time, and keeps its columns' sums of
+// dgamma and dbeta in registers: a grid of no more CTAs than the GPU holds, so
+// that few partial sums are left.  Asynchronous copies bring the next R rows
+// into shared memory; a row is read from there twice, for its sums and for
+// dx: with d = x - mean and a = dy * gamma,
 //   dx = rstd a - rstd sum(a) / cols - d rstd^3 sum(a d) / cols,
-// dgamma += (dy rstd) d, dbeta += dy.
+// dgamma += (dy rstd) d, dbeta += dy.  R rows share a barrier, and their sums'
+// latencies overlap.
 template <typename T, int V, int E, int R, int MODE, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
   __shared__ SumWords words[R];
-  constexpr int NV = E / V;
+  constexpr int NV = E / V, P = V / 2;
   constexpr bool WIDE = kWide<T, V>;
   constexpr bool kKeepGamma = E <= 16;                   // else in shared memory, a unit per thread as the rows'
   const int threads = MODE == kWarp ? 32 : prm.threads;
@@ -447,88 +475,91 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
   const unsigned len = row_bytes<T, V>(threads, E);
   char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * stages * R * 2 * len;   // [group][stage][r][x, dy]
   const unsigned slot_s = (unsigned)__cvta_generic_to_shared(slot);
-  const Rows<T, V> xr = {static_cast<const T*>(prm.x) + c0, prm.x_stride, static_cast<const T*>(prm.x), cols};
-  const Rows<T, V> dr = {static_cast<const T*>(prm.dy) + c0, prm.dy_stride, static_cast<const T*>(prm.dy), cols};
-  const u64 step = (u64)prm.nparts * groups * R;
-  const u64 first = ((u64)part * groups + group) * R;
+  const int rows = (int)prm.rows, step = (int)prm.nparts * groups * R;
+  const int first = ((int)part * groups + group) * R;
   clear_slots<T, V, NV>(slot, len, stages * R * 2, cols, tid, threads);
-  if constexpr (!WIDE) group_sync<MODE>(group, threads);
+  if constexpr (MODE != kWarp) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) clear_words(words[r]);
+    __syncthreads();
+  } else if constexpr (!WIDE) {
+    __syncwarp();
+  }
   wait_for_predecessors();
   let_successor_start();
 
-  auto fetch_piecewise = [&](u64 row, int stage) {
+  // The row in work; what a turn, and a row, is further in each matrix.
+  const T* x = static_cast<const T*>(prm.x) + (u64)first * prm.x_stride + c0;
+  const T* dy = static_cast<const T*>(prm.dy) + (u64)first * prm.dy_stride + c0;
+  T* dx = static_cast<T*>(prm.out) + (u64)first * prm.out_stride + c0;
+  const u64 x_turn = step * prm.x_stride, dy_turn = step * prm.dy_stride;
+  // `left` rows from a turn's first one on, to stage `to`
+  auto fetch_rows = [&](const T* fx, const T* fd, int left, int to) {
+    unsigned at = to * R * 2 * len;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (row + r < prm.rows) {
-        xr.fetch_pieces(row + r, slot + ((stage * R + r) * 2) * len, tid, threads);
-        dr.fetch_pieces(row + r, slot + ((stage * R + r) * 2 + 1) * len, tid, threads);
+    for (int r = 0; r < R; ++r, at += 2 * len, fx += prm.x_stride, fd += prm.dy_stride) {
+      if (r < left) {
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            fetch_unit<T, V>(fx, cols, slot_s + at, k * threads + tid);
+            fetch_unit<T, V>(fd, cols, slot_s + at + len, k * threads + tid);
+          }
+        } else {
+          fetch_pieces(fx, cols, static_cast<const T*>(prm.x), slot + at, tid, threads);
+          fetch_pieces(fd, cols, static_cast<const T*>(prm.dy), slot + at + len, tid, threads);
+        }
       }
     }
     commit();
   };
-  auto fetch_units = [&](const T* x, const T* dy, int stage, int r, int k) {
-    xr.fetch_unit(x, slot_s + ((stage * R + r) * 2) * len, k * threads + tid);
-    dr.fetch_unit(dy, slot_s + ((stage * R + r) * 2 + 1) * len, k * threads + tid);
-  };
-  for (int s = 0; s < stages; ++s) {
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const u64 row = first + s * step + r;
-        if (row < prm.rows) {
-#pragma unroll
-          for (int k = 0; k < NV; ++k) fetch_units(xr.row(row), dr.row(row), s, r, k);
-        }
-      }
-      commit();
-    } else {
-      fetch_piecewise(first + s * step, s);
-    }
-  }
+  for (int s = 0; s < stages; ++s) fetch_rows(x + s * x_turn, dy + s * dy_turn, rows - first - s * step, s);
 
-  float dg[E], db[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
-  float gam[kKeepGamma ? E : 1];
+  float2 dg[NV][P], db[NV][P];
+  float2 gam[kKeepGamma ? NV : 1][P];
   float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len) + group * width;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * threads + tid) * V;
-    float w[V];
-    load_w<V>(prm.gamma, prm.gamma_bf16, c0 + c, cols - c, 1.f, w);
+    float2 w[P];
+    if (prm.gamma_bf16)
+      load_w<bf16, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+    else
+      load_w<float, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < P; ++i) {
+      dg[k][i] = db[k][i] = make_float2(0.f, 0.f);
       if constexpr (kKeepGamma)
-        gam[k * V + i] = w[i];
+        gam[k][i] = w[i];
       else
-        s_gam[c + i] = w[i];   // read back by this thread alone
+        reinterpret_cast<float2*>(s_gam + c)[i] = w[i];   // read back by this thread alone
     }
   }
-  auto gammas = [&](int k, float (&w)[V]) {
+  auto gammas = [&](int k, float2 (&w)[P]) {
+    if constexpr (kKeepGamma) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if constexpr (kKeepGamma) w[i] = gam[k * V + i];
-    }
-    if constexpr (!kKeepGamma) {
+      for (int i = 0; i < P; ++i) w[i] = gam[k][i];
+    } else {
       const float* p = s_gam + (k * threads + tid) * V;
-      if constexpr (V % 4 == 0) {
+      if constexpr (P >= 2) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(p + i);
-          w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+        for (int i = 0; i < P; i += 2) {
+          const float4 q = reinterpret_cast<const float4*>(p)[i / 2];
+          w[i] = make_float2(q.x, q.y);
+          w[i + 1] = make_float2(q.z, q.w);
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[i] = p[i];
+        w[0] = *reinterpret_cast<const float2*>(p);
       }
     }
   };
-  float mean_next[R], rstd_next[R];
-  auto statistics = [&](u64 row) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      mean_next[r] = row + r < prm.rows ? __ldg(prm.mean + row + r) : 0.f;
-      rstd_next[r] = row + r < prm.rows ? __ldg(prm.rstd + row + r) : 0.f;
+  // lane r of each warp holds the statistics of the turn's row r
+  const int lane = threadIdx.x & 31;
+  float mean_next = 0.f, rstd_next = 0.f;
+  auto statistics = [&](int row) {
+    if (lane < R && row + lane < rows) {
+      mean_next = __ldg(prm.mean + row + lane);
+      rstd_next = __ldg(prm.rstd + row + lane);
     }
   };
   statistics(first);
@@ -537,86 +568,90 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     cluster_wait();
   }
   int stage = 0, last = 0, buf = 0;
-  for (u64 row = first; row < prm.rows; row += step) {
-    float mean[R], rstd[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) mean[r] = mean_next[r], rstd[r] = rstd_next[r];
+  for (int row = first; row < rows; row += step, x += x_turn, dy += dy_turn, dx += step * prm.out_stride) {
+    const float means = mean_next, rstds = rstd_next;
+    const int left = rows - row;
     statistics(row + step);
-    // the group of copies for these rows: the newest but stages - 1, and one newer where they were asked for a turn later
+    // the copies of these rows: the newest but stages - 1, and one newer where they were asked for a turn later
     wait_groups(WIDE ? stages - 1 : stages > 2 ? stages - 2 : 0);
     if constexpr (!WIDE) group_sync<MODE>(group, threads);   // the others' copies have landed too
-    const char* here = slot + stage * R * 2 * len;
+    const unsigned here = slot_s + stage * R * 2 * len;
     float2 s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = make_float2(0.f, 0.f);
-      if (row + r < prm.rows) {
+      float2 sa = make_float2(0.f, 0.f), sd = sa;
+      if (r < left) {
+        const float2 mean = both(-__shfl_sync(0xffffffffu, means, r)), rstd = both(__shfl_sync(0xffffffffu, rstds, r));
+        const Landed<T, V> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          float fx[V], fd[V], w[V];
-          xr.read(row + r, here + r * 2 * len, k * threads + tid, fx);
-          dr.read(row + r, here + (r * 2 + 1) * len, k * threads + tid, fd);
+          float2 fx[P], fd[P], w[P];
+          hx.read(k * threads + tid, fx);
+          hd.read(k * threads + tid, fd);
           gammas(k, w);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {   // dy is 0 past the row's end
-            const float d = fx[i] - mean[r], a = fd[i] * w[i];
-            s[r].x += a;
-            s[r].y = fmaf(a, d, s[r].y);
-            dg[k * V + i] = fmaf(fd[i] * rstd[r], d, dg[k * V + i]);
-            db[k * V + i] += fd[i];
+          for (int i = 0; i < P; ++i) {   // dy is 0 past the row's end
+            const float2 d = __fadd2_rn(fx[i], mean), a = __fmul2_rn(fd[i], w[i]);
+            sa = __fadd2_rn(sa, a);
+            sd = __ffma2_rn(a, d, sd);
+            dg[k][i] = __ffma2_rn(__fmul2_rn(fd[i], rstd), d, dg[k][i]);
+            db[k][i] = __fadd2_rn(db[k][i], fd[i]);
           }
         }
       }
+      s[r] = row_partial<MODE>(make_float2(sa.x + sa.y, sd.x + sd.y), words[r], buf, group, threads);
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = row_partial<MODE>(s[r], words[r], buf);
     row_meet<MODE>(group, threads);
-#pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = row_total<MODE>(s[r], words[r], buf, group, threads);
     if constexpr (MODE == kCluster) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) row_send(s[r], words[r], buf);
+      for (int r = 0; r < R; ++r) {
+        s[r] = row_total<MODE>(s[r], words[r], buf, group, threads);
+        row_send(s[r], words[r], buf);
+      }
       cluster_arrive();
       cluster_wait();
-#pragma unroll
-      for (int r = 0; r < R; ++r) s[r] = row_join(words[r], buf, csize);
     }
-    buf ^= 1;
-    // 4-byte units: the group has met since it read the previous rows for dx, so their slots are free
+    // pairs: the group has met since it read the previous rows for dx, so their slots are free
     if constexpr (!WIDE) {
-      if (stages > 1 && row != first) fetch_piecewise(row + (u64)(stages - 1) * step, last);
-      else commit();
+      if (stages > 1 && row != first)
+        fetch_rows(x + (stages - 1) * x_turn, dy + (stages - 1) * dy_turn, left - (stages - 1) * step, last);
+      else
+        commit();
     }
+    T* out = dx;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (row + r < prm.rows) {
-        T* dx = static_cast<T*>(prm.out) + (row + r) * prm.out_stride + c0;
-        const bool p4 = (reinterpret_cast<uintptr_t>(dx) & 3u) == 0;
-        const u64 next = row + (u64)stages * step + r;
-        const T *x_next = xr.row(next), *dy_next = dr.row(next);
-        const float k1 = -rstd[r] * (s[r].x * inv);
-        const float k2 = -rstd[r] * rstd[r] * rstd[r] * (s[r].y * inv);
+    for (int r = 0; r < R; ++r, out += prm.out_stride) {
+      if (r < left) {
+        const float mean = __shfl_sync(0xffffffffu, means, r), rstd = __shfl_sync(0xffffffffu, rstds, r);
+        if constexpr (MODE == kCluster)
+          s[r] = row_join(words[r], buf);
+        else
+          s[r] = row_total<MODE>(s[r], words[r], buf, group, threads);
+        const Landed<T, V> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
+        const bool p4 = (reinterpret_cast<uintptr_t>(out) & 3u) == 0;
+        const float2 k1 = both(-rstd * (s[r].x * inv)), k2 = both(-rstd * rstd * rstd * (s[r].y * inv));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int c = (k * threads + tid) * V;
-          float fx[V], fd[V], w[V];
-          xr.read(row + r, here + r * 2 * len, k * threads + tid, fx);
-          dr.read(row + r, here + (r * 2 + 1) * len, k * threads + tid, fd);
-          if constexpr (WIDE) {   // this unit's slot is free
-            if (next < prm.rows) fetch_units(x_next, dy_next, stage, r, k);
-          }
+          const int u = k * threads + tid;
+          float2 fx[P], fd[P], w[P];
+          hx.read(u, fx);
+          hd.read(u, fd);
           gammas(k, w);
 #pragma unroll
-          for (int i = 0; i < V; ++i) fd[i] = fmaf(fx[i] - mean[r], k2, fmaf(fd[i] * w[i], rstd[r], k1));
-          store_unit<T, V>(dx + c, cols - c, p4, fd);
+          for (int i = 0; i < P; ++i)
+            fd[i] = __ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(__fmul2_rn(fd[i], w[i]), both(rstd), k1));
+          store_unit<T, P>(out + u * V, cols - u * V, p4, fd);
         }
       }
     }
-    if constexpr (WIDE) {
-      commit();
+    buf ^= 1;
+    if constexpr (WIDE) {   // a thread's slots are its own: free
+      fetch_rows(x + stages * x_turn, dy + stages * dy_turn, left - stages * step, stage);
     } else if (stages == 1) {
       group_sync<MODE>(group, threads);
-      fetch_piecewise(row + step, 0);
+      fetch_rows(x + x_turn, dy + dy_turn, left - step, 0);
+    } else if (MODE == kWarp) {
+      __syncwarp();   // the next turn refills these rows' slots with no barrier in between
     }
     last = stage;
     if (++stage == stages) stage = 0;
@@ -636,10 +671,11 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = (k * threads + tid) * V + i;
-          acc[c] = g ? acc[c] + dg[k * V + i] : dg[k * V + i];
-          acc[width + c] = g ? acc[width + c] + db[k * V + i] : db[k * V + i];
+        for (int i = 0; i < P; ++i) {
+          float2* a = reinterpret_cast<float2*>(acc + (k * threads + tid) * V) + i;
+          float2* b = reinterpret_cast<float2*>(acc + width + (k * threads + tid) * V) + i;
+          *a = g ? __fadd2_rn(*a, dg[k][i]) : dg[k][i];
+          *b = g ? __fadd2_rn(*b, db[k][i]) : db[k][i];
         }
       }
     }
@@ -655,8 +691,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
       for (int i = 0; i < V; ++i) {
         const int c = (k * threads + tid) * V + i;
         if (c < cols) {
-          out_g[c] = add ? out_g[c] + dg[k * V + i] : dg[k * V + i];
-          out_b[c] = add ? out_b[c] + db[k * V + i] : db[k * V + i];
+          const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
+          out_g[c] = add ? out_g[c] + vg : vg;
+          out_b[c] = add ? out_b[c] + vb : vb;
         }
       }
     }
@@ -664,32 +701,37 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
 }
 
 // The parts' sums, column by column: 32 columns per CTA, 16 warps that each
-// add every 16th part in fp64, then the warps' sums in order.
+// add every 16th part in four chains, then the warps' sums in order.  fp32:
+// the depth is 304 / 64 + 2 + 16 additions, and fp64 runs at 2 additions per
+// clock and SM here (22 us instead of 6 for 304 parts of 5120 columns).
 constexpr int kPartWarps = 16;
 __global__ void __launch_bounds__(32 * kPartWarps) ln_parts_kernel(const float* partial, unsigned nparts, unsigned cols,
                                                                   float* dgamma, float* dbeta, int accumulate) {
-  __shared__ double s[kPartWarps][32];
+  __shared__ float s[kPartWarps][32];
   wait_for_predecessors();
   let_successor_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned c = blockIdx.x * 32 + lane;
   const float* p = partial + (size_t)blockIdx.y * cols + c;
-  double sum = 0.0;
+  const size_t stride = (size_t)2 * cols;
+  float sum[4] = {};
   if (c < cols) {
-    unsigned k = warp;
-    for (; k + 3 * kPartWarps < nparts; k += 4 * kPartWarps) {
-      const float a0 = p[(size_t)k * 2 * cols], a1 = p[(size_t)(k + kPartWarps) * 2 * cols];
-      const float a2 = p[(size_t)(k + 2 * kPartWarps) * 2 * cols], a3 = p[(size_t)(k + 3 * kPartWarps) * 2 * cols];
-      sum += ((double)a0 + a1) + ((double)a2 + a3);
+    for (unsigned k = warp; k < nparts; k += 4 * kPartWarps) {
+      float a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = k + i * kPartWarps < nparts ? p[(k + i * kPartWarps) * stride] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += a[i];
     }
-    for (; k < nparts; k += kPartWarps) sum += p[(size_t)k * 2 * cols];
   }
-  s[warp][lane] = sum;
+  s[warp][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   __syncthreads();
   if (warp == 0 && c < cols) {
-    for (int w = 1; w < kPartWarps; ++w) sum += s[w][lane];
+    float total = s[0][lane];
+#pragma unroll
+    for (int w = 1; w < kPartWarps; ++w) total += s[w][lane];
     float* out = (blockIdx.y ? dbeta : dgamma) + c;
-    *out = accumulate ? *out + (float)sum : (float)sum;
+    *out = accumulate ? *out + total : total;
   }
 }
 
@@ -729,43 +771,57 @@ int stages_for(size_t budget, size_t per_stage, u64 turns) {
 
 constexpr size_t kSmemSm = 224 * 1024;   // of an SM, less what CTAs take statically
 
-template <typename T, int V, int E, int MODE, int MAXT, int MINB>
+template <typename T, int V, int E, int MODE, int MAXT>
 cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st) {
-  const int groups = MODE == kCluster ? 1 : MAXT / threads > 15 && MODE == kCta ? 15 : MAXT / threads;
-  const size_t want = div_up(p.rows, groups), most = (size_t)MINB * sm_count() / csize;
-  const unsigned n = (unsigned)(want < most ? want : most);
-  p.threads = threads;
-  const size_t row = (size_t)groups * row_bytes<T, V>(threads, E);
-  p.stages = stages_for(kSmemSm / MINB - 2048, row, div_up(want, n));
-  return launch_dependent(ln_forward_kernel<T, V, E, MODE, MAXT, MINB>, n * csize, groups * threads, row * p.stages, csize, st, p);
+  const int groups = MODE == kWarp ? MAXT / 32 : 1;
+  const size_t smem = kWide<T, V> ? 0 : (size_t)groups * row_bytes<T, V>(threads, E);
+  return launch_dependent(ln_forward_kernel<T, V, E, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, groups) * csize)), groups * threads, smem,
+                          csize, st, p);
 }
 
+// A thread takes 32 elements (8 in rows of 256 and fewer), which keeps a CTA
+// small; with rows too few to fill the GPU it takes 8, and more threads share
+// a row.
 template <typename T, int V>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
-  if (p.cols <= 512) return forward_e<T, V, 16, kWarp, 256, 3>(p, 32, 1, st);
-  const int c = cluster_for(p.rows, p.cols, 1024 * 16);
-  const int threads = threads_for(div_up(p.cols, c), 16);
-  if (c > 1) return threads <= 256 ? forward_e<T, V, 16, kCluster, 256, 3>(p, threads, c, st) : forward_e<T, V, 16, kCluster, 1024, 1>(p, threads, c, st);
-  return threads <= 256 ? forward_e<T, V, 16, kCta, 256, 3>(p, threads, 1, st) : forward_e<T, V, 16, kCta, 1024, 1>(p, threads, 1, st);
+  if (p.cols <= 256) return forward_e<T, V, 8, kWarp, 128>(p, 32, 1, st);
+  const int c = cluster_for(p.rows, p.cols, 1024 * 32);
+  const size_t slice = div_up(p.cols, c);
+  const bool few = p.rows * c <= 2 * (size_t)sm_count() && slice <= 4096;
+  if (c > 1) {
+    if (few) return forward_e<T, V, 8, kCluster, 512>(p, threads_for(slice, 8), c, st);
+    return forward_e<T, V, 32, kCluster, 1024>(p, threads_for(slice, 32), c, st);
+  }
+  if (few) return forward_e<T, V, 8, kCta, 512>(p, threads_for(slice, 8), 1, st);
+  if (p.cols <= 1024) return forward_e<T, V, 32, kWarp, 128>(p, 32, 1, st);
+  return forward_e<T, V, 32, kCta, 1024>(p, threads_for(slice, 32), 1, st);
 }
 
 // The shape of a backward launch, from the sizes alone (the workspace depends
-// on it).  Up to 8192 columns a CTA has 256 threads, so that two to four are
-// on an SM and one's barrier is another's work.
+// on it).  A thread has 16 columns (8 in rows of 256 and fewer): with their
+// sums and gamma they take 48 registers, which leaves room for what is in
+// work.  Up to 5120 columns two CTAs of up to 320 threads are on an SM, so
+// that one's barrier is another's work; up to 8192 one of 512; longer rows are split
+// over a cluster, in CTAs of 512 threads with 32 columns each beyond 65536.
+//   Measured at 24576 x 5120 bf16 (755 MB): 4 rows a turn 123 us, 2 rows 128,
+//   1 row 136; 8 columns per thread and 640 threads, 4 rows 133; 24 columns
+//   and 224 threads, 1 row 181.
 struct BackwardShape {
-  int e, r, threads, groups, csize, ctas;   // ctas: per SM
+  int e, r4, threads, groups, csize, ctas;   // r4: 4 rows a turn (fp32: 2), else 1; ctas: per SM
   unsigned nparts;
 };
 BackwardShape backward_shape(size_t rows, size_t cols) {
   BackwardShape s;
-  s.csize = cols <= 256 ? 1 : cluster_for(rows, cols, 512 * 32);
+  s.csize = cols <= 512 ? 1 : cluster_for(rows, cols, 512 * 16);
   const size_t slice = div_up(cols, s.csize);
-  s.e = slice <= 2048 ? 8 : slice <= 4096 ? 16 : slice <= 6144 ? 24 : 32;
+  s.e = slice <= 256 ? 8 : slice <= 8192 ? 16 : 32;
   s.threads = threads_for(slice, s.e);
-  s.r = s.e <= 16 ? 2 : 1;
-  s.ctas = slice > 8192 ? 1 : s.e == 8 ? 3 : 2;
+  s.ctas = s.threads > 320 ? 1 : 2;
   s.groups = s.csize > 1 || s.threads > 256 ? 1 : 256 / s.threads;
-  const size_t want = div_up(rows, (size_t)s.groups * s.r), most = (size_t)s.ctas * sm_count() / s.csize;
+  while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
+  const size_t most = (size_t)s.ctas * sm_count() / s.csize;
+  s.r4 = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
+  const size_t want = div_up(rows, (size_t)s.groups);
   s.nparts = (unsigned)(want < most ? want : most);
   if (s.nparts < 1) s.nparts = 1;
   return s;
@@ -778,25 +834,23 @@ cudaError_t backward_e(NormRowsParams& p, const BackwardShape& s, cudaStream_t s
   const size_t stage = (size_t)s.groups * R * 2 * row_bytes<T, V>(s.threads, E);
   const size_t gam = E > 16 ? (size_t)s.groups * E * s.threads * 4 : 0;
   const size_t acc = s.groups > 1 ? (size_t)2 * E * s.threads * 4 : 0;
-  p.stages = stages_for(kSmemSm / MINB - 2048 - gam, stage, div_up(p.rows, (u64)s.nparts * s.groups * R));
+  p.stages = stages_for(kSmemSm / s.ctas - 4096 - gam, stage, div_up(p.rows, (u64)s.nparts * s.groups * R));
   size_t smem = stage * p.stages + gam;
   if (smem < acc) smem = acc;
-  return launch_dependent(ln_backward_kernel<T, V, E, R, MODE, MAXT, MINB>, s.nparts * s.csize, s.groups * s.threads, smem, s.csize, st, p);
+  return launch_dependent(ln_backward_kernel<T, V, E, R, MODE, MAXT, MINB>, dim3(s.nparts * s.csize), s.groups * s.threads, smem, s.csize, st, p);
 }
 
 template <typename T, int V>
 cudaError_t backward(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
+  constexpr int R = sizeof(T) == 2 ? 4 : 2;
   if (s.csize > 1) {
-    if (s.e == 8) return backward_e<T, V, 8, 2, kCluster, 256, 3>(p, s, st);
-    if (s.e == 16) return backward_e<T, V, 16, 2, kCluster, 256, 2>(p, s, st);
-    if (s.e == 24) return backward_e<T, V, 24, 1, kCluster, 256, 2>(p, s, st);
-    return s.threads <= 256 ? backward_e<T, V, 32, 1, kCluster, 256, 2>(p, s, st) : backward_e<T, V, 32, 1, kCluster, 512, 1>(p, s, st);
+    if (s.e == 32) return backward_e<T, V, 32, 1, kCluster, 512, 1>(p, s, st);
+    return s.r4 ? backward_e<T, V, 16, R, kCluster, 512, 1>(p, s, st) : backward_e<T, V, 16, 1, kCluster, 512, 1>(p, s, st);
   }
-  if (s.threads == 32) return backward_e<T, V, 8, 2, kWarp, 256, 3>(p, s, st);
-  if (s.e == 8) return backward_e<T, V, 8, 2, kCta, 256, 3>(p, s, st);
-  if (s.e == 16) return backward_e<T, V, 16, 2, kCta, 256, 2>(p, s, st);
-  if (s.e == 24) return backward_e<T, V, 24, 1, kCta, 256, 2>(p, s, st);
-  return s.threads <= 256 ? backward_e<T, V, 32, 1, kCta, 256, 2>(p, s, st) : backward_e<T, V, 32, 1, kCta, 512, 1>(p, s, st);
+  if (s.threads == 32 && s.e == 8) return s.r4 ? backward_e<T, V, 8, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 8, 1, kWarp, 256, 2>(p, s, st);
+  if (s.threads == 32) return s.r4 ? backward_e<T, V, 16, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 16, 1, kWarp, 256, 2>(p, s, st);
+  if (s.threads <= 320) return s.r4 ? backward_e<T, V, 16, R, kCta, 320, 2>(p, s, st) : backward_e<T, V, 16, 1, kCta, 320, 2>(p, s, st);
+  return s.r4 ? backward_e<T, V, 16, R, kCta, 512, 1>(p, s, st) : backward_e<T, V, 16, 1, kCta, 512, 1>(p, s, st);
 }
 
 bool wide_rows(const void* base, u64 stride, size_t cols, size_t esize) {
@@ -809,7 +863,7 @@ bool wide_w(const void* w) { return (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
 cudaError_t launch_ln_forward(NormRowsParams& p, int dtype, cudaStream_t st) {
   const size_t es = dtype == XP_F32 ? 4 : 2;
   const bool wide = wide_rows(p.x, p.x_stride, p.cols, es) && wide_rows(p.out, p.out_stride, p.cols, es) && wide_w(p.gamma) && wide_w(p.beta);
-  if (dtype == XP_F32) return wide ? forward<float, 4>(p, st) : forward<float, 1>(p, st);
+  if (dtype == XP_F32) return wide ? forward<float, 4>(p, st) : forward<float, 2>(p, st);
   return wide ? forward<bf16, 8>(p, st) : forward<bf16, 2>(p, st);
 }
 
@@ -824,7 +878,7 @@ cudaError_t launch_ln_backward(NormRowsParams& p, int dtype, cudaStream_t st) {
   const bool wide = wide_rows(p.x, p.x_stride, p.cols, es) && wide_rows(p.dy, p.dy_stride, p.cols, es) && wide_rows(p.out, p.out_stride, p.cols, es) && wide_w(p.gamma);
   cudaError_t e;
   if (dtype == XP_F32)
-    e = wide ? backward<float, 4>(p, s, st) : backward<float, 1>(p, s, st);
+    e = wide ? backward<float, 4>(p, s, st) : backward<float, 2>(p, s, st);
   else
     e = wide ? backward<bf16, 8>(p, s, st) : backward<bf16, 2>(p, s, st);
   if (e != cudaSuccess || !p.dgamma || s.nparts == 1) return e;
