@@ -99,20 +99,6 @@ __device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float n
 }
 
 // ---- sums over the threads of a row
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-// Two sums at once: lanes 0-15 end with x's, lanes 16-31 with y's.
-__device__ __forceinline__ float warp_sum_halves(float x, float y) {
-  const bool upper = threadIdx.x & 16;
-  float mine = upper ? y : x;
-  mine += __shfl_xor_sync(0xffffffffu, upper ? x : y, 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  return mine;
-}
 __device__ __forceinline__ void group_bar(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
@@ -128,95 +114,78 @@ __device__ __forceinline__ unsigned cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void store_remote(const float2* p, unsigned rank, float2 v) {
+__device__ __forceinline__ void store_remote(const float* p, unsigned rank, float v) {
   unsigned a = (unsigned)__cvta_generic_to_shared(p), r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
 }
 
-// Shared words of the sums.  Two buffers in turn: a thread that reads one
-// meets the others at the next sum's barrier before it is written again.  A
-// group's warps have kWarpWords words or a multiple of it, 0 where there is
-// no warp.
-constexpr int kWarpWords = 8;
-struct alignas(16) SumWords {
-  float2 warp[2][kMaxWarps + kWarpWords];
-  float2 cta[2][kMaxCluster8];
-};
-__device__ __forceinline__ void clear_words(SumWords& w) {   // before a barrier
-  float2* p = &w.warp[0][0];
-  for (int i = threadIdx.x; i < 2 * (kMaxWarps + kWarpWords); i += blockDim.x) p[i] = make_float2(0.f, 0.f);
-}
+__host__ __device__ constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// Both components summed over the row's threads, the same value in each; the
-// order of the additions is fixed.  In steps, so that several rows share a
-// barrier: each warp's sum, the group meets, the warps' sums added up; in a
-// cluster then the same among its CTAs, through their shared memory.  (TWO:
-// else x alone.)
-__device__ __forceinline__ int words_span(int threads) { return ((threads >> 5) + kWarpWords - 1) & ~(kWarpWords - 1); }
-template <int MODE, bool TWO = true>
-__device__ __forceinline__ float2 row_partial(float2 v, SumWords& w, int buf, int group, int threads) {
-  if constexpr (MODE == kWarp) {
-    if constexpr (TWO) {
-      const float h = warp_sum_halves(v.x, v.y);
-      return make_float2(__shfl_sync(0xffffffffu, h, 0), __shfl_sync(0xffffffffu, h, 16));
-    }
-    return make_float2(warp_sum(v.x), 0.f);
-  }
+// N sums at once (a power of two): at each step a lane keeps half of its
+// values and hands the other half to its partner, so N of them cost
+// N - 1 + 5 - log2 N shuffles and not 5 N.  Lane l ends with the warp's sum of
+// value l >> (5 - log2 N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
-  float* mine = reinterpret_cast<float*>(w.warp[buf] + group * words_span(threads) + (threadIdx.x >> 5) - group * (threads >> 5));
-  if constexpr (TWO) {
-    const float h = warp_sum_halves(v.x, v.y);
-    if ((lane & 15) == 0) mine[lane >> 4] = h;
-  } else {
-    v.x = warp_sum(v.x);
-    if (lane == 0) *mine = v.x;
-  }
-  return v;
-}
-template <int MODE>
-__device__ __forceinline__ void row_meet(int group, int threads) {
-  if constexpr (MODE == kCluster) __syncthreads();
-  if constexpr (MODE == kCta) group_bar(group, threads);
-}
-template <int MODE, bool TWO = true>
-__device__ __forceinline__ float2 row_total(float2 v, const SumWords& w, int buf, int group, int threads) {
-  if constexpr (MODE == kWarp) return v;
-  const int span = words_span(threads);
-  const float2* all = w.warp[buf] + group * span;
-  v = make_float2(0.f, 0.f);
-  for (int at = 0; at < span; at += kWarpWords) {
+  int o = 16;
 #pragma unroll
-    for (int i = 0; i < kWarpWords; i += 2) {
-      const float4 q = *reinterpret_cast<const float4*>(all + at + i);
-      if constexpr (TWO)
-        v = __fadd2_rn(__fadd2_rn(v, make_float2(q.x, q.y)), make_float2(q.z, q.w));
-      else
-        v.x = (v.x + q.x) + q.z;
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[n + i] : v[i], give = upper ? v[i] : v[n + i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  return v;
+#pragma unroll
+  for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
-__device__ __forceinline__ void row_send(float2 v, SumWords& w, int buf) {
-  if (threadIdx.x < cluster_size()) store_remote(&w.cta[buf][cluster_rank()], threadIdx.x, v);
-}
-__device__ __forceinline__ float2 row_join(const SumWords& w, int buf) {
-  float2 v = make_float2(0.f, 0.f);
-  for (unsigned r = 0, n = cluster_size(); r < n; ++r) v = __fadd2_rn(v, w.cta[buf][r]);
-  return v;
-}
-template <int MODE, bool TWO>
-__device__ __forceinline__ float2 row_sum(float2 v, SumWords& w, int buf, int group, int threads) {
-  v = row_partial<MODE, TWO>(v, w, buf, group, threads);
-  row_meet<MODE>(group, threads);
-  v = row_total<MODE, TWO>(v, w, buf, group, threads);
+
+// Shared words of N sums.  Two buffers in turn: a thread that reads one meets
+// the others at the next sums' barrier before it is written again.
+template <int N>
+struct SumWords {
+  float warp[2][kMaxWarps][N];
+  float cta[2][kMaxCluster8][N];
+};
+
+// N values summed over the row's threads: value i of the result is in lane i
+// (and i + N, ...) of every warp.  Each warp's sums, the group meets, the
+// warps' sums added up; in a cluster the same once more among its CTAs,
+// through their shared memory.  The order of the additions is fixed.
+template <int MODE, int N>
+__device__ __forceinline__ float row_sums(float (&v)[N], SumWords<N>& w, int buf, int group, int threads) {
+  constexpr int L = log2_of(N);
+  const int lane = threadIdx.x & 31;
+  float t = warp_sums<N>(v);
+  if constexpr (MODE == kWarp) return __shfl_sync(0xffffffffu, t, (lane & (N - 1)) << (5 - L));
+  if ((lane & ((32 >> L) - 1)) == 0) w.warp[buf][threadIdx.x >> 5][lane >> (5 - L)] = t;
+  if constexpr (MODE == kCluster)
+    __syncthreads();
+  else
+    group_bar(group, threads);
+  const int nw = threads >> 5, first = group * nw;
+  t = 0.f;
+  for (int j = lane >> L; j < nw; j += 32 >> L) t += w.warp[buf][first + j][lane & (N - 1)];
+#pragma unroll
+  for (int o = N; o < 32; o *= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
   if constexpr (MODE == kCluster) {
-    row_send(v, w, buf);
+    const unsigned n = cluster_size();
+    if (threadIdx.x < N * n) store_remote(&w.cta[buf][cluster_rank()][lane & (N - 1)], threadIdx.x >> L, t);
     cluster_arrive();
     cluster_wait();
-    v = row_join(w, buf);
+    t = 0.f;
+    for (unsigned r = 0; r < n; ++r) t += w.cta[buf][r][lane & (N - 1)];
   }
-  return v;
+  return t;
+}
+template <int MODE>
+__device__ __forceinline__ float row_sum(float x, SumWords<1>& w, int buf, int threads) {
+  float v[1] = {x};
+  return row_sums<MODE, 1>(v, w, buf, 0, threads);
 }
 
 // ---- rows on their way from global to shared memory
@@ -252,14 +221,23 @@ __host__ __device__ constexpr unsigned row_bytes(unsigned threads, unsigned e) {
 // How the threads of a group bring a row of a matrix.  Past its end they read
 // zeros.
 //
-// Wide units: a thread copies the units it will use itself, unit k at slot
-// k * threads + thread, so nothing but its own copies has to have landed; it
-// clears the slots of units that the row does not have once.
+// Thread t's unit k is unit first_unit(t) + 32 k of the row: a warp has 32 NV
+// units side by side, and the distance between a thread's units is the same
+// for every row length.
+//
+// Wide units: a thread copies the units it will use itself, so nothing but its
+// own copies has to have landed; it clears the slots of units that the row
+// does not have once.
 //
 // Pairs: the group copies the 16-byte pieces that cover the row, at the row's
 // own offset within them, and zeros behind them up to what a row at the
 // largest offset would touch; the group meets before it reads.  A first piece
 // that begins before the matrix does is copied element by element.
+template <int NV>
+__device__ __forceinline__ int first_unit(int tid) {
+  return (tid & ~31) * NV + (tid & 31);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void fetch_unit(const T* row, int cols, unsigned smem, int u) {
   if (u * V < cols) copy_async16(smem + u * 16, row + u * V);
@@ -329,7 +307,7 @@ __device__ __forceinline__ void clear_slots(char* slot, unsigned row_len, int nr
   if constexpr (kWide<T, V>) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int u = k * threads + tid;
+      const int u = first_unit<NV>(tid) + 32 * k;
       if (u * V >= cols)
         for (int r = 0; r < nrows; ++r) *reinterpret_cast<uint4*>(slot + r * row_len + 16 * u) = zero;
     }
@@ -349,7 +327,7 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 // ---------------------------------------------------------------- forward
 
 // One row per group, in registers from its load to its output: E elements per
-// thread, unit k at column (k * threads + thread) * V.  The CTAs are small and
+// thread.  The CTAs are small and
 // many: eight of 128 threads are on an SM, so that one's sums are another's
 // loads, and the hardware hands the rows out.
 //   Measured at 16384 x 4096 bf16 (268 MB, a plain copy of it takes 42 us):
@@ -358,19 +336,18 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 template <typename T, int V, int E, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
-  __shared__ SumWords words;
+  __shared__ SumWords<1> words;
   constexpr int NV = E / V, P = V / 2;
   constexpr bool WIDE = kWide<T, V>;
   const int threads = MODE == kWarp ? 32 : blockDim.x;
   const int group = MODE == kWarp ? threadIdx.x >> 5 : 0;
-  const int tid = threadIdx.x - group * threads;
+  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid);
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
   const u64 row = MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + group : blockIdx.x / csize;
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
   const int cols = c0 < prm.cols ? (int)min((unsigned)E * threads, prm.cols - c0) : 0;   // a cluster's last CTA may have none
   const T* x = static_cast<const T*>(prm.x) + row * prm.x_stride + c0;
   if (MODE == kCluster) cluster_arrive();   // its end: every CTA of the cluster runs
-  if constexpr (MODE != kWarp) clear_words(words);
   wait_for_predecessors();
   let_successor_start();
   if (MODE == kWarp && row >= prm.rows) return;
@@ -380,10 +357,9 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
     const uint4* a = reinterpret_cast<const uint4*>(x);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int u = k * threads + tid;
+      const int u = u0 + 32 * k;
       unpack16<T, P>(u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0), f[k]);
     }
-    if constexpr (MODE != kWarp) __syncthreads();   // the words are clear
   } else {
     const unsigned len = row_bytes<T, V>(threads, E);
     char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * len;
@@ -395,7 +371,7 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
     if constexpr (MODE == kWarp) __syncwarp(); else __syncthreads();
     const Landed<T, V> here((unsigned)__cvta_generic_to_shared(slot), x);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) here.read(k * threads + tid, f[k]);
+    for (int k = 0; k < NV; ++k) here.read(u0 + 32 * k, f[k]);
   }
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -405,11 +381,11 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
   }
   if (MODE == kCluster) cluster_wait();
   const float inv = 1.0f / (float)prm.cols;
-  const float mean = row_sum<MODE, false>(make_float2(sum.x + sum.y, 0.f), words, 0, 0, threads).x * inv;
+  const float mean = row_sum<MODE>(sum.x + sum.y, words, 0, threads) * inv;
   float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int n = cols - (k * threads + tid) * V;   // wide units are whole or absent
+    const int n = cols - (u0 + 32 * k) * V;   // wide units are whole or absent
     const float2 m = make_float2(n > 0 ? -mean : 0.f, (WIDE ? n > 0 : n > 1) ? -mean : 0.f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -417,7 +393,7 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
       sq = __ffma2_rn(f[k][i], f[k][i], sq);
     }
   }
-  const float var = row_sum<MODE, false>(make_float2(sq.x + sq.y, 0.f), words, 1, 0, threads).x * inv;
+  const float var = row_sum<MODE>(sq.x + sq.y, words, 1, threads) * inv;
   const float rstd = 1.0f / sqrtf(var + prm.eps);
   if (tid == 0 && c0 == 0) {
     if (prm.mean) prm.mean[row] = mean;
@@ -429,7 +405,7 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
     typedef decltype(w) W;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * threads + tid) * V;
+      const int c = (u0 + 32 * k) * V;
       float2 g[P], b[P];
       load_w<W, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
       load_w<W, P>(prm.beta, c0 + c, cols - c, 0.f, b);
@@ -457,13 +433,13 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
 template <typename T, int V, int E, int R, int MODE, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
-  __shared__ SumWords words[R];
+  __shared__ SumWords<2 * R> words;
   constexpr int NV = E / V, P = V / 2;
   constexpr bool WIDE = kWide<T, V>;
   constexpr bool kKeepGamma = E <= 16;                   // else in shared memory, a unit per thread as the rows'
   const int threads = MODE == kWarp ? 32 : prm.threads;
   const int group = MODE == kCluster ? 0 : threadIdx.x / threads;
-  const int tid = threadIdx.x - group * threads;
+  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid);
   const int groups = MODE == kCluster ? 1 : blockDim.x / threads;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
   const unsigned part = blockIdx.x / csize;
@@ -478,13 +454,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
   const int rows = (int)prm.rows, step = (int)prm.nparts * groups * R;
   const int first = ((int)part * groups + group) * R;
   clear_slots<T, V, NV>(slot, len, stages * R * 2, cols, tid, threads);
-  if constexpr (MODE != kWarp) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) clear_words(words[r]);
-    __syncthreads();
-  } else if constexpr (!WIDE) {
-    __syncwarp();
-  }
+  if constexpr (!WIDE) group_sync<MODE>(group, threads);
   wait_for_predecessors();
   let_successor_start();
 
@@ -502,8 +472,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
         if constexpr (WIDE) {
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
-            fetch_unit<T, V>(fx, cols, slot_s + at, k * threads + tid);
-            fetch_unit<T, V>(fd, cols, slot_s + at + len, k * threads + tid);
+            fetch_unit<T, V>(fx, cols, slot_s + at, u0 + 32 * k);
+            fetch_unit<T, V>(fd, cols, slot_s + at + len, u0 + 32 * k);
           }
         } else {
           fetch_pieces(fx, cols, static_cast<const T*>(prm.x), slot + at, tid, threads);
@@ -520,7 +490,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
   float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len) + group * width;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * threads + tid) * V;
+    const int c = (u0 + 32 * k) * V;
     float2 w[P];
     if (prm.gamma_bf16)
       load_w<bf16, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
@@ -540,7 +510,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
 #pragma unroll
       for (int i = 0; i < P; ++i) w[i] = gam[k][i];
     } else {
-      const float* p = s_gam + (k * threads + tid) * V;
+      const float* p = s_gam + (u0 + 32 * k) * V;
       if constexpr (P >= 2) {
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
@@ -576,7 +546,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     wait_groups(WIDE ? stages - 1 : stages > 2 ? stages - 2 : 0);
     if constexpr (!WIDE) group_sync<MODE>(group, threads);   // the others' copies have landed too
     const unsigned here = slot_s + stage * R * 2 * len;
-    float2 s[R];
+    float v[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 sa = make_float2(0.f, 0.f), sd = sa;
@@ -586,8 +556,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           float2 fx[P], fd[P], w[P];
-          hx.read(k * threads + tid, fx);
-          hd.read(k * threads + tid, fd);
+          hx.read(u0 + 32 * k, fx);
+          hd.read(u0 + 32 * k, fd);
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i) {   // dy is 0 past the row's end
@@ -599,18 +569,11 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
           }
         }
       }
-      s[r] = row_partial<MODE>(make_float2(sa.x + sa.y, sd.x + sd.y), words[r], buf, group, threads);
+      v[2 * r] = sa.x + sa.y;
+      v[2 * r + 1] = sd.x + sd.y;
     }
-    row_meet<MODE>(group, threads);
-    if constexpr (MODE == kCluster) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        s[r] = row_total<MODE>(s[r], words[r], buf, group, threads);
-        row_send(s[r], words[r], buf);
-      }
-      cluster_arrive();
-      cluster_wait();
-    }
+    const float sums = row_sums<MODE, 2 * R>(v, words, buf, group, threads) * inv;
+    buf ^= 1;
     // pairs: the group has met since it read the previous rows for dx, so their slots are free
     if constexpr (!WIDE) {
       if (stages > 1 && row != first)
@@ -623,16 +586,13 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     for (int r = 0; r < R; ++r, out += prm.out_stride) {
       if (r < left) {
         const float mean = __shfl_sync(0xffffffffu, means, r), rstd = __shfl_sync(0xffffffffu, rstds, r);
-        if constexpr (MODE == kCluster)
-          s[r] = row_join(words[r], buf);
-        else
-          s[r] = row_total<MODE>(s[r], words[r], buf, group, threads);
+        const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1);
         const Landed<T, V> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
         const bool p4 = (reinterpret_cast<uintptr_t>(out) & 3u) == 0;
-        const float2 k1 = both(-rstd * (s[r].x * inv)), k2 = both(-rstd * rstd * rstd * (s[r].y * inv));
+        const float2 k1 = both(-rstd * sum_a), k2 = both(-rstd * rstd * rstd * sum_ad);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int u = k * threads + tid;
+          const int u = u0 + 32 * k;
           float2 fx[P], fd[P], w[P];
           hx.read(u, fx);
           hd.read(u, fd);
@@ -644,7 +604,6 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
         }
       }
     }
-    buf ^= 1;
     if constexpr (WIDE) {   // a thread's slots are its own: free
       fetch_rows(x + stages * x_turn, dy + stages * dy_turn, left - stages * step, stage);
     } else if (stages == 1) {
@@ -672,8 +631,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          float2* a = reinterpret_cast<float2*>(acc + (k * threads + tid) * V) + i;
-          float2* b = reinterpret_cast<float2*>(acc + width + (k * threads + tid) * V) + i;
+          float2* a = reinterpret_cast<float2*>(acc + (u0 + 32 * k) * V) + i;
+          float2* b = reinterpret_cast<float2*>(acc + width + (u0 + 32 * k) * V) + i;
           *a = g ? __fadd2_rn(*a, dg[k][i]) : dg[k][i];
           *b = g ? __fadd2_rn(*b, db[k][i]) : db[k][i];
         }
@@ -689,7 +648,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (k * threads + tid) * V + i;
+        const int c = (u0 + 32 * k) * V + i;
         if (c < cols) {
           const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
           out_g[c] = add ? out_g[c] + vg : vg;
@@ -816,7 +775,7 @@ BackwardShape backward_shape(size_t rows, size_t cols) {
   const size_t slice = div_up(cols, s.csize);
   s.e = slice <= 256 ? 8 : slice <= 8192 ? 16 : 32;
   s.threads = threads_for(slice, s.e);
-  s.ctas = s.threads > 320 ? 1 : 2;
+  s.ctas = s.threads > 256 ? 1 : 2;
   s.groups = s.csize > 1 || s.threads > 256 ? 1 : 256 / s.threads;
   while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
   const size_t most = (size_t)s.ctas * sm_count() / s.csize;
@@ -849,7 +808,7 @@ cudaError_t backward(NormRowsParams& p, const BackwardShape& s, cudaStream_t st)
   }
   if (s.threads == 32 && s.e == 8) return s.r4 ? backward_e<T, V, 8, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 8, 1, kWarp, 256, 2>(p, s, st);
   if (s.threads == 32) return s.r4 ? backward_e<T, V, 16, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 16, 1, kWarp, 256, 2>(p, s, st);
-  if (s.threads <= 320) return s.r4 ? backward_e<T, V, 16, R, kCta, 320, 2>(p, s, st) : backward_e<T, V, 16, 1, kCta, 320, 2>(p, s, st);
+  if (s.threads <= 256) return s.r4 ? backward_e<T, V, 16, R, kCta, 256, 2>(p, s, st) : backward_e<T, V, 16, 1, kCta, 256, 2>(p, s, st);
   return s.r4 ? backward_e<T, V, 16, R, kCta, 512, 1>(p, s, st) : backward_e<T, V, 16, 1, kCta, 512, 1>(p, s, st);
 }
 
