@@ -5,6 +5,8 @@
 // move.  A group's tensors are cut into units once, at creation, and one
 // launch covers every tensor, so many small tensors cost no more launches
 // than one.
+#include <cuda_fp16.h>
+
 #include "xp_train_device.cuh"
 
 namespace xp {
@@ -148,11 +150,75 @@ __device__ __forceinline__ unsigned encode_one(float x, unsigned noise, int e) {
   return (unsigned)c;
 }
 
+// Two products at once, and two sums one by one: a product that feeds a sum
+// must be rounded by itself, and a packed product before a packed sum is fused
+// into one operation whatever the flags (seen as 1 ulp of the weights).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
+// The same for a thread's eight elements, in fewer operations; the results are
+// the same bits.
+//
+// Decoding: an exponent and 3 mantissa bits below a half's sign make a half
+// when they are shifted to its exponent and mantissa, and the block's scale is
+// a power of two that multiplies it exactly.  Two codes go in one register.
+// The codes are exact that way unless they are below 2^-27 of the block's
+// largest (v's codes 1 to 22, whose halves would be subnormal) or the block is
+// next to subnormal or not finite: then false.
+__device__ __forceinline__ float2 halves_to_floats(unsigned h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ bool decode8(uint2 cm, uint2 cv, int em, int ev, float2 (&m)[kVec / 2], float2 (&v)[kVec / 2]) {
+  const float sm = __int_as_float(max(em - 1, 1) << 23), sv = __int_as_float(max(ev - 14, 1) << 23);
+  unsigned least = 0xffffffffu;   // of v's codes - 1, 0 as the largest
+#pragma unroll
+  for (int i = 0; i < kVec / 2; ++i) {
+    const unsigned pick = i & 1 ? 0x4342u : 0x4140u;
+    const unsigned x = __byte_perm(i < 2 ? cm.x : cm.y, 0, pick), y = __byte_perm(i < 2 ? cv.x : cv.y, 0, pick);
+    // m: (magnitude + 9) << 7 is the half, 0 for magnitude 0
+    const unsigned mag = x & 0x007f007fu;
+    const unsigned hm = (mag * 128u + __vminu2(mag, 0x00010001u) * 1152u) | ((x << 8) & 0x80008000u);
+    m[i] = mul2(halves_to_floats(hm), sm);
+    // v: (code - 15) << 7, whose exponent is 30 at most (31 would be an infinity)
+    least = __viaddmin_u16x2(y, 0xffffffffu, least);
+    v[i] = mul2(halves_to_floats(__viaddmax_s16x2(y, 0xfff1fff1u, 0u) << 7), sv);
+  }
+  return min(least & 0xffffu, least >> 16) >= 22u && em != 255 && ev != 255 && (em >= 32 || (cm.x | cm.y) == 0) &&
+         (ev >= 32 || (cv.x | cv.y) == 0);
+}
+
+// Encoding: z = pattern + noise - (base << 20) has the code in bits 20 to 27;
+// shifted to the top byte, four of them are gathered by byte permutations.
+// em >= 16 and ev >= 32 (so that 0 gives 0).
+struct Encoder {
+  int cm, cv;
+  uint2 m, v;
+  unsigned zm[4], zv[4];
+  __device__ __forceinline__ Encoder(int em, int ev)
+      : cm(8 - ((8 * em - kShift<true>) << 20)), cv(8 - ((8 * ev - kShift<false>) << 20)) {}
+  // element k: m's pattern, v's pattern, the hashes in two registers
+  __device__ __forceinline__ void put(int k, unsigned bm, unsigned bv, unsigned hm, unsigned hv) {
+    const int a = __viaddmax_s32((int)(hm * 16u + (bm & 0x7fffffffu)), cm, 0);
+    const int b = __viaddmax_s32((int)(hv * 16u + bv), cv, (int)(min(bv, 1u) << 20));   // a positive v keeps code 1
+    zm[k & 3] = ((unsigned)a << 4) | (bm & 0x80000000u);
+    zv[k & 3] = (unsigned)b << 4;
+    if ((k & 3) == 3) {
+      unsigned c = __byte_perm(__byte_perm(zm[0], zm[1], 0x0073), __byte_perm(zm[2], zm[3], 0x0073), 0x5410);
+      c &= ((c & 0x7f7f7f7fu) + 0x7f7f7f7fu) | 0x7f7f7f7fu;   // no sign without a magnitude
+      const unsigned d = __byte_perm(__byte_perm(zv[0], zv[1], 0x0073), __byte_perm(zv[2], zv[3], 0x0073), 0x5410);
+      (k < 4 ? m.x : m.y) = c;
+      (k < 4 ? v.x : v.y) = d;
+    }
+  }
+};
+
 // A 32-bit mix of the step and the position: multiplications by odd constants
 // and shifts, each invertible, so that positions never collide within a key.
-__device__ __forceinline__ unsigned mix(unsigned x) {
+__device__ __forceinline__ unsigned mix_last(unsigned x) {   // but for its last xor
   x = (x ^ (x >> 16)) * 0xDDF15BA9u;
-  x = (x ^ (x >> 15)) * 0xE31B8755u;
+  return (x ^ (x >> 15)) * 0xE31B8755u;
+}
+__device__ __forceinline__ unsigned mix(unsigned x) {
+  x = mix_last(x);
   return x ^ (x >> 16);
 }
 constexpr unsigned kPosLo = 0x8ED88009u, kPosHi = 0xB86D3E2Fu;
@@ -160,43 +226,41 @@ __device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { ret
 
 // ---------------------------------------------------------------- the step
 
-// One unit per CTA, kVec elements per thread at a time.  The last warp keeps
-// the books: it reads the words that live from step to step and, in the CTA
-// that is last to have read them, writes the next step's, while the others
-// work on the elements.
+// What a thread's eight elements with 8-bit states take from memory.
+template <typename P, typename G>
+struct Codes8 {
+  Raw<G> g;
+  Raw<P> p;
+  uint2 cm, cv;
+  int em, ev;
+  __device__ __forceinline__ void load(const G* grad, const P* param, const GroupTensor& t, unsigned long long i) {
+    g = load_vec(grad);
+    p = load_vec(param);
+    cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
+    cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
+    em = t.m_scale[i / XP_STATE8_BLOCK];
+    ev = t.v_scale[i / XP_STATE8_BLOCK];
+  }
+};
+
+// One unit per CTA, kVec elements per thread at a time.  Thread 0 keeps the
+// books besides: it reads the words that live from step to step for its CTA,
+// counts it in, and in the CTA that was last to be counted it writes the next
+// step's words at the end, when all have read these.
 template <typename P, typename G, bool S8>
-__global__ void __launch_bounds__(kStepThreads + 32) adamw_kernel(const __grid_constant__ StepParams prm) {
+__global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const __grid_constant__ StepParams prm) {
   __shared__ float s_coef[2];
   __shared__ unsigned s_step;
   const GroupUnit u = prm.units[blockIdx.x];   // never written after the group's creation
   wait_for_predecessors();
   let_successor_start();
   if (prm.report && prm.skip_nonfinite && prm.report->nonfinite) return;   // the same answer in every CTA
-  if (threadIdx.x >= kStepThreads) {
-    volatile GroupState* st = prm.state;
-    unsigned long long step = 0;
-    double p1 = 0, p2 = 0;
-    if (threadIdx.x == kStepThreads) {
-      step = st->step;
-      p1 = st->power1, p2 = st->power2;
-      s_coef[0] = st->inv_bias1;
-      s_coef[1] = st->inv_sqrt_bias2;
-      s_step = (unsigned)(step + 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == kStepThreads) {
-      __threadfence();
-      if (atomicAdd(&prm.state->arrived_step, 1u) == gridDim.x - 1) {
-        const double n1 = p1 * prm.beta1_d, n2 = p2 * prm.beta2_d;
-        st->step = step + 1;
-        st->power1 = n1;
-        st->power2 = n2;
-        st->inv_bias1 = (float)(1.0 / (1.0 - n1));
-        st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
-        st->arrived_step = 0;
-      }
-    }
-    return;
+  unsigned arrived = 0;
+  if (threadIdx.x == 0) {
+    const volatile GroupState* st = prm.state;
+    s_coef[0] = st->inv_bias1;
+    s_coef[1] = st->inv_sqrt_bias2;
+    s_step = (unsigned)(st->step + 1);
   }
   const GroupTensor t = prm.tensors[u.tensor];
   const float lr = prm.lr_dev ? *prm.lr_dev : prm.lr;
@@ -208,78 +272,161 @@ __global__ void __launch_bounds__(kStepThreads + 32) adamw_kernel(const __grid_c
 
   // every thread of a warp makes the same number of turns: 8-bit blocks
   // share their exponent by shuffles
-  const unsigned turns = (u.n + kStepThreads * kVec - 1) / (kStepThreads * kVec);
-  unsigned at = threadIdx.x * kVec;
-  int n = 0;
-  float p[kVec], g[kVec], m[kVec], v[kVec];
-  uint2 cm, cv;
-  int em = 0, ev = 0;
-  auto load = [&] {
-    n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
+  constexpr unsigned kTurn = kStepThreads * kVec;
+  const unsigned turns = (u.n + kTurn - 1) / kTurn;
+  float alpha = 0.f, rs = 0.f;
+  unsigned key = 0;
+  auto coefficients = [&](unsigned turn) {   // after the first turn's loads are on their way
+    if (turn) return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      arrived = atomicAdd(&prm.state->arrived_step, 1u) + 1;
+    }
+    alpha = lr * s_coef[0];
+    rs = s_coef[1];
+    if (S8) key = step_key(prm.seed, s_step);
+  };
+  if (turns == 0) coefficients(0);
+  Codes8<P, G> next;
+  for (unsigned turn = 0; turn < turns; ++turn) {
+    const unsigned at = turn * kTurn + threadIdx.x * kVec;
+    const unsigned long long i = u.start + at, pos = t.pos + i;
+    uint8_t* const code_m = static_cast<uint8_t*>(t.m) + i;
+    uint8_t* const code_v = static_cast<uint8_t*>(t.v) + i;
+    unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi;   // kVec positions share the high word
+    if (S8 && vec && u.n - turn * kTurn >= kTurn) {
+      if (turn == 0) next.load(grad + at, param + at, t, i);
+      Codes8<P, G> now = next;
+      if (u.n - turn * kTurn >= 2 * kTurn) next.load(grad + at + kTurn, param + at + kTurn, t, i + kTurn);
+      coefficients(turn);
+      float2 m[kVec / 2], v[kVec / 2];
+      if (!decode8(now.cm, now.cv, now.em, now.ev, m, v)) {
+        float fm[kVec], fv[kVec];
+        decode_codes<true>(now.cm, now.em, fm);
+        decode_codes<false>(now.cv, now.ev, fv);
+#pragma unroll
+        for (int k = 0; k < kVec / 2; ++k) {
+          m[k] = make_float2(fm[2 * k], fm[2 * k + 1]);
+          v[k] = make_float2(fv[2 * k], fv[2 * k + 1]);
+        }
+      }
+      float g[kVec], p[kVec];
+      widen(now.g, g);
+      widen(now.p, p);
+#pragma unroll
+      for (int k = 0; k < kVec / 2; ++k) {
+        const float2 gi = mul2(make_float2(g[2 * k], g[2 * k + 1]), gscale);
+        m[k] = add2(mul2(m[k], prm.beta1), mul2(gi, prm.one_minus_beta1));
+        v[k] = add2(mul2(v[k], prm.beta2),
+                          mul2(mul2(gi, prm.one_minus_beta2), gi));
+        const float2 d = add2(mul2(make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y)), rs), make_float2(prm.eps, prm.eps));
+        const float2 a = mul2(m[k], alpha);
+        const float2 q = add2(mul2(make_float2(p[2 * k], p[2 * k + 1]), keep),
+                                    make_float2(-__fdiv_rn(a.x, d.x), -__fdiv_rn(a.y, d.y)));
+        p[2 * k] = q.x;
+        p[2 * k + 1] = q.y;
+      }
+      store_vec(param + at, p);
+      if (t.copy) store_vec(static_cast<__nv_bfloat16*>(t.copy) + i, p);
+      unsigned tm = 0, tv = 0;
+#pragma unroll
+      for (int k = 0; k < kVec / 2; ++k) {
+        tm = max(max(tm, __float_as_uint(m[k].x) & 0x7fffffffu), __float_as_uint(m[k].y) & 0x7fffffffu);
+        tv = max(max(tv, __float_as_uint(v[k].x) & 0x7fffffffu), __float_as_uint(v[k].y) & 0x7fffffffu);
+      }
+      unsigned top = (tm >> 23) << 16 | tv >> 23;
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
+      uint2 cm, cv;
+      h += key;
+      if (em >= 16 && ev >= 32) {
+        Encoder enc(em, ev);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k, h += kPosLo) {
+          const unsigned r = mix_last(h);
+          const float2 mk = m[k / 2], vk = v[k / 2];
+          enc.put(k, __float_as_uint(k & 1 ? mk.y : mk.x), __float_as_uint(k & 1 ? vk.y : vk.x), r >> 16, (r ^ (r >> 16)) & 0xffffu);
+        }
+        cm = enc.m;
+        cv = enc.v;
+      } else {
+        cm = cv = make_uint2(0, 0);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k, h += kPosLo) {
+          const unsigned r = mix(h);
+          const float2 mk = m[k / 2], vk = v[k / 2];
+          (k < 4 ? cm.x : cm.y) |= encode_one<true>(k & 1 ? mk.y : mk.x, ((r >> 16) << 4) + 8u, em) << (8 * (k & 3));
+          (k < 4 ? cv.x : cv.y) |= encode_one<false>(k & 1 ? vk.y : vk.x, ((r & 0xffffu) << 4) + 8u, ev) << (8 * (k & 3));
+        }
+      }
+      *reinterpret_cast<uint2*>(code_m) = cm;
+      *reinterpret_cast<uint2*>(code_v) = cv;
+      if ((threadIdx.x & 3) == 0) {   // a block is four threads' elements
+        t.m_scale[i / XP_STATE8_BLOCK] = (uint8_t)em;
+        t.v_scale[i / XP_STATE8_BLOCK] = (uint8_t)ev;
+      }
+      continue;
+    }
+    const int n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
+    float p[kVec], g[kVec], m[kVec], v[kVec];
     load_some(grad + at, n, vec, g);
     load_some(param + at, n, vec, p);
     if constexpr (S8) {
-      const unsigned long long i = u.start + at;
-      cm = load_codes(static_cast<const uint8_t*>(t.m) + i, n, vec);
-      cv = load_codes(static_cast<const uint8_t*>(t.v) + i, n, vec);
-      em = n ? t.m_scale[i / XP_STATE8_BLOCK] : 0;
-      ev = n ? t.v_scale[i / XP_STATE8_BLOCK] : 0;
+      decode_codes<true>(load_codes(code_m, n, vec), n ? t.m_scale[i / XP_STATE8_BLOCK] : 0, m);
+      decode_codes<false>(load_codes(code_v, n, vec), n ? t.v_scale[i / XP_STATE8_BLOCK] : 0, v);
     } else {
-      load_some(static_cast<const float*>(t.m) + u.start + at, n, vec, m);
-      load_some(static_cast<const float*>(t.v) + u.start + at, n, vec, v);
+      load_some(static_cast<const float*>(t.m) + i, n, vec, m);
+      load_some(static_cast<const float*>(t.v) + i, n, vec, v);
     }
-  };
-  load();
-  __syncthreads();
-  const float alpha = lr * s_coef[0], rs = s_coef[1];
-  const unsigned key = S8 ? step_key(prm.seed, s_step) : 0;
-  for (unsigned turn = 0; turn < turns;) {
-    if constexpr (S8) {
-      decode_codes<true>(cm, em, m);
-      decode_codes<false>(cv, ev, v);
-    }
+    coefficients(turn);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float gi = g[i] * gscale;
-      m[i] = m[i] * prm.beta1 + gi * prm.one_minus_beta1;
-      v[i] = v[i] * prm.beta2 + gi * prm.one_minus_beta2 * gi;
-      const float d = __fsqrt_rn(v[i]) * rs + prm.eps;
-      p[i] = p[i] * keep - __fdiv_rn(m[i] * alpha, d);
+    for (int k = 0; k < kVec; ++k) {
+      const float gi = g[k] * gscale;
+      m[k] = m[k] * prm.beta1 + gi * prm.one_minus_beta1;
+      v[k] = v[k] * prm.beta2 + gi * prm.one_minus_beta2 * gi;
+      const float d = __fsqrt_rn(v[k]) * rs + prm.eps;
+      p[k] = p[k] * keep - __fdiv_rn(m[k] * alpha, d);
     }
     store_some(param + at, n, vec, p);
-    if (t.copy) store_some(static_cast<__nv_bfloat16*>(t.copy) + u.start + at, n, vec, p);
+    if (t.copy) store_some(static_cast<__nv_bfloat16*>(t.copy) + i, n, vec, p);
     if constexpr (S8) {
-      const unsigned long long i = u.start + at, pos = t.pos + i;
 #pragma unroll
       for (int k = 0; k < kVec; ++k)
         if (k >= n) m[k] = v[k] = 0.f;
       unsigned top = top_exponent(m) << 16 | top_exponent(v);
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      em = (int)(top >> 16), ev = (int)(top & 0xffffu);
-      unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi + key;   // kVec positions share the high word
-      cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+      const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
+      uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+      h += key;
 #pragma unroll
       for (int k = 0; k < kVec; ++k, h += kPosLo) {
         const unsigned r = mix(h);
-        const unsigned a = encode_one<true>(m[k], ((r >> 16) << 4) + 8u, em);
-        const unsigned b = encode_one<false>(v[k], ((r & 0xffffu) << 4) + 8u, ev);
-        (k < 4 ? cm.x : cm.y) |= a << (8 * (k & 3));
-        (k < 4 ? cv.x : cv.y) |= b << (8 * (k & 3));
+        (k < 4 ? cm.x : cm.y) |= encode_one<true>(m[k], ((r >> 16) << 4) + 8u, em) << (8 * (k & 3));
+        (k < 4 ? cv.x : cv.y) |= encode_one<false>(v[k], ((r & 0xffffu) << 4) + 8u, ev) << (8 * (k & 3));
       }
-      store_codes(static_cast<uint8_t*>(t.m) + i, n, vec, cm);
-      store_codes(static_cast<uint8_t*>(t.v) + i, n, vec, cv);
-      if (n && (i & (XP_STATE8_BLOCK - 1)) == 0) {
+      store_codes(code_m, n, vec, cm);
+      store_codes(code_v, n, vec, cv);
+      if (n && (threadIdx.x & 3) == 0) {
         t.m_scale[i / XP_STATE8_BLOCK] = (uint8_t)em;
         t.v_scale[i / XP_STATE8_BLOCK] = (uint8_t)ev;
       }
     } else {
-      store_some(static_cast<float*>(t.m) + u.start + at, n, vec, m);
-      store_some(static_cast<float*>(t.v) + u.start + at, n, vec, v);
+      store_some(static_cast<float*>(t.m) + i, n, vec, m);
+      store_some(static_cast<float*>(t.v) + i, n, vec, v);
     }
-    if (++turn == turns) break;
-    at += kStepThreads * kVec;
-    load();
+  }
+  if (arrived == gridDim.x) {   // thread 0 of the last CTA
+    GroupState* st = prm.state;
+    const double n1 = st->power1 * prm.beta1_d, n2 = st->power2 * prm.beta2_d;
+    st->step = st->step + 1;
+    st->power1 = n1;
+    st->power2 = n2;
+    st->inv_bias1 = (float)(1.0 / (1.0 - n1));
+    st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
+    st->arrived_step = 0;
   }
 }
 
@@ -393,7 +540,7 @@ __global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_const
 
 template <typename P, typename G, bool S8>
 cudaError_t run_adamw(const StepParams& p, unsigned nunits, cudaStream_t st) {
-  return launch_dependent(adamw_kernel<P, G, S8>, dim3(nunits), kStepThreads + 32, 0, 1, st, p);
+  return launch_dependent(adamw_kernel<P, G, S8>, dim3(nunits), kStepThreads, 0, 1, st, p);
 }
 
 }  // namespace
