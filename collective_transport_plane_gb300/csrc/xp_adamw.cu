@@ -5,8 +5,6 @@
 // move.  A group's tensors are cut into units once, at creation, and one
 // launch covers every tensor, so many small tensors cost no more launches
 // than one.
-#include <cuda_fp16.h>
-
 #include "xp_train_device.cuh"
 
 namespace xp {
@@ -160,30 +158,24 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(
 // The same for a thread's eight elements, in fewer operations; the results are
 // the same bits.
 //
-// Decoding: an exponent and 3 mantissa bits below a half's sign make a half
-// when they are shifted to its exponent and mantissa, and the block's scale is
-// a power of two that multiplies it exactly.  Two codes go in one register.
-// The codes are exact that way unless they are below 2^-27 of the block's
-// largest (v's codes 1 to 22, whose halves would be subnormal) or the block is
-// next to subnormal or not finite: then false.
-__device__ __forceinline__ float2 halves_to_floats(unsigned h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
-__device__ __forceinline__ bool decode8(uint2 cm, uint2 cv, int em, int ev, float2 (&m)[kVec / 2], float2 (&v)[kVec / 2]) {
-  const float sm = __int_as_float(max(em - 1, 1) << 23), sv = __int_as_float(max(ev - 14, 1) << 23);
-  unsigned least = 0xffffffffu;   // of v's codes - 1, 0 as the largest
+// Decoding: a code's fp32 pattern has nothing below its upper half, which is
+// (magnitude + base) << 4: two codes go in one register, as a pair of bf16.
+// em and ev >= 32, or all codes 0; finite.
+__device__ __forceinline__ bool pairs_ok(uint2 c, int e) { return (e >= 32 || (c.x | c.y) == 0) && e != 255; }
+template <bool SIGNED>
+__device__ __forceinline__ void decode_pairs(uint2 c, int e, unsigned (&w)[kVec / 2]) {
+  const unsigned base = 16u * (unsigned)max(8 * e - kShift<SIGNED>, 0);
 #pragma unroll
   for (int i = 0; i < kVec / 2; ++i) {
-    const unsigned pick = i & 1 ? 0x4342u : 0x4140u;
-    const unsigned x = __byte_perm(i < 2 ? cm.x : cm.y, 0, pick), y = __byte_perm(i < 2 ? cv.x : cv.y, 0, pick);
-    // m: (magnitude + 9) << 7 is the half, 0 for magnitude 0
-    const unsigned mag = x & 0x007f007fu;
-    const unsigned hm = (mag * 128u + __vminu2(mag, 0x00010001u) * 1152u) | ((x << 8) & 0x80008000u);
-    m[i] = mul2(halves_to_floats(hm), sm);
-    // v: (code - 15) << 7, whose exponent is 30 at most (31 would be an infinity)
-    least = __viaddmin_u16x2(y, 0xffffffffu, least);
-    v[i] = mul2(halves_to_floats(__viaddmax_s16x2(y, 0xfff1fff1u, 0u) << 7), sv);
+    const unsigned x = __byte_perm(i < 2 ? c.x : c.y, 0, i & 1 ? 0x4342u : 0x4140u);
+    const unsigned mag = SIGNED ? x & 0x007f007fu : x;
+    w[i] = mag * 16u + __vminu2(mag, 0x00010001u) * base;   // 0 for magnitude 0
+    if (SIGNED) w[i] |= (x << 8) & 0x80008000u;
   }
-  return min(least & 0xffffu, least >> 16) >= 22u && em != 255 && ev != 255 && (em >= 32 || (cm.x | cm.y) == 0) &&
-         (ev >= 32 || (cv.x | cv.y) == 0);
+}
+__device__ __forceinline__ void widen_pairs(const unsigned (&w)[kVec / 2], float2 (&f)[kVec / 2]) {
+#pragma unroll
+  for (int i = 0; i < kVec / 2; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
 // Encoding: z = pattern + noise - (base << 20) has the code in bits 20 to 27;
@@ -243,12 +235,16 @@ struct Codes8 {
   }
 };
 
-// One unit per CTA, kVec elements per thread at a time.  Thread 0 keeps the
-// books besides: it reads the words that live from step to step for its CTA,
-// counts it in, and in the CTA that was last to be counted it writes the next
-// step's words at the end, when all have read these.
+// One unit per CTA, kVec elements per thread at a time.  One thread keeps the
+// books: it reads the words that live from step to step for its CTA, counts it
+// in, and in the CTA that was counted last writes the next step's words, as
+// all have read these.  With fp32 states it is in a warp of its own, beside
+// the work (a step of 5000 elements: 4.0 us, and 5.6 with thread 0 keeping the
+// books at the end); with 8-bit states, where registers are short, thread 0.
+template <bool S8>
+constexpr int kBooksThreads = S8 ? 0 : 32;
 template <typename P, typename G, bool S8>
-__global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const __grid_constant__ StepParams prm) {
+__global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_kernel(const __grid_constant__ StepParams prm) {
   __shared__ float s_coef[2];
   __shared__ unsigned s_step;
   const GroupUnit u = prm.units[blockIdx.x];   // never written after the group's creation
@@ -256,12 +252,42 @@ __global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const _
   let_successor_start();
   if (prm.report && prm.skip_nonfinite && prm.report->nonfinite) return;   // the same answer in every CTA
   unsigned arrived = 0;
-  if (threadIdx.x == 0) {
+  unsigned long long step = 0;
+  double power1 = 0.0, power2 = 0.0;
+  auto read_words = [&] {
     const volatile GroupState* st = prm.state;
+    step = st->step;
+    if (!S8) power1 = st->power1, power2 = st->power2;
     s_coef[0] = st->inv_bias1;
     s_coef[1] = st->inv_sqrt_bias2;
-    s_step = (unsigned)(st->step + 1);
+    s_step = (unsigned)(step + 1);
+  };
+  auto count_in = [&] {
+    __threadfence();
+    arrived = atomicAdd(&prm.state->arrived_step, 1u) + 1;
+  };
+  auto next_words = [&] {
+    if (arrived != gridDim.x) return;
+    GroupState* st = prm.state;
+    if (S8) power1 = st->power1, power2 = st->power2;   // not held through the work
+    const double n1 = power1 * prm.beta1_d, n2 = power2 * prm.beta2_d;
+    st->step = step + 1;
+    st->power1 = n1;
+    st->power2 = n2;
+    st->inv_bias1 = (float)(1.0 / (1.0 - n1));
+    st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
+    st->arrived_step = 0;
+  };
+  if (!S8 && threadIdx.x >= kStepThreads) {
+    if (threadIdx.x == kStepThreads) read_words();
+    __syncthreads();
+    if (threadIdx.x == kStepThreads) {
+      count_in();
+      next_words();
+    }
+    return;
   }
+  if (S8 && threadIdx.x == 0) read_words();
   const GroupTensor t = prm.tensors[u.tensor];
   const float lr = prm.lr_dev ? *prm.lr_dev : prm.lr;
   const float gscale = prm.report ? prm.report->scale : prm.grad_scale;
@@ -279,10 +305,7 @@ __global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const _
   auto coefficients = [&](unsigned turn) {   // after the first turn's loads are on their way
     if (turn) return;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      arrived = atomicAdd(&prm.state->arrived_step, 1u) + 1;
-    }
+    if (S8 && threadIdx.x == 0) count_in();
     alpha = lr * s_coef[0];
     rs = s_coef[1];
     if (S8) key = step_key(prm.seed, s_step);
@@ -301,7 +324,13 @@ __global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const _
       if (u.n - turn * kTurn >= 2 * kTurn) next.load(grad + at + kTurn, param + at + kTurn, t, i + kTurn);
       coefficients(turn);
       float2 m[kVec / 2], v[kVec / 2];
-      if (!decode8(now.cm, now.cv, now.em, now.ev, m, v)) {
+      if (pairs_ok(now.cm, now.em) && pairs_ok(now.cv, now.ev)) {
+        unsigned wm[kVec / 2], wv[kVec / 2];
+        decode_pairs<true>(now.cm, now.em, wm);
+        decode_pairs<false>(now.cv, now.ev, wv);
+        widen_pairs(wm, m);
+        widen_pairs(wv, v);
+      } else {
         float fm[kVec], fv[kVec];
         decode_codes<true>(now.cm, now.em, fm);
         decode_codes<false>(now.cv, now.ev, fv);
@@ -418,16 +447,7 @@ __global__ void __launch_bounds__(kStepThreads, S8 ? 3 : 4) adamw_kernel(const _
       store_some(static_cast<float*>(t.v) + i, n, vec, v);
     }
   }
-  if (arrived == gridDim.x) {   // thread 0 of the last CTA
-    GroupState* st = prm.state;
-    const double n1 = st->power1 * prm.beta1_d, n2 = st->power2 * prm.beta2_d;
-    st->step = st->step + 1;
-    st->power1 = n1;
-    st->power2 = n2;
-    st->inv_bias1 = (float)(1.0 / (1.0 - n1));
-    st->inv_sqrt_bias2 = (float)(1.0 / sqrt(1.0 - n2));
-    st->arrived_step = 0;
-  }
+  if (S8 && threadIdx.x == 0) next_words();
 }
 
 // ---------------------------------------------------------------- the norm
@@ -442,29 +462,57 @@ __device__ __forceinline__ F warp_sum(F x) {
 // Each CTA adds up its units' squares and leaves one fp64 sum; the CTA that
 // arrives last adds the sums up in their order, so the result does not depend
 // on which CTA that is.  fp32 up to a warp's sum, fp64 above: an SM does 2 fp64
-// additions per clock.
+// additions per clock.  The units are taken from the last to the first, so
+// that L2 holds the gradients a step reads first; the next unit's place is
+// looked up while one is added.
 template <typename G>
-__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormParams prm) {
+__global__ void __launch_bounds__(kNormThreads, 5) grad_norm_kernel(const __grid_constant__ NormParams prm) {
   __shared__ double s_sum[kNormThreads / 32];
   __shared__ bool s_last;
+  constexpr unsigned kTurn = kNormThreads * kVec;
+  constexpr int kDeep = sizeof(G) == 2 ? 4 : 2;   // loads of a thread in flight, 64 bytes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned k = blockIdx.x;
+  GroupUnit u = prm.units[prm.nunits - 1 - k];   // never written after the group's creation
   wait_for_predecessors();
   let_successor_start();
+  const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
   double sum = 0.0;
-  for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) {
-    const GroupUnit u = prm.units[k];
-    const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
-    const bool vec = vec_ok(grad);
-    grad += u.start;
+  while (true) {
+    const G* g = grad + u.start + threadIdx.x * kVec;
+    const unsigned n = u.n, after = k + gridDim.x;
+    const bool vec = vec_ok(grad), more = after < prm.nunits;
     float acc[kVec] = {};
-    for (unsigned at = threadIdx.x * kVec; at < u.n; at += kNormThreads * kVec) {
-      float g[kVec];
-      load_some(grad + at, (int)min((unsigned)kVec, u.n - at), vec, g);
+    auto add = [&](const float (&f)[kVec]) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(g[i], g[i], acc[i]);
+      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(f[i], f[i], acc[i]);
+    };
+    if (more) u = prm.units[prm.nunits - 1 - after];
+    unsigned at = 0;
+    if (vec) {
+      for (; n - at >= kDeep * kTurn; at += kDeep * kTurn) {
+        Raw<G> r[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) r[i] = load_vec(g + at + i * kTurn);
+        if (more) grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+          float f[kVec];
+          widen(r[i], f);
+          add(f);
+        }
+      }
     }
+    for (; at + threadIdx.x * kVec < n; at += kTurn) {
+      float f[kVec];
+      load_some(g + at, (int)min((unsigned)kVec, n - at - threadIdx.x * kVec), vec, f);
+      add(f);
+    }
+    if (more) grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
     const float w = warp_sum(((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
     if (lane == 0) sum += (double)w;
+    if (!more) break;
+    k = after;
   }
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
@@ -517,6 +565,7 @@ __global__ void set_step_kernel(GroupState* s, unsigned long long step, double p
   s->arrived_norm = 0;
 }
 
+// m in the grid's row 0, v in row 1; a thread takes kVec codes at each of two places.
 template <typename O>
 __global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_constant__ DecodeParams prm) {
   wait_for_predecessors();
@@ -524,23 +573,49 @@ __global__ void __launch_bounds__(kStepThreads) decode_kernel(const __grid_const
   const int which = blockIdx.y;
   O* out = static_cast<O*>(prm.out[which]);
   if (!out) return;
-  const unsigned long long at = ((unsigned long long)blockIdx.x * kStepThreads + threadIdx.x) * kVec;
-  if (at >= prm.count) return;
-  const int n = (int)min((unsigned long long)kVec, prm.count - at);
   const uint8_t* code = prm.code[which];
-  const uint2 c = load_codes(code + at, n, (reinterpret_cast<uintptr_t>(code) & 7u) == 0);
-  const int e = prm.scale[which][at / XP_STATE8_BLOCK];
-  float f[kVec];
-  if (which == 0)
-    decode_codes<true>(c, e, f);
-  else
-    decode_codes<false>(c, e, f);
-  store_some(out + at, n, vec_ok(out), f);
+  const bool vec = (reinterpret_cast<uintptr_t>(code) & 7u) == 0, vec_out = vec_ok(out);
+  const unsigned long long first = (unsigned long long)blockIdx.x * kDecodeCta + threadIdx.x * kVec;
+  uint2 c[2];
+  int e[2], n[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const unsigned long long at = first + j * (kDecodeCta / 2);
+    n[j] = at < prm.count ? (int)min((unsigned long long)kVec, prm.count - at) : 0;
+    c[j] = load_codes(code + at, n[j], vec);
+    e[j] = n[j] ? prm.scale[which][at / XP_STATE8_BLOCK] : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    O* to = out + first + j * (kDecodeCta / 2);
+    if (n[j] == kVec && vec_out && pairs_ok(c[j], e[j])) {
+      unsigned w[kVec / 2];
+      if (which == 0)
+        decode_pairs<true>(c[j], e[j], w);
+      else
+        decode_pairs<false>(c[j], e[j], w);
+      if constexpr (sizeof(O) == 2) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        float2 f[kVec / 2];
+        widen_pairs(w, f);
+        reinterpret_cast<float4*>(to)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        reinterpret_cast<float4*>(to)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+      }
+    } else if (n[j]) {
+      float f[kVec];
+      if (which == 0)
+        decode_codes<true>(c[j], e[j], f);
+      else
+        decode_codes<false>(c[j], e[j], f);
+      store_some(to, n[j], vec_out, f);
+    }
+  }
 }
 
 template <typename P, typename G, bool S8>
 cudaError_t run_adamw(const StepParams& p, unsigned nunits, cudaStream_t st) {
-  return launch_dependent(adamw_kernel<P, G, S8>, dim3(nunits), kStepThreads, 0, 1, st, p);
+  return launch_dependent(adamw_kernel<P, G, S8>, dim3(nunits), kStepThreads + kBooksThreads<S8>, 0, 1, st, p);
 }
 
 }  // namespace
@@ -571,8 +646,7 @@ cudaError_t launch_set_step(GroupState* s, unsigned long long step, double p1, d
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int out_dtype, cudaStream_t st) {
-  const unsigned long long per = (unsigned long long)kStepThreads * kVec;
-  const dim3 grid((unsigned)((p.count + per - 1) / per), 2);
+  const dim3 grid((unsigned)((p.count + kDecodeCta - 1) / kDecodeCta), 2);
   return launch_dependent(out_dtype == XP_F32 ? decode_kernel<float> : decode_kernel<__nv_bfloat16>, grid, kStepThreads, 0, 1, st, p);
 }
 

@@ -47,8 +47,9 @@ struct GroupState {
 
 constexpr int kStepThreads = 256;
 constexpr int kVec = 8;                  // elements a thread moves at once
-constexpr int kNormThreads = 512;
-constexpr int kNormMaxCtas = 152 * 4;
+constexpr int kDecodeCta = 2 * kStepThreads * kVec;   // codes of one CTA of a decode
+constexpr int kNormThreads = 256;
+constexpr int kNormMaxCtas = 152 * 5;
 constexpr int kSetGradsMax = 448;        // pointers passed in one launch's parameters
 
 struct StepParams {

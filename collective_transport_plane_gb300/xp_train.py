@@ -57,23 +57,20 @@ for _name, _args in {
 }.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = ctypes.c_int
+_forward, _backward, _norm, _step = (_lib.xp_layernorm_forward, _lib.xp_layernorm_backward, _lib.xp_grad_norm,
+                                     _lib.xp_adamw_step)
 
 _DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
 _types = {}   # torch dtype -> xp_dtype, filled as types are met
 
 
 def _dtype(t) -> int:
-    d = t.dtype
-    found = _types.get(d)
+    found = _types.get(t.dtype)
     if found is None:
-        if str(d) not in _DTYPES:
-            raise ValueError(f"no xp_dtype for {d}")
-        found = _types[d] = _DTYPES[str(d)]
+        if str(t.dtype) not in _DTYPES:
+            raise ValueError(f"no xp_dtype for {t.dtype}")
+        found = _types[t.dtype] = _DTYPES[str(t.dtype)]
     return found
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
 
 
 def _check(st: int, where: str):
@@ -81,37 +78,35 @@ def _check(st: int, where: str):
         xp._check(st, where)
 
 
-def _rows(t, shape, what):
+def _row(t, shape, dtype, what):
     """A matrix's row stride in elements; its columns lie side by side."""
-    if t.shape != shape:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of {dtype}")
     row, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError(f"{what}'s columns are {col} elements apart")
     return row
 
 
-def _vector(t, n, what, dtype=None):
-    if t is not None and (t.numel() != n or not t.is_contiguous() or (dtype is not None and _dtype(t) != dtype)):
+def _vector(t, n, what, dtype):
+    """The address of n contiguous elements (None: none)."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous() or _dtype(t) != dtype:
         raise ValueError(f"{what} is not {n} contiguous elements of its type")
+    return t.data_ptr()
 
 
 def xp_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
     """y = layer norm of each row of x (rows x cols), with its statistics where mean and rstd are given."""
-    shape = x.shape
+    shape, dtype = x.shape, x.dtype
     rows, cols = shape
     dt = _dtype(x)
-    w = gamma if gamma is not None else beta
-    wdt = dt if w is None else _dtype(w)
-    xs, ys = _rows(x, shape, "x"), _rows(y, shape, "y")
-    if _dtype(y) != dt:
-        raise ValueError("x and y differ in type")
-    _vector(gamma, cols, "gamma", wdt)
-    _vector(beta, cols, "beta", wdt)
-    _vector(mean, rows, "mean", XP_F32)
-    _vector(rstd, rows, "rstd", XP_F32)
-    _check(_lib.xp_layernorm_forward(x.data_ptr(), xs, _p(gamma), _p(beta), y.data_ptr(), ys, _p(mean), _p(rstd), rows, cols,
-                                     eps, dt, wdt, _stream(stream)), "xp_layernorm_forward")
+    wdt = _dtype(gamma) if gamma is not None else dt if beta is None else _dtype(beta)
+    xs, ys = _row(x, shape, dtype, "x"), _row(y, shape, dtype, "y")
+    _check(_forward(x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(beta, cols, "beta", wdt), y.data_ptr(), ys,
+                    _vector(mean, rows, "mean", XP_F32), _vector(rstd, rows, "rstd", XP_F32), rows, cols, eps, dt, wdt,
+                    stream if stream is None else _stream(stream)), "xp_layernorm_forward")
 
 
 def xp_layernorm_workspace(rows: int, cols: int) -> int:
@@ -123,22 +118,16 @@ def xp_layernorm_workspace(rows: int, cols: int) -> int:
 def xp_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, accumulate: bool = False,
                           stream=None) -> None:
     """dx, and over the rows dgamma and dbeta, from dy and what the forward pass gave."""
-    shape = x.shape
+    shape, dtype = x.shape, x.dtype
     rows, cols = shape
     dt = _dtype(x)
     wdt = dt if gamma is None else _dtype(gamma)
-    xs, dys, dxs = _rows(x, shape, "x"), _rows(dy, shape, "dy"), _rows(dx, shape, "dx")
-    if _dtype(dy) != dt or _dtype(dx) != dt:
-        raise ValueError("dy, x and dx differ in type")
-    _vector(gamma, cols, "gamma", wdt)
-    _vector(mean, rows, "mean", XP_F32)
-    _vector(rstd, rows, "rstd", XP_F32)
-    _vector(dgamma, cols, "dgamma", XP_F32)
-    _vector(dbeta, cols, "dbeta", XP_F32)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.xp_layernorm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _p(gamma), mean.data_ptr(), rstd.data_ptr(),
-                                      dx.data_ptr(), dxs, _p(dgamma), _p(dbeta), rows, cols, dt, wdt, 1 if accumulate else 0,
-                                      _p(workspace), nbytes, _stream(stream)), "xp_layernorm_backward")
+    dys, xs, dxs = _row(dy, shape, dtype, "dy"), _row(x, shape, dtype, "x"), _row(dx, shape, dtype, "dx")
+    _check(_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(mean, rows, "mean", XP_F32),
+                     _vector(rstd, rows, "rstd", XP_F32), dx.data_ptr(), dxs, _vector(dgamma, cols, "dgamma", XP_F32),
+                     _vector(dbeta, cols, "dbeta", XP_F32), rows, cols, dt, wdt, 1 if accumulate else 0,
+                     None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+                     stream if stream is None else _stream(stream)), "xp_layernorm_backward")
 
 
 def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=None, copies=None, weight_decay=0.0,
@@ -163,8 +152,8 @@ def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=No
             t = None if tensors is None else tensors[i]
             if t is None:
                 continue
-            _vector(t, -(-count // XP_STATE8_BLOCK) if name.endswith("scale") else count, f"{name} {i}", want[name])
-            setattr(table[i], name, t.data_ptr())
+            n_here = -(-count // XP_STATE8_BLOCK) if name.endswith("scale") else count
+            setattr(table[i], name, _vector(t, n_here, f"{name} {i}", want[name]))
         table[i].count = count
         table[i].weight_decay = decay[i]
     out = ctypes.c_void_p()
@@ -194,14 +183,15 @@ def xp_group_get_step(group: int, stream=None) -> int:
 
 def xp_grad_norm(group: int, report, grad_scale: float = 1.0, max_norm: float = 0.0, accumulate: bool = False, stream=None) -> None:
     """The norm of the group's gradients into `report`, 32 bytes of device memory laid out as xp_grad_report."""
-    _check(_lib.xp_grad_norm(group, grad_scale, max_norm, 1 if accumulate else 0, report.data_ptr(), _stream(stream)), "xp_grad_norm")
+    _check(_norm(group, grad_scale, max_norm, 1 if accumulate else 0, report.data_ptr(), stream if stream is None else _stream(stream)),
+           "xp_grad_norm")
 
 
 def xp_adamw_step(group: int, lr: float, report=None, grad_scale: float = 1.0, skip_nonfinite: bool = False, lr_dev=None,
                   stream=None) -> None:
     """One AdamW step on the group's tensors, gradients scaled by the report's scale if there is one."""
-    _check(_lib.xp_adamw_step(group, lr, _p(lr_dev), grad_scale, _p(report), XP_ADAMW_SKIP_NONFINITE if skip_nonfinite else 0,
-                              _stream(stream)), "xp_adamw_step")
+    _check(_step(group, lr, None if lr_dev is None else lr_dev.data_ptr(), grad_scale, None if report is None else report.data_ptr(),
+                 XP_ADAMW_SKIP_NONFINITE if skip_nonfinite else 0, stream if stream is None else _stream(stream)), "xp_adamw_step")
 
 
 def xp_state8_decode(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
@@ -210,10 +200,8 @@ def xp_state8_decode(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
     if out is None:
         return
     count, dt = out.numel(), _dtype(out)
-    for name, code, scale, to in (("m", m, m_scale, m_out), ("v", v, v_scale, v_out)):
-        if to is not None:
-            _vector(to, count, name + "_out", dt)
-            _vector(code, count, name, XP_U8)
-            _vector(scale, -(-count // XP_STATE8_BLOCK), name + "_scale", XP_U8)
-    _check(_lib.xp_state8_decode(_p(m), _p(m_scale), _p(v), _p(v_scale), count, _p(m_out), _p(v_out), dt, _stream(stream)),
-           "xp_state8_decode")
+    blocks = -(-count // XP_STATE8_BLOCK)
+    args = [_vector(m_out, count, "m_out", dt), _vector(v_out, count, "v_out", dt)]
+    for to, code, scale, name in ((v_out, v, v_scale, "v"), (m_out, m, m_scale, "m")):
+        args[:0] = [None, None] if to is None else [_vector(code, count, name, XP_U8), _vector(scale, blocks, name + "_scale", XP_U8)]
+    _check(_lib.xp_state8_decode(*args[:4], count, *args[4:], dt, stream if stream is None else _stream(stream)), "xp_state8_decode")
