@@ -21,15 +21,13 @@ constexpr int kMaxCluster8 = 8;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float f) { *p = f; }
-__device__ __forceinline__ void put(bf16* p, float f) { *p = __float2bfloat16_rn(f); }
 
-// ---- units: the V elements a thread takes at once, as V / 2 pairs.  Rows that
-// allow it move in units of 16 bytes; others (lengths, strides or addresses
-// that are no multiple of 16 bytes) in units of two elements, read from
-// shared memory at any offset.
-template <typename T, int V>
-constexpr bool kWide = V * sizeof(T) == 16;
+// ---- units: the V elements (16 bytes) a thread takes at once, as V / 2 pairs.
+// Rows that allow it move between global and shared memory or registers in
+// units; in others (NARROW: lengths, strides or addresses that are no multiple
+// of 16 bytes) in 4-byte words, and are units in shared memory only.
+template <typename T>
+constexpr int kUnit = 16 / (int)sizeof(T);
 
 __device__ __forceinline__ float lo_of(unsigned w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
@@ -51,30 +49,26 @@ __device__ __forceinline__ unsigned pack2(float2 f) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const unsigned*>(&h);
 }
-// The first n elements of a unit (wide units are whole or absent) to global
-// memory; p4: a pair of bf16 may go in one store.
 template <typename T, int P>
-__device__ __forceinline__ void store_unit(T* p, int n, bool p4, const float2 (&f)[P]) {
-  if constexpr (P == 4) {
-    if (n > 0) *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
-  } else if constexpr (P == 2) {
-    if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-  } else if (sizeof(T) == 2 && n >= 2 && p4) {
-    *reinterpret_cast<unsigned*>(p) = pack2(f[0]);
-  } else {
-    if (n > 0) put(p, f[0].x);
-    if (n > 1) put(p + 1, f[0].y);
-  }
+__device__ __forceinline__ uint4 pack16(const float2 (&f)[P]) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+  else
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
-// A unit of gamma or beta; `none` where there is none.  No branches: the loads
-// of several units are in flight together.
-template <typename W, int P>
+// A unit of gamma or beta; `none` where there is none, and past the row's end.
+// WHOLE: units are whole or absent, and their loads branch nowhere, so that
+// those of several units are in flight together.
+template <typename W, bool WHOLE, int P>
 __device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float none, float2 (&f)[P]) {
   const W* p = static_cast<const W*>(w) + c;
   const bool has = w && n > 0;
-  if constexpr (P == 1) {
-    f[0].x = has ? to_f(__ldg(p)) : none;
-    f[0].y = has && n > 1 ? to_f(__ldg(p + 1)) : none;
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f[i].x = w && 2 * i < n ? to_f(__ldg(p + 2 * i)) : none;
+      f[i].y = w && 2 * i + 1 < n ? to_f(__ldg(p + 2 * i + 1)) : none;
+    }
   } else if constexpr (sizeof(W) == 4) {
     const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
@@ -192,9 +186,12 @@ __device__ __forceinline__ float row_sum(float x, SumWords<1>& w, int buf, int t
 __device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
-// the first `bytes` of them, zeros after
-__device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+// a word: its first `bytes` bytes, zeros after
+__device__ __forceinline__ void copy_async4(unsigned smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy_async4(unsigned smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest n groups of this thread's copies have landed
@@ -212,51 +209,57 @@ __device__ __forceinline__ void wait_groups(int n) {
 }
 constexpr int kMaxStages = 8;
 
-// Bytes of shared memory that one row (one CTA's slice of it) takes.
-template <typename T, int V>
-__host__ __device__ constexpr unsigned row_bytes(unsigned threads, unsigned e) {
-  return kWide<T, V> ? e * threads * (unsigned)sizeof(T) : (e * threads * (unsigned)sizeof(T) + 48u) & ~15u;
-}
+// A row (one CTA's slice of it) in shared memory: each warp's 32 NV units side
+// by side, and 16 bytes more where a row may begin within a word.
+template <typename T, bool NARROW, int NV>
+constexpr unsigned kWarpBytes = 32 * NV * 16 + (NARROW ? 16 : 0);
+template <typename T, bool NARROW, int NV>
+__host__ __device__ constexpr unsigned row_bytes(unsigned threads) { return (threads >> 5) * kWarpBytes<T, NARROW, NV>; }
 
-// How the threads of a group bring a row of a matrix.  Past its end they read
-// zeros.
+// How a row of a matrix gets there: every warp copies the units it will use
+// itself.  Thread t's unit k is unit first_unit(t) + 32 k of the row, so the
+// distance between a thread's units is the same for every row length.  Past a
+// row's end there are zeros, where no copy ever writes.
 //
-// Thread t's unit k is unit first_unit(t) + 32 k of the row: a warp has 32 NV
-// units side by side, and the distance between a thread's units is the same
-// for every row length.
-//
-// Wide units: a thread copies the units it will use itself, so nothing but its
-// own copies has to have landed; it clears the slots of units that the row
-// does not have once.
-//
-// Pairs: the group copies the 16-byte pieces that cover the row, at the row's
-// own offset within them, and zeros behind them up to what a row at the
-// largest offset would touch; the group meets before it reads.  A first piece
-// that begins before the matrix does is copied element by element.
+// Else (NARROW): the row's words, the first of which begins 2 bytes before it where a
+// row of bf16 lies so; a warp takes one word more than its units have, and
+// words behind the row are cleared up to what the other phase would touch.
 template <int NV>
 __device__ __forceinline__ int first_unit(int tid) {
   return (tid & ~31) * NV + (tid & 31);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void fetch_unit(const T* row, int cols, unsigned smem, int u) {
-  if (u * V < cols) copy_async16(smem + u * 16, row + u * V);
-}
-template <typename T>
-__device__ __forceinline__ void fetch_pieces(const T* row, int cols, const T* matrix, char* smem, int tid, int threads) {
-  const char* a = reinterpret_cast<const char*>(row);
-  const int len = cols * (int)sizeof(T), off = (int)(reinterpret_cast<uintptr_t>(a) & 15u);
-  const char* first = a - off;
-  const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(matrix) & ~(uintptr_t)15);   // of which 0 bytes are read
-  const int pieces = (len + 29) >> 4;
-  const unsigned to = (unsigned)__cvta_generic_to_shared(smem);
-  for (int j = tid; j < pieces; j += threads) {
-    const int here = min(max(off + len - 16 * j, 0), 16);   // bytes of this piece up to the row's end
-    if (j == 0 && first < reinterpret_cast<const char*>(matrix)) {
-      for (int b = 0; b < 16; b += sizeof(T))
-        *reinterpret_cast<T*>(smem + b) = b >= off && b < here ? *reinterpret_cast<const T*>(first + b) : T(0.f);
-    } else {
-      copy_async16(to + 16 * j, here ? first + 16 * j : nothing, here);
+template <typename T, bool NARROW, int NV>
+__device__ __forceinline__ void fetch_row(const T* row, int cols, const T* matrix, unsigned smem, int tid) {
+  const int lane = tid & 31;
+  if constexpr (!NARROW) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (first_unit<NV>(tid) + 32 * k) * kUnit<T>;
+      if (c < cols) copy_async16(smem + (lane + 32 * k) * 16, row + c);
+    }
+  } else {
+    constexpr int kWords = 4 * NV;                       // of a lane
+    const int phase = sizeof(T) == 2 ? (int)(reinterpret_cast<uintptr_t>(row) & 2u) : 0;
+    const int first = (tid >> 5) * 32 * kWords;          // the warp's first word
+    const int bytes = phase + cols * (int)sizeof(T) - 4 * first;   // of the row, from there
+    const char* from = reinterpret_cast<const char*>(row) - phase + 4 * first;
+    const bool before = from < reinterpret_cast<const char*>(matrix);   // the half word before the row is not the matrix's
+    if (bytes >= 128 * kWords + 4 && !before) {          // all its words and one more are the row's
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) copy_async4(smem + 4 * lane + 128 * i, from + 4 * lane + 128 * i);
+      if (sizeof(T) == 2 && lane == 0) copy_async4(smem + 128 * kWords, from + 128 * kWords);
+      return;
+    }
+    const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(matrix) & ~(uintptr_t)3);   // of which 0 bytes are read
+    const int most = min(cols > 0 ? (cols * (int)sizeof(T) + (sizeof(T) == 2 ? 5 : 3)) / 4 - first : 0,   // words, for either phase
+                         32 * kWords + (sizeof(T) == 2 ? 1 : 0));
+#pragma unroll 1
+    for (int j = lane; j < most; j += 32) {
+      if (j == 0 && before)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem), "r"((unsigned)*reinterpret_cast<const unsigned short*>(row) << 16) : "memory");
+      else
+        copy_async4(smem + 4 * j, 4 * j < bytes ? from + 4 * j : nothing, min(max(bytes - 4 * j, 0), 4));
     }
   }
 }
@@ -274,54 +277,79 @@ __device__ __forceinline__ unsigned load_shared4(unsigned a) {
   return w;
 }
 
-// A row in shared memory.
-template <typename T, int V>
+// A row in shared memory, as a warp reads it.
+template <typename T, bool NARROW>
 struct Landed {
-  unsigned at;
-  unsigned select;   // pairs of bf16: which halves of two words are a pair
+  unsigned at;       // the warp's units
+  unsigned select;   // which halves of two words are a pair
 
-  __device__ __forceinline__ Landed(unsigned smem, const T* row) : at(smem), select(0) {
-    if constexpr (!kWide<T, V>) {
-      const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);
-      at = smem + (off & ~3u);
-      select = off & 2 ? 0x5432u : 0x3210u;
+  __device__ __forceinline__ Landed(unsigned smem, const T* row) : at(smem), select(reinterpret_cast<uintptr_t>(row) & 2u ? 0x5432u : 0x3210u) {}
+  // the unit at place u among the warp's
+  __device__ __forceinline__ void read(int u, float2 (&f)[kUnit<T> / 2]) const {
+    uint4 q = load_shared16(at + 16 * u);
+    if constexpr (NARROW && sizeof(T) == 2) {
+      const unsigned more = load_shared4(at + 16 * u + 16);
+      q = make_uint4(__byte_perm(q.x, q.y, select), __byte_perm(q.y, q.z, select), __byte_perm(q.z, q.w, select),
+                     __byte_perm(q.w, more, select));
     }
-  }
-  __device__ __forceinline__ void read(int u, float2 (&f)[V / 2]) const {
-    if constexpr (kWide<T, V>) {
-      unpack16<T, V / 2>(load_shared16(at + 16 * u), f);
-    } else if constexpr (sizeof(T) == 4) {
-      f[0] = make_float2(__uint_as_float(load_shared4(at + 8 * u)), __uint_as_float(load_shared4(at + 8 * u + 4)));
-    } else {
-      const unsigned q = __byte_perm(load_shared4(at + 4 * u), load_shared4(at + 4 * u + 4), select);
-      f[0] = make_float2(lo_of(q), hi_of(q));
-    }
+    unpack16<T, kUnit<T> / 2>(q, f);
   }
 };
 
-// Clears what no copy will ever write: a thread's slots of units its rows do
-// not have, or (pairs) all of the group's rows.
-template <typename T, int V, int NV>
-__device__ __forceinline__ void clear_slots(char* slot, unsigned row_len, int nrows, int cols, int tid, int threads) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if constexpr (kWide<T, V>) {
+// Clears what no copy will ever write.
+template <typename T, bool NARROW, int NV>
+__device__ __forceinline__ void clear_rows(unsigned smem, unsigned row_len, int nrows, int cols, int tid) {
+  const int lane = tid & 31;
+  for (int r = 0; r < nrows; ++r, smem += row_len) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int u = first_unit<NV>(tid) + 32 * k;
-      if (u * V >= cols)
-        for (int r = 0; r < nrows; ++r) *reinterpret_cast<uint4*>(slot + r * row_len + 16 * u) = zero;
+      if (NARROW || (first_unit<NV>(tid) + 32 * k) * kUnit<T> >= cols)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + (lane + 32 * k) * 16), "r"(0) : "memory");
     }
-  } else {
-    for (unsigned b = 16 * tid; b < nrows * row_len; b += 16 * threads) *reinterpret_cast<uint4*>(slot + b) = zero;
+    if (NARROW && lane == 0) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + 32 * NV * 16), "r"(0) : "memory");
   }
+  if (NARROW) __syncwarp();
 }
 
-template <int MODE>
-__device__ __forceinline__ void group_sync(int group, int threads) {
-  if constexpr (MODE == kWarp)
-    __syncwarp();
-  else
-    group_bar(group, threads);
+// A warp's part of an output row (NARROW): its units go to shared memory (the
+// lanes' stores, then __syncwarp), and from there in words to global memory;
+// n elements from `out` on.  Reading the words again needs no unit.
+template <typename T, int NV>
+__device__ __forceinline__ void store_words(T* out, int n, unsigned smem, int lane) {
+  constexpr int kWords = 4 * NV, kAll = 32 * NV * kUnit<T>;
+  if constexpr (sizeof(T) == 4) {
+    if (n >= kAll) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<unsigned*>(out)[lane + 32 * i] = load_shared4(smem + 4 * lane + 128 * i);
+    } else {
+#pragma unroll 1
+      for (int j = lane; j < n; j += 32) reinterpret_cast<unsigned*>(out)[j] = load_shared4(smem + 4 * j);
+    }
+  } else {
+    unsigned short* o = reinterpret_cast<unsigned short*>(out);
+    const int odd = (int)(reinterpret_cast<uintptr_t>(out) >> 1) & 1;   // then words begin at element 1
+    if (odd && lane == 0 && n > 0) o[0] = (unsigned short)load_shared4(smem);
+    const unsigned select = odd ? 0x5432u : 0x3210u;
+    auto word = [&](int j) { return __byte_perm(load_shared4(smem + 4 * j), load_shared4(smem + 4 * j + 4), select); };
+    o += odd;
+    n = min(n, kAll) - odd;
+    int j = lane;
+    if (n >= kAll - 1) {
+#pragma unroll
+      for (int i = 0; i < kWords - 1; ++i) reinterpret_cast<unsigned*>(o)[lane + 32 * i] = word(lane + 32 * i);
+      j += 32 * (kWords - 1);
+    }
+#pragma unroll 1
+    for (; 2 * j < n; j += 32) {
+      if (2 * j + 1 < n)
+        reinterpret_cast<unsigned*>(o)[j] = word(j);
+      else
+        o[2 * j] = (unsigned short)word(j);
+    }
+  }
+}
+__device__ __forceinline__ void store_shared16(unsigned a, uint4 q) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
 }
 
 // ---------------------------------------------------------------- forward
@@ -333,27 +361,27 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 //   Measured at 16384 x 4096 bf16 (268 MB, a plain copy of it takes 42 us):
 //   32 elements per thread 43 us, 16 elements 49, 8 elements 75; one
 //   persistent CTA per SM with a warp per row and rows copied ahead 50.
-template <typename T, int V, int E, int MODE, int MAXT>
+template <typename T, bool NARROW, int E, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
   __shared__ SumWords<1> words;
-  constexpr int NV = E / V, P = V / 2;
-  constexpr bool WIDE = kWide<T, V>;
+  constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
   const int threads = MODE == kWarp ? 32 : blockDim.x;
-  const int group = MODE == kWarp ? threadIdx.x >> 5 : 0;
-  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid);
+  const int tid = MODE == kWarp ? threadIdx.x & 31 : threadIdx.x, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
-  const u64 row = MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + group : blockIdx.x / csize;
+  const u64 row = MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x / csize;
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
   const int cols = c0 < prm.cols ? (int)min((unsigned)E * threads, prm.cols - c0) : 0;   // a cluster's last CTA may have none
   const T* x = static_cast<const T*>(prm.x) + row * prm.x_stride + c0;
+  const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + (threadIdx.x >> 5) * kWarpBytes<T, NARROW, NV>;
   if (MODE == kCluster) cluster_arrive();   // its end: every CTA of the cluster runs
+  if constexpr (NARROW) clear_rows<T, NARROW, NV>(slot, 0, 1, cols, tid);
   wait_for_predecessors();
   let_successor_start();
   if (MODE == kWarp && row >= prm.rows) return;
 
   float2 f[NV][P];
-  if constexpr (WIDE) {
+  if constexpr (!NARROW) {
     const uint4* a = reinterpret_cast<const uint4*>(x);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -361,17 +389,13 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
       unpack16<T, P>(u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0), f[k]);
     }
   } else {
-    const unsigned len = row_bytes<T, V>(threads, E);
-    char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * len;
-    clear_slots<T, V, NV>(slot, len, 1, cols, tid, threads);
-    if constexpr (MODE == kWarp) __syncwarp(); else __syncthreads();
-    fetch_pieces(x, cols, static_cast<const T*>(prm.x), slot, tid, threads);
+    fetch_row<T, NARROW, NV>(x, cols, static_cast<const T*>(prm.x), slot, tid);
     commit();
     wait_groups(0);
-    if constexpr (MODE == kWarp) __syncwarp(); else __syncthreads();
-    const Landed<T, V> here((unsigned)__cvta_generic_to_shared(slot), x);
+    __syncwarp();
+    const Landed<T, NARROW> here(slot, x);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) here.read(u0 + 32 * k, f[k]);
+    for (int k = 0; k < NV; ++k) here.read(lane + 32 * k, f[k]);
   }
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -385,10 +409,10 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
   float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int n = cols - (u0 + 32 * k) * V;   // wide units are whole or absent
-    const float2 m = make_float2(n > 0 ? -mean : 0.f, (WIDE ? n > 0 : n > 1) ? -mean : 0.f);
+    const int n = cols - (u0 + 32 * k) * V;   // whole or absent, unless NARROW
 #pragma unroll
     for (int i = 0; i < P; ++i) {
+      const float2 m = make_float2(n > (NARROW ? 2 * i : 0) ? -mean : 0.f, n > (NARROW ? 2 * i + 1 : 0) ? -mean : 0.f);
       f[k][i] = __fadd2_rn(f[k][i], m);
       sq = __ffma2_rn(f[k][i], f[k][i], sq);
     }
@@ -400,24 +424,33 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
     if (prm.rstd) prm.rstd[row] = rstd;
   }
   T* y = static_cast<T*>(prm.out) + row * prm.out_stride + c0;
-  const bool p4 = (reinterpret_cast<uintptr_t>(y) & 3u) == 0;
+  if constexpr (NARROW) __syncwarp();   // every lane has read the row: its place takes the output
   auto output = [&](auto w) {
     typedef decltype(w) W;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (u0 + 32 * k) * V;
       float2 g[P], b[P];
-      load_w<W, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
-      load_w<W, P>(prm.beta, c0 + c, cols - c, 0.f, b);
+      load_w<W, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
+      load_w<W, !NARROW, P>(prm.beta, c0 + c, cols - c, 0.f, b);
 #pragma unroll
       for (int i = 0; i < P; ++i) f[k][i] = __ffma2_rn(__fmul2_rn(f[k][i], both(rstd)), g[i], b[i]);
-      store_unit<T, P>(y + c, cols - c, p4, f[k]);
+      if constexpr (NARROW) {
+        store_shared16(slot + (lane + 32 * k) * 16, pack16<T, P>(f[k]));
+      } else {
+        if (c < cols) *reinterpret_cast<uint4*>(y + c) = pack16<T, P>(f[k]);
+      }
     }
   };
   if (prm.gamma_bf16)
     output(bf16());
   else
     output(float());
+  if constexpr (NARROW) {
+    __syncwarp();
+    const int c = (tid & ~31) * E;
+    store_words<T, NV>(y + c, cols - c, slot, lane);
+  }
 }
 
 // ---------------------------------------------------------------- backward
@@ -430,16 +463,15 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
 //   dx = rstd a - rstd sum(a) / cols - d rstd^3 sum(a d) / cols,
 // dgamma += (dy rstd) d, dbeta += dy.  R rows share a barrier, and their sums'
 // latencies overlap.
-template <typename T, int V, int E, int R, int MODE, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_constant__ NormRowsParams prm) {
+template <typename T, bool NARROW, int E, int R, int MODE>
+__global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
   __shared__ SumWords<2 * R> words;
-  constexpr int NV = E / V, P = V / 2;
-  constexpr bool WIDE = kWide<T, V>;
+  constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
   constexpr bool kKeepGamma = E <= 16;                   // else in shared memory, a unit per thread as the rows'
   const int threads = MODE == kWarp ? 32 : prm.threads;
   const int group = MODE == kCluster ? 0 : threadIdx.x / threads;
-  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid);
+  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
   const int groups = MODE == kCluster ? 1 : blockDim.x / threads;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
   const unsigned part = blockIdx.x / csize;
@@ -448,37 +480,29 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
   const int cols = c0 < prm.cols ? (int)min(width, prm.cols - c0) : 0;   // a cluster's last CTA may have none
   const float inv = 1.0f / (float)prm.cols;
   const int stages = prm.stages;
-  const unsigned len = row_bytes<T, V>(threads, E);
-  char* slot = reinterpret_cast<char*>(s_dyn) + (size_t)group * stages * R * 2 * len;   // [group][stage][r][x, dy]
-  const unsigned slot_s = (unsigned)__cvta_generic_to_shared(slot);
+  // shared memory: [group][stage][r][x, dy][warp], then (NARROW) a row's part per warp for the output, or gamma
+  const unsigned len = row_bytes<T, NARROW, NV>(threads);
+  const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + group * stages * R * 2 * len + (tid >> 5) * kWarpBytes<T, NARROW, NV>;
+  const unsigned s_out = (unsigned)__cvta_generic_to_shared(s_dyn) + groups * stages * R * 2 * len + (threadIdx.x >> 5) * kWarpBytes<T, NARROW, NV>;
   const int rows = (int)prm.rows, step = (int)prm.nparts * groups * R;
   const int first = ((int)part * groups + group) * R;
-  clear_slots<T, V, NV>(slot, len, stages * R * 2, cols, tid, threads);
-  if constexpr (!WIDE) group_sync<MODE>(group, threads);
+  clear_rows<T, NARROW, NV>(slot, len, stages * R * 2, cols, tid);
   wait_for_predecessors();
   let_successor_start();
 
-  // The row in work; what a turn, and a row, is further in each matrix.
+  // The row in work; what a turn is further in each matrix.
   const T* x = static_cast<const T*>(prm.x) + (u64)first * prm.x_stride + c0;
   const T* dy = static_cast<const T*>(prm.dy) + (u64)first * prm.dy_stride + c0;
   T* dx = static_cast<T*>(prm.out) + (u64)first * prm.out_stride + c0;
   const u64 x_turn = step * prm.x_stride, dy_turn = step * prm.dy_stride;
   // `left` rows from a turn's first one on, to stage `to`
   auto fetch_rows = [&](const T* fx, const T* fd, int left, int to) {
-    unsigned at = to * R * 2 * len;
+    unsigned at = slot + to * R * 2 * len;
 #pragma unroll
     for (int r = 0; r < R; ++r, at += 2 * len, fx += prm.x_stride, fd += prm.dy_stride) {
       if (r < left) {
-        if constexpr (WIDE) {
-#pragma unroll
-          for (int k = 0; k < NV; ++k) {
-            fetch_unit<T, V>(fx, cols, slot_s + at, u0 + 32 * k);
-            fetch_unit<T, V>(fd, cols, slot_s + at + len, u0 + 32 * k);
-          }
-        } else {
-          fetch_pieces(fx, cols, static_cast<const T*>(prm.x), slot + at, tid, threads);
-          fetch_pieces(fd, cols, static_cast<const T*>(prm.dy), slot + at + len, tid, threads);
-        }
+        fetch_row<T, NARROW, NV>(fx, cols, static_cast<const T*>(prm.x), at, tid);
+        fetch_row<T, NARROW, NV>(fd, cols, static_cast<const T*>(prm.dy), at + len, tid);
       }
     }
     commit();
@@ -487,15 +511,16 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
 
   float2 dg[NV][P], db[NV][P];
   float2 gam[kKeepGamma ? NV : 1][P];
-  float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len) + group * width;
+  float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len +
+                                          (NARROW ? (blockDim.x >> 5) * kWarpBytes<T, NARROW, NV> : 0)) + group * width;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (u0 + 32 * k) * V;
     float2 w[P];
     if (prm.gamma_bf16)
-      load_w<bf16, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<bf16, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
     else
-      load_w<float, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<float, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       dg[k][i] = db[k][i] = make_float2(0.f, 0.f);
@@ -511,20 +536,15 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
       for (int i = 0; i < P; ++i) w[i] = gam[k][i];
     } else {
       const float* p = s_gam + (u0 + 32 * k) * V;
-      if constexpr (P >= 2) {
 #pragma unroll
-        for (int i = 0; i < P; i += 2) {
-          const float4 q = reinterpret_cast<const float4*>(p)[i / 2];
-          w[i] = make_float2(q.x, q.y);
-          w[i + 1] = make_float2(q.z, q.w);
-        }
-      } else {
-        w[0] = *reinterpret_cast<const float2*>(p);
+      for (int i = 0; i < P; i += 2) {
+        const float4 q = reinterpret_cast<const float4*>(p)[i / 2];
+        w[i] = make_float2(q.x, q.y);
+        w[i + 1] = make_float2(q.z, q.w);
       }
     }
   };
   // lane r of each warp holds the statistics of the turn's row r
-  const int lane = threadIdx.x & 31;
   float mean_next = 0.f, rstd_next = 0.f;
   auto statistics = [&](int row) {
     if (lane < R && row + lane < rows) {
@@ -537,27 +557,27 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     cluster_arrive();
     cluster_wait();
   }
-  int stage = 0, last = 0, buf = 0;
+  int stage = 0, buf = 0;
   for (int row = first; row < rows; row += step, x += x_turn, dy += dy_turn, dx += step * prm.out_stride) {
     const float means = mean_next, rstds = rstd_next;
     const int left = rows - row;
     statistics(row + step);
-    // the copies of these rows: the newest but stages - 1, and one newer where they were asked for a turn later
-    wait_groups(WIDE ? stages - 1 : stages > 2 ? stages - 2 : 0);
-    if constexpr (!WIDE) group_sync<MODE>(group, threads);   // the others' copies have landed too
-    const unsigned here = slot_s + stage * R * 2 * len;
+    wait_groups(stages - 1);
+    if constexpr (NARROW) __syncwarp();   // the other lanes' copies have landed too
+    const unsigned here = slot + stage * R * 2 * len;
     float v[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 sa = make_float2(0.f, 0.f), sd = sa;
       if (r < left) {
         const float2 mean = both(-__shfl_sync(0xffffffffu, means, r)), rstd = both(__shfl_sync(0xffffffffu, rstds, r));
-        const Landed<T, V> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
+        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+          if (NARROW && (u0 - lane + 32 * k) * V >= cols) continue;   // nothing there for this warp
           float2 fx[P], fd[P], w[P];
-          hx.read(u0 + 32 * k, fx);
-          hd.read(u0 + 32 * k, fd);
+          hx.read(lane + 32 * k, fx);
+          hd.read(lane + 32 * k, fd);
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i) {   // dy is 0 past the row's end
@@ -574,45 +594,41 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_backward_kernel(const __grid_co
     }
     const float sums = row_sums<MODE, 2 * R>(v, words, buf, group, threads) * inv;
     buf ^= 1;
-    // pairs: the group has met since it read the previous rows for dx, so their slots are free
-    if constexpr (!WIDE) {
-      if (stages > 1 && row != first)
-        fetch_rows(x + (stages - 1) * x_turn, dy + (stages - 1) * dy_turn, left - (stages - 1) * step, last);
-      else
-        commit();
-    }
     T* out = dx;
 #pragma unroll
     for (int r = 0; r < R; ++r, out += prm.out_stride) {
       if (r < left) {
         const float mean = __shfl_sync(0xffffffffu, means, r), rstd = __shfl_sync(0xffffffffu, rstds, r);
         const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1);
-        const Landed<T, V> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
-        const bool p4 = (reinterpret_cast<uintptr_t>(out) & 3u) == 0;
+        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
         const float2 k1 = both(-rstd * sum_a), k2 = both(-rstd * rstd * rstd * sum_ad);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int u = u0 + 32 * k;
+          if (NARROW && (u0 - lane + 32 * k) * V >= cols) continue;
           float2 fx[P], fd[P], w[P];
-          hx.read(u, fx);
-          hd.read(u, fd);
+          hx.read(lane + 32 * k, fx);
+          hd.read(lane + 32 * k, fd);
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i)
             fd[i] = __ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(__fmul2_rn(fd[i], w[i]), both(rstd), k1));
-          store_unit<T, P>(out + u * V, cols - u * V, p4, fd);
+          const int c = (u0 + 32 * k) * V;
+          if constexpr (NARROW) {
+            store_shared16(s_out + (lane + 32 * k) * 16, pack16<T, P>(fd));
+          } else {
+            if (c < cols) *reinterpret_cast<uint4*>(out + c) = pack16<T, P>(fd);
+          }
+        }
+        if constexpr (NARROW) {
+          __syncwarp();
+          const int c = (tid & ~31) * E;
+          store_words<T, NV>(out + c, cols - c, s_out, lane);
+          __syncwarp();   // before the next row's units
         }
       }
     }
-    if constexpr (WIDE) {   // a thread's slots are its own: free
-      fetch_rows(x + stages * x_turn, dy + stages * dy_turn, left - stages * step, stage);
-    } else if (stages == 1) {
-      group_sync<MODE>(group, threads);
-      fetch_rows(x + x_turn, dy + dy_turn, left - step, 0);
-    } else if (MODE == kWarp) {
-      __syncwarp();   // the next turn refills these rows' slots with no barrier in between
-    }
-    last = stage;
+    if constexpr (NARROW) __syncwarp();   // every lane has read these rows
+    fetch_rows(x + stages * x_turn, dy + stages * dy_turn, left - stages * step, stage);
     if (++stage == stages) stage = 0;
   }
   wait_groups(0);
@@ -730,30 +746,30 @@ int stages_for(size_t budget, size_t per_stage, u64 turns) {
 
 constexpr size_t kSmemSm = 224 * 1024;   // of an SM, less what CTAs take statically
 
-template <typename T, int V, int E, int MODE, int MAXT>
+template <typename T, bool NARROW, int E, int MODE, int MAXT>
 cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st) {
   const int groups = MODE == kWarp ? MAXT / 32 : 1;
-  const size_t smem = kWide<T, V> ? 0 : (size_t)groups * row_bytes<T, V>(threads, E);
-  return launch_dependent(ln_forward_kernel<T, V, E, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, groups) * csize)), groups * threads, smem,
+  const size_t smem = NARROW ? (size_t)row_bytes<T, NARROW, E / kUnit<T>>(groups * threads) : 0;
+  return launch_dependent(ln_forward_kernel<T, NARROW, E, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, groups) * csize)), groups * threads, smem,
                           csize, st, p);
 }
 
 // A thread takes 32 elements (8 in rows of 256 and fewer), which keeps a CTA
 // small; with rows too few to fill the GPU it takes 8, and more threads share
 // a row.
-template <typename T, int V>
+template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
-  if (p.cols <= 256) return forward_e<T, V, 8, kWarp, 128>(p, 32, 1, st);
+  if (p.cols <= 256) return forward_e<T, NARROW, 8, kWarp, 128>(p, 32, 1, st);
   const int c = cluster_for(p.rows, p.cols, 1024 * 32);
   const size_t slice = div_up(p.cols, c);
   const bool few = p.rows * c <= 2 * (size_t)sm_count() && slice <= 4096;
   if (c > 1) {
-    if (few) return forward_e<T, V, 8, kCluster, 512>(p, threads_for(slice, 8), c, st);
-    return forward_e<T, V, 32, kCluster, 1024>(p, threads_for(slice, 32), c, st);
+    if (few) return forward_e<T, NARROW, 8, kCluster, 512>(p, threads_for(slice, 8), c, st);
+    return forward_e<T, NARROW, 32, kCluster, 1024>(p, threads_for(slice, 32), c, st);
   }
-  if (few) return forward_e<T, V, 8, kCta, 512>(p, threads_for(slice, 8), 1, st);
-  if (p.cols <= 1024) return forward_e<T, V, 32, kWarp, 128>(p, 32, 1, st);
-  return forward_e<T, V, 32, kCta, 1024>(p, threads_for(slice, 32), 1, st);
+  if (few) return forward_e<T, NARROW, 8, kCta, 512>(p, threads_for(slice, 8), 1, st);
+  if (p.cols <= 1024) return forward_e<T, NARROW, 32, kWarp, 128>(p, 32, 1, st);
+  return forward_e<T, NARROW, 32, kCta, 1024>(p, threads_for(slice, 32), 1, st);
 }
 
 // The shape of a backward launch, from the sizes alone (the workspace depends
@@ -766,7 +782,7 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 //   1 row 136; 8 columns per thread and 640 threads, 4 rows 133; 24 columns
 //   and 224 threads, 1 row 181.
 struct BackwardShape {
-  int e, r4, threads, groups, csize, ctas;   // r4: 4 rows a turn (fp32: 2), else 1; ctas: per SM
+  int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, NARROW: 2), else 1
   unsigned nparts;
 };
 BackwardShape backward_shape(size_t rows, size_t cols) {
@@ -775,41 +791,41 @@ BackwardShape backward_shape(size_t rows, size_t cols) {
   const size_t slice = div_up(cols, s.csize);
   s.e = slice <= 256 ? 8 : slice <= 8192 ? 16 : 32;
   s.threads = threads_for(slice, s.e);
-  s.ctas = s.threads > 256 ? 1 : 2;
-  s.groups = s.csize > 1 || s.threads > 256 ? 1 : 256 / s.threads;
+  s.groups = s.csize > 1 ? 1 : 512 / s.threads;
+  if (s.threads > 32 && s.groups > 15) s.groups = 15;   // named barriers
   while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
-  const size_t most = (size_t)s.ctas * sm_count() / s.csize;
-  s.r4 = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
+  const size_t most = (size_t)sm_count() / s.csize;
+  s.many = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
   const size_t want = div_up(rows, (size_t)s.groups);
   s.nparts = (unsigned)(want < most ? want : most);
   if (s.nparts < 1) s.nparts = 1;
   return s;
 }
 
-template <typename T, int V, int E, int R, int MODE, int MAXT, int MINB>
+template <typename T, bool NARROW, int E, int R, int MODE>
 cudaError_t backward_e(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
   p.threads = s.threads;
   p.nparts = s.nparts;
-  const size_t stage = (size_t)s.groups * R * 2 * row_bytes<T, V>(s.threads, E);
-  const size_t gam = E > 16 ? (size_t)s.groups * E * s.threads * 4 : 0;
+  constexpr int NV = E / kUnit<T>;
+  const size_t stage = (size_t)s.groups * R * 2 * row_bytes<T, NARROW, NV>(s.threads);
+  const size_t rest = (NARROW ? (size_t)row_bytes<T, NARROW, NV>(s.groups * s.threads) : 0) + (E > 16 ? (size_t)s.groups * E * s.threads * 4 : 0);
   const size_t acc = s.groups > 1 ? (size_t)2 * E * s.threads * 4 : 0;
-  p.stages = stages_for(kSmemSm / s.ctas - 4096 - gam, stage, div_up(p.rows, (u64)s.nparts * s.groups * R));
-  size_t smem = stage * p.stages + gam;
+  p.stages = stages_for(kSmemSm - 4096 - rest, stage, div_up(p.rows, (u64)s.nparts * s.groups * R));
+  size_t smem = stage * p.stages + rest;
   if (smem < acc) smem = acc;
-  return launch_dependent(ln_backward_kernel<T, V, E, R, MODE, MAXT, MINB>, dim3(s.nparts * s.csize), s.groups * s.threads, smem, s.csize, st, p);
+  return launch_dependent(ln_backward_kernel<T, NARROW, E, R, MODE>, dim3(s.nparts * s.csize), s.groups * s.threads, smem, s.csize, st, p);
 }
 
-template <typename T, int V>
+template <typename T, bool NARROW>
 cudaError_t backward(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
-  constexpr int R = sizeof(T) == 2 ? 4 : 2;
+  constexpr int R = sizeof(T) == 2 && !NARROW ? 4 : 2;
   if (s.csize > 1) {
-    if (s.e == 32) return backward_e<T, V, 32, 1, kCluster, 512, 1>(p, s, st);
-    return s.r4 ? backward_e<T, V, 16, R, kCluster, 512, 1>(p, s, st) : backward_e<T, V, 16, 1, kCluster, 512, 1>(p, s, st);
+    if (s.e == 32) return backward_e<T, NARROW, 32, 1, kCluster>(p, s, st);
+    return s.many ? backward_e<T, NARROW, 16, R, kCluster>(p, s, st) : backward_e<T, NARROW, 16, 1, kCluster>(p, s, st);
   }
-  if (s.threads == 32 && s.e == 8) return s.r4 ? backward_e<T, V, 8, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 8, 1, kWarp, 256, 2>(p, s, st);
-  if (s.threads == 32) return s.r4 ? backward_e<T, V, 16, R, kWarp, 256, 2>(p, s, st) : backward_e<T, V, 16, 1, kWarp, 256, 2>(p, s, st);
-  if (s.threads <= 256) return s.r4 ? backward_e<T, V, 16, R, kCta, 256, 2>(p, s, st) : backward_e<T, V, 16, 1, kCta, 256, 2>(p, s, st);
-  return s.r4 ? backward_e<T, V, 16, R, kCta, 512, 1>(p, s, st) : backward_e<T, V, 16, 1, kCta, 512, 1>(p, s, st);
+  if (s.threads == 32 && s.e == 8) return s.many ? backward_e<T, NARROW, 8, R, kWarp>(p, s, st) : backward_e<T, NARROW, 8, 1, kWarp>(p, s, st);
+  if (s.threads == 32) return s.many ? backward_e<T, NARROW, 16, R, kWarp>(p, s, st) : backward_e<T, NARROW, 16, 1, kWarp>(p, s, st);
+  return s.many ? backward_e<T, NARROW, 16, R, kCta>(p, s, st) : backward_e<T, NARROW, 16, 1, kCta>(p, s, st);
 }
 
 bool wide_rows(const void* base, u64 stride, size_t cols, size_t esize) {
@@ -822,8 +838,8 @@ bool wide_w(const void* w) { return (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
 cudaError_t launch_ln_forward(NormRowsParams& p, int dtype, cudaStream_t st) {
   const size_t es = dtype == XP_F32 ? 4 : 2;
   const bool wide = wide_rows(p.x, p.x_stride, p.cols, es) && wide_rows(p.out, p.out_stride, p.cols, es) && wide_w(p.gamma) && wide_w(p.beta);
-  if (dtype == XP_F32) return wide ? forward<float, 4>(p, st) : forward<float, 2>(p, st);
-  return wide ? forward<bf16, 8>(p, st) : forward<bf16, 2>(p, st);
+  if (dtype == XP_F32) return wide ? forward<float, false>(p, st) : forward<float, true>(p, st);
+  return wide ? forward<bf16, false>(p, st) : forward<bf16, true>(p, st);
 }
 
 cudaError_t ln_backward_parts(size_t rows, size_t cols, unsigned* nparts) {
@@ -837,9 +853,9 @@ cudaError_t launch_ln_backward(NormRowsParams& p, int dtype, cudaStream_t st) {
   const bool wide = wide_rows(p.x, p.x_stride, p.cols, es) && wide_rows(p.dy, p.dy_stride, p.cols, es) && wide_rows(p.out, p.out_stride, p.cols, es) && wide_w(p.gamma);
   cudaError_t e;
   if (dtype == XP_F32)
-    e = wide ? backward<float, 4>(p, s, st) : backward<float, 2>(p, s, st);
+    e = wide ? backward<float, false>(p, s, st) : backward<float, true>(p, s, st);
   else
-    e = wide ? backward<bf16, 8>(p, s, st) : backward<bf16, 2>(p, s, st);
+    e = wide ? backward<bf16, false>(p, s, st) : backward<bf16, true>(p, s, st);
   if (e != cudaSuccess || !p.dgamma || s.nparts == 1) return e;
   return launch_dependent(ln_parts_kernel, dim3((unsigned)div_up(p.cols, 32), 2), 32 * kPartWarps, 0, 1, st, (const float*)p.partial, s.nparts,
                           p.cols, p.dgamma, p.dbeta, p.accumulate);
