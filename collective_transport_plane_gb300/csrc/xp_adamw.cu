@@ -216,6 +216,14 @@ __device__ __forceinline__ unsigned mix(unsigned x) {
 constexpr unsigned kPosLo = 0x8ED88009u, kPosHi = 0xB86D3E2Fu;
 __device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { return mix(seed * kPosLo + mix(step)); }
 
+// a / d.  The division's fast path does not take a numerator of 0, which
+// weights without gradients have; one in a warp would send it the slow way.
+__device__ __forceinline__ float quotient(float a, float d) {
+  const bool zero = a == 0.f;
+  const float q = __fdiv_rn(zero ? 1.f : a, d);
+  return zero ? 0.f : q;
+}
+
 // ---------------------------------------------------------------- the step
 
 // What a thread's eight elements with 8-bit states take from memory.
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
         const float2 d = add2(mul2(make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y)), rs), make_float2(prm.eps, prm.eps));
         const float2 a = mul2(m[k], alpha);
         const float2 q = add2(mul2(make_float2(p[2 * k], p[2 * k + 1]), keep),
-                                    make_float2(-__fdiv_rn(a.x, d.x), -__fdiv_rn(a.y, d.y)));
+                                    make_float2(-quotient(a.x, d.x), -quotient(a.y, d.y)));
         p[2 * k] = q.x;
         p[2 * k + 1] = q.y;
       }

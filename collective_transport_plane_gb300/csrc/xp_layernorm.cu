@@ -56,20 +56,11 @@ __device__ __forceinline__ uint4 pack16(const float2 (&f)[P]) {
   else
     return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
-// A unit of gamma or beta; `none` where there is none, and past the row's end.
-// WHOLE: units are whole or absent, and their loads branch nowhere, so that
-// those of several units are in flight together.
-template <typename W, bool WHOLE, int P>
-__device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float none, float2 (&f)[P]) {
-  const W* p = static_cast<const W*>(w) + c;
-  const bool has = w && n > 0;
-  if constexpr (!WHOLE) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      f[i].x = w && 2 * i < n ? to_f(__ldg(p + 2 * i)) : none;
-      f[i].y = w && 2 * i + 1 < n ? to_f(__ldg(p + 2 * i + 1)) : none;
-    }
-  } else if constexpr (sizeof(W) == 4) {
+// A unit of gamma or beta (w is aligned to 16 bytes); `none` where there is
+// none.  No branches: the loads of several units are in flight together.
+template <typename W, int P>
+__device__ __forceinline__ void load_whole_w(const W* p, bool has, float none, float2 (&f)[P]) {
+  if constexpr (sizeof(W) == 4) {
     const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
@@ -89,6 +80,20 @@ __device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float n
     const unsigned words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < P; ++i) f[i] = make_float2(lo_of(words[i]), hi_of(words[i]));
+  }
+}
+// n elements of the row are left from column c on.
+template <typename W, bool NARROW, int P>
+__device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float none, float2 (&f)[P]) {
+  const W* p = static_cast<const W*>(w) + c;
+  if (!NARROW || !w || n <= 0 || (n >= 2 * P && (reinterpret_cast<uintptr_t>(w) & 15u) == 0)) {
+    load_whole_w<W, P>(p, w && n > 0, none, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f[i].x = 2 * i < n ? to_f(__ldg(p + 2 * i)) : none;
+      f[i].y = 2 * i + 1 < n ? to_f(__ldg(p + 2 * i + 1)) : none;
+    }
   }
 }
 
@@ -431,8 +436,8 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
     for (int k = 0; k < NV; ++k) {
       const int c = (u0 + 32 * k) * V;
       float2 g[P], b[P];
-      load_w<W, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
-      load_w<W, !NARROW, P>(prm.beta, c0 + c, cols - c, 0.f, b);
+      load_w<W, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
+      load_w<W, NARROW, P>(prm.beta, c0 + c, cols - c, 0.f, b);
 #pragma unroll
       for (int i = 0; i < P; ++i) f[k][i] = __ffma2_rn(__fmul2_rn(f[k][i], both(rstd)), g[i], b[i]);
       if constexpr (NARROW) {
@@ -518,9 +523,9 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
     const int c = (u0 + 32 * k) * V;
     float2 w[P];
     if (prm.gamma_bf16)
-      load_w<bf16, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<bf16, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
     else
-      load_w<float, !NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<float, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       dg[k][i] = db[k][i] = make_float2(0.f, 0.f);
