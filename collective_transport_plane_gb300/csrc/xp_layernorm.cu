@@ -181,11 +181,6 @@ __device__ __forceinline__ float row_sums(float (&v)[N], SumWords<N>& w, int buf
   }
   return t;
 }
-template <int MODE>
-__device__ __forceinline__ float row_sum(float x, SumWords<1>& w, int buf, int threads) {
-  float v[1] = {x};
-  return row_sums<MODE, 1>(v, w, buf, 0, threads);
-}
 
 // ---- rows on their way from global to shared memory
 __device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem) {
@@ -289,16 +284,18 @@ struct Landed {
   unsigned select;   // which halves of two words are a pair
 
   __device__ __forceinline__ Landed(unsigned smem, const T* row) : at(smem), select(reinterpret_cast<uintptr_t>(row) & 2u ? 0x5432u : 0x3210u) {}
+  __device__ __forceinline__ bool even() const { return !NARROW || sizeof(T) == 4 || select == 0x3210u; }
   // the unit at place u among the warp's
-  __device__ __forceinline__ void read(int u, float2 (&f)[kUnit<T> / 2]) const {
+  __device__ __forceinline__ uint4 raw(int u) const {
     uint4 q = load_shared16(at + 16 * u);
     if constexpr (NARROW && sizeof(T) == 2) {
       const unsigned more = load_shared4(at + 16 * u + 16);
       q = make_uint4(__byte_perm(q.x, q.y, select), __byte_perm(q.y, q.z, select), __byte_perm(q.z, q.w, select),
                      __byte_perm(q.w, more, select));
     }
-    unpack16<T, kUnit<T> / 2>(q, f);
+    return q;
   }
+  __device__ __forceinline__ void read(int u, float2 (&f)[kUnit<T> / 2]) const { unpack16<T, kUnit<T> / 2>(raw(u), f); }
 };
 
 // Clears what no copy will ever write.
@@ -339,6 +336,11 @@ __device__ __forceinline__ void store_words(T* out, int n, unsigned smem, int la
     o += odd;
     n = min(n, kAll) - odd;
     int j = lane;
+    if (n >= kAll && !odd) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<unsigned*>(o)[lane + 32 * i] = load_shared4(smem + 4 * lane + 128 * i);
+      return;
+    }
     if (n >= kAll - 1) {
 #pragma unroll
       for (int i = 0; i < kWords - 1; ++i) reinterpret_cast<unsigned*>(o)[lane + 32 * i] = word(lane + 32 * i);
@@ -366,70 +368,101 @@ __device__ __forceinline__ void store_shared16(unsigned a, uint4 q) {
 //   Measured at 16384 x 4096 bf16 (268 MB, a plain copy of it takes 42 us):
 //   32 elements per thread 43 us, 16 elements 49, 8 elements 75; one
 //   persistent CTA per SM with a warp per row and rows copied ahead 50.
-template <typename T, bool NARROW, int E, int MODE, int MAXT>
-__global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
+constexpr int kForwardThreads = 1024;
+// R > 1: rows side by side, in rows of 256 columns and fewer, so that a warp has
+// more in flight (60000 x 96 bf16: FIGURE).
+template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
-  __shared__ SumWords<1> words;
+  __shared__ SumWords<R> words;
   constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
   const int threads = MODE == kWarp ? 32 : blockDim.x;
   const int tid = MODE == kWarp ? threadIdx.x & 31 : threadIdx.x, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
-  const u64 row = MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x / csize;
+  const u64 row = R * (MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x / csize);
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
   const int cols = c0 < prm.cols ? (int)min((unsigned)E * threads, prm.cols - c0) : 0;   // a cluster's last CTA may have none
+  const int left = (int)min(prm.rows - min(row, prm.rows), (u64)R);
   const T* x = static_cast<const T*>(prm.x) + row * prm.x_stride + c0;
-  const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + (threadIdx.x >> 5) * kWarpBytes<T, NARROW, NV>;
+  constexpr unsigned kRow = kWarpBytes<T, NARROW, NV>;
+  const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + (threadIdx.x >> 5) * R * kRow;   // [warp][r]
   if (MODE == kCluster) cluster_arrive();   // its end: every CTA of the cluster runs
-  if constexpr (NARROW) clear_rows<T, NARROW, NV>(slot, 0, 1, cols, tid);
+  if constexpr (NARROW) clear_rows<T, NARROW, NV>(slot, kRow, R, cols, tid);
   wait_for_predecessors();
   let_successor_start();
-  if (MODE == kWarp && row >= prm.rows) return;
+  if (MODE == kWarp && left == 0) return;
 
-  float2 f[NV][P];
+  uint4 q[R][NV];   // as they came: bf16 take half the registers their values would
   if constexpr (!NARROW) {
-    const uint4* a = reinterpret_cast<const uint4*>(x);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int u = u0 + 32 * k;
-      unpack16<T, P>(u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0), f[k]);
+    for (int r = 0; r < R; ++r) {
+      const uint4* a = reinterpret_cast<const uint4*>(x + r * prm.x_stride);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int u = u0 + 32 * k;
+        q[r][k] = r < left && u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0);
+      }
     }
   } else {
-    fetch_row<T, NARROW, NV>(x, cols, static_cast<const T*>(prm.x), slot, tid);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < left) fetch_row<T, NARROW, NV>(x + r * prm.x_stride, cols, static_cast<const T*>(prm.x), slot + r * kRow, tid);
     commit();
     wait_groups(0);
     __syncwarp();
-    const Landed<T, NARROW> here(slot, x);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) here.read(lane + 32 * k, f[k]);
+    for (int r = 0; r < R; ++r) {
+      const Landed<T, NARROW> here(slot + r * kRow, x + r * prm.x_stride);
+      if (here.even()) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) q[r][k] = load_shared16(here.at + (lane + 32 * k) * 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) q[r][k] = here.raw(lane + 32 * k);
+      }
+    }
   }
-  float2 sum = make_float2(0.f, 0.f);
+  float v[R];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
+  for (int r = 0; r < R; ++r) {
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum = __fadd2_rn(sum, f[k][i]);
+    for (int k = 0; k < NV; ++k) {
+      float2 f[P];
+      unpack16<T, P>(q[r][k], f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) sum = __fadd2_rn(sum, f[i]);
+    }
+    v[r] = sum.x + sum.y;
   }
   if (MODE == kCluster) cluster_wait();
   const float inv = 1.0f / (float)prm.cols;
-  const float mean = row_sum<MODE>(sum.x + sum.y, words, 0, threads) * inv;
-  float2 sq = make_float2(0.f, 0.f);
+  const float means = row_sums<MODE, R>(v, words, 0, 0, threads) * inv;   // row r's in lane r
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int n = cols - (u0 + 32 * k) * V;   // whole or absent, unless NARROW
+  for (int r = 0; r < R; ++r) {
+    const float mean = R > 1 ? __shfl_sync(0xffffffffu, means, r) : means;
+    float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 m = make_float2(n > (NARROW ? 2 * i : 0) ? -mean : 0.f, n > (NARROW ? 2 * i + 1 : 0) ? -mean : 0.f);
-      f[k][i] = __fadd2_rn(f[k][i], m);
-      sq = __ffma2_rn(f[k][i], f[k][i], sq);
+    for (int k = 0; k < NV; ++k) {
+      const int n = cols - (u0 + 32 * k) * V;   // whole or absent, unless NARROW
+      float2 f[P];
+      unpack16<T, P>(q[r][k], f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 m = make_float2(n > (NARROW ? 2 * i : 0) ? -mean : 0.f, n > (NARROW ? 2 * i + 1 : 0) ? -mean : 0.f);
+        const float2 d = __fadd2_rn(f[i], m);
+        sq = __ffma2_rn(d, d, sq);
+      }
     }
+    v[r] = sq.x + sq.y;
   }
-  const float var = row_sum<MODE>(sq.x + sq.y, words, 1, threads) * inv;
-  const float rstd = 1.0f / sqrtf(var + prm.eps);
-  if (tid == 0 && c0 == 0) {
-    if (prm.mean) prm.mean[row] = mean;
-    if (prm.rstd) prm.rstd[row] = rstd;
+  const float rstds = 1.0f / sqrtf(row_sums<MODE, R>(v, words, 1, 0, threads) * inv + prm.eps);
+  if (tid < left && c0 == 0) {
+    if (prm.mean) prm.mean[row + tid] = means;
+    if (prm.rstd) prm.rstd[row + tid] = rstds;
   }
   T* y = static_cast<T*>(prm.out) + row * prm.out_stride + c0;
-  if constexpr (NARROW) __syncwarp();   // every lane has read the row: its place takes the output
+  if constexpr (NARROW) __syncwarp();   // every lane has read the rows: their places take the output
   auto output = [&](auto w) {
     typedef decltype(w) W;
 #pragma unroll
@@ -439,11 +472,17 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
       load_w<W, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
       load_w<W, NARROW, P>(prm.beta, c0 + c, cols - c, 0.f, b);
 #pragma unroll
-      for (int i = 0; i < P; ++i) f[k][i] = __ffma2_rn(__fmul2_rn(f[k][i], both(rstd)), g[i], b[i]);
-      if constexpr (NARROW) {
-        store_shared16(slot + (lane + 32 * k) * 16, pack16<T, P>(f[k]));
-      } else {
-        if (c < cols) *reinterpret_cast<uint4*>(y + c) = pack16<T, P>(f[k]);
+      for (int r = 0; r < R; ++r) {
+        const float2 mean = both(-(R > 1 ? __shfl_sync(0xffffffffu, means, r) : means)), rstd = both(R > 1 ? __shfl_sync(0xffffffffu, rstds, r) : rstds);
+        float2 o[P];
+        unpack16<T, P>(q[r][k], o);
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(o[i], mean), rstd), g[i], b[i]);
+        if constexpr (NARROW) {
+          store_shared16(slot + r * kRow + (lane + 32 * k) * 16, pack16<T, P>(o));
+        } else {
+          if (r < left && c < cols) *reinterpret_cast<uint4*>(y + r * prm.out_stride + c) = pack16<T, P>(o);
+        }
       }
     }
   };
@@ -454,7 +493,9 @@ __global__ void __launch_bounds__(MAXT) ln_forward_kernel(const __grid_constant_
   if constexpr (NARROW) {
     __syncwarp();
     const int c = (tid & ~31) * E;
-    store_words<T, NV>(y + c, cols - c, slot, lane);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < left) store_words<T, NV>(y + r * prm.out_stride + c, cols - c, slot + r * kRow, lane);
   }
 }
 
@@ -493,7 +534,6 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   const int first = ((int)part * groups + group) * R;
   clear_rows<T, NARROW, NV>(slot, len, stages * R * 2, cols, tid);
   wait_for_predecessors();
-  let_successor_start();
 
   // The row in work; what a turn is further in each matrix.
   const T* x = static_cast<const T*>(prm.x) + (u64)first * prm.x_stride + c0;
@@ -637,6 +677,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
     if (++stage == stages) stage = 0;
   }
   wait_groups(0);
+  let_successor_start();
   if (!prm.dgamma) return;
 
   // the groups' sums, added in their order, then one part of the CTA or cluster
@@ -667,51 +708,81 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = (u0 + 32 * k) * V + i;
+      const int c = (u0 + 32 * k) * V;
+      if (!NARROW && !add && prm.nparts > 1) {   // the parts' rows are aligned as the units are
         if (c < cols) {
-          const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
-          out_g[c] = add ? out_g[c] + vg : vg;
-          out_b[c] = add ? out_b[c] + vb : vb;
+#pragma unroll
+          for (int i = 0; i < P; i += 2) {
+            reinterpret_cast<float4*>(out_g + c)[i / 2] = make_float4(dg[k][i].x, dg[k][i].y, dg[k][i + 1].x, dg[k][i + 1].y);
+            reinterpret_cast<float4*>(out_b + c)[i / 2] = make_float4(db[k][i].x, db[k][i].y, db[k][i + 1].x, db[k][i + 1].y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (c + i < cols) {
+            const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
+            out_g[c + i] = add ? out_g[c + i] + vg : vg;
+            out_b[c + i] = add ? out_b[c + i] + vb : vb;
+          }
         }
       }
     }
   }
 }
 
-// The parts' sums, column by column: 32 columns per CTA, 16 warps that each
-// add every 16th part in four chains, then the warps' sums in order.  fp32:
-// the depth is 304 / 64 + 2 + 16 additions, and fp64 runs at 2 additions per
-// clock and SM here (22 us instead of 6 for 304 parts of 5120 columns).
+// The parts' sums, column by column: a lane has C columns (4 where the rows are
+// aligned for it), the warps of a CTA every kPartWarps-th part each in two
+// chains, then the warps' sums in order.  fp32: the depth is 152 / 32 + 2 + 16
+// additions, and fp64 runs at 2 additions per clock and SM here (304 parts of
+// 5120 columns took 22 us by it).
 constexpr int kPartWarps = 16;
+template <int C>
 __global__ void __launch_bounds__(32 * kPartWarps) ln_parts_kernel(const float* partial, unsigned nparts, unsigned cols,
                                                                   float* dgamma, float* dbeta, int accumulate) {
-  __shared__ float s[kPartWarps][32];
+  __shared__ float s[kPartWarps][32][C];
   wait_for_predecessors();
   let_successor_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned c = blockIdx.x * 32 + lane;
+  const unsigned c = (blockIdx.x * 32 + lane) * C;
   const float* p = partial + (size_t)blockIdx.y * cols + c;
   const size_t stride = (size_t)2 * cols;
-  float sum[4] = {};
+  float sum[2][C] = {};
   if (c < cols) {
-    for (unsigned k = warp; k < nparts; k += 4 * kPartWarps) {
-      float a[4];
+    for (unsigned k = warp; k < nparts; k += 2 * kPartWarps) {
+      float a[2][C] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = k + i * kPartWarps < nparts ? p[(k + i * kPartWarps) * stride] : 0.f;
+      for (int i = 0; i < 2; ++i) {
+        if (k + i * kPartWarps < nparts) {
+          const float* q = p + (k + i * kPartWarps) * stride;
+          if constexpr (C == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(q);
+            a[i][0] = f.x, a[i][1] = f.y, a[i][2] = f.z, a[i][3] = f.w;
+          } else {
+            a[i][0] = *q;
+          }
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] += a[i];
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) sum[i][j] += a[i][j];
+      }
     }
   }
-  s[warp][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    float total = s[0][lane];
 #pragma unroll
-    for (int w = 1; w < kPartWarps; ++w) total += s[w][lane];
-    float* out = (blockIdx.y ? dbeta : dgamma) + c;
-    *out = accumulate ? *out + total : total;
+  for (int j = 0; j < C; ++j) s[warp][lane][j] = sum[0][j] + sum[1][j];
+  __syncthreads();
+  if (threadIdx.x < 32 * C) {
+    const int l = threadIdx.x / C, j = threadIdx.x % C;
+    const unsigned at = (blockIdx.x * 32 + l) * C + j;
+    if (at < cols) {
+      float total = s[0][l][j];
+#pragma unroll
+      for (int w = 1; w < kPartWarps; ++w) total += s[w][l][j];
+      float* out = (blockIdx.y ? dbeta : dgamma) + at;
+      *out = accumulate ? *out + total : total;
+    }
   }
 }
 
@@ -732,11 +803,12 @@ int sm_count() {
 size_t div_up(size_t a, size_t b) { return (a + b - 1) / b; }
 int threads_for(size_t elems, int e) { return elems ? 32 * (int)div_up(elems, (size_t)32 * e) : 32; }
 
-// A row's CTAs: enough that a slice fits, and more where the rows are too few
-// for the GPU's SMs, as long as a slice keeps 2048 columns.
+// A row's CTAs: enough that a slice has `most` columns at most, and more where
+// the rows are too few for the GPU's SMs, as long as a slice keeps 2048.
 int cluster_for(size_t rows, size_t cols, size_t most) {
-  int c = 1;
-  while (c < kMaxCluster8 && (div_up(cols, c) > most || (rows * c < (size_t)sm_count() && cols / (2 * c) >= 2048))) c *= 2;
+  int c = (int)div_up(cols, most);
+  if (c > kMaxCluster8) c = kMaxCluster8;
+  while (2 * c <= kMaxCluster8 && rows * c < (size_t)sm_count() && cols / (2 * c) >= 2048) c *= 2;
   return c;
 }
 
@@ -751,30 +823,42 @@ int stages_for(size_t budget, size_t per_stage, u64 turns) {
 
 constexpr size_t kSmemSm = 224 * 1024;   // of an SM, less what CTAs take statically
 
-template <typename T, bool NARROW, int E, int MODE, int MAXT>
+template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
 cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st) {
   const int groups = MODE == kWarp ? MAXT / 32 : 1;
-  const size_t smem = NARROW ? (size_t)row_bytes<T, NARROW, E / kUnit<T>>(groups * threads) : 0;
-  return launch_dependent(ln_forward_kernel<T, NARROW, E, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, groups) * csize)), groups * threads, smem,
-                          csize, st, p);
+  const size_t smem = NARROW ? (size_t)R * row_bytes<T, NARROW, E / kUnit<T>>(groups * threads) : 0;
+  return launch_dependent(ln_forward_kernel<T, NARROW, E, R, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, (size_t)groups * R) * csize)),
+                          groups * threads, smem, csize, st, p);
 }
 
-// A thread takes 32 elements (8 in rows of 256 and fewer), which keeps a CTA
-// small; with rows too few to fill the GPU it takes 8, and more threads share
-// a row.
+// A thread takes 32 elements, which keeps a CTA small; with rows too few to
+// fill the GPU it takes 8, and more threads share a row; rows of bf16 beyond
+// 32768 columns stay in one CTA with 64 (40032 columns: FIGURE2 in a cluster).
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
-  if (p.cols <= 256) return forward_e<T, NARROW, 8, kWarp, 128>(p, 32, 1, st);
-  const int c = cluster_for(p.rows, p.cols, 1024 * 32);
+  if (p.cols <= 256) {
+    if (p.rows >= 32 * (size_t)sm_count()) return forward_e<T, NARROW, 8, 4, kWarp, 128>(p, 32, 1, st);
+    return forward_e<T, NARROW, 8, 1, kWarp, 128>(p, 32, 1, st);
+  }
+  constexpr size_t kOneCta = sizeof(T) == 2 ? 65536 : 32768;
+  int c = cluster_for(p.rows, p.cols, 16384);
+  if (p.cols <= kOneCta && p.rows >= (size_t)sm_count()) c = 1;
   const size_t slice = div_up(p.cols, c);
   const bool few = p.rows * c <= 2 * (size_t)sm_count() && slice <= 4096;
   if (c > 1) {
-    if (few) return forward_e<T, NARROW, 8, kCluster, 512>(p, threads_for(slice, 8), c, st);
-    return forward_e<T, NARROW, 32, kCluster, 1024>(p, threads_for(slice, 32), c, st);
+    if (few) return forward_e<T, NARROW, 8, 1, kCluster, 512>(p, threads_for(slice, 8), c, st);
+    return forward_e<T, NARROW, 32, 1, kCluster, 512>(p, threads_for(slice, 32), c, st);
   }
-  if (few) return forward_e<T, NARROW, 8, kCta, 512>(p, threads_for(slice, 8), 1, st);
-  if (p.cols <= 1024) return forward_e<T, NARROW, 32, kWarp, 128>(p, 32, 1, st);
-  return forward_e<T, NARROW, 32, kCta, 1024>(p, threads_for(slice, 32), 1, st);
+  if (few) return forward_e<T, NARROW, 8, 1, kCta, 512>(p, threads_for(slice, 8), 1, st);
+  if (p.cols <= 512) return forward_e<T, NARROW, 16, 1, kWarp, 128>(p, 32, 1, st);
+  if (p.cols <= 1024) return forward_e<T, NARROW, 32, 1, kWarp, 128>(p, 32, 1, st);
+  if constexpr (sizeof(T) == 2 && !NARROW) {
+    if (p.cols <= 1536) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
+  }
+  if (p.cols <= 16384) return forward_e<T, NARROW, 32, 1, kCta, 512>(p, threads_for(slice, 32), 1, st);
+  if (p.cols <= 32768) return forward_e<T, NARROW, 32, 1, kCta, 1024>(p, threads_for(slice, 32), 1, st);
+  if constexpr (sizeof(T) == 2) return forward_e<T, NARROW, 64, 1, kCta, 1024>(p, threads_for(slice, 64), 1, st);
+  return cudaErrorInvalidValue;   // not reached: fp32 rows beyond 32768 columns have a cluster
 }
 
 // The shape of a backward launch, from the sizes alone (the workspace depends
@@ -786,6 +870,7 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 //   Measured at 24576 x 5120 bf16 (755 MB): 4 rows a turn 123 us, 2 rows 128,
 //   1 row 136; 8 columns per thread and 640 threads, 4 rows 133; 24 columns
 //   and 224 threads, 1 row 181.
+int resident_clusters(int csize);
 struct BackwardShape {
   int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, NARROW: 2), else 1
   unsigned nparts;
@@ -799,12 +884,39 @@ BackwardShape backward_shape(size_t rows, size_t cols) {
   s.groups = s.csize > 1 ? 1 : 512 / s.threads;
   if (s.threads > 32 && s.groups > 15) s.groups = 15;   // named barriers
   while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
-  const size_t most = (size_t)sm_count() / s.csize;
+  const size_t most = (size_t)resident_clusters(s.csize);
   s.many = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
   const size_t want = div_up(rows, (size_t)s.groups);
   s.nparts = (unsigned)(want < most ? want : most);
   if (s.nparts < 1) s.nparts = 1;
   return s;
+}
+
+// Clusters of backward CTAs the GPU holds at once: fewer than its SMs would
+// suggest, as a cluster lies within one GPC (of 152 SMs' worth of 5-CTA clusters, a second
+// wave of a few doubles the time).
+int resident_clusters(int csize) {
+  static int known[kMaxCluster8 + 1] = {};
+  if (csize == 1) return sm_count();
+  if (known[csize] > 0) return known[csize];
+  const auto kernel = ln_backward_kernel<bf16, false, 16, 1, kCluster>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(csize);
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = 200 * 1024;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = csize;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = sm_count() / csize;
+  }
+  return known[csize] = n;
 }
 
 template <typename T, bool NARROW, int E, int R, int MODE>
@@ -821,16 +933,24 @@ cudaError_t backward_e(NormRowsParams& p, const BackwardShape& s, cudaStream_t s
   return launch_dependent(ln_backward_kernel<T, NARROW, E, R, MODE>, dim3(s.nparts * s.csize), s.groups * s.threads, smem, s.csize, st, p);
 }
 
+// Rows a turn: 4, 2 or 1, as two stages of them fit in shared memory, or one
+// in a cluster, whose barrier costs more than the loads it then waits for.
+template <typename T, bool NARROW, int E, int MODE>
+cudaError_t backward_r(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
+  const size_t row = (size_t)s.groups * 2 * row_bytes<T, NARROW, E / kUnit<T>>(s.threads);
+  const size_t fit = (kSmemSm - 4096 - (NARROW ? row / 2 : 0)) / ((MODE == kCluster ? 1 : 2) * row);
+  if constexpr (!NARROW && sizeof(T) == 2) {
+    if (s.many && fit >= 4) return backward_e<T, NARROW, E, 4, MODE>(p, s, st);
+  }
+  if (s.many && fit >= 2) return backward_e<T, NARROW, E, 2, MODE>(p, s, st);
+  return backward_e<T, NARROW, E, 1, MODE>(p, s, st);
+}
+
 template <typename T, bool NARROW>
 cudaError_t backward(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
-  constexpr int R = sizeof(T) == 2 && !NARROW ? 4 : 2;
-  if (s.csize > 1) {
-    if (s.e == 32) return backward_e<T, NARROW, 32, 1, kCluster>(p, s, st);
-    return s.many ? backward_e<T, NARROW, 16, R, kCluster>(p, s, st) : backward_e<T, NARROW, 16, 1, kCluster>(p, s, st);
-  }
-  if (s.threads == 32 && s.e == 8) return s.many ? backward_e<T, NARROW, 8, R, kWarp>(p, s, st) : backward_e<T, NARROW, 8, 1, kWarp>(p, s, st);
-  if (s.threads == 32) return s.many ? backward_e<T, NARROW, 16, R, kWarp>(p, s, st) : backward_e<T, NARROW, 16, 1, kWarp>(p, s, st);
-  return s.many ? backward_e<T, NARROW, 16, R, kCta>(p, s, st) : backward_e<T, NARROW, 16, 1, kCta>(p, s, st);
+  if (s.csize > 1) return s.e == 32 ? backward_e<T, NARROW, 32, 1, kCluster>(p, s, st) : backward_r<T, NARROW, 16, kCluster>(p, s, st);
+  if (s.threads > 32) return backward_r<T, NARROW, 16, kCta>(p, s, st);
+  return s.e == 8 ? backward_r<T, NARROW, 8, kWarp>(p, s, st) : backward_r<T, NARROW, 16, kWarp>(p, s, st);
 }
 
 bool wide_rows(const void* base, u64 stride, size_t cols, size_t esize) {
@@ -862,8 +982,9 @@ cudaError_t launch_ln_backward(NormRowsParams& p, int dtype, cudaStream_t st) {
   else
     e = wide ? backward<bf16, false>(p, s, st) : backward<bf16, true>(p, s, st);
   if (e != cudaSuccess || !p.dgamma || s.nparts == 1) return e;
-  return launch_dependent(ln_parts_kernel, dim3((unsigned)div_up(p.cols, 32), 2), 32 * kPartWarps, 0, 1, st, (const float*)p.partial, s.nparts,
-                          p.cols, p.dgamma, p.dbeta, p.accumulate);
+  const bool four = p.cols % 4 == 0;   // and the workspace is aligned to 16 bytes
+  return launch_dependent(four ? ln_parts_kernel<4> : ln_parts_kernel<1>, dim3((unsigned)div_up(p.cols, four ? 128 : 32), 2), 32 * kPartWarps,
+                          0, 1, st, (const float*)p.partial, s.nparts, p.cols, p.dgamma, p.dbeta, p.accumulate);
 }
 
 }  // namespace xp

@@ -16,9 +16,11 @@ __device__ __forceinline__ void wait_for_predecessors() { asm volatile("griddepc
 // The successor's CTAs may be placed from now on, as this grid's make room.
 __device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// One launch, with programmatic dependence on the work before it; csize > 1:
-// in clusters of that many CTAs.  The gap between two small kernels in a
-// stream falls from 2.5 us to 1 us by it.
+// One launch, with programmatic dependence on the work before it (a stream of
+// small steps: 8.3 us each without, 4.0 with it); csize > 1: in clusters of
+// that many CTAs, and without it, as clusters placed beside a kernel that
+// drains held each other up (layer norm backward 2000 x 40032: 169 us with it,
+// 116 without).
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, size_t smem, int csize, cudaStream_t st,
                              Args... args) {
@@ -37,8 +39,8 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, si
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = csize;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 2 : 1;
+  cfg.attrs = csize > 1 ? at + 1 : at;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
