@@ -216,30 +216,72 @@ __device__ __forceinline__ unsigned mix(unsigned x) {
 constexpr unsigned kPosLo = 0x8ED88009u, kPosHi = 0xB86D3E2Fu;
 __device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { return mix(seed * kPosLo + mix(step)); }
 
-// a / d.  The division's fast path does not take a numerator of 0, which
-// weights without gradients have; one in a warp would send it the slow way.
-__device__ __forceinline__ float quotient(float a, float d) {
-  const bool zero = a == 0.f;
-  const float q = __fdiv_rn(zero ? 1.f : a, d);
-  return zero ? 0.f : q;
+// Square roots and quotients, two at a time and without the range checks and
+// branches of the functions' own: Markstein's iterations (P. W. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", IBM Journal of Research and Development 34, 1990), in which
+// fused multiply-adds give exact remainders.  Correctly rounded where nothing
+// over- or underflows, as the callers see to (every significand of a square
+// root, and 5e10 random quotients, equal __fsqrt_rn's and __fdiv_rn's).
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float approximate_rsqrt(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float approximate_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Signs are changed by exact products, which are packed too.
+__device__ __forceinline__ float2 root2(float2 v) {
+  const float2 y = make_float2(approximate_rsqrt(v.x), approximate_rsqrt(v.y));
+  float2 g = mul2(v, y), h = mul2(y, -0.5f);
+  const float2 r = __ffma2_rn(h, g, both(0.5f));
+  g = __ffma2_rn(g, r, g);
+  h = __ffma2_rn(h, r, h);
+  return __ffma2_rn(h, __ffma2_rn(g, g, mul2(v, -1.f)), g);
+}
+__device__ __forceinline__ float2 quotient2(float2 a, float2 d) {
+  float2 y = make_float2(approximate_rcp(d.x), approximate_rcp(d.y));
+  d = mul2(d, -1.f);
+  y = __ffma2_rn(y, __ffma2_rn(d, y, both(1.f)), y);
+  const float2 q = mul2(a, y);
+  return __ffma2_rn(__ffma2_rn(d, q, a), y, q);
 }
 
-// ---------------------------------------------------------------- the step
-
-// What a thread's eight elements with 8-bit states take from memory.
+// Where a thread's eight elements with 8-bit states are, and what they take
+// from memory.
 template <typename P, typename G>
-struct Codes8 {
+struct Place8 {
+  P* param;
+  const G* grad;
+  uint8_t *m, *v, *m_scale, *v_scale;
+  __nv_bfloat16* copy;
+  __device__ __forceinline__ Place8(const GroupTensor& t, unsigned long long i)
+      : param(static_cast<P*>(t.param) + i), grad(static_cast<const G*>(t.grad) + i), m(static_cast<uint8_t*>(t.m) + i),
+        v(static_cast<uint8_t*>(t.v) + i), m_scale(t.m_scale + i / XP_STATE8_BLOCK), v_scale(t.v_scale + i / XP_STATE8_BLOCK),
+        copy(t.copy ? static_cast<__nv_bfloat16*>(t.copy) + i : nullptr) {}
+  __device__ __forceinline__ void advance(int n) {
+    param += n, grad += n, m += n, v += n;
+    m_scale += n / XP_STATE8_BLOCK, v_scale += n / XP_STATE8_BLOCK;
+    if (copy) copy += n;
+  }
+};
+template <typename P, typename G>
+struct Values8 {
   Raw<G> g;
   Raw<P> p;
   uint2 cm, cv;
   int em, ev;
-  __device__ __forceinline__ void load(const G* grad, const P* param, const GroupTensor& t, unsigned long long i) {
-    g = load_vec(grad);
-    p = load_vec(param);
-    cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
-    cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
-    em = t.m_scale[i / XP_STATE8_BLOCK];
-    ev = t.v_scale[i / XP_STATE8_BLOCK];
+  __device__ __forceinline__ void load(const Place8<P, G>& at, int ahead) {
+    g = load_vec(at.grad + ahead);
+    p = load_vec(at.param + ahead);
+    cm = *reinterpret_cast<const uint2*>(at.m + ahead);
+    cv = *reinterpret_cast<const uint2*>(at.v + ahead);
+    em = at.m_scale[ahead / XP_STATE8_BLOCK];
+    ev = at.v_scale[ahead / XP_STATE8_BLOCK];
   }
 };
 
@@ -319,17 +361,16 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
     if (S8) key = step_key(prm.seed, s_step);
   };
   if (turns == 0) coefficients(0);
-  Codes8<P, G> next;
-  for (unsigned turn = 0; turn < turns; ++turn) {
-    const unsigned at = turn * kTurn + threadIdx.x * kVec;
-    const unsigned long long i = u.start + at, pos = t.pos + i;
-    uint8_t* const code_m = static_cast<uint8_t*>(t.m) + i;
-    uint8_t* const code_v = static_cast<uint8_t*>(t.v) + i;
-    unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi;   // kVec positions share the high word
-    if (S8 && vec && u.n - turn * kTurn >= kTurn) {
-      if (turn == 0) next.load(grad + at, param + at, t, i);
-      Codes8<P, G> now = next;
-      if (u.n - turn * kTurn >= 2 * kTurn) next.load(grad + at + kTurn, param + at + kTurn, t, i + kTurn);
+  unsigned turn = 0;
+  const unsigned whole = vec ? u.n / kTurn : 0;   // turns of eight aligned elements for every thread
+  if constexpr (S8) {
+    Place8<P, G> place(t, u.start + threadIdx.x * kVec);
+    unsigned long long pos = t.pos + u.start + threadIdx.x * kVec;
+    Values8<P, G> next;
+    if (whole > 0) next.load(place, 0);
+    for (; turn < whole; ++turn, pos += kTurn) {
+      const Values8<P, G> now = next;
+      if (turn + 1 < whole) next.load(place, kTurn);
       coefficients(turn);
       float2 m[kVec / 2], v[kVec / 2];
       if (pairs_ok(now.cm, now.em) && pairs_ok(now.cv, now.ev)) {
@@ -355,29 +396,39 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
       for (int k = 0; k < kVec / 2; ++k) {
         const float2 gi = mul2(make_float2(g[2 * k], g[2 * k + 1]), gscale);
         m[k] = add2(mul2(m[k], prm.beta1), mul2(gi, prm.one_minus_beta1));
-        v[k] = add2(mul2(v[k], prm.beta2),
-                          mul2(mul2(gi, prm.one_minus_beta2), gi));
-        const float2 d = add2(mul2(make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y)), rs), make_float2(prm.eps, prm.eps));
-        const float2 a = mul2(m[k], alpha);
-        const float2 q = add2(mul2(make_float2(p[2 * k], p[2 * k + 1]), keep),
-                                    make_float2(-quotient(a.x, d.x), -quotient(a.y, d.y)));
-        p[2 * k] = q.x;
-        p[2 * k + 1] = q.y;
+        v[k] = add2(mul2(v[k], prm.beta2), mul2(mul2(gi, prm.one_minus_beta2), gi));
       }
-      store_vec(param + at, p);
-      if (t.copy) store_vec(static_cast<__nv_bfloat16*>(t.copy) + i, p);
-      unsigned tm = 0, tv = 0;
+      unsigned tm = 0, tv = 0, lv = 0xffffffffu;   // largest magnitudes, smallest v
 #pragma unroll
       for (int k = 0; k < kVec / 2; ++k) {
         tm = max(max(tm, __float_as_uint(m[k].x) & 0x7fffffffu), __float_as_uint(m[k].y) & 0x7fffffffu);
-        tv = max(max(tv, __float_as_uint(v[k].x) & 0x7fffffffu), __float_as_uint(v[k].y) & 0x7fffffffu);
+        tv = max(max(tv, __float_as_uint(v[k].x)), __float_as_uint(v[k].y));
+        lv = min(min(lv, __float_as_uint(v[k].x)), __float_as_uint(v[k].y));
       }
-      unsigned top = (tm >> 23) << 16 | tv >> 23;
+      // v in [2^-100, 2^100] and m up to 2^100: roots, denominators and remainders are in range
+      const bool in_range = lv >= 27u << 23 && tv <= 227u << 23 && tm <= 227u << 23 && fabsf(alpha) <= 1e6f;
+      auto weights = [&](auto root, auto quotient) {
+#pragma unroll
+        for (int k = 0; k < kVec / 2; ++k) {
+          const float2 d = add2(mul2(root(v[k]), rs), both(prm.eps)), q = quotient(mul2(m[k], alpha), d);
+          const float2 kept = mul2(make_float2(p[2 * k], p[2 * k + 1]), keep);
+          p[2 * k] = __fsub_rn(kept.x, q.x);
+          p[2 * k + 1] = __fsub_rn(kept.y, q.y);
+        }
+      };
+      if (in_range)
+        weights([](float2 x) { return root2(x); }, [](float2 a, float2 d) { return quotient2(a, d); });
+      else
+        weights([](float2 x) { return make_float2(__fsqrt_rn(x.x), __fsqrt_rn(x.y)); },
+                [](float2 a, float2 d) { return make_float2(__fdiv_rn(a.x, d.x), __fdiv_rn(a.y, d.y)); });
+      store_vec(place.param, p);
+      if (place.copy) store_vec(place.copy, p);
+      unsigned top = (tm >> 23) << 16 | (tv >> 23 & 0xffu);
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
       uint2 cm, cv;
-      h += key;
+      unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi + key;   // kVec positions share the high word
       if (em >= 16 && ev >= 32) {
         Encoder enc(em, ev);
 #pragma unroll
@@ -398,14 +449,20 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
           (k < 4 ? cv.x : cv.y) |= encode_one<false>(k & 1 ? vk.y : vk.x, ((r & 0xffffu) << 4) + 8u, ev) << (8 * (k & 3));
         }
       }
-      *reinterpret_cast<uint2*>(code_m) = cm;
-      *reinterpret_cast<uint2*>(code_v) = cv;
+      *reinterpret_cast<uint2*>(place.m) = cm;
+      *reinterpret_cast<uint2*>(place.v) = cv;
       if ((threadIdx.x & 3) == 0) {   // a block is four threads' elements
-        t.m_scale[i / XP_STATE8_BLOCK] = (uint8_t)em;
-        t.v_scale[i / XP_STATE8_BLOCK] = (uint8_t)ev;
+        *place.m_scale = (uint8_t)em;
+        *place.v_scale = (uint8_t)ev;
       }
-      continue;
+      place.advance(kTurn);
     }
+  }
+  for (; turn < turns; ++turn) {
+    const unsigned at = turn * kTurn + threadIdx.x * kVec;
+    const unsigned long long i = u.start + at, pos = t.pos + i;
+    uint8_t* const code_m = static_cast<uint8_t*>(t.m) + i;
+    uint8_t* const code_v = static_cast<uint8_t*>(t.v) + i;
     const int n = at < u.n ? (int)min((unsigned)kVec, u.n - at) : 0;
     float p[kVec], g[kVec], m[kVec], v[kVec];
     load_some(grad + at, n, vec, g);
@@ -437,7 +494,7 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);
       uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
-      h += key;
+      unsigned h = (unsigned)pos * kPosLo + (unsigned)(pos >> 32) * kPosHi + key;
 #pragma unroll
       for (int k = 0; k < kVec; ++k, h += kPosLo) {
         const unsigned r = mix(h);

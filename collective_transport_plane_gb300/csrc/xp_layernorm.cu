@@ -362,15 +362,14 @@ __device__ __forceinline__ void store_shared16(unsigned a, uint4 q) {
 // ---------------------------------------------------------------- forward
 
 // One row per group, in registers from its load to its output: E elements per
-// thread.  The CTAs are small and
-// many: eight of 128 threads are on an SM, so that one's sums are another's
-// loads, and the hardware hands the rows out.
+// thread.  The CTAs are small and many: eight of 128 threads are on an SM, so
+// that one's sums are another's loads, and the hardware hands the rows out.
 //   Measured at 16384 x 4096 bf16 (268 MB, a plain copy of it takes 42 us):
-//   32 elements per thread 43 us, 16 elements 49, 8 elements 75; one
+//   32 elements per thread 45 us, 6.0 TB/s; 16 elements 49, 8 elements 68; one
 //   persistent CTA per SM with a warp per row and rows copied ahead 50.
-constexpr int kForwardThreads = 1024;
-// R > 1: rows side by side, in rows of 256 columns and fewer, so that a warp has
-// more in flight (60000 x 96 bf16: FIGURE).
+// R > 1: rows side by side, in rows of 256 columns and fewer, so that a warp
+// has more in flight (60000 x 96 bf16: 9 us, 16 with one row).
+constexpr int kForwardThreads = 1024;   // of an SM at least
 template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
@@ -832,8 +831,11 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 }
 
 // A thread takes 32 elements, which keeps a CTA small; with rows too few to
-// fill the GPU it takes 8, and more threads share a row; rows of bf16 beyond
-// 32768 columns stay in one CTA with 64 (40032 columns: FIGURE2 in a cluster).
+// fill the GPU it takes 8, and more threads share a row.  bf16 take half the
+// registers, so a thread may have 64: in rows up to 1536 columns, which then
+// are one warp's (60000 x 1056: 53 us, 66 with two warps; beyond, the warps of
+// 32 are as fast), and beyond 32768 columns, which then are one CTA's (2000 x
+// 40032: 106 us, 125 in a cluster of 3).
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
   if (p.cols <= 256) {
@@ -864,12 +866,12 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 // The shape of a backward launch, from the sizes alone (the workspace depends
 // on it).  A thread has 16 columns (8 in rows of 256 and fewer): with their
 // sums and gamma they take 48 registers, which leaves room for what is in
-// work.  Up to 5120 columns two CTAs of up to 320 threads are on an SM, so
-// that one's barrier is another's work; up to 8192 one of 512; longer rows are split
-// over a cluster, in CTAs of 512 threads with 32 columns each beyond 65536.
-//   Measured at 24576 x 5120 bf16 (755 MB): 4 rows a turn 123 us, 2 rows 128,
-//   1 row 136; 8 columns per thread and 640 threads, 4 rows 133; 24 columns
-//   and 224 threads, 1 row 181.
+// work.  One CTA of up to 512 threads is on an SM, with as many rows side by
+// side as it has room for, and leaves one partial sum per column; rows beyond
+// 8192 columns are split over a cluster, and beyond 65536 a thread has 32.
+//   Measured at 24576 x 5120 bf16 (755 MB), the kernel without the parts' sum:
+//   120 us, 6.3 TB/s; 2 rows a turn 128, 1 row 136; 8 columns per thread, 640
+//   threads and 4 rows 133; 24 columns, 224 threads and 1 row 175.
 int resident_clusters(int csize);
 struct BackwardShape {
   int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, NARROW: 2), else 1

@@ -109,6 +109,14 @@ def test_forward_strides_and_alignment(xt, rows, cols, pad, offset):
         _check_forward(torch, xt, rows, cols, name, "f32", pad, offset)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(5001, 96), (4999, 95), (6000, 256), (700, 1100), (330, 1536), (330, 1537), (320, 9000), (160, 20000),
+                                       (155, 32768), (160, 40032), (158, 40031), (155, 66001), (153, 70000)])
+def test_forward_many_rows(xt, rows, cols, name):
+    torch = torch_cuda()
+    _check_forward(torch, xt, rows, cols, name, "f32")
+
+
 def test_forward_far_from_zero_and_large_eps(xt):
     torch = torch_cuda()
     _check_forward(torch, xt, 20, 1536, "f32", "f32", shift=30.0)
@@ -172,6 +180,14 @@ def test_backward_strides_and_alignment(xt, rows, cols, pad, offset):
 def test_backward_many_rows(xt, rows, cols):
     torch = torch_cuda()
     _check_backward(torch, xt, rows, cols, "bf16", "f32")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(30001, 96), (29999, 95), (9000, 257), (7001, 300), (3001, 2080), (2999, 2081), (1300, 5120),
+                                       (1250, 8192), (620, 12000), (610, 12001), (170, 66000)])
+def test_backward_more_rows(xt, rows, cols, name):
+    torch = torch_cuda()
+    _check_backward(torch, xt, rows, cols, name, "bf16", accumulate=cols % 2 == 1)
 
 
 @pytest.mark.parametrize("rows,cols", [(37, 200), (37, 1000), (5, 30000)])
