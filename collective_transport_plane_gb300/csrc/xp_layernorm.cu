@@ -229,6 +229,21 @@ __device__ __forceinline__ int first_unit(int tid) {
   return (tid & ~31) * NV + (tid & 31);
 }
 
+// f(j) for the words j < n of a warp, n <= 32 COUNT: unrolled, unless the warp
+// has few.
+template <int COUNT, typename F>
+__device__ __forceinline__ void for_words(int n, int lane, F f) {
+  if (n >= 16 * COUNT) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      if (lane + 32 * i < n) f(lane + 32 * i);
+    }
+  } else {
+#pragma unroll 1
+    for (int j = lane; j < n; j += 32) f(j);
+  }
+}
+
 template <typename T, bool NARROW, int NV>
 __device__ __forceinline__ void fetch_row(const T* row, int cols, const T* matrix, unsigned smem, int tid) {
   const int lane = tid & 31;
@@ -251,16 +266,18 @@ __device__ __forceinline__ void fetch_row(const T* row, int cols, const T* matri
       if (sizeof(T) == 2 && lane == 0) copy_async4(smem + 128 * kWords, from + 128 * kWords);
       return;
     }
+    const int full = min(max(bytes, 0) >> 2, 32 * kWords);   // words that are the row's
+    for_words<kWords>(full, lane, [&](int j) {
+      if (j > 0 || !before) copy_async4(smem + 4 * j, from + 4 * j);
+    });
+    // the words at the row's end, for either phase: at most three
     const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(matrix) & ~(uintptr_t)3);   // of which 0 bytes are read
-    const int most = min(cols > 0 ? (cols * (int)sizeof(T) + (sizeof(T) == 2 ? 5 : 3)) / 4 - first : 0,   // words, for either phase
-                         32 * kWords + (sizeof(T) == 2 ? 1 : 0));
-#pragma unroll 1
-    for (int j = lane; j < most; j += 32) {
-      if (j == 0 && before)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem), "r"((unsigned)*reinterpret_cast<const unsigned short*>(row) << 16) : "memory");
-      else
-        copy_async4(smem + 4 * j, 4 * j < bytes ? from + 4 * j : nothing, min(max(bytes - 4 * j, 0), 4));
-    }
+    const int most = min((cols * (int)sizeof(T) + (sizeof(T) == 2 ? 5 : 3)) / 4 - first, 32 * kWords + (sizeof(T) == 2 ? 1 : 0));
+    const int j = full + lane;
+    if (lane < 3 && j < most && (j > 0 || !before))
+      copy_async4(smem + 4 * j, 4 * j < bytes ? from + 4 * j : nothing, min(max(bytes - 4 * j, 0), 4));
+    if (lane == 0 && before)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem), "r"((unsigned)*reinterpret_cast<const unsigned short*>(row) << 16) : "memory");
   }
 }
 
@@ -302,6 +319,7 @@ struct Landed {
 template <typename T, bool NARROW, int NV>
 __device__ __forceinline__ void clear_rows(unsigned smem, unsigned row_len, int nrows, int cols, int tid) {
   const int lane = tid & 31;
+  if (NARROW && ((tid >> 5) + 1) * 32 * NV * kUnit<T> + 2 <= cols) return;   // every word of the warp's is the row's
   for (int r = 0; r < nrows; ++r, smem += row_len) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -319,39 +337,20 @@ __device__ __forceinline__ void clear_rows(unsigned smem, unsigned row_len, int 
 template <typename T, int NV>
 __device__ __forceinline__ void store_words(T* out, int n, unsigned smem, int lane) {
   constexpr int kWords = 4 * NV, kAll = 32 * NV * kUnit<T>;
+  n = min(n, kAll);
   if constexpr (sizeof(T) == 4) {
-    if (n >= kAll) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) reinterpret_cast<unsigned*>(out)[lane + 32 * i] = load_shared4(smem + 4 * lane + 128 * i);
-    } else {
-#pragma unroll 1
-      for (int j = lane; j < n; j += 32) reinterpret_cast<unsigned*>(out)[j] = load_shared4(smem + 4 * j);
-    }
+    for_words<kWords>(n, lane, [&](int j) { reinterpret_cast<unsigned*>(out)[j] = load_shared4(smem + 4 * j); });
   } else {
     unsigned short* o = reinterpret_cast<unsigned short*>(out);
-    const int odd = (int)(reinterpret_cast<uintptr_t>(out) >> 1) & 1;   // then words begin at element 1
-    if (odd && lane == 0 && n > 0) o[0] = (unsigned short)load_shared4(smem);
-    const unsigned select = odd ? 0x5432u : 0x3210u;
-    auto word = [&](int j) { return __byte_perm(load_shared4(smem + 4 * j), load_shared4(smem + 4 * j + 4), select); };
-    o += odd;
-    n = min(n, kAll) - odd;
-    int j = lane;
-    if (n >= kAll && !odd) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) reinterpret_cast<unsigned*>(o)[lane + 32 * i] = load_shared4(smem + 4 * lane + 128 * i);
-      return;
-    }
-    if (n >= kAll - 1) {
-#pragma unroll
-      for (int i = 0; i < kWords - 1; ++i) reinterpret_cast<unsigned*>(o)[lane + 32 * i] = word(lane + 32 * i);
-      j += 32 * (kWords - 1);
-    }
-#pragma unroll 1
-    for (; 2 * j < n; j += 32) {
-      if (2 * j + 1 < n)
-        reinterpret_cast<unsigned*>(o)[j] = word(j);
-      else
-        o[2 * j] = (unsigned short)word(j);
+    if ((reinterpret_cast<uintptr_t>(out) & 2u) == 0) {
+      for_words<kWords>(n >> 1, lane, [&](int j) { reinterpret_cast<unsigned*>(o)[j] = load_shared4(smem + 4 * j); });
+      if (lane == 0 && (n & 1) && n > 0) o[n - 1] = (unsigned short)load_shared4(smem + 2 * (n - 1));
+    } else {   // words begin at element 1
+      for_words<kWords>((n - 1) >> 1, lane, [&](int j) {
+        reinterpret_cast<unsigned*>(o + 1)[j] = __byte_perm(load_shared4(smem + 4 * j), load_shared4(smem + 4 * j + 4), 0x5432);
+      });
+      if (lane == 0 && n > 0) o[0] = (unsigned short)load_shared4(smem);
+      if (lane == 1 && !(n & 1) && n > 0) o[n - 1] = (unsigned short)(load_shared4(smem + 2 * (n - 2)) >> 16);
     }
   }
 }
