@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <new>
 #include <vector>
 
@@ -137,14 +138,20 @@ xp_status create(const xp_group_config& cfg, int ntensors, const xp_tensor* tens
   g->units = reinterpret_cast<xp::GroupUnit*>(g->mem + at_units);
   g->partial = reinterpret_cast<double*>(g->mem + at_partial);
   g->state = reinterpret_cast<xp::GroupState*>(g->mem + at_state);
+  std::vector<char> image(at_state + 256, 0);
+  memcpy(image.data(), table.data(), table.size() * sizeof(xp::GroupTensor));
+  memcpy(image.data() + at_units, units.data(), units.size() * sizeof(xp::GroupUnit));
+  xp::GroupState state = {};
+  state.step = cfg.step;
+  state.power1 = std::pow(cfg.beta1, (double)(cfg.step + 1));
+  state.power2 = std::pow(cfg.beta2, (double)(cfg.step + 1));
+  state.inv_bias1 = (float)(1.0 / (1.0 - state.power1));
+  state.inv_sqrt_bias2 = (float)(1.0 / std::sqrt(1.0 - state.power2));
+  memcpy(image.data() + at_state, &state, sizeof state);
   // on a stream of its own, waited for here: never behind the caller's work
   cudaStream_t st = nullptr;
   XP_CUDA(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking));
-  cudaError_t e = cudaMemcpyAsync(g->tensors, table.data(), table.size() * sizeof(xp::GroupTensor), cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess)
-    e = cudaMemcpyAsync(g->units, units.data(), units.size() * sizeof(xp::GroupUnit), cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess)
-    e = xp::launch_set_step(g->state, cfg.step, std::pow(cfg.beta1, (double)(cfg.step + 1)), std::pow(cfg.beta2, (double)(cfg.step + 1)), st);
+  cudaError_t e = cudaMemcpyAsync(g->mem, image.data(), image.size(), cudaMemcpyHostToDevice, st);
   const cudaError_t e2 = cudaStreamSynchronize(st);
   cudaStreamDestroy(st);
   XP_CUDA(e);

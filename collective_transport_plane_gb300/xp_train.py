@@ -145,17 +145,15 @@ def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=No
     want = {"param": cfg.param_dtype, "grad": cfg.grad_dtype, "m": cfg.state_dtype, "v": cfg.state_dtype, "copy": XP_BF16,
             "m_scale": XP_U8, "v_scale": XP_U8}
     named["grad"] = grads
-    table = (xp_tensor * max(n, 1))()
-    for i in range(n):
-        count = grads[i].numel()
-        for name, tensors in named.items():
-            t = None if tensors is None else tensors[i]
-            if t is None:
-                continue
-            n_here = -(-count // XP_STATE8_BLOCK) if name.endswith("scale") else count
-            setattr(table[i], name, _vector(t, n_here, f"{name} {i}", want[name]))
-        table[i].count = count
-        table[i].weight_decay = decay[i]
+    counts = [t.numel() for t in grads]
+    blocks = [-(-c // XP_STATE8_BLOCK) for c in counts]
+    columns = {}
+    for name, tensors in named.items():
+        sizes, dtype = blocks if name.endswith("scale") else counts, want[name]
+        columns[name] = [None] * n if tensors is None else [_vector(t, k, f"{name} {i}", dtype) for i, (t, k) in enumerate(zip(tensors, sizes))]
+    rows = zip(columns["param"], columns["grad"], columns["m"], columns["v"], columns["m_scale"], columns["v_scale"], columns["copy"],
+               counts, decay)
+    table = (xp_tensor * max(n, 1))(*[xp_tensor(*row) for row in rows])
     out = ctypes.c_void_p()
     _check(_lib.xp_group_create(ctypes.byref(cfg), n, table, ctypes.byref(out)), "xp_group_create")
     return out.value
