@@ -58,13 +58,15 @@ __device__ __forceinline__ uint4 pack16(const float2 (&f)[P]) {
 }
 // A unit of gamma or beta (w is aligned to 16 bytes); `none` where there is
 // none.  No branches: the loads of several units are in flight together.
+// (Plain loads, here and of the statistics: a load that may assume read-only
+// memory could be moved before the wait for the kernel that writes it.)
 template <typename W, int P>
 __device__ __forceinline__ void load_whole_w(const W* p, bool has, float none, float2 (&f)[P]) {
   if constexpr (sizeof(W) == 4) {
     const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
-      const float4 q = has ? __ldg(reinterpret_cast<const float4*>(p) + i) : rest;
+      const float4 q = has ? reinterpret_cast<const float4*>(p)[i] : rest;
       f[2 * i] = make_float2(q.x, q.y);
       f[2 * i + 1] = make_float2(q.z, q.w);
     }
@@ -72,9 +74,9 @@ __device__ __forceinline__ void load_whole_w(const W* p, bool has, float none, f
     const unsigned rest = pack2(both(none));
     uint4 q = make_uint4(rest, rest, rest, rest);
     if constexpr (P == 4) {
-      q = has ? __ldg(reinterpret_cast<const uint4*>(p)) : q;
+      q = has ? *reinterpret_cast<const uint4*>(p) : q;
     } else {
-      const uint2 h = has ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(rest, rest);
+      const uint2 h = has ? *reinterpret_cast<const uint2*>(p) : make_uint2(rest, rest);
       q.x = h.x, q.y = h.y;
     }
     const unsigned words[4] = {q.x, q.y, q.z, q.w};
@@ -91,8 +93,8 @@ __device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float n
   } else {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      f[i].x = 2 * i < n ? to_f(__ldg(p + 2 * i)) : none;
-      f[i].y = 2 * i + 1 < n ? to_f(__ldg(p + 2 * i + 1)) : none;
+      f[i].x = 2 * i < n ? to_f(p[2 * i]) : none;
+      f[i].y = 2 * i + 1 < n ? to_f(p[2 * i + 1]) : none;
     }
   }
 }
@@ -591,8 +593,8 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   float mean_next = 0.f, rstd_next = 0.f;
   auto statistics = [&](int row) {
     if (lane < R && row + lane < rows) {
-      mean_next = __ldg(prm.mean + row + lane);
-      rstd_next = __ldg(prm.rstd + row + lane);
+      mean_next = prm.mean[row + lane];
+      rstd_next = prm.rstd[row + lane];
     }
   };
   statistics(first);

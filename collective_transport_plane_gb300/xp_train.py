@@ -78,21 +78,20 @@ def _check(st: int, where: str):
         xp._check(st, where)
 
 
-def _row(t, shape, dtype, what):
-    """A matrix's row stride in elements; its columns lie side by side."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of {dtype}")
-    row, col = t.stride()
-    if col != 1 and shape[1] > 1:
-        raise ValueError(f"{what}'s columns are {col} elements apart")
-    return row
+def _refuse_rows(named, shape, dtype):
+    """Says which of several matrices does not have the first one's shape and type, or its columns side by side."""
+    for what, t in named:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of {dtype}")
+        if shape[1] > 1 and t.stride()[1] != 1:
+            raise ValueError(f"{what}'s columns are {t.stride()[1]} elements apart")
 
 
 def _vector(t, n, what, dtype):
     """The address of n contiguous elements (None: none)."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_contiguous() or _dtype(t) != dtype:
+    if t.numel() != n or not t.is_contiguous() or _types.get(t.dtype) != dtype and _dtype(t) != dtype:
         raise ValueError(f"{what} is not {n} contiguous elements of its type")
     return t.data_ptr()
 
@@ -101,12 +100,16 @@ def xp_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1
     """y = layer norm of each row of x (rows x cols), with its statistics where mean and rstd are given."""
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
-    dt = _dtype(x)
+    (xs, xc), (ys, yc) = x.stride(), y.stride()
+    if y.shape != shape or y.dtype != dtype or (xc != 1 or yc != 1) and cols > 1:
+        _refuse_rows((("x", x), ("y", y)), shape, dtype)
+    dt = _types.get(dtype) or _dtype(x)
     wdt = _dtype(gamma) if gamma is not None else dt if beta is None else _dtype(beta)
-    xs, ys = _row(x, shape, dtype, "x"), _row(y, shape, dtype, "y")
-    _check(_forward(x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(beta, cols, "beta", wdt), y.data_ptr(), ys,
-                    _vector(mean, rows, "mean", XP_F32), _vector(rstd, rows, "rstd", XP_F32), rows, cols, eps, dt, wdt,
-                    stream if stream is None else _stream(stream)), "xp_layernorm_forward")
+    st = _forward(x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(beta, cols, "beta", wdt), y.data_ptr(), ys,
+                  _vector(mean, rows, "mean", XP_F32), _vector(rstd, rows, "rstd", XP_F32), rows, cols, eps, dt, wdt,
+                  stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_layernorm_forward")
 
 
 def xp_layernorm_workspace(rows: int, cols: int) -> int:
@@ -120,14 +123,19 @@ def xp_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None,
     """dx, and over the rows dgamma and dbeta, from dy and what the forward pass gave."""
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
-    dt = _dtype(x)
+    (dys, dyc), (xs, xc), (dxs, dxc) = dy.stride(), x.stride(), dx.stride()
+    if (dy.shape != shape or dx.shape != shape or dy.dtype != dtype or dx.dtype != dtype
+            or (dyc != 1 or xc != 1 or dxc != 1) and cols > 1):
+        _refuse_rows((("dy", dy), ("x", x), ("dx", dx)), shape, dtype)
+    dt = _types.get(dtype) or _dtype(x)
     wdt = dt if gamma is None else _dtype(gamma)
-    dys, xs, dxs = _row(dy, shape, dtype, "dy"), _row(x, shape, dtype, "x"), _row(dx, shape, dtype, "dx")
-    _check(_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(mean, rows, "mean", XP_F32),
-                     _vector(rstd, rows, "rstd", XP_F32), dx.data_ptr(), dxs, _vector(dgamma, cols, "dgamma", XP_F32),
-                     _vector(dbeta, cols, "dbeta", XP_F32), rows, cols, dt, wdt, 1 if accumulate else 0,
-                     None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
-                     stream if stream is None else _stream(stream)), "xp_layernorm_backward")
+    work, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    st = _backward(dy.data_ptr(), dys, x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(mean, rows, "mean", XP_F32),
+                   _vector(rstd, rows, "rstd", XP_F32), dx.data_ptr(), dxs, _vector(dgamma, cols, "dgamma", XP_F32),
+                   _vector(dbeta, cols, "dbeta", XP_F32), rows, cols, dt, wdt, 1 if accumulate else 0, work, nbytes,
+                   stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_layernorm_backward")
 
 
 def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=None, copies=None, weight_decay=0.0,

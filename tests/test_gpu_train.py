@@ -610,3 +610,44 @@ def test_refusals_on_the_gpu(xt):
         xt.xp_layernorm_backward(x, x.clone(), None, s, s, torch.empty_like(x), torch.empty(64, device="cuda"), torch.empty(64, device="cuda"),
                                  torch.empty(16, dtype=torch.uint8, device="cuda"))
     g.close()
+
+
+@pytest.mark.parametrize("cols", [200, 1000, 3001, 40000])
+def test_each_call_waits_for_the_one_before(xt, cols):
+    # kernels may be placed while their predecessors drain: a chain in which each call reads what the call before it wrote
+    # gives the same bits with and without a pause between the calls
+    torch = torch_cuda()
+    rows = 30
+
+    def chain(pause):
+        x, dy, gamma, beta = _inputs(torch, rows, cols, torch.float32, torch.float32)
+        mean, rstd = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+        dg, db = torch.zeros(cols, device="cuda"), torch.zeros(cols, device="cuda")
+        m, v = [torch.zeros(cols, device="cuda") for _ in range(2)], [torch.zeros(cols, device="cuda") for _ in range(2)]
+        spare = [torch.full((cols,), 7.0, device="cuda"), torch.full((cols,), 7.0, device="cuda")]
+        group = xt.xp_group_create([gamma, beta], spare, m, v)
+        report = torch.zeros(8, device="cuda")
+        work = torch.empty(xt.xp_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+        a, b = x, torch.empty_like(x)
+        out = []
+        for k in range(12):
+            y = torch.empty_like(x)
+            dx = torch.empty_like(x)
+            calls = [lambda: xt.xp_layernorm_forward(a, gamma, beta, y, mean, rstd),
+                     lambda: xt.xp_layernorm_backward(dy, a, gamma, mean, rstd, dx, dg, db, work),
+                     lambda: xt.xp_group_set_grads(group, [dg, db] if k % 3 else [db, dg]),
+                     lambda: xt.xp_grad_norm(group, report, max_norm=0.5),
+                     lambda: xt.xp_adamw_step(group, 1e-2, report=report)]
+            for call in calls:
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+            a, b = y, a
+            out += [y, dx, report.clone()]
+        torch.cuda.synchronize()
+        xt.xp_group_destroy(group)
+        return out + [gamma, beta, m[0], v[1]]
+
+    want = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(chain(False), want))
