@@ -834,9 +834,9 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 // A thread takes 32 elements, which keeps a CTA small; with rows too few to
 // fill the GPU it takes 8, and more threads share a row.  bf16 take half the
 // registers, so a thread may have 64: in rows up to 1536 columns, which then
-// are one warp's (60000 x 1056: 53 us, 66 with two warps; beyond, the warps of
-// 32 are as fast), and beyond 32768 columns, which then are one CTA's (2000 x
-// 40032: 106 us, 125 in a cluster of 3).
+// are one warp's (60000 x 1056: 54 us, 66 with two warps; beyond, 32 are as
+// fast or faster), and beyond 16384 columns (4000 x 20000: 67 us, 90 with 32;
+// 2000 x 40032: 87 us, 125 in a cluster of 3).
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
   if (p.cols <= 256) {
@@ -859,9 +859,7 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
     if (p.cols <= 1536) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
   }
   if (p.cols <= 16384) return forward_e<T, NARROW, 32, 1, kCta, 512>(p, threads_for(slice, 32), 1, st);
-  if (p.cols <= 32768) return forward_e<T, NARROW, 32, 1, kCta, 1024>(p, threads_for(slice, 32), 1, st);
-  if constexpr (sizeof(T) == 2) return forward_e<T, NARROW, 64, 1, kCta, 1024>(p, threads_for(slice, 64), 1, st);
-  return cudaErrorInvalidValue;   // not reached: fp32 rows beyond 32768 columns have a cluster
+  return forward_e<T, NARROW, sizeof(T) == 2 ? 64 : 32, 1, kCta, 1024>(p, threads_for(slice, sizeof(T) == 2 ? 64 : 32), 1, st);
 }
 
 // The shape of a backward launch, from the sizes alone (the workspace depends
