@@ -57,8 +57,8 @@ for _name, _args in {
 }.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = ctypes.c_int
-_forward, _backward, _norm, _step = (_lib.xp_layernorm_forward, _lib.xp_layernorm_backward, _lib.xp_grad_norm,
-                                     _lib.xp_adamw_step)
+_forward, _backward, _norm, _step, _decode = (_lib.xp_layernorm_forward, _lib.xp_layernorm_backward, _lib.xp_grad_norm,
+                                              _lib.xp_adamw_step, _lib.xp_state8_decode)
 
 _DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
 _types = {}   # torch dtype -> xp_dtype, filled as types are met
@@ -207,7 +207,11 @@ def xp_state8_decode(m, m_scale, v, v_scale, m_out, v_out, stream=None) -> None:
         return
     count, dt = out.numel(), _dtype(out)
     blocks = -(-count // XP_STATE8_BLOCK)
-    args = [_vector(m_out, count, "m_out", dt), _vector(v_out, count, "v_out", dt)]
-    for to, code, scale, name in ((v_out, v, v_scale, "v"), (m_out, m, m_scale, "m")):
-        args[:0] = [None, None] if to is None else [_vector(code, count, name, XP_U8), _vector(scale, blocks, name + "_scale", XP_U8)]
-    _check(_lib.xp_state8_decode(*args[:4], count, *args[4:], dt, stream if stream is None else _stream(stream)), "xp_state8_decode")
+    pm = pms = pmo = pv = pvs = pvo = None
+    if m_out is not None:
+        pm, pms, pmo = _vector(m, count, "m", XP_U8), _vector(m_scale, blocks, "m_scale", XP_U8), _vector(m_out, count, "m_out", dt)
+    if v_out is not None:
+        pv, pvs, pvo = _vector(v, count, "v", XP_U8), _vector(v_scale, blocks, "v_scale", XP_U8), _vector(v_out, count, "v_out", dt)
+    st = _decode(pm, pms, pv, pvs, count, pmo, pvo, dt, stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_state8_decode")
