@@ -23,11 +23,15 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 
 // ---- units: the V elements (16 bytes) a thread takes at once, as V / 2 pairs.
-// Rows that allow it move between global and shared memory or registers in
-// units; in others (NARROW: lengths, strides or addresses that are no multiple
-// of 16 bytes) in 4-byte words, and are units in shared memory only.
+// In rows that allow it they lie side by side.  In others (NARROW: lengths,
+// strides or addresses that are no multiple of 16 bytes) a warp's lanes take
+// neighbouring pairs, 64 columns at a time (of fp32 a pair is 32 columns apart),
+// so that words at any offset are read and written side by side.
 template <typename T>
 constexpr int kUnit = 16 / (int)sizeof(T);
+
+template <typename T, bool NARROW>
+constexpr int kApart = NARROW && sizeof(T) == 4 ? 32 : 1;   // of a pair's columns
 
 __device__ __forceinline__ float lo_of(unsigned w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
@@ -84,17 +88,31 @@ __device__ __forceinline__ void load_whole_w(const W* p, bool has, float none, f
     for (int i = 0; i < P; ++i) f[i] = make_float2(lo_of(words[i]), hi_of(words[i]));
   }
 }
-// n elements of the row are left from column c on.
-template <typename W, bool NARROW, int P>
-__device__ __forceinline__ void load_w(const void* w, unsigned c, int n, float none, float2 (&f)[P]) {
-  const W* p = static_cast<const W*>(w) + c;
-  if (!NARROW || !w || n <= 0 || (n >= 2 * P && (reinterpret_cast<uintptr_t>(w) & 15u) == 0)) {
-    load_whole_w<W, P>(p, w && n > 0, none, f);
-  } else {
+// A unit of gamma or beta: pair i begins at column c + i * 64 (NARROW) or c + 2 i
+// of the slice, which begins at column c0 and has `cols`.  `whole`, the same
+// for a warp: every lane's unit lies in the slice.
+template <typename T, typename W, bool NARROW, int P>
+__device__ __forceinline__ void load_w(const void* w, unsigned c0, int c, int cols, bool whole, float none, float2 (&f)[P]) {
+  const W* p = static_cast<const W*>(w) + c0 + c;
+  if constexpr (!NARROW) {
+    load_whole_w<W, P>(p, w && c < cols, none, f);
+  } else if (sizeof(T) == 2 && whole && w && (reinterpret_cast<uintptr_t>(w) & (2 * sizeof(W) - 1)) == 0) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      f[i].x = 2 * i < n ? to_f(p[2 * i]) : none;
-      f[i].y = 2 * i + 1 < n ? to_f(p[2 * i + 1]) : none;
+      if constexpr (sizeof(W) == 4) {
+        f[i] = *reinterpret_cast<const float2*>(p + 64 * i);
+      } else {
+        const unsigned q = *reinterpret_cast<const unsigned*>(p + 64 * i);
+        f[i] = make_float2(lo_of(q), hi_of(q));
+      }
+    }
+  } else {
+    constexpr int kNext = kApart<T, NARROW>;
+    const int n = w ? cols - c : 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f[i].x = 64 * i < n ? to_f(p[64 * i]) : none;
+      f[i].y = 64 * i + kNext < n ? to_f(p[64 * i + kNext]) : none;
     }
   }
 }
@@ -188,31 +206,24 @@ __device__ __forceinline__ float row_sums(float (&v)[N], SumWords<N>& w, int buf
 __device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
-// a word: its first `bytes` bytes, zeros after
-__device__ __forceinline__ void copy_async4(unsigned smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void copy_async4(unsigned smem, const void* gmem, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+// the first `bytes` bytes, zeros after
+__device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest n groups of this thread's copies have landed
 __device__ __forceinline__ void wait_groups(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
+  if (n == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
-constexpr int kMaxStages = 8;
+// One turn's rows are in work, the next ones' on their way.  (More would be
+// filled before the first turn: 60000 x 304 bf16 31.9 us, 33.1 with up to 8.)
+constexpr int kMaxStages = 2;
 
 // A row (one CTA's slice of it) in shared memory: each warp's 32 NV units side
-// by side, and 16 bytes more where a row may begin within a word.
+// by side, and one more where a row may begin within one.
 template <typename T, bool NARROW, int NV>
 constexpr unsigned kWarpBytes = 32 * NV * 16 + (NARROW ? 16 : 0);
 template <typename T, bool NARROW, int NV>
@@ -223,27 +234,20 @@ __host__ __device__ constexpr unsigned row_bytes(unsigned threads) { return (thr
 // distance between a thread's units is the same for every row length.  Past a
 // row's end there are zeros, where no copy ever writes.
 //
-// Else (NARROW): the row's words, the first of which begins 2 bytes before it where a
-// row of bf16 lies so; a warp takes one word more than its units have, and
-// words behind the row are cleared up to what the other phase would touch.
+// NARROW: the 16-byte pieces of memory that hold the warp's columns, from the
+// one on which its first lies, and zeros from the row's end to the end of the
+// units that are read.  The bytes of the first piece before the row are copied
+// and not used; the matrix's first row has none.
 template <int NV>
 __device__ __forceinline__ int first_unit(int tid) {
   return (tid & ~31) * NV + (tid & 31);
 }
-
-// f(j) for the words j < n of a warp, n <= 32 COUNT: unrolled, unless the warp
-// has few.
-template <int COUNT, typename F>
-__device__ __forceinline__ void for_words(int n, int lane, F f) {
-  if (n >= 16 * COUNT) {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      if (lane + 32 * i < n) f(lane + 32 * i);
-    }
-  } else {
-#pragma unroll 1
-    for (int j = lane; j < n; j += 32) f(j);
-  }
+// The first column of a thread's pair i of unit k.
+template <typename T, bool NARROW, int E>
+__device__ __forceinline__ int column(int tid, int k, int i) {
+  constexpr int V = kUnit<T>;
+  if (!NARROW) return (first_unit<E / V>(tid) + 32 * k) * V + 2 * i;
+  return (tid & ~31) * E + (k * V / 2 + i) * 64 + (tid & 31) * (sizeof(T) == 2 ? 2 : 1);
 }
 
 template <typename T, bool NARROW, int NV>
@@ -256,30 +260,36 @@ __device__ __forceinline__ void fetch_row(const T* row, int cols, const T* matri
       if (c < cols) copy_async16(smem + (lane + 32 * k) * 16, row + c);
     }
   } else {
-    constexpr int kWords = 4 * NV;                       // of a lane
-    const int phase = sizeof(T) == 2 ? (int)(reinterpret_cast<uintptr_t>(row) & 2u) : 0;
-    const int first = (tid >> 5) * 32 * kWords;          // the warp's first word
-    const int bytes = phase + cols * (int)sizeof(T) - 4 * first;   // of the row, from there
-    const char* from = reinterpret_cast<const char*>(row) - phase + 4 * first;
-    const bool before = from < reinterpret_cast<const char*>(matrix);   // the half word before the row is not the matrix's
-    if (bytes >= 128 * kWords + 4 && !before) {          // all its words and one more are the row's
+    const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15u), first = (tid & ~31) * NV * 16;
+    const char* from = reinterpret_cast<const char*>(row) - shift + first;
+    const int bytes = shift + cols * (int)sizeof(T) - first;   // of the row, from there
+    if (bytes <= shift) return;
+    const bool before = from < reinterpret_cast<const char*>(matrix);
+    if (bytes >= 32 * NV * 16 + 16 && !before) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) copy_async4(smem + 4 * lane + 128 * i, from + 4 * lane + 128 * i);
-      if (sizeof(T) == 2 && lane == 0) copy_async4(smem + 128 * kWords, from + 128 * kWords);
+      for (int k = 0; k < NV; ++k) copy_async16(smem + (lane + 32 * k) * 16, from + (lane + 32 * k) * 16);
+      if (lane == 0) copy_async16(smem + 32 * NV * 16, from + 32 * NV * 16);
       return;
     }
-    const int full = min(max(bytes, 0) >> 2, 32 * kWords);   // words that are the row's
-    for_words<kWords>(full, lane, [&](int j) {
-      if (j > 0 || !before) copy_async4(smem + 4 * j, from + 4 * j);
-    });
-    // the words at the row's end, for either phase: at most three
-    const char* nothing = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(matrix) & ~(uintptr_t)3);   // of which 0 bytes are read
-    const int most = min((cols * (int)sizeof(T) + (sizeof(T) == 2 ? 5 : 3)) / 4 - first, 32 * kWords + (sizeof(T) == 2 ? 1 : 0));
-    const int j = full + lane;
-    if (lane < 3 && j < most && (j > 0 || !before))
-      copy_async4(smem + 4 * j, 4 * j < bytes ? from + 4 * j : nothing, min(max(bytes - 4 * j, 0), 4));
-    if (lane == 0 && before)
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem), "r"((unsigned)*reinterpret_cast<const unsigned short*>(row) << 16) : "memory");
+#pragma unroll
+    for (int k = 0; k <= NV; ++k) {
+      const int at = (lane + 32 * k) * 16;
+      // a unit that is read, or the piece behind the last of them
+      if (k == NV || 32 * k * 16 >= bytes - shift) {
+        if (lane == 0) copy_async16(smem + at, from + min(at, (bytes - 1) & ~15), min(max(bytes - at, 0), 16));
+        break;
+      }
+      if (k > 0 || lane > 0 || !before) copy_async16(smem + at, from + min(at, (bytes - 1) & ~15), min(max(bytes - at, 0), 16));
+    }
+    if (lane == 0 && before) {
+      for (int j = 0; j < 16 / (int)sizeof(T); ++j) {
+        const int c = j - shift / (int)sizeof(T);
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem + 4 * j), "r"(c >= 0 && c < cols ? reinterpret_cast<const unsigned*>(row)[c] : 0u) : "memory");
+        else
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(smem + 2 * j), "h"(c >= 0 && c < cols ? reinterpret_cast<const unsigned short*>(row)[c] : (unsigned short)0) : "memory");
+      }
+    }
   }
 }
 
@@ -299,66 +309,105 @@ __device__ __forceinline__ unsigned load_shared4(unsigned a) {
 // A row in shared memory, as a warp reads it.
 template <typename T, bool NARROW>
 struct Landed {
-  unsigned at;       // the warp's units
+  unsigned at;       // the lane's unit, or (NARROW) the word with its first column
   unsigned select;   // which halves of two words are a pair
 
-  __device__ __forceinline__ Landed(unsigned smem, const T* row) : at(smem), select(reinterpret_cast<uintptr_t>(row) & 2u ? 0x5432u : 0x3210u) {}
-  __device__ __forceinline__ bool even() const { return !NARROW || sizeof(T) == 4 || select == 0x3210u; }
-  // the unit at place u among the warp's
-  __device__ __forceinline__ uint4 raw(int u) const {
-    uint4 q = load_shared16(at + 16 * u);
-    if constexpr (NARROW && sizeof(T) == 2) {
-      const unsigned more = load_shared4(at + 16 * u + 16);
-      q = make_uint4(__byte_perm(q.x, q.y, select), __byte_perm(q.y, q.z, select), __byte_perm(q.z, q.w, select),
-                     __byte_perm(q.w, more, select));
-    }
-    return q;
+  __device__ __forceinline__ Landed(unsigned smem, const T* row, int lane) {
+    const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);
+    at = NARROW ? smem + (shift & ~3u) + 4 * lane : smem + 16 * lane;
+    select = shift & 2u ? 0x5432u : 0x3210u;
   }
-  __device__ __forceinline__ void read(int u, float2 (&f)[kUnit<T> / 2]) const { unpack16<T, kUnit<T> / 2>(raw(u), f); }
+  // the lane's unit k
+  __device__ __forceinline__ uint4 raw(int k) const {
+    if constexpr (!NARROW) {
+      return load_shared16(at + 512 * k);
+    } else {
+      unsigned w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = load_shared4(at + 512 * k + 128 * i);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], load_shared4(at + 512 * k + 128 * i + 4), select);
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void read(int k, float2 (&f)[kUnit<T> / 2]) const { unpack16<T, kUnit<T> / 2>(raw(k), f); }
 };
 
-// Clears what no copy will ever write.
-template <typename T, bool NARROW, int NV>
+// Clears what no copy will ever write (not NARROW).
+template <typename T, int NV>
 __device__ __forceinline__ void clear_rows(unsigned smem, unsigned row_len, int nrows, int cols, int tid) {
   const int lane = tid & 31;
-  if (NARROW && ((tid >> 5) + 1) * 32 * NV * kUnit<T> + 2 <= cols) return;   // every word of the warp's is the row's
   for (int r = 0; r < nrows; ++r, smem += row_len) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (NARROW || (first_unit<NV>(tid) + 32 * k) * kUnit<T> >= cols)
+      if ((first_unit<NV>(tid) + 32 * k) * kUnit<T> >= cols)
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + (lane + 32 * k) * 16), "r"(0) : "memory");
     }
-    if (NARROW && lane == 0) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + 32 * NV * 16), "r"(0) : "memory");
   }
-  if (NARROW) __syncwarp();
 }
 
-// A warp's part of an output row (NARROW): its units go to shared memory (the
-// lanes' stores, then __syncwarp), and from there in words to global memory;
-// n elements from `out` on.  Reading the words again needs no unit.
-template <typename T, int NV>
-__device__ __forceinline__ void store_words(T* out, int n, unsigned smem, int lane) {
-  constexpr int kWords = 4 * NV, kAll = 32 * NV * kUnit<T>;
-  n = min(n, kAll);
-  if constexpr (sizeof(T) == 4) {
-    for_words<kWords>(n, lane, [&](int j) { reinterpret_cast<unsigned*>(out)[j] = load_shared4(smem + 4 * j); });
-  } else {
-    unsigned short* o = reinterpret_cast<unsigned short*>(out);
-    if ((reinterpret_cast<uintptr_t>(out) & 2u) == 0) {
-      for_words<kWords>(n >> 1, lane, [&](int j) { reinterpret_cast<unsigned*>(o)[j] = load_shared4(smem + 4 * j); });
-      if (lane == 0 && (n & 1) && n > 0) o[n - 1] = (unsigned short)load_shared4(smem + 2 * (n - 1));
-    } else {   // words begin at element 1
-      for_words<kWords>((n - 1) >> 1, lane, [&](int j) {
-        reinterpret_cast<unsigned*>(o + 1)[j] = __byte_perm(load_shared4(smem + 4 * j), load_shared4(smem + 4 * j + 4), 0x5432);
-      });
-      if (lane == 0 && n > 0) o[0] = (unsigned short)load_shared4(smem);
-      if (lane == 1 && !(n & 1) && n > 0) o[n - 1] = (unsigned short)(load_shared4(smem + 2 * (n - 2)) >> 16);
+// A warp's part of an output row (NARROW), unit by unit in their order, in
+// words: where they begin at odd columns, a lane's word has the second half
+// of the pair before its own.  n columns are left at the warp's first, `out`.
+template <typename T, int E>
+struct Written {
+  T* out;
+  int n, lane;
+  unsigned last;   // lane 0: the last lane's pair of the 64 columns before
+
+  __device__ __forceinline__ Written(T* row, int cols, int tid) : out(row + (tid & ~31) * E), n(cols - (tid & ~31) * E), lane(tid & 31), last(0) {}
+  __device__ __forceinline__ void put(int k, const float2 (&f)[kUnit<T> / 2]) {
+    if (32 * kUnit<T> * (k + 1) <= n)
+      put_unit<true>(k, f);
+    else
+      put_unit<false>(k, f);
+  }
+  template <bool whole>
+  __device__ __forceinline__ void put_unit(int k, const float2 (&f)[kUnit<T> / 2]) {
+    constexpr int P = kUnit<T> / 2;
+    const int at = 64 * P * k;
+    if constexpr (sizeof(T) == 4) {
+      float* o = out + at + lane;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (whole || at + 64 * i + lane < n) o[64 * i] = f[i].x;
+        if (whole || at + 64 * i + 32 + lane < n) o[64 * i + 32] = f[i].y;
+      }
+    } else {
+      unsigned short* o = reinterpret_cast<unsigned short*>(out) + at + 2 * lane;
+      const int mine = n - at - 2 * lane;   // columns from this lane's first on
+      if ((reinterpret_cast<uintptr_t>(out) & 2u) == 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const unsigned w = pack2(f[i]);
+          if (whole || 64 * i + 1 < mine)
+            *reinterpret_cast<unsigned*>(o + 64 * i) = w;
+          else if (64 * i < mine)
+            o[64 * i] = (unsigned short)w;
+        }
+      } else {
+        unsigned w = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          w = pack2(f[i]);
+          const unsigned left = __shfl_sync(0xffffffffu, w, (lane + 31) & 31);
+          const unsigned word = __byte_perm(lane ? left : last, w, 0x5432);
+          last = left;
+          if (i == 0 && k == 0 && lane == 0) {
+            if (whole || n > 0) o[0] = (unsigned short)w;
+          } else if (whole || 64 * i < mine) {
+            *reinterpret_cast<unsigned*>(o + 64 * i - 1) = word;
+          }
+          if (!whole && 64 * i + 2 == mine) o[64 * i + 1] = (unsigned short)(w >> 16);   // the row's last column
+        }
+        // the warp's last column, or the row's
+        if (whole && lane == 31 && (k == E / (2 * P) - 1 || at + 64 * P == n)) o[64 * P - 63] = (unsigned short)(w >> 16);
+      }
     }
   }
-}
-__device__ __forceinline__ void store_shared16(unsigned a, uint4 q) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
-}
+};
 
 // ---------------------------------------------------------------- forward
 
@@ -378,6 +427,8 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
   constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
   const int threads = MODE == kWarp ? 32 : blockDim.x;
   const int tid = MODE == kWarp ? threadIdx.x & 31 : threadIdx.x, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
+  const int w0 = (tid & ~31) * E;   // the warp's first column
+  constexpr bool kSkip = NARROW || E > 32;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
   const u64 row = R * (MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x / csize);
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
@@ -387,7 +438,6 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
   constexpr unsigned kRow = kWarpBytes<T, NARROW, NV>;
   const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + (threadIdx.x >> 5) * R * kRow;   // [warp][r]
   if (MODE == kCluster) cluster_arrive();   // its end: every CTA of the cluster runs
-  if constexpr (NARROW) clear_rows<T, NARROW, NV>(slot, kRow, R, cols, tid);
   wait_for_predecessors();
   let_successor_start();
   if (MODE == kWarp && left == 0) return;
@@ -412,14 +462,9 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const Landed<T, NARROW> here(slot + r * kRow, x + r * prm.x_stride);
-      if (here.even()) {
+      const Landed<T, NARROW> here(slot + r * kRow, x + r * prm.x_stride, lane);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) q[r][k] = load_shared16(here.at + (lane + 32 * k) * 16);
-      } else {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) q[r][k] = here.raw(lane + 32 * k);
-      }
+      for (int k = 0; k < NV; ++k) q[r][k] = r < left && w0 + 32 * k * V < cols ? here.raw(k) : make_uint4(0, 0, 0, 0);
     }
   }
   float v[R];
@@ -428,6 +473,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      if (kSkip && w0 + 32 * k * V >= cols) break;   // nothing there for this warp
       float2 f[P];
       unpack16<T, P>(q[r][k], f);
 #pragma unroll
@@ -444,14 +490,23 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int n = cols - (u0 + 32 * k) * V;   // whole or absent, unless NARROW
+      if (kSkip && w0 + 32 * k * V >= cols) break;
       float2 f[P];
       unpack16<T, P>(q[r][k], f);
+      if (NARROW && w0 + 32 * (k + 1) * V > cols) {
+        const int n = cols - column<T, NARROW, E>(tid, k, 0);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float2 m = make_float2(n > (NARROW ? 2 * i : 0) ? -mean : 0.f, n > (NARROW ? 2 * i + 1 : 0) ? -mean : 0.f);
-        const float2 d = __fadd2_rn(f[i], m);
-        sq = __ffma2_rn(d, d, sq);
+        for (int i = 0; i < P; ++i) {
+          const float2 d = __fadd2_rn(f[i], make_float2(n > 64 * i ? -mean : 0.f, n > 64 * i + kApart<T, NARROW> ? -mean : 0.f));
+          sq = __ffma2_rn(d, d, sq);
+        }
+      } else {
+        const float2 m = both(NARROW || (u0 + 32 * k) * V < cols ? -mean : 0.f);   // a unit is whole or absent
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 d = __fadd2_rn(f[i], m);
+          sq = __ffma2_rn(d, d, sq);
+        }
       }
     }
     v[r] = sq.x + sq.y;
@@ -462,15 +517,17 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     if (prm.rstd) prm.rstd[row + tid] = rstds;
   }
   T* y = static_cast<T*>(prm.out) + row * prm.out_stride + c0;
-  if constexpr (NARROW) __syncwarp();   // every lane has read the rows: their places take the output
   auto output = [&](auto w) {
     typedef decltype(w) W;
+    [[maybe_unused]] unsigned last[R] = {};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (u0 + 32 * k) * V;
+      const int c = column<T, NARROW, E>(tid, k, 0);
+      if (kSkip && w0 + 32 * k * V >= cols) break;
+      const bool whole = w0 + 32 * (k + 1) * V <= cols;
       float2 g[P], b[P];
-      load_w<W, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, g);
-      load_w<W, NARROW, P>(prm.beta, c0 + c, cols - c, 0.f, b);
+      load_w<T, W, NARROW, P>(prm.gamma, c0, c, cols, whole, 1.f, g);
+      load_w<T, W, NARROW, P>(prm.beta, c0, c, cols, whole, 0.f, b);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float2 mean = both(-(R > 1 ? __shfl_sync(0xffffffffu, means, r) : means)), rstd = both(R > 1 ? __shfl_sync(0xffffffffu, rstds, r) : rstds);
@@ -479,7 +536,10 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
 #pragma unroll
         for (int i = 0; i < P; ++i) o[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(o[i], mean), rstd), g[i], b[i]);
         if constexpr (NARROW) {
-          store_shared16(slot + r * kRow + (lane + 32 * k) * 16, pack16<T, P>(o));
+          Written<T, E> to(y + r * prm.out_stride, r < left ? cols : 0, tid);
+          to.last = last[r];
+          to.put(k, o);
+          last[r] = to.last;
         } else {
           if (r < left && c < cols) *reinterpret_cast<uint4*>(y + r * prm.out_stride + c) = pack16<T, P>(o);
         }
@@ -490,13 +550,6 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     output(bf16());
   else
     output(float());
-  if constexpr (NARROW) {
-    __syncwarp();
-    const int c = (tid & ~31) * E;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < left) store_words<T, NV>(y + r * prm.out_stride + c, cols - c, slot + r * kRow, lane);
-  }
 }
 
 // ---------------------------------------------------------------- backward
@@ -526,13 +579,12 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   const int cols = c0 < prm.cols ? (int)min(width, prm.cols - c0) : 0;   // a cluster's last CTA may have none
   const float inv = 1.0f / (float)prm.cols;
   const int stages = prm.stages;
-  // shared memory: [group][stage][r][x, dy][warp], then (NARROW) a row's part per warp for the output, or gamma
+  // shared memory: [group][stage][r][x, dy][warp], then gamma
   const unsigned len = row_bytes<T, NARROW, NV>(threads);
   const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + group * stages * R * 2 * len + (tid >> 5) * kWarpBytes<T, NARROW, NV>;
-  const unsigned s_out = (unsigned)__cvta_generic_to_shared(s_dyn) + groups * stages * R * 2 * len + (threadIdx.x >> 5) * kWarpBytes<T, NARROW, NV>;
   const int rows = (int)prm.rows, step = (int)prm.nparts * groups * R;
   const int first = ((int)part * groups + group) * R;
-  clear_rows<T, NARROW, NV>(slot, len, stages * R * 2, cols, tid);
+  if constexpr (!NARROW) clear_rows<T, NV>(slot, len, stages * R * 2, cols, tid);
   wait_for_predecessors();
 
   // The row in work; what a turn is further in each matrix.
@@ -556,23 +608,22 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
 
   float2 dg[NV][P], db[NV][P];
   float2 gam[kKeepGamma ? NV : 1][P];
-  float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len +
-                                          (NARROW ? (blockDim.x >> 5) * kWarpBytes<T, NARROW, NV> : 0)) + group * width;
+  float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len) + group * width;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (u0 + 32 * k) * V;
+    const int c = column<T, NARROW, E>(tid, k, 0);
     float2 w[P];
     if (prm.gamma_bf16)
-      load_w<bf16, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<T, bf16, NARROW, P>(prm.gamma, c0, c, cols, false, 1.f, w);
     else
-      load_w<float, NARROW, P>(prm.gamma, c0 + c, cols - c, 1.f, w);
+      load_w<T, float, NARROW, P>(prm.gamma, c0, c, cols, false, 1.f, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       dg[k][i] = db[k][i] = make_float2(0.f, 0.f);
       if constexpr (kKeepGamma)
         gam[k][i] = w[i];
       else
-        reinterpret_cast<float2*>(s_gam + c)[i] = w[i];   // read back by this thread alone
+        reinterpret_cast<float2*>(s_gam + (u0 + 32 * k) * V)[i] = w[i];   // read back by this thread alone
     }
   }
   auto gammas = [&](int k, float2 (&w)[P]) {
@@ -616,13 +667,13 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       float2 sa = make_float2(0.f, 0.f), sd = sa;
       if (r < left) {
         const float2 mean = both(-__shfl_sync(0xffffffffu, means, r)), rstd = both(__shfl_sync(0xffffffffu, rstds, r));
-        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
+        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           if (NARROW && (u0 - lane + 32 * k) * V >= cols) continue;   // nothing there for this warp
           float2 fx[P], fd[P], w[P];
-          hx.read(lane + 32 * k, fx);
-          hd.read(lane + 32 * k, fd);
+          hx.read(k, fx);
+          hd.read(k, fd);
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i) {   // dy is 0 past the row's end
@@ -645,30 +696,25 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       if (r < left) {
         const float mean = __shfl_sync(0xffffffffu, means, r), rstd = __shfl_sync(0xffffffffu, rstds, r);
         const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1);
-        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride);
+        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
         const float2 k1 = both(-rstd * sum_a), k2 = both(-rstd * rstd * rstd * sum_ad);
+        Written<T, E> to(out, cols, tid);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           if (NARROW && (u0 - lane + 32 * k) * V >= cols) continue;
           float2 fx[P], fd[P], w[P];
-          hx.read(lane + 32 * k, fx);
-          hd.read(lane + 32 * k, fd);
+          hx.read(k, fx);
+          hd.read(k, fd);
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i)
             fd[i] = __ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(__fmul2_rn(fd[i], w[i]), both(rstd), k1));
           const int c = (u0 + 32 * k) * V;
           if constexpr (NARROW) {
-            store_shared16(s_out + (lane + 32 * k) * 16, pack16<T, P>(fd));
+            to.put(k, fd);
           } else {
             if (c < cols) *reinterpret_cast<uint4*>(out + c) = pack16<T, P>(fd);
           }
-        }
-        if constexpr (NARROW) {
-          __syncwarp();
-          const int c = (tid & ~31) * E;
-          store_words<T, NV>(out + c, cols - c, s_out, lane);
-          __syncwarp();   // before the next row's units
         }
       }
     }
@@ -693,10 +739,19 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          float2* a = reinterpret_cast<float2*>(acc + (u0 + 32 * k) * V) + i;
-          float2* b = reinterpret_cast<float2*>(acc + width + (u0 + 32 * k) * V) + i;
-          *a = g ? __fadd2_rn(*a, dg[k][i]) : dg[k][i];
-          *b = g ? __fadd2_rn(*b, db[k][i]) : db[k][i];
+          float* a = acc + column<T, NARROW, E>(tid, k, i);
+          float* b = a + width;
+          if constexpr (kApart<T, NARROW> == 1) {
+            float2* a2 = reinterpret_cast<float2*>(a);
+            float2* b2 = reinterpret_cast<float2*>(b);
+            *a2 = g ? __fadd2_rn(*a2, dg[k][i]) : dg[k][i];
+            *b2 = g ? __fadd2_rn(*b2, db[k][i]) : db[k][i];
+          } else {
+            a[0] = g ? a[0] + dg[k][i].x : dg[k][i].x;
+            a[32] = g ? a[32] + dg[k][i].y : dg[k][i].y;
+            b[0] = g ? b[0] + db[k][i].x : db[k][i].x;
+            b[32] = g ? b[32] + db[k][i].y : db[k][i].y;
+          }
         }
       }
     }
@@ -720,10 +775,11 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (c + i < cols) {
+          const int at = column<T, NARROW, E>(tid, k, i / 2) + (i & 1) * kApart<T, NARROW>;
+          if (at < cols) {
             const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
-            out_g[c + i] = add ? out_g[c + i] + vg : vg;
-            out_b[c + i] = add ? out_b[c + i] + vb : vb;
+            out_g[at] = add ? out_g[at] + vg : vg;
+            out_b[at] = add ? out_b[at] + vb : vb;
           }
         }
       }
@@ -833,10 +889,14 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 
 // A thread takes 32 elements, which keeps a CTA small; with rows too few to
 // fill the GPU it takes 8, and more threads share a row.  bf16 take half the
-// registers, so a thread may have 64: in rows up to 1536 columns, which then
-// are one warp's (60000 x 1056: 54 us, 66 with two warps; beyond, 32 are as
-// fast or faster), and beyond 16384 columns (4000 x 20000: 67 us, 90 with 32;
-// 2000 x 40032: 87 us, 125 in a cluster of 3).
+// registers, so a thread may have 64: in rows up to 1792 columns, which then
+// are one warp's (40000 x 1704: 53 us, 63 with two warps of 32; 30000 x 2016: 42 and
+// 41), and beyond 16384 columns (4000 x 20000: 58 us, 90 with 32; 2000 x 40032:
+// 86 us, 125 in a cluster of 3).  Such a warp skips the units of which it has
+// no column (60000 x 1056: 46 us, 54 without); with 32 that cost more than it
+// gave (8000 x 8160: 48 us, 46 without).
+//   Rows in NARROW's layout: 60000 x 1031 71 us (aligned 1056: 46; 107 when the row
+// moved in 4-byte words and was units in shared memory), 20046 x 3877 75.
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
   if (p.cols <= 256) {
@@ -855,8 +915,8 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
   if (few) return forward_e<T, NARROW, 8, 1, kCta, 512>(p, threads_for(slice, 8), 1, st);
   if (p.cols <= 512) return forward_e<T, NARROW, 16, 1, kWarp, 128>(p, 32, 1, st);
   if (p.cols <= 1024) return forward_e<T, NARROW, 32, 1, kWarp, 128>(p, 32, 1, st);
-  if constexpr (sizeof(T) == 2 && !NARROW) {
-    if (p.cols <= 1536) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
+  if constexpr (sizeof(T) == 2) {
+    if (p.cols <= 1792) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
   }
   if (p.cols <= 16384) return forward_e<T, NARROW, 32, 1, kCta, 512>(p, threads_for(slice, 32), 1, st);
   return forward_e<T, NARROW, sizeof(T) == 2 ? 64 : 32, 1, kCta, 1024>(p, threads_for(slice, sizeof(T) == 2 ? 64 : 32), 1, st);
@@ -869,8 +929,10 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 // side as it has room for, and leaves one partial sum per column; rows beyond
 // 8192 columns are split over a cluster, and beyond 65536 a thread has 32.
 //   Measured at 24576 x 5120 bf16 (755 MB), the kernel without the parts' sum:
-//   120 us, 6.3 TB/s; 2 rows a turn 128, 1 row 136; 8 columns per thread, 640
-//   threads and 4 rows 133; 24 columns, 224 threads and 1 row 175.
+//   118 us, 6.4 TB/s; 2 rows a turn 128, 1 row 136; 8 columns per thread, 640
+//   threads and 4 rows 133; 24 columns, 224 threads and 1 row 175.  In
+//   NARROW's layout 9973 x 1031 takes 29 us with 2 rows, 32 with 4 (the code
+//   of a turn outgrows the instruction cache) and 35 with 1.
 int resident_clusters(int csize);
 struct BackwardShape {
   int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, NARROW: 2), else 1
@@ -926,7 +988,7 @@ cudaError_t backward_e(NormRowsParams& p, const BackwardShape& s, cudaStream_t s
   p.nparts = s.nparts;
   constexpr int NV = E / kUnit<T>;
   const size_t stage = (size_t)s.groups * R * 2 * row_bytes<T, NARROW, NV>(s.threads);
-  const size_t rest = (NARROW ? (size_t)row_bytes<T, NARROW, NV>(s.groups * s.threads) : 0) + (E > 16 ? (size_t)s.groups * E * s.threads * 4 : 0);
+  const size_t rest = (E > 16 ? (size_t)s.groups * E * s.threads * 4 : 0);
   const size_t acc = s.groups > 1 ? (size_t)2 * E * s.threads * 4 : 0;
   p.stages = stages_for(kSmemSm - 4096 - rest, stage, div_up(p.rows, (u64)s.nparts * s.groups * R));
   size_t smem = stage * p.stages + rest;
@@ -939,7 +1001,7 @@ cudaError_t backward_e(NormRowsParams& p, const BackwardShape& s, cudaStream_t s
 template <typename T, bool NARROW, int E, int MODE>
 cudaError_t backward_r(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
   const size_t row = (size_t)s.groups * 2 * row_bytes<T, NARROW, E / kUnit<T>>(s.threads);
-  const size_t fit = (kSmemSm - 4096 - (NARROW ? row / 2 : 0)) / ((MODE == kCluster ? 1 : 2) * row);
+  const size_t fit = (kSmemSm - 4096) / ((MODE == kCluster ? 1 : 2) * row);
   if constexpr (!NARROW && sizeof(T) == 2) {
     if (s.many && fit >= 4) return backward_e<T, NARROW, E, 4, MODE>(p, s, st);
   }

@@ -176,6 +176,40 @@ def test_backward_strides_and_alignment(xt, rows, cols, pad, offset):
         _check_backward(torch, xt, rows, cols, name, "f32", pad, offset)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(40, 1), (5000, 95), (37, 257), (300, 601), (40, 1031), (700, 1505), (330, 1793), (9, 4097), (3, 9001), (2, 40001)])
+def test_each_tensor_has_its_own_alignment(xt, rows, cols, name):
+    """Rows of odd lengths: where each matrix and the weights begin, and how far apart their rows are, changes no bit."""
+    torch = torch_cuda()
+    dtype, _ = _types(torch, name)
+    rng = np.random.default_rng(rows + cols)
+    x, dy = rng.standard_normal((rows, cols)), rng.standard_normal((rows, cols))
+    weights = [torch.from_numpy(rng.standard_normal(cols)).to(t) for t in (torch.float32, torch.bfloat16)]
+    work = torch.empty(xt.xp_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    first = {}
+    for turn in range(9):
+        place = rng.integers(0, 9, (4, 2)) if turn else np.zeros((4, 2), int)
+        xm, dm = _matrix(torch, x, dtype, *map(int, place[0])), _matrix(torch, dy, dtype, *map(int, place[1]))
+        y, dx = (_matrix(torch, np.zeros((rows, cols)), dtype, *map(int, place[k])) for k in (2, 3))
+        for which, w in enumerate(weights):
+            buf = torch.full((cols + 40,), float("nan"), dtype=w.dtype, device="cuda")
+            gamma = buf[turn % 5:turn % 5 + cols]
+            gamma.copy_(w)
+            mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+            dgamma, dbeta = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+            xt.xp_layernorm_forward(xm, gamma, gamma, y, mean, rstd, 1e-5)
+            xt.xp_layernorm_backward(dm, xm, gamma, mean, rstd, dx, dgamma, dbeta, work)
+            got = [t.clone() for t in (y, mean, rstd, dx, dgamma, dbeta)]
+            assert all(torch.isfinite(t).all() for t in got)
+            for a, b in zip(got, first.setdefault(which, got)):
+                assert torch.equal(a, b), (turn, which, place.tolist())
+            for m, (pad, offset) in ((y, place[2]), (dx, place[3])):   # and nothing around the rows is written
+                flat = m._base.flatten()
+                assert torch.isnan(flat[:offset]).all() and torch.isnan(flat[offset + rows * (cols + pad):]).all()
+                if pad:
+                    assert torch.isnan(flat[offset:offset + rows * (cols + pad)].view(rows, -1)[:, cols:]).all()
+
+
 @pytest.mark.parametrize("rows,cols", [(20000, 48), (5000, 1000), (1000, 6000)])
 def test_backward_many_rows(xt, rows, cols):
     torch = torch_cuda()
