@@ -64,9 +64,27 @@ __device__ __forceinline__ uint4 pack16(const float2 (&f)[P]) {
 // none.  No branches: the loads of several units are in flight together.
 // (Plain loads, here and of the statistics: a load that may assume read-only
 // memory could be moved before the wait for the kernel that writes it.)
+// Eight floats are one load of 32 bytes where they are aligned for it: in two of
+// 16 a warp takes every other piece of its lines, twice the L1 cycles (16384 x
+// 4096 bf16 with fp32 weights: 48.4 us, 57.6 by two loads).
 template <typename W, int P>
 __device__ __forceinline__ void load_whole_w(const W* p, bool has, float none, float2 (&f)[P]) {
-  if constexpr (sizeof(W) == 4) {
+  if constexpr (sizeof(W) == 4 && P == 4) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = none;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %9, 0;\nsetp.ne.u32 q, %10, 0;\n"
+        "@p ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+        "@q ld.global.v4.f32 {%0, %1, %2, %3}, [%8];\n"
+        "@q ld.global.v4.f32 {%4, %5, %6, %7}, [%8 + 16];\n}"
+        : "+f"(e[0]), "+f"(e[1]), "+f"(e[2]), "+f"(e[3]), "+f"(e[4]), "+f"(e[5]), "+f"(e[6]), "+f"(e[7])
+        : "l"(p), "r"((unsigned)(has && aligned)), "r"((unsigned)(has && !aligned))
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(e[2 * i], e[2 * i + 1]);
+  } else if constexpr (sizeof(W) == 4) {
     const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
@@ -890,11 +908,15 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 // A thread takes 32 elements, which keeps a CTA small; with rows too few to
 // fill the GPU it takes 8, and more threads share a row.  bf16 take half the
 // registers, so a thread may have 64: in rows up to 1792 columns, which then
-// are one warp's (40000 x 1704: 53 us, 63 with two warps of 32; 30000 x 2016: 42 and
-// 41), and beyond 16384 columns (4000 x 20000: 58 us, 90 with 32; 2000 x 40032:
-// 86 us, 125 in a cluster of 3).  Such a warp skips the units of which it has
-// no column (60000 x 1056: 46 us, 54 without); with 32 that cost more than it
-// gave (8000 x 8160: 48 us, 46 without).
+// are one warp's (40000 x 1704: 45 us, 49 with two warps of 32; 30000 x 2016: 42 and
+// 41), and beyond 4096, where fewer warps hold the SM's place for a row (12000 columns:
+// 50 us, 63 with 32; 8192: 45 and 46; 4000 x 20000: 58 and 90; 4096 itself 46.5
+// and 45) unless the rows are few (310 x 8193: 8.5 us, 6.8 with 32).  40 where that makes
+// two or four full warps of what were three or five (30000 x 2400: 50 us, 56 with 32;
+// 13000 x 5120: 45, 46 with 64).  Warps of 40 and 64 skip the units of which
+// they have no column (60000 x 1056: 46 us, 54 without); with 32 that cost more
+// than it gave (8000 x 8160: 48 us, 46 without).  2000 x 40032 takes 86 us (125
+// in a cluster of 3).
 //   Rows in NARROW's layout: 60000 x 1031 71 us (aligned 1056: 46; 107 when the row
 // moved in 4-byte words and was units in shared memory), 20046 x 3877 75.
 template <typename T, bool NARROW>
@@ -917,6 +939,9 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
   if (p.cols <= 1024) return forward_e<T, NARROW, 32, 1, kWarp, 128>(p, 32, 1, st);
   if constexpr (sizeof(T) == 2) {
     if (p.cols <= 1792) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
+    if (p.cols > 2048 && p.cols <= 2 * 32 * 40) return forward_e<T, NARROW, 40, 1, kCta, 512>(p, 64, 1, st);
+    if (p.cols > 4096 && p.cols <= 4 * 32 * 40) return forward_e<T, NARROW, 40, 1, kCta, 512>(p, 128, 1, st);
+    if (p.cols > 4096 && p.cols <= 16384 && p.rows >= 4 * (size_t)sm_count()) return forward_e<T, NARROW, 64, 1, kCta, 512>(p, threads_for(slice, 64), 1, st);
   }
   if (p.cols <= 16384) return forward_e<T, NARROW, 32, 1, kCta, 512>(p, threads_for(slice, 32), 1, st);
   return forward_e<T, NARROW, sizeof(T) == 2 ? 64 : 32, 1, kCta, 1024>(p, threads_for(slice, sizeof(T) == 2 ? 64 : 32), 1, st);

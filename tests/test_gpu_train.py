@@ -117,6 +117,27 @@ def test_forward_many_rows(xt, rows, cols, name):
     _check_forward(torch, xt, rows, cols, name, "f32")
 
 
+@pytest.mark.parametrize("rows,cols", [(620, 2056), (611, 2401), (620, 2560), (700, 1704), (650, 1792), (609, 4104), (613, 5119), (610, 5120), (615, 7000),
+                                       (608, 12001), (612, 16384), (607, 9000)])
+def test_forward_threads_of_40_and_64(xt, rows, cols):
+    torch = torch_cuda()
+    for wname in ("f32", "bf16"):
+        _check_forward(torch, xt, rows, cols, "bf16", wname)
+
+
+@pytest.mark.parametrize("cols", [64, 1024, 1704, 2400, 4096, 12000, 20000])
+def test_forward_weights_aligned_to_16_and_32_bytes(xt, cols):
+    torch = torch_cuda()
+    x, _, gamma, beta = _inputs(torch, 330, cols, torch.bfloat16, torch.float32)
+    got = []
+    for at in (0, 4, 8, 12):
+        g, b = (torch.full((cols + 16,), float("nan"), device="cuda")[at:at + cols].copy_(w) for w in (gamma, beta))
+        y = torch.zeros(330, cols, dtype=torch.bfloat16, device="cuda")
+        xt.xp_layernorm_forward(x, g, b, y)
+        got.append(y)
+    assert torch.isfinite(got[0]).all() and all(torch.equal(got[0], y) for y in got[1:])
+
+
 def test_forward_far_from_zero_and_large_eps(xt):
     torch = torch_cuda()
     _check_forward(torch, xt, 20, 1536, "f32", "f32", shift=30.0)
