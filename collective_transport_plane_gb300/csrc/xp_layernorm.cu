@@ -15,7 +15,10 @@ typedef __nv_bfloat16 bf16;
 typedef unsigned long long u64;
 
 // who shares a row
-enum { kWarp = 0, kCta = 1, kCluster = 2 };
+enum { kWarp = 0, kCta = 1, kCluster = 2, kHalf = 3 };   // kHalf: half a warp
+// A row's threads in one warp, side by side.
+template <int MODE>
+constexpr int kLanes = MODE == kHalf ? 16 : 32;
 constexpr int kMaxWarps = 32;
 constexpr int kMaxCluster8 = 8;
 
@@ -163,10 +166,10 @@ __host__ __device__ constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_
 // values and hands the other half to its partner, so N of them cost
 // N - 1 + 5 - log2 N shuffles and not 5 N.  Lane l ends with the warp's sum of
 // value l >> (5 - log2 N).
-template <int N>
+template <int N, int LANES>
 __device__ __forceinline__ float warp_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
-  int o = 16;
+  int o = LANES / 2;
 #pragma unroll
   for (int n = N / 2; n > 0; n /= 2, o /= 2) {
     const bool upper = lane & o;
@@ -197,8 +200,9 @@ template <int MODE, int N>
 __device__ __forceinline__ float row_sums(float (&v)[N], SumWords<N>& w, int buf, int group, int threads) {
   constexpr int L = log2_of(N);
   const int lane = threadIdx.x & 31;
-  float t = warp_sums<N>(v);
-  if constexpr (MODE == kWarp) return __shfl_sync(0xffffffffu, t, (lane & (N - 1)) << (5 - L));
+  float t = warp_sums<N, kLanes<MODE>>(v);
+  if constexpr (MODE == kWarp || MODE == kHalf)
+    return __shfl_sync(0xffffffffu, t, (lane & (N - 1)) << (log2_of(kLanes<MODE>) - L), kLanes<MODE>);
   if ((lane & ((32 >> L) - 1)) == 0) w.warp[buf][threadIdx.x >> 5][lane >> (5 - L)] = t;
   if constexpr (MODE == kCluster)
     __syncthreads();
@@ -245,7 +249,9 @@ constexpr int kMaxStages = 2;
 template <typename T, bool NARROW, int NV>
 constexpr unsigned kWarpBytes = 32 * NV * 16 + (NARROW ? 16 : 0);
 template <typename T, bool NARROW, int NV>
-__host__ __device__ constexpr unsigned row_bytes(unsigned threads) { return (threads >> 5) * kWarpBytes<T, NARROW, NV>; }
+__host__ __device__ constexpr unsigned row_bytes(unsigned threads) {
+  return threads == 16 ? 16 * NV * 16 : (threads >> 5) * kWarpBytes<T, NARROW, NV>;
+}
 
 // How a row of a matrix gets there: every warp copies the units it will use
 // itself.  Thread t's unit k is unit first_unit(t) + 32 k of the row, so the
@@ -256,26 +262,27 @@ __host__ __device__ constexpr unsigned row_bytes(unsigned threads) { return (thr
 // one on which its first lies, and zeros from the row's end to the end of the
 // units that are read.  The bytes of the first piece before the row are copied
 // and not used; the matrix's first row has none.
+// (kHalf: LANES = 16, and the half's units for the warp's.)
 template <int NV>
 __device__ __forceinline__ int first_unit(int tid) {
   return (tid & ~31) * NV + (tid & 31);
 }
 // The first column of a thread's pair i of unit k.
-template <typename T, bool NARROW, int E>
+template <typename T, bool NARROW, int E, int LANES = 32>
 __device__ __forceinline__ int column(int tid, int k, int i) {
   constexpr int V = kUnit<T>;
-  if (!NARROW) return (first_unit<E / V>(tid) + 32 * k) * V + 2 * i;
+  if (!NARROW) return (first_unit<E / V>(tid) + LANES * k) * V + 2 * i;
   return (tid & ~31) * E + (k * V / 2 + i) * 64 + (tid & 31) * (sizeof(T) == 2 ? 2 : 1);
 }
 
-template <typename T, bool NARROW, int NV>
+template <typename T, bool NARROW, int NV, int LANES = 32>
 __device__ __forceinline__ void fetch_row(const T* row, int cols, const T* matrix, unsigned smem, int tid) {
   const int lane = tid & 31;
   if constexpr (!NARROW) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (first_unit<NV>(tid) + 32 * k) * kUnit<T>;
-      if (c < cols) copy_async16(smem + (lane + 32 * k) * 16, row + c);
+      const int c = (first_unit<NV>(tid) + LANES * k) * kUnit<T>;
+      if (c < cols) copy_async16(smem + (lane + LANES * k) * 16, row + c);
     }
   } else {
     const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15u), first = (tid & ~31) * NV * 16;
@@ -325,7 +332,7 @@ __device__ __forceinline__ unsigned load_shared4(unsigned a) {
 }
 
 // A row in shared memory, as a warp reads it.
-template <typename T, bool NARROW>
+template <typename T, bool NARROW, int LANES = 32>
 struct Landed {
   unsigned at;       // the lane's unit, or (NARROW) the word with its first column
   unsigned select;   // which halves of two words are a pair
@@ -338,7 +345,7 @@ struct Landed {
   // the lane's unit k
   __device__ __forceinline__ uint4 raw(int k) const {
     if constexpr (!NARROW) {
-      return load_shared16(at + 512 * k);
+      return load_shared16(at + 16 * LANES * k);
     } else {
       unsigned w[4];
 #pragma unroll
@@ -354,14 +361,14 @@ struct Landed {
 };
 
 // Clears what no copy will ever write (not NARROW).
-template <typename T, int NV>
+template <typename T, int NV, int LANES>
 __device__ __forceinline__ void clear_rows(unsigned smem, unsigned row_len, int nrows, int cols, int tid) {
   const int lane = tid & 31;
   for (int r = 0; r < nrows; ++r, smem += row_len) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if ((first_unit<NV>(tid) + 32 * k) * kUnit<T> >= cols)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + (lane + 32 * k) * 16), "r"(0) : "memory");
+      if ((first_unit<NV>(tid) + LANES * k) * kUnit<T> >= cols)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(smem + (lane + LANES * k) * 16), "r"(0) : "memory");
     }
   }
 }
@@ -436,19 +443,23 @@ struct Written {
 //   32 elements per thread 45 us, 6.0 TB/s; 16 elements 49, 8 elements 68; one
 //   persistent CTA per SM with a warp per row and rows copied ahead 50.
 // R > 1: rows side by side, in rows of 256 columns and fewer, so that a warp
-// has more in flight (60000 x 96 bf16: 9 us, 16 with one row).
+// has more in flight (60000 x 96 bf16: 9 us, 16 with one row).  Up to 128 columns
+// a row is half a warp's, or half of the lanes would have none (6.4 us; 200000 x
+// 64: 14, 25 with whole warps).
 constexpr int kForwardThreads = 1024;   // of an SM at least
 template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
   __shared__ SumWords<R> words;
   constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
-  const int threads = MODE == kWarp ? 32 : blockDim.x;
-  const int tid = MODE == kWarp ? threadIdx.x & 31 : threadIdx.x, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
+  constexpr int L = kLanes<MODE>;
+  constexpr bool kRows = MODE == kWarp || MODE == kHalf;   // a CTA has several
+  const int threads = kRows ? L : blockDim.x;
+  const int tid = kRows ? threadIdx.x & (L - 1) : threadIdx.x, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
   const int w0 = (tid & ~31) * E;   // the warp's first column
   constexpr bool kSkip = NARROW || E > 32;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
-  const u64 row = R * (MODE == kWarp ? (u64)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x / csize);
+  const u64 row = R * (kRows ? (u64)blockIdx.x * (blockDim.x / L) + threadIdx.x / L : blockIdx.x / csize);
   const unsigned c0 = MODE == kCluster ? cluster_rank() * E * threads : 0;
   const int cols = c0 < prm.cols ? (int)min((unsigned)E * threads, prm.cols - c0) : 0;   // a cluster's last CTA may have none
   const int left = (int)min(prm.rows - min(row, prm.rows), (u64)R);
@@ -467,7 +478,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
       const uint4* a = reinterpret_cast<const uint4*>(x + r * prm.x_stride);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int u = u0 + 32 * k;
+        const int u = u0 + L * k;
         q[r][k] = r < left && u * V < cols ? __ldcs(a + u) : make_uint4(0, 0, 0, 0);
       }
     }
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
   const float means = row_sums<MODE, R>(v, words, 0, 0, threads) * inv;   // row r's in lane r
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float mean = R > 1 ? __shfl_sync(0xffffffffu, means, r) : means;
+    const float mean = R > 1 ? __shfl_sync(0xffffffffu, means, r, L) : means;
     float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
           sq = __ffma2_rn(d, d, sq);
         }
       } else {
-        const float2 m = both(NARROW || (u0 + 32 * k) * V < cols ? -mean : 0.f);   // a unit is whole or absent
+        const float2 m = both(NARROW || (u0 + L * k) * V < cols ? -mean : 0.f);   // a unit is whole or absent
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const float2 d = __fadd2_rn(f[i], m);
@@ -540,7 +551,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
     [[maybe_unused]] unsigned last[R] = {};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = column<T, NARROW, E>(tid, k, 0);
+      const int c = column<T, NARROW, E, L>(tid, k, 0);
       if (kSkip && w0 + 32 * k * V >= cols) break;
       const bool whole = w0 + 32 * (k + 1) * V <= cols;
       float2 g[P], b[P];
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
       load_w<T, W, NARROW, P>(prm.beta, c0, c, cols, whole, 0.f, b);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float2 mean = both(-(R > 1 ? __shfl_sync(0xffffffffu, means, r) : means)), rstd = both(R > 1 ? __shfl_sync(0xffffffffu, rstds, r) : rstds);
+        const float2 mean = both(-(R > 1 ? __shfl_sync(0xffffffffu, means, r, L) : means)), rstd = both(R > 1 ? __shfl_sync(0xffffffffu, rstds, r, L) : rstds);
         float2 o[P];
         unpack16<T, P>(q[r][k], o);
 #pragma unroll
@@ -586,9 +597,10 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   __shared__ SumWords<2 * R> words;
   constexpr int V = kUnit<T>, NV = E / V, P = V / 2;
   constexpr bool kKeepGamma = E <= 16;                   // else in shared memory, a unit per thread as the rows'
-  const int threads = MODE == kWarp ? 32 : prm.threads;
+  constexpr int L = kLanes<MODE>;
+  const int threads = MODE == kWarp || MODE == kHalf ? L : prm.threads;
   const int group = MODE == kCluster ? 0 : threadIdx.x / threads;
-  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid), lane = threadIdx.x & 31;
+  const int tid = threadIdx.x - group * threads, u0 = first_unit<NV>(tid), lane = threadIdx.x & (L - 1);
   const int groups = MODE == kCluster ? 1 : blockDim.x / threads;
   const unsigned csize = MODE == kCluster ? cluster_size() : 1;
   const unsigned part = blockIdx.x / csize;
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   const unsigned slot = (unsigned)__cvta_generic_to_shared(s_dyn) + group * stages * R * 2 * len + (tid >> 5) * kWarpBytes<T, NARROW, NV>;
   const int rows = (int)prm.rows, step = (int)prm.nparts * groups * R;
   const int first = ((int)part * groups + group) * R;
-  if constexpr (!NARROW) clear_rows<T, NV>(slot, len, stages * R * 2, cols, tid);
+  if constexpr (!NARROW) clear_rows<T, NV, L>(slot, len, stages * R * 2, cols, tid);
   wait_for_predecessors();
 
   // The row in work; what a turn is further in each matrix.
@@ -616,8 +628,8 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
 #pragma unroll
     for (int r = 0; r < R; ++r, at += 2 * len, fx += prm.x_stride, fd += prm.dy_stride) {
       if (r < left) {
-        fetch_row<T, NARROW, NV>(fx, cols, static_cast<const T*>(prm.x), at, tid);
-        fetch_row<T, NARROW, NV>(fd, cols, static_cast<const T*>(prm.dy), at + len, tid);
+        fetch_row<T, NARROW, NV, L>(fx, cols, static_cast<const T*>(prm.x), at, tid);
+        fetch_row<T, NARROW, NV, L>(fd, cols, static_cast<const T*>(prm.dy), at + len, tid);
       }
     }
     commit();
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   float* s_gam = reinterpret_cast<float*>(reinterpret_cast<char*>(s_dyn) + (size_t)groups * stages * R * 2 * len) + group * width;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = column<T, NARROW, E>(tid, k, 0);
+    const int c = column<T, NARROW, E, L>(tid, k, 0);
     float2 w[P];
     if (prm.gamma_bf16)
       load_w<T, bf16, NARROW, P>(prm.gamma, c0, c, cols, false, 1.f, w);
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       if constexpr (kKeepGamma)
         gam[k][i] = w[i];
       else
-        reinterpret_cast<float2*>(s_gam + (u0 + 32 * k) * V)[i] = w[i];   // read back by this thread alone
+        reinterpret_cast<float2*>(s_gam + (u0 + L * k) * V)[i] = w[i];   // read back by this thread alone
     }
   }
   auto gammas = [&](int k, float2 (&w)[P]) {
@@ -649,7 +661,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < P; ++i) w[i] = gam[k][i];
     } else {
-      const float* p = s_gam + (u0 + 32 * k) * V;
+      const float* p = s_gam + (u0 + L * k) * V;
 #pragma unroll
       for (int i = 0; i < P; i += 2) {
         const float4 q = reinterpret_cast<const float4*>(p)[i / 2];
@@ -672,7 +684,8 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
     cluster_wait();
   }
   int stage = 0, buf = 0;
-  for (int row = first; row < rows; row += step, x += x_turn, dy += dy_turn, dx += step * prm.out_stride) {
+  const int behind = MODE == kHalf ? (group & 1) * R : 0;   // the halves of a warp end their loops together
+  for (int row = first; row - behind < rows; row += step, x += x_turn, dy += dy_turn, dx += step * prm.out_stride) {
     const float means = mean_next, rstds = rstd_next;
     const int left = rows - row;
     statistics(row + step);
@@ -683,9 +696,9 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 sa = make_float2(0.f, 0.f), sd = sa;
+      const float2 mean = both(-__shfl_sync(0xffffffffu, means, r, L)), rstd = both(__shfl_sync(0xffffffffu, rstds, r, L));
       if (r < left) {
-        const float2 mean = both(-__shfl_sync(0xffffffffu, means, r)), rstd = both(__shfl_sync(0xffffffffu, rstds, r));
-        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
+        const Landed<T, NARROW, L> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           if (NARROW && (u0 - lane + 32 * k) * V >= cols) continue;   // nothing there for this warp
@@ -711,10 +724,10 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
     T* out = dx;
 #pragma unroll
     for (int r = 0; r < R; ++r, out += prm.out_stride) {
+      const float mean = __shfl_sync(0xffffffffu, means, r, L), rstd = __shfl_sync(0xffffffffu, rstds, r, L);
+      const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r, L), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1, L);
       if (r < left) {
-        const float mean = __shfl_sync(0xffffffffu, means, r), rstd = __shfl_sync(0xffffffffu, rstds, r);
-        const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1);
-        const Landed<T, NARROW> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
+        const Landed<T, NARROW, L> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
         const float2 k1 = both(-rstd * sum_a), k2 = both(-rstd * rstd * rstd * sum_ad);
         Written<T, E> to(out, cols, tid);
 #pragma unroll
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < P; ++i)
             fd[i] = __ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(__fmul2_rn(fd[i], w[i]), both(rstd), k1));
-          const int c = (u0 + 32 * k) * V;
+          const int c = (u0 + L * k) * V;
           if constexpr (NARROW) {
             to.put(k, fd);
           } else {
@@ -748,16 +761,28 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   float* out_g = (prm.nparts > 1 ? prm.partial + (size_t)part * 2 * prm.cols : prm.dgamma) + c0;
   float* out_b = (prm.nparts > 1 ? prm.partial + ((size_t)part * 2 + 1) * prm.cols : prm.dbeta) + c0;
   const bool add = prm.nparts == 1 && prm.accumulate;
+  if constexpr (MODE == kHalf) {   // a warp's two groups first: the sums of the lower one
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        dg[k][i].x += __shfl_down_sync(0xffffffffu, dg[k][i].x, 16);
+        dg[k][i].y += __shfl_down_sync(0xffffffffu, dg[k][i].y, 16);
+        db[k][i].x += __shfl_down_sync(0xffffffffu, db[k][i].x, 16);
+        db[k][i].y += __shfl_down_sync(0xffffffffu, db[k][i].y, 16);
+      }
+    }
+  }
   if (groups > 1) {
     float* acc = reinterpret_cast<float*>(s_dyn);   // [2][width]
-    for (int g = 0; g < groups; ++g) {
+    for (int g = 0; g < groups; g += 32 / L) {
       __syncthreads();
       if (g != group) continue;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          float* a = acc + column<T, NARROW, E>(tid, k, i);
+          float* a = acc + column<T, NARROW, E, L>(tid, k, i);
           float* b = a + width;
           if constexpr (kApart<T, NARROW> == 1) {
             float2* a2 = reinterpret_cast<float2*>(a);
@@ -781,7 +806,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (u0 + 32 * k) * V;
+      const int c = (u0 + L * k) * V;
       if (!NARROW && !add && prm.nparts > 1) {   // the parts' rows are aligned as the units are
         if (c < cols) {
 #pragma unroll
@@ -793,7 +818,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int at = column<T, NARROW, E>(tid, k, i / 2) + (i & 1) * kApart<T, NARROW>;
+          const int at = column<T, NARROW, E, L>(tid, k, i / 2) + (i & 1) * kApart<T, NARROW>;
           if (at < cols) {
             const float vg = i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x, vb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
             out_g[at] = add ? out_g[at] + vg : vg;
@@ -899,7 +924,7 @@ constexpr size_t kSmemSm = 224 * 1024;   // of an SM, less what CTAs take static
 
 template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
 cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st) {
-  const int groups = MODE == kWarp ? MAXT / 32 : 1;
+  const int groups = MODE == kWarp || MODE == kHalf ? MAXT / threads : 1;
   const size_t smem = NARROW ? (size_t)R * row_bytes<T, NARROW, E / kUnit<T>>(groups * threads) : 0;
   return launch_dependent(ln_forward_kernel<T, NARROW, E, R, MODE, MAXT>, dim3((unsigned)(div_up(p.rows, (size_t)groups * R) * csize)),
                           groups * threads, smem, csize, st, p);
@@ -921,6 +946,9 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 // moved in 4-byte words and was units in shared memory), 20046 x 3877 75.
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
+  if constexpr (!NARROW) {
+    if (p.cols <= 128 && p.rows >= 64 * (size_t)sm_count()) return forward_e<T, NARROW, 8, 4, kHalf, 128>(p, 16, 1, st);
+  }
   if (p.cols <= 256) {
     if (p.rows >= 32 * (size_t)sm_count()) return forward_e<T, NARROW, 8, 4, kWarp, 128>(p, 32, 1, st);
     return forward_e<T, NARROW, 8, 1, kWarp, 128>(p, 32, 1, st);
@@ -953,6 +981,8 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 // work.  One CTA of up to 512 threads is on an SM, with as many rows side by
 // side as it has room for, and leaves one partial sum per column; rows beyond
 // 8192 columns are split over a cluster, and beyond 65536 a thread has 32.
+// Rows up to 128 columns take half a warp each (200000 x 64 bf16: 26 us, 43 with whole
+// warps; 100000 x 128: 22, 28).
 //   Measured at 24576 x 5120 bf16 (755 MB), the kernel without the parts' sum:
 //   118 us, 6.4 TB/s; 2 rows a turn 128, 1 row 136; 8 columns per thread, 640
 //   threads and 4 rows 133; 24 columns, 224 threads and 1 row 175.  In
@@ -968,10 +998,11 @@ BackwardShape backward_shape(size_t rows, size_t cols) {
   s.csize = cols <= 512 ? 1 : cluster_for(rows, cols, 512 * 16);
   const size_t slice = div_up(cols, s.csize);
   s.e = slice <= 256 ? 8 : slice <= 8192 ? 16 : 32;
-  s.threads = threads_for(slice, s.e);
+  s.threads = cols <= 128 ? 16 : threads_for(slice, s.e);
   s.groups = s.csize > 1 ? 1 : 512 / s.threads;
   if (s.threads > 32 && s.groups > 15) s.groups = 15;   // named barriers
   while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
+  if (s.threads == 16 && s.groups == 1) s.threads = 32;   // a whole warp
   const size_t most = (size_t)resident_clusters(s.csize);
   s.many = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
   const size_t want = div_up(rows, (size_t)s.groups);
@@ -1038,6 +1069,16 @@ template <typename T, bool NARROW>
 cudaError_t backward(NormRowsParams& p, const BackwardShape& s, cudaStream_t st) {
   if (s.csize > 1) return s.e == 32 ? backward_e<T, NARROW, 32, 1, kCluster>(p, s, st) : backward_r<T, NARROW, 16, kCluster>(p, s, st);
   if (s.threads > 32) return backward_r<T, NARROW, 16, kCta>(p, s, st);
+  if (s.threads == 16) {
+    if constexpr (!NARROW) {
+      return backward_r<T, NARROW, 8, kHalf>(p, s, st);
+    } else {
+      BackwardShape warps = s;
+      warps.threads = 32;
+      if (warps.groups > 16) warps.groups = 16;
+      return backward_r<T, NARROW, 8, kWarp>(p, warps, st);
+    }
+  }
   return s.e == 8 ? backward_r<T, NARROW, 8, kWarp>(p, s, st) : backward_r<T, NARROW, 16, kWarp>(p, s, st);
 }
 

@@ -245,6 +245,36 @@ def test_backward_more_rows(xt, rows, cols, name):
     _check_backward(torch, xt, rows, cols, name, "bf16", accumulate=cols % 2 == 1)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(9729, 8), (12003, 64), (10007, 120), (20001, 128), (305, 64), (611, 128), (4865, 16), (40000, 96)])
+def test_rows_of_half_a_warp(xt, rows, cols, name):
+    torch = torch_cuda()
+    _check_forward(torch, xt, rows, cols, name, "f32")
+    _check_forward(torch, xt, rows, cols, name, "bf16", pad=8)
+    _check_backward(torch, xt, rows, cols, name, "f32", accumulate=True)
+    _check_backward(torch, xt, rows, cols, name, "bf16", pad=8)
+
+
+@pytest.mark.parametrize("rows", [306, 10007])
+def test_half_warps_keep_bad_rows_apart(xt, rows):
+    """Rows that hold an infinity or NaN leave every other row's bits as they are, the one of the warp's other half among them."""
+    torch = torch_cuda()
+    x, dy, gamma, beta = _inputs(torch, rows, 64, torch.bfloat16, torch.float32)
+    bad = torch.arange(rows, device="cuda") % 3 == 1
+    out = []
+    for spoil in (False, True):
+        if spoil:
+            x[bad, 5] = float("inf")
+            dy[bad, 7] = float("nan")
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        xt.xp_layernorm_forward(x, gamma, beta, y, mean, rstd, 1e-5)
+        xt.xp_layernorm_backward(dy, x, gamma, mean, rstd, dx)
+        out.append([t[~bad].clone() for t in (y, mean, rstd, dx)])
+        assert not spoil or (torch.isnan(y[bad]).any(1).all() and torch.isnan(dx[bad]).any(1).all())
+    assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(*out))
+
+
 @pytest.mark.parametrize("rows,cols", [(37, 200), (37, 1000), (5, 30000)])
 def test_layernorm_in_place_repeatable_and_optional(xt, rows, cols):
     torch = torch_cuda()
