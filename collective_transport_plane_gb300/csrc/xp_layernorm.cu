@@ -588,9 +588,11 @@ __global__ void __launch_bounds__(MAXT, kForwardThreads / MAXT) ln_forward_kerne
 // that few partial sums are left.  Asynchronous copies bring the next R rows
 // into shared memory; a row is read from there twice, for its sums and for
 // dx: with d = x - mean and a = dy * gamma,
-//   dx = rstd a - rstd sum(a) / cols - d rstd^3 sum(a d) / cols,
-// dgamma += (dy rstd) d, dbeta += dy.  R rows share a barrier, and their sums'
-// latencies overlap.
+//   dx = rstd (a - sum(a) / cols - d rstd (rstd sum(a d) / cols)),
+// dgamma += (dy rstd) d, dbeta += dy.  (No power of rstd is formed: its cube
+// leaves fp32's range for rows beyond 1e13 and below 1e-13, while sum(a d)
+// rstd and d rstd are of the size of a and 1.)  R rows share a barrier, and
+// their sums' latencies overlap.
 template <typename T, bool NARROW, int E, int R, int MODE>
 __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_constant__ NormRowsParams prm) {
   extern __shared__ uint4 s_dyn[];
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
       const float sum_a = __shfl_sync(0xffffffffu, sums, 2 * r, L), sum_ad = __shfl_sync(0xffffffffu, sums, 2 * r + 1, L);
       if (r < left) {
         const Landed<T, NARROW, L> hx(here + r * 2 * len, x + r * prm.x_stride, lane), hd(here + (r * 2 + 1) * len, dy + r * prm.dy_stride, lane);
-        const float2 k1 = both(-rstd * sum_a), k2 = both(-rstd * rstd * rstd * sum_ad);
+        const float2 k1 = both(-sum_a), k2 = both(-(rstd * sum_ad) * rstd);
         Written<T, E> to(out, cols, tid);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -739,7 +741,7 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const __grid_consta
           gammas(k, w);
 #pragma unroll
           for (int i = 0; i < P; ++i)
-            fd[i] = __ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(__fmul2_rn(fd[i], w[i]), both(rstd), k1));
+            fd[i] = __fmul2_rn(__ffma2_rn(__fadd2_rn(fx[i], both(-mean)), k2, __ffma2_rn(fd[i], w[i], k1)), both(rstd));
           const int c = (u0 + L * k) * V;
           if constexpr (NARROW) {
             to.put(k, fd);
