@@ -481,11 +481,12 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
       m[k] = m[k] * prm.beta1 + gi * prm.one_minus_beta1;
       v[k] = v[k] * prm.beta2 + gi * prm.one_minus_beta2 * gi;
       const float d = __fsqrt_rn(v[k]) * rs + prm.eps;
-      // a numerator of 0, which weights without gradients have, would take the division's slow path, and its warp with it
+      // a numerator of 0, which weights without gradients have, would take the division's slow path, and its warp with
+      // it; d > 0 or NaN, and over a NaN it is a NaN too
       const float a = m[k] * alpha;
-      const bool zero = a == 0.f;
+      const bool zero = a == 0.f && d == d;
       const float q = __fdiv_rn(zero ? 1.f : a, d);
-      p[k] = p[k] * keep - (zero ? 0.f : q);
+      p[k] = p[k] * keep - (zero ? a : q);
     }
     store_some(param + at, n, vec, p);
     if (t.copy) store_some(static_cast<__nv_bfloat16*>(t.copy) + i, n, vec, p);

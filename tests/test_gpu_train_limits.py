@@ -5,7 +5,7 @@ import pytest
 
 from oracle import train
 from tests.gpu_util import torch_cuda
-from tests.test_gpu_train import U, _f64, _forward_bounds, _matrix, _types, xt  # noqa: F401
+from tests.test_gpu_train import U, Group, _f64, _forward_bounds, _matrix, _types, xt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,59 @@ def test_gradient_of_constant_rows(xt, cols):
     assert torch.equal(mean, x[:, 0]) and not y.any()
     want, bound = _dx_bound(_f64(dy), _f64(x), None, _f64(mean), _f64(rstd), 0.0)
     assert (np.abs(_f64(dx) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n,lead", [(5000, 0), (5000, 3), (100, 0)])
+@pytest.mark.parametrize("param,state", [("f32", "f32"), ("bf16", "f32"), ("f32", "8bit"), ("bf16", "8bit")])
+def test_a_second_moment_that_is_not_finite(xt, param, state, n, lead, value):
+    # gradient and m are 0: over a NaN the weight is NaN, over an infinity it stays, whole turns of a CTA or not
+    torch = torch_cuda()
+    g = Group(torch, xt, [n], param, param, state, lead=lead, step=3, decay=0.0)
+    g.g[0].zero_()
+    g.m[0].zero_()
+    bad = [37, n - 1]
+    if state == "8bit":
+        if value == float("inf"):
+            g.vs[0][[b // 32 for b in bad]], g.v[0][bad] = 254, 255    # the code beyond fp32's largest number
+        else:
+            g.vs[0][[b // 32 for b in bad]] = 255
+    else:
+        g.v[0][bad] = value
+    before = g.p[0].float().cpu().numpy()
+    (f32, _, _), = g.twin(1e-2)
+    xt.xp_adamw_step(g.handle, 1e-2)
+    got = g.p[0].float().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(f32[0])) and np.isnan(got[bad]).all() == (value != float("inf"))
+    assert np.array_equal(got[~np.isnan(got)], before[~np.isnan(got)])
+    g.close()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("param,state", [("f32", "f32"), ("f32", "8bit"), ("bf16", "8bit")])
+def test_gradients_that_are_not_finite(xt, param, state, value):
+    # two steps, in whole turns and at the tensor's end: an element's own weight first; in 8 bits its block's states are
+    # lost with it, and every other block's codes are what they would be
+    torch = torch_cuda()
+    n, bad = 5000, [5, 2048 + 77, 4999]
+    g = Group(torch, xt, [n], param, param, state, step=3)
+    lost = np.zeros(n, bool)
+    lost[bad] = True
+    blocks = np.unique(np.array(bad) // 32)
+    for k in range(2):
+        g.g[0][bad] = value if k == 0 else 0.25
+        (f32, _, codes), = g.twin(1e-2)
+        xt.xp_adamw_step(g.handle, 1e-2)
+        got = g.p[0].float().cpu().numpy()
+        assert np.array_equal(np.isnan(got), lost)
+        want = torch.from_numpy(f32[0]).to(g.p[0].dtype).float().numpy()
+        assert np.array_equal(got, want, equal_nan=True)
+        if state == "8bit":
+            for code, scale, (c, e) in ((g.m[0], g.ms[0], codes[0]), (g.v[0], g.vs[0], codes[1])):
+                scale, code = scale.cpu().numpy(), code.cpu().numpy()
+                assert (scale[blocks] == 255).all()
+                fine = np.ones(len(e), bool)
+                fine[blocks] = False
+                assert np.array_equal(scale[fine], e[fine]) and np.array_equal(code[np.repeat(fine, 32)[:n]], c[np.repeat(fine, 32)[:n]])
+            lost[np.repeat(np.isin(np.arange(len(fine)), blocks), 32)[:n]] = True
+    g.close()
