@@ -62,6 +62,7 @@ _forward, _backward, _norm, _step, _decode = (_lib.xp_layernorm_forward, _lib.xp
 
 _DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
 _types = {}   # torch dtype -> xp_dtype, filled as types are met
+_gradients = {}   # group -> (its tensors' lengths, their gradients' xp_dtype)
 
 
 def _dtype(t) -> int:
@@ -164,16 +165,23 @@ def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=No
     table = (xp_tensor * max(n, 1))(*[xp_tensor(*row) for row in rows])
     out = ctypes.c_void_p()
     _check(_lib.xp_group_create(ctypes.byref(cfg), n, table, ctypes.byref(out)), "xp_group_create")
+    _gradients[out.value] = counts, cfg.grad_dtype
     return out.value
 
 
 def xp_group_destroy(group: int) -> None:
+    _gradients.pop(group, None)
     _check(_lib.xp_group_destroy(group), "xp_group_destroy")
 
 
 def xp_group_set_grads(group: int, grads, stream=None) -> None:
     """Other gradient buffers, of the lengths and type the group was made with."""
-    ptrs = (ctypes.c_void_p * max(len(grads), 1))(*[t.data_ptr() for t in grads])
+    if group not in _gradients:
+        raise ValueError("not a group that xp_group_create made")
+    counts, dtype = _gradients[group]
+    if len(grads) != len(counts):
+        raise ValueError(f"{len(grads)} gradients for {len(counts)} tensors")
+    ptrs = (ctypes.c_void_p * len(counts))(*[_vector(t, n, f"grad {i}", dtype) for i, (t, n) in enumerate(zip(grads, counts))])
     _check(_lib.xp_group_set_grads(group, ptrs, _stream(stream)), "xp_group_set_grads")
 
 

@@ -1,0 +1,63 @@
+"""What the binding of the training operators refuses before a call, on the CPU, against a library that records its calls
+and launches nothing."""
+import pytest
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The binding over a library whose calls succeed and are recorded."""
+    from collective_transport_plane_gb300 import build
+    build.build()
+    import collective_transport_plane_gb300.xp_train as xt
+
+    class Library:
+        def __init__(self):
+            self.calls = []
+
+        def xp_group_create(self, cfg, n, table, out):
+            out._obj.value = 0x1000 + 16 * len(self.calls)
+            return self.record("xp_group_create", n)
+
+        def record(self, name, *args):
+            self.calls.append((name, args))
+            return 0
+
+        def __getattr__(self, name):
+            return lambda *args: self.record(name, *args)
+
+    lib = Library()
+    monkeypatch.setattr(xt, "_lib", lib)
+    for alias, name in (("_norm", "xp_grad_norm"), ("_step", "xp_adamw_step"), ("_backward", "xp_layernorm_backward")):
+        monkeypatch.setattr(xt, alias, getattr(lib, name))
+    monkeypatch.setattr(xt, "lib", lib, raising=False)
+    return xt
+
+
+def test_other_gradients_have_the_groups_lengths_and_type(fake):
+    torch = pytest.importorskip("torch")
+    group = fake.xp_group_create(None, [torch.zeros(10), torch.zeros(2, 3), torch.zeros(0)])
+    good = [torch.ones(10), torch.ones(3, 2), torch.ones(0)]
+    made = len(fake.lib.calls)
+    for bad in ([], good[:1], good[:2], good + [torch.ones(1)],                         # the library reads one pointer per tensor
+                [torch.ones(9), *good[1:]], [torch.ones(11), *good[1:]],                # other lengths
+                [good[0].bfloat16(), *good[1:]], [good[0].double(), *good[1:]],         # other types
+                [good[0], torch.ones(2, 3).t(), good[2]], [torch.ones(20)[::2], *good[1:]]):   # not contiguous
+        with pytest.raises(ValueError):
+            fake.xp_group_set_grads(group, bad)
+    assert len(fake.lib.calls) == made
+    fake.xp_group_set_grads(group, good)
+    name, (to, ptrs, _) = fake.lib.calls[-1]
+    assert name == "xp_group_set_grads" and to == group and len(ptrs) == 3 and ptrs[0] == good[0].data_ptr() and ptrs[1] == good[1].data_ptr()
+    fake.xp_group_destroy(group)
+    with pytest.raises(ValueError):
+        fake.xp_group_set_grads(group, good)
+    assert fake.lib.calls[-1][0] == "xp_group_destroy"
+
+
+def test_gradients_of_bf16_groups(fake):
+    torch = pytest.importorskip("torch")
+    group = fake.xp_group_create(None, [torch.zeros(10).bfloat16()])
+    with pytest.raises(ValueError):
+        fake.xp_group_set_grads(group, [torch.zeros(10)])
+    fake.xp_group_set_grads(group, [torch.zeros(10).bfloat16()])
+    fake.xp_group_destroy(group)
