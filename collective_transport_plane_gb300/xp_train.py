@@ -62,6 +62,7 @@ _forward, _backward, _norm, _step, _decode = (_lib.xp_layernorm_forward, _lib.xp
 
 _DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
 _types = {}   # torch dtype -> xp_dtype, filled as types are met
+_REPORT_BYTES = ctypes.sizeof(xp_grad_report)
 _gradients = {}   # group -> (its tensors' lengths, their gradients' xp_dtype)
 
 
@@ -95,6 +96,14 @@ def _vector(t, n, what, dtype):
     if t.numel() != n or not t.is_contiguous() or _types.get(t.dtype) != dtype and _dtype(t) != dtype:
         raise ValueError(f"{what} is not {n} contiguous elements of its type")
     return t.data_ptr()
+
+
+def _report(t):
+    """The address of an xp_grad_report's 32 bytes.  (One that is not 16-byte aligned is for the library to refuse.)"""
+    p = t.data_ptr()
+    if (t.nbytes < _REPORT_BYTES or not t.is_contiguous()) and p & 15 == 0:
+        raise ValueError(f"report is not {_REPORT_BYTES} contiguous bytes")
+    return p
 
 
 def xp_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
@@ -197,14 +206,17 @@ def xp_group_get_step(group: int, stream=None) -> int:
 
 def xp_grad_norm(group: int, report, grad_scale: float = 1.0, max_norm: float = 0.0, accumulate: bool = False, stream=None) -> None:
     """The norm of the group's gradients into `report`, 32 bytes of device memory laid out as xp_grad_report."""
-    _check(_norm(group, grad_scale, max_norm, 1 if accumulate else 0, report.data_ptr(), stream if stream is None else _stream(stream)),
+    _check(_norm(group, grad_scale, max_norm, 1 if accumulate else 0, _report(report), stream if stream is None else _stream(stream)),
            "xp_grad_norm")
 
 
 def xp_adamw_step(group: int, lr: float, report=None, grad_scale: float = 1.0, skip_nonfinite: bool = False, lr_dev=None,
                   stream=None) -> None:
-    """One AdamW step on the group's tensors, gradients scaled by the report's scale if there is one."""
-    _check(_step(group, lr, None if lr_dev is None else lr_dev.data_ptr(), grad_scale, None if report is None else report.data_ptr(),
+    """One AdamW step on the group's tensors, gradients scaled by the report's scale if there is one; the rate is lr_dev's
+    first element if there is one."""
+    if lr_dev is not None and (lr_dev.numel() < 1 or _dtype(lr_dev) != XP_F32):
+        raise ValueError("lr_dev is not an fp32 number")
+    _check(_step(group, lr, None if lr_dev is None else lr_dev.data_ptr(), grad_scale, None if report is None else _report(report),
                  XP_ADAMW_SKIP_NONFINITE if skip_nonfinite else 0, stream if stream is None else _stream(stream)), "xp_adamw_step")
 
 

@@ -1,5 +1,7 @@
 """What the binding of the training operators refuses before a call, on the CPU, against a library that records its calls
 and launches nothing."""
+import ctypes
+
 import pytest
 
 
@@ -33,6 +35,12 @@ def fake(monkeypatch):
     return xt
 
 
+def _aligned(torch, n, dtype):
+    """n elements that begin at a multiple of 16 bytes."""
+    buf = torch.zeros(n + 16, dtype=dtype)
+    return buf[-buf.data_ptr() % 16 // buf.element_size():][:n]
+
+
 def test_other_gradients_have_the_groups_lengths_and_type(fake):
     torch = pytest.importorskip("torch")
     group = fake.xp_group_create(None, [torch.zeros(10), torch.zeros(2, 3), torch.zeros(0)])
@@ -61,3 +69,23 @@ def test_gradients_of_bf16_groups(fake):
         fake.xp_group_set_grads(group, [torch.zeros(10)])
     fake.xp_group_set_grads(group, [torch.zeros(10).bfloat16()])
     fake.xp_group_destroy(group)
+
+
+def test_reports_and_rates(fake):
+    torch = pytest.importorskip("torch")
+    assert ctypes.sizeof(fake.xp_grad_report) == 32
+    good, none = _aligned(torch, 8, torch.float32), len(fake.lib.calls)
+    for bad in (_aligned(torch, 7, torch.float32), _aligned(torch, 31, torch.uint8), _aligned(torch, 1, torch.float32).expand(8),
+                _aligned(torch, 16, torch.float32)[::2]):
+        with pytest.raises(ValueError):
+            fake.xp_grad_norm(1, bad)
+        with pytest.raises(ValueError):
+            fake.xp_adamw_step(1, 0.1, report=bad)
+    for bad in (torch.zeros(0), torch.zeros(1, dtype=torch.float64), torch.zeros(1, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            fake.xp_adamw_step(1, 0.1, lr_dev=bad)
+    assert len(fake.lib.calls) == none
+    fake.xp_grad_norm(1, good)
+    fake.xp_grad_norm(1, _aligned(torch, 32, torch.uint8))
+    fake.xp_adamw_step(1, 0.1, report=good, lr_dev=torch.zeros(3))
+    assert [name for name, _ in fake.lib.calls[none:]] == ["xp_grad_norm", "xp_grad_norm", "xp_adamw_step"]
