@@ -140,6 +140,8 @@ def xp_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None,
     dt = _types.get(dtype) or _dtype(x)
     wdt = dt if gamma is None else _dtype(gamma)
     work, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    if work is not None and not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous")
     st = _backward(dy.data_ptr(), dys, x.data_ptr(), xs, _vector(gamma, cols, "gamma", wdt), _vector(mean, rows, "mean", XP_F32),
                    _vector(rstd, rows, "rstd", XP_F32), dx.data_ptr(), dxs, _vector(dgamma, cols, "dgamma", XP_F32),
                    _vector(dbeta, cols, "dbeta", XP_F32), rows, cols, dt, wdt, 1 if accumulate else 0, work, nbytes,

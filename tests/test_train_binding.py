@@ -89,3 +89,12 @@ def test_reports_and_rates(fake):
     fake.xp_grad_norm(1, _aligned(torch, 32, torch.uint8))
     fake.xp_adamw_step(1, 0.1, report=good, lr_dev=torch.zeros(3))
     assert [name for name, _ in fake.lib.calls[none:]] == ["xp_grad_norm", "xp_grad_norm", "xp_adamw_step"]
+
+
+def test_workspaces(fake):
+    torch = pytest.importorskip("torch")
+    x, s = torch.zeros(4, 8), torch.zeros(4)
+    with pytest.raises(ValueError):    # 4096 bytes by its shape, one in memory
+        fake.xp_layernorm_backward(x, x, None, s, s, torch.zeros(4, 8), torch.zeros(8), torch.zeros(8), torch.zeros(1, dtype=torch.uint8).expand(4096))
+    fake.xp_layernorm_backward(x, x, None, s, s, torch.zeros(4, 8), torch.zeros(8), torch.zeros(8), torch.zeros(4096, dtype=torch.uint8))
+    assert fake.lib.calls[-1][0] == "xp_layernorm_backward"
