@@ -67,7 +67,7 @@ size_t unit_elements(unsigned long long total) {
 
 xp_status check_tensor(const xp_group_config& c, int i, const xp_tensor& t, bool has_params) {
   if (t.reserved != 0) return fail(XP_ERR_INVALID, "tensor %d: reserved is %d, not 0", i, t.reserved);
-  if ((unsigned long long)t.count > (1ull << 48)) return fail(XP_ERR_INVALID, "tensor %d: %zu elements", i, t.count);
+  if (t.count > XP_GROUP_MAX_ELEMENTS) return fail(XP_ERR_INVALID, "tensor %d: %zu elements", i, t.count);
   if ((t.param != nullptr) != has_params && t.count) return fail(XP_ERR_INVALID, "tensor %d: param in some tensors only", i);
   if (t.count && !t.grad) return fail(XP_ERR_INVALID, "tensor %d: grad is NULL", i);
   if (!aligned(t.grad, size_of(c.grad_dtype))) return fail(XP_ERR_INVALID, "tensor %d: grad is not aligned to its element", i);
@@ -98,6 +98,7 @@ xp_status create(const xp_group_config& cfg, int ntensors, const xp_tensor* tens
     const xp_status s = check_tensor(cfg, i, tensors[i], g->has_params);
     if (s != XP_OK) return s;
     total += tensors[i].count;
+    if (total > XP_GROUP_MAX_ELEMENTS) return fail(XP_ERR_INVALID, "the group's elements are more than 2^40 with tensor %d", i);
   }
   const size_t unit = unit_elements(total);
   std::vector<xp::GroupTensor> table(ntensors);
@@ -126,7 +127,6 @@ xp_status create(const xp_group_config& cfg, int ntensors, const xp_tensor* tens
     pos += round_up(t.count, XP_STATE8_BLOCK);
   }
   if (units.empty()) units.push_back({0u, 0u, 0ull});   // a step of an empty group still counts
-  if (units.size() > 0x7fffffffull) return fail(XP_ERR_INVALID, "the group's %llu elements are too many", total);
   g->nunits = (unsigned)units.size();
 
   const size_t at_units = round_up(table.size() * sizeof(xp::GroupTensor), 256);

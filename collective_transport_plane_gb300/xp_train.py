@@ -14,6 +14,7 @@ from .xp import XP_BF16, XP_F32, XP_OK, XP_U8, XpError, _stream  # noqa: F401
 XP_LAYERNORM_MAX_COLS = 131072
 XP_LAYERNORM_MAX_ROWS = 1 << 28
 XP_STATE8_BLOCK = 32
+XP_GROUP_MAX_ELEMENTS = 1 << 40
 XP_ADAMW_SKIP_NONFINITE = 1
 
 # every entry point include/xp_train.h declares

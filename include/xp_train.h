@@ -121,9 +121,14 @@ typedef struct {
   int32_t reserved[3];
 } xp_grad_report;
 
+/* Elements of a group at most, all tensors together. */
+#define XP_GROUP_MAX_ELEMENTS ((size_t)1 << 40)
+
 /* Make a group of `ntensors` tensors (1 <= ntensors <= 2^20) on the current
- * device: its tables are laid out once and reused by every call.  Errors:
- * XP_ERR_INVALID (bad argument, *out untouched), XP_ERR_CUDA. */
+ * device: its tables (16 bytes per 2048 to 8192 elements, 80 per tensor) are
+ * laid out once and reused by every call.  Errors: XP_ERR_INVALID (bad
+ * argument), XP_ERR_CUDA, XP_ERR_INTERNAL (no host memory for the tables);
+ * *out is untouched by all of them. */
 xp_status xp_group_create(const xp_group_config* cfg, int ntensors, const xp_tensor* tensors, xp_group** out);
 
 /* Synchronise the device, then free the group (not its tensors).  NULL is a

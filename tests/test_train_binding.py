@@ -1,8 +1,13 @@
 """What the binding of the training operators refuses before a call, on the CPU, against a library that records its calls
 and launches nothing."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture
@@ -98,3 +103,25 @@ def test_workspaces(fake):
         fake.xp_layernorm_backward(x, x, None, s, s, torch.zeros(4, 8), torch.zeros(8), torch.zeros(8), torch.zeros(1, dtype=torch.uint8).expand(4096))
     fake.xp_layernorm_backward(x, x, None, s, s, torch.zeros(4, 8), torch.zeros(8), torch.zeros(8), torch.zeros(4096, dtype=torch.uint8))
     assert fake.lib.calls[-1][0] == "xp_layernorm_backward"
+
+
+@pytest.mark.parametrize("counts", ["[(1 << 40) + 1]", "[1 << 48]", "[1 << 40, 1]", "[1 << 39] * 300", "[1 << 40] * (1 << 20)"])
+def test_a_group_of_too_many_elements_is_refused_before_its_tables(counts):
+    # in a process of its own that may take 6 GiB: tables for them would be far larger
+    code = f"""if True:
+        import ctypes, re, resource, sys
+        sys.path.insert(0, {ROOT!r})
+        from collective_transport_plane_gb300 import xp_train as xt
+        limit = int(re.search(r"XP_GROUP_MAX_ELEMENTS \\(\\(size_t\\)1 << (\\d+)\\)", open({ROOT!r} + "/include/xp_train.h").read()).group(1))
+        assert xt.XP_GROUP_MAX_ELEMENTS == 1 << limit
+        counts, A = {counts}, 1 << 20
+        cfg = xt.xp_group_config(beta1=0.9, beta2=0.99, eps=1e-8, param_dtype=xt.XP_F32, grad_dtype=xt.XP_F32, state_dtype=xt.XP_F32)
+        table = (xt.xp_tensor * len(counts))()
+        for t, n in zip(table, counts):
+            t.grad, t.count = A, n
+        out = ctypes.c_void_p(77)
+        resource.setrlimit(resource.RLIMIT_AS, (6 << 30, 6 << 30))
+        status = xt._lib.xp_group_create(ctypes.byref(cfg), len(counts), table, ctypes.byref(out))
+        print(status, out.value)"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert done.stdout.split() == ["1", "77"], (done.stdout, done.stderr[-500:])
