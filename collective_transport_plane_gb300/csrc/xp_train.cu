@@ -54,6 +54,7 @@ bool is_float_type(int dt) { return dt == XP_F32 || dt == XP_BF16; }
 size_t size_of(int dt) { return dt == XP_F32 ? 4 : dt == XP_BF16 ? 2 : 1; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
+bool step_ok(uint64_t step) { return step <= XP_GROUP_MAX_STEP; }
 
 // Elements of a unit.  Small groups are cut finer, so that their elements
 // spread over the SMs; a unit is a whole number of turns of its CTA.
@@ -201,6 +202,7 @@ xp_status xp_group_create(const xp_group_config* cfg, int ntensors, const xp_ten
   if (!is_float_type(cfg->param_dtype) || !is_float_type(cfg->grad_dtype))
     return fail(XP_ERR_INVALID, "param_dtype %d / grad_dtype %d is neither XP_F32 nor XP_BF16", cfg->param_dtype, cfg->grad_dtype);
   if (cfg->state_dtype != XP_F32 && cfg->state_dtype != XP_U8) return fail(XP_ERR_INVALID, "state_dtype %d is neither XP_F32 nor XP_U8", cfg->state_dtype);
+  if (!step_ok(cfg->step)) return fail(XP_ERR_INVALID, "step %llu above 2^52", (unsigned long long)cfg->step);
   xp_group* g = nullptr;
   try {
     g = new xp_group();
@@ -251,6 +253,7 @@ xp_status xp_group_set_grads(xp_group* g, const void* const* grads, xp_stream_t 
 xp_status xp_group_set_step(xp_group* g, uint64_t step, xp_stream_t stream) {
   xp_status s = check_group(g);
   if (s != XP_OK) return s;
+  if (!step_ok(step)) return fail(XP_ERR_INVALID, "step %llu above 2^52", (unsigned long long)step);
   XP_CUDA(xp::launch_set_step(g->state, step, std::pow(g->cfg.beta1, (double)(step + 1)), std::pow(g->cfg.beta2, (double)(step + 1)), stream));
   return XP_OK;
 }

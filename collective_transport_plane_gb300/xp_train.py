@@ -15,6 +15,7 @@ XP_LAYERNORM_MAX_COLS = 131072
 XP_LAYERNORM_MAX_ROWS = 1 << 28
 XP_STATE8_BLOCK = 32
 XP_GROUP_MAX_ELEMENTS = 1 << 40
+XP_GROUP_MAX_STEP = 1 << 52
 XP_ADAMW_SKIP_NONFINITE = 1
 
 # every entry point include/xp_train.h declares

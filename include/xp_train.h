@@ -95,7 +95,7 @@ typedef struct {
   int32_t grad_dtype;   /* XP_F32 or XP_BF16 */
   int32_t state_dtype;  /* XP_F32, or XP_U8: 8-bit codes */
   uint32_t seed;        /* of the 8-bit states' rounding */
-  uint64_t step;        /* steps already taken */
+  uint64_t step;        /* steps already taken, XP_GROUP_MAX_STEP at most */
 } xp_group_config;
 
 /* An 8-bit state.  A block of 32 elements (block k holds elements 32 k ..
@@ -121,8 +121,10 @@ typedef struct {
   int32_t reserved[3];
 } xp_grad_report;
 
-/* Elements of a group at most, all tensors together. */
+/* Elements of a group at most, all tensors together, and the steps it may be
+ * said to have taken (a step's number is exact in fp64). */
 #define XP_GROUP_MAX_ELEMENTS ((size_t)1 << 40)
+#define XP_GROUP_MAX_STEP ((uint64_t)1 << 52)
 
 /* Make a group of `ntensors` tensors (1 <= ntensors <= 2^20) on the current
  * device: its tables (16 bytes per 2048 to 8192 elements, 80 per tensor) are

@@ -119,3 +119,18 @@ def test_gradients_that_are_not_finite(xt, param, state, value):
                 assert np.array_equal(scale[fine], e[fine]) and np.array_equal(code[np.repeat(fine, 32)[:n]], c[np.repeat(fine, 32)[:n]])
             lost[np.repeat(np.isin(np.arange(len(fine)), blocks), 32)[:n]] = True
     g.close()
+
+
+def test_step_counts_that_would_wrap(xt):
+    torch = torch_cuda()
+    g = Group(torch, xt, [100], step=7)
+    for step in (-1, (1 << 64) - 1, xt.XP_GROUP_MAX_STEP + 1):
+        with pytest.raises(xt.XpError):
+            xt.xp_group_set_step(g.handle, step)
+    assert xt.xp_group_get_step(g.handle) == 7
+    xt.xp_group_set_step(g.handle, xt.XP_GROUP_MAX_STEP)
+    g.step = xt.XP_GROUP_MAX_STEP
+    want = g.twin(1e-2)
+    xt.xp_adamw_step(g.handle, 1e-2)
+    g.check(want)
+    g.close()

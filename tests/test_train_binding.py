@@ -2,6 +2,7 @@
 and launches nothing."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -125,3 +126,16 @@ def test_a_group_of_too_many_elements_is_refused_before_its_tables(counts):
         print(status, out.value)"""
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert done.stdout.split() == ["1", "77"], (done.stdout, done.stderr[-500:])
+
+
+@pytest.mark.parametrize("step", [(1 << 52) + 1, (1 << 64) - 1, -1])
+def test_a_group_with_a_step_count_that_would_wrap_is_refused(step):
+    # the bias corrections of step 2^64 would be those of step 0, infinite; -1 becomes 2^64 - 1 on its way
+    from collective_transport_plane_gb300 import build
+    build.build()
+    import collective_transport_plane_gb300.xp_train as xt
+    assert 1 << int(re.search(r"XP_GROUP_MAX_STEP \(\(uint64_t\)1 << (\d+)\)", open(os.path.join(ROOT, "include", "xp_train.h")).read()).group(1)) == xt.XP_GROUP_MAX_STEP
+    cfg = xt.xp_group_config(beta1=0.9, beta2=0.99, eps=1e-8, param_dtype=xt.XP_F32, grad_dtype=xt.XP_F32, state_dtype=xt.XP_F32, step=step)
+    table, out = (xt.xp_tensor * 1)(xt.xp_tensor(grad=1 << 20, count=5)), ctypes.c_void_p()
+    assert xt._lib.xp_group_create(ctypes.byref(cfg), 1, table, ctypes.byref(out)) == xt.xp.XP_ERR_INVALID
+    assert b"step" in xt._lib.xp_last_error()
