@@ -168,19 +168,25 @@ xp_status check_rows(const char* what, const void* p, size_t stride, size_t rows
   return XP_OK;
 }
 
-// Whether two buffers of `rows` rows share bytes, other than being the same
-// buffer with the same rows.
+// Where a matrix of `rows` rows lies.
 struct Span {
-  const char* name;
   uintptr_t lo, hi;
-  size_t stride;
+  size_t rows, width, pitch;   // bytes of a row, and from one row to the next
 };
-Span span_of(const char* name, const void* p, size_t stride, size_t rows, size_t cols, size_t es) {
+Span span_of(const void* p, size_t stride, size_t rows, size_t cols, size_t es) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {name, lo, p ? lo + ((rows - 1) * stride + cols) * es : lo, stride};
+  return {lo, lo + ((rows - 1) * stride + cols) * es, rows, cols * es, stride * es};
 }
-bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
-bool same(const Span& a, const Span& b) { return a.lo == b.lo && a.stride == b.stride; }
+// Whether two matrices of the same size share bytes.  At equal strides rows may
+// lie between rows, as side-by-side columns of one buffer do: b's rows begin at
+// the same place between two of a's.  At different strides that is not followed up.
+bool overlap(const Span& a, const Span& b) {
+  if (a.hi <= b.lo || b.hi <= a.lo) return false;
+  if (a.rows == 1 || a.pitch != b.pitch) return true;
+  const size_t at = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
+  return at < a.width || a.pitch - at < a.width;
+}
+bool same(const Span& a, const Span& b) { return a.lo == b.lo && (a.rows == 1 || a.pitch == b.pitch); }
 
 xp_status check_sizes(size_t rows, size_t cols, int dtype, int wdtype) {
   if (!is_float_type(dtype) || !is_float_type(wdtype)) return fail(XP_ERR_INVALID, "dtype %d / %d is neither XP_F32 nor XP_BF16", dtype, wdtype);
@@ -343,7 +349,7 @@ xp_status xp_layernorm_forward(const void* x, size_t x_stride, const void* gamma
   if (!aligned(gamma, size_of(wdtype)) || !aligned(beta, size_of(wdtype)) || !aligned(mean, 4) || !aligned(rstd, 4))
     return fail(XP_ERR_INVALID, "gamma, beta, mean or rstd is not aligned to its element");
   if (!(eps >= 0) || !std::isfinite(eps)) return fail(XP_ERR_INVALID, "eps %g is negative or not finite", eps);
-  const Span sx = span_of("x", x, x_stride, rows, cols, size_of(dtype)), sy = span_of("y", y, y_stride, rows, cols, size_of(dtype));
+  const Span sx = span_of(x, x_stride, rows, cols, size_of(dtype)), sy = span_of(y, y_stride, rows, cols, size_of(dtype));
   if (overlap(sx, sy) && !same(sx, sy)) return fail(XP_ERR_INVALID, "x and y overlap");
   xp::NormRowsParams p = {};
   p.x = x;
@@ -392,8 +398,8 @@ xp_status xp_layernorm_backward(const void* dy, size_t dy_stride, const void* x,
   if (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)) return fail(XP_ERR_INVALID, "mean or rstd is NULL or not aligned");
   if (!aligned(gamma, size_of(wdtype))) return fail(XP_ERR_INVALID, "gamma is not aligned to its element");
   const size_t es = size_of(dtype);
-  const Span sdy = span_of("dy", dy, dy_stride, rows, cols, es), sx = span_of("x", x, x_stride, rows, cols, es);
-  const Span sdx = span_of("dx", dx, dx_stride, rows, cols, es);
+  const Span sdy = span_of(dy, dy_stride, rows, cols, es), sx = span_of(x, x_stride, rows, cols, es);
+  const Span sdx = span_of(dx, dx_stride, rows, cols, es);
   if (overlap(sdx, sx) || (overlap(sdx, sdy) && !same(sdx, sdy))) return fail(XP_ERR_INVALID, "dx overlaps x or dy");
   size_t need = 0;
   if (dgamma) {

@@ -17,7 +17,9 @@
  * Every call but *_create and *_destroy may be captured in a CUDA graph.
  * Unlike the transfers, tensors here need only their element's alignment;
  * 16-byte aligned ones are faster.  Buffers a call writes must not overlap
- * any other buffer of the call, except where said.
+ * any other buffer of the call, except where said.  (Matrices may be
+ * side-by-side columns of one wider buffer; matrices whose rows are at
+ * different distances and lie between one another's are refused.)
  */
 #ifndef XP_TRAIN_H
 #define XP_TRAIN_H

@@ -134,3 +134,35 @@ def test_step_counts_that_would_wrap(xt):
     xt.xp_adamw_step(g.handle, 1e-2)
     g.check(want)
     g.close()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 64), (8, 64), (9, 65), (10000, 64), (300, 1000), (310, 1031), (2, 9001), (3, 20000)])
+def test_layernorm_of_side_by_side_columns(xt, rows, cols, name):
+    # matrices that are columns of one buffer, in every order, give what matrices of their own give
+    torch = torch_cuda()
+    dtype, _ = _types(torch, name)
+    gen = torch.Generator("cuda").manual_seed(rows + cols)
+    x, dy = (torch.randn(rows, cols, device="cuda", generator=gen).to(dtype) for _ in range(2))
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    xt.xp_layernorm_forward(x, None, None, y, mean, rstd)
+    xt.xp_layernorm_backward(dy, x, None, mean, rstd, dx)
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0), (2, 0, 3, 1)):
+        wide = torch.full((rows, 4 * cols), 7.0, dtype=dtype, device="cuda")
+        xw, dyw, yw, dxw = (wide[:, k * cols:(k + 1) * cols] for k in order)
+        xw.copy_(x)
+        dyw.copy_(dy)
+        xt.xp_layernorm_forward(xw, None, None, yw, mean, rstd)
+        assert torch.equal(yw, y) and torch.equal(xw, x) and torch.equal(dyw, dy) and (dxw == 7).all()
+        xt.xp_layernorm_backward(dyw, xw, None, mean, rstd, dxw)
+        assert torch.equal(dxw, dx) and torch.equal(yw, y) and torch.equal(xw, x) and torch.equal(dyw, dy)
+
+
+def test_one_row_in_place_at_any_stride(xt):
+    torch = torch_cuda()
+    x = torch.randn(1, 500, device="cuda")
+    y = torch.empty_like(x)
+    xt.xp_layernorm_forward(x, None, None, y.as_strided((1, 500), (7, 1)))
+    xt.xp_layernorm_forward(x, None, None, x.as_strided((1, 500), (7, 1)))
+    assert torch.equal(x, y)

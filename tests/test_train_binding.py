@@ -139,3 +139,22 @@ def test_a_group_with_a_step_count_that_would_wrap_is_refused(step):
     table, out = (xt.xp_tensor * 1)(xt.xp_tensor(grad=1 << 20, count=5)), ctypes.c_void_p()
     assert xt._lib.xp_group_create(ctypes.byref(cfg), 1, table, ctypes.byref(out)) == xt.xp.XP_ERR_INVALID
     assert b"step" in xt._lib.xp_last_error()
+
+
+@pytest.mark.parametrize("between", [0, 1, 39, 61, 99, 100, 101, 700, 739, -1, -39, -61, -100, -739])
+def test_rows_that_share_bytes_are_refused(between):
+    # 8 rows of 40 fp32, 100 apart: a second matrix shares bytes unless its rows lie whole in the 60 between
+    from collective_transport_plane_gb300 import build
+    build.build()
+    import collective_transport_plane_gb300.xp_train as xt
+    at, stride = 1 << 20, 100
+    used = {r * stride + c for r in range(8) for c in range(40)}
+    shared = any(r * stride + c + between in used for r in range(8) for c in range(40))
+    assert shared
+    if between != 0:     # x itself is allowed
+        assert xt._lib.xp_layernorm_forward(at, stride, None, None, at + 4 * between, stride, None, None, 8, 40, 1e-5, xt.XP_F32, xt.XP_F32, None) == 1
+        assert b"overlap" in xt._lib.xp_last_error()
+    # dx never shares x
+    assert xt._lib.xp_layernorm_backward(at * 2, stride, at, stride, None, at * 3, at * 4, at + 4 * between, stride, None, None, 8, 40,
+                                         xt.XP_F32, xt.XP_F32, 0, None, 0, None) == 1
+    assert b"overlap" in xt._lib.xp_last_error()
