@@ -529,10 +529,28 @@ __device__ __forceinline__ F warp_sum(F x) {
   return x;
 }
 
+// The squares of all of a thread's elements, added in fp64: for warps whose sum
+// went out of range.  Not inlined, and after the loop over the units: kept in
+// that loop it cost registers (2^27 fp32: 85 us, 80 so).
+template <typename G>
+__device__ __noinline__ double squares64(const NormParams& prm) {
+  double sum = 0.0;
+  for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) {
+    const GroupUnit u = prm.units[prm.nunits - 1 - k];
+    const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
+    for (unsigned at = threadIdx.x * kVec; at < u.n; at += kNormThreads * kVec) {
+      float f[kVec];
+      load_some(grad + u.start + at, (int)min((unsigned)kVec, u.n - at), vec_ok(grad), f);
+      for (int i = 0; i < kVec; ++i) sum += (double)(f[i] * f[i]);
+    }
+  }
+  return sum;
+}
+
 // Each CTA adds up its units' squares and leaves one fp64 sum; the CTA that
 // arrives last adds the sums up in their order, so the result does not depend
-// on which CTA that is.  fp32 up to a warp's sum, fp64 above: an SM does 2 fp64
-// additions per clock.  The units are taken from the last to the first, so
+// on which CTA that is.  fp32 up to a warp's sum (fp64 if that overflows), fp64
+// above: an SM does 2 fp64 additions per clock.  The units are taken from the last to the first, so
 // that L2 holds the gradients a step reads first; the next unit's place is
 // looked up while one is added.
 template <typename G>
@@ -584,6 +602,7 @@ __global__ void __launch_bounds__(kNormThreads, 5) grad_norm_kernel(const __grid
     if (!more) break;
     k = after;
   }
+  if (__any_sync(0xffffffffu, !isfinite(sum))) sum = warp_sum(squares64<G>(prm));
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {

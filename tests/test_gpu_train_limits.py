@@ -166,3 +166,28 @@ def test_one_row_in_place_at_any_stride(xt):
     xt.xp_layernorm_forward(x, None, None, y.as_strided((1, 500), (7, 1)))
     xt.xp_layernorm_forward(x, None, None, x.as_strided((1, 500), (7, 1)))
     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("n,largest,lead", [(33, 1.8e19, 0), (100001, 1e19, 0), (100001, 1e19, 1), (12_000_001, 1e18, 0), (21_000_000, 7e17, 0)])
+def test_norm_of_finite_gradients_up_to_the_limit(xt, grad, n, largest, lead):
+    # every square is in fp32's range, the sum of a few is not.  As for ordinary sizes: 20 u of the sum, half of it and
+    # 2 u for the root
+    torch = torch_cuda()
+    gen = torch.Generator("cuda").manual_seed(n)
+    t = (torch.rand(n + lead, device="cuda", generator=gen) * 0.5 + 0.5).mul_(largest).to(_types(torch, grad)[0])[lead:]
+    t[::2].neg_()
+    group, report = xt.xp_group_create(None, [t]), torch.zeros(8, device="cuda")
+    xt.xp_grad_norm(group, report, max_norm=1.0)
+    sumsq = float(t.double().square().sum())
+    got = xt.xp_grad_report.from_buffer_copy(report.cpu().numpy().tobytes())
+    assert got.nonfinite == 0 and abs(got.sumsq - sumsq) <= 20 * U * sumsq
+    assert abs(got.norm - sumsq ** 0.5) <= 12 * U * sumsq ** 0.5 and abs(got.scale * sumsq ** 0.5 - 1) <= 14 * U
+    # and what is not finite still shows
+    for bad in (float("nan"), -float("inf"), 2e19):
+        keep = t[n // 2].clone()
+        t[n // 2] = bad
+        xt.xp_grad_norm(group, report, max_norm=1.0)
+        t[n // 2] = keep
+        assert report.view(torch.int32)[4].item() == 1
+    xt.xp_group_destroy(group)
