@@ -268,6 +268,9 @@ xp_status xp_group_get_step(xp_group* g, uint64_t* step, xp_stream_t stream) {
   xp_status s = check_group(g);
   if (s != XP_OK) return s;
   if (!step) return fail(XP_ERR_INVALID, "step is NULL");
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  XP_CUDA(cudaStreamIsCapturing(stream, &capture));
+  if (capture != cudaStreamCaptureStatusNone) return fail(XP_ERR_INVALID, "the step count cannot be read within a stream's capture");
   unsigned long long v = 0;
   XP_CUDA(cudaMemcpyAsync(&v, &g->state->step, sizeof v, cudaMemcpyDeviceToHost, stream));
   XP_CUDA(cudaStreamSynchronize(stream));

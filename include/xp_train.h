@@ -14,7 +14,8 @@
  * xp_last_error(), streams (every call here is asynchronous on its stream;
  * NULL = the legacy default stream), argument errors without a launch, and
  * memory owned by the caller.  No call allocates except xp_group_create.
- * Every call but *_create and *_destroy may be captured in a CUDA graph.
+ * Every call but *_create, *_destroy and xp_group_get_step may be captured in a
+ * CUDA graph.
  * Unlike the transfers, tensors here need only their element's alignment;
  * 16-byte aligned ones are faster.  Buffers a call writes must not overlap
  * any other buffer of the call, except where said.  (Matrices may be
@@ -144,7 +145,7 @@ xp_status xp_group_destroy(xp_group* g);
 xp_status xp_group_set_grads(xp_group* g, const void* const* grads, xp_stream_t stream);
 
 /* The number of steps taken, set for the calls that follow on `stream`, or
- * read (waits for `stream`). */
+ * read (waits for `stream`, and is refused while it is captured, which goes on). */
 xp_status xp_group_set_step(xp_group* g, uint64_t step, xp_stream_t stream);
 xp_status xp_group_get_step(xp_group* g, uint64_t* step, xp_stream_t stream);
 

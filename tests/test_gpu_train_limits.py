@@ -191,3 +191,22 @@ def test_norm_of_finite_gradients_up_to_the_limit(xt, grad, n, largest, lead):
         t[n // 2] = keep
         assert report.view(torch.int32)[4].item() == 1
     xt.xp_group_destroy(group)
+
+
+def test_reading_the_step_count_leaves_a_capture_as_it_is(xt):
+    torch = torch_cuda()
+    g = Group(torch, xt, [100])
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        xt.xp_adamw_step(g.handle, 1e-2, stream=stream)
+        with pytest.raises(xt.XpError) as refused:
+            xt.xp_group_get_step(g.handle, stream)
+        assert refused.value.status == xt.xp.XP_ERR_INVALID
+    assert xt.xp_group_get_step(g.handle) == 0
+    for k in range(3):
+        want = g.twin(1e-2)
+        graph.replay()
+        torch.cuda.synchronize()
+        g.check(want)
+    assert xt.xp_group_get_step(g.handle, stream) == 3
+    g.close()
