@@ -922,7 +922,8 @@ int stages_for(size_t budget, size_t per_stage, u64 turns) {
   return n < 1 ? 1 : (int)n;
 }
 
-constexpr size_t kSmemSm = 224 * 1024;   // of an SM, less what CTAs take statically
+constexpr size_t kSmemSm = kMaxDynamicSmem;   // of an SM, less what CTAs take statically
+static_assert(sizeof(SumWords<8>) <= kMaxStaticSmem, "a backward CTA's static shared memory");
 
 template <typename T, bool NARROW, int E, int R, int MODE, int MAXT>
 cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st) {
@@ -1032,7 +1033,7 @@ int resident_clusters(int csize) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
+  if (allow_dynamic_smem(kernel) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
     n = sm_count() / csize;

@@ -1,5 +1,8 @@
 """The training operators at the ends of their ranges, on the GPU: magnitudes far from 1, values that are not finite, and
 calls that a program may make although few do."""
+import threading
+import time
+
 import numpy as np
 import pytest
 
@@ -210,3 +213,43 @@ def test_reading_the_step_count_leaves_a_capture_as_it_is(xt):
         g.check(want)
     assert xt.xp_group_get_step(g.handle, stream) == 3
     g.close()
+
+
+def test_calls_of_several_threads(xt):
+    # four threads, each on its own stream, with rows of lengths that want different amounts of shared memory of the same
+    # kernel: every call is made, and gives what it gives alone
+    torch = torch_cuda()
+    rows, failed, made = 153, [], []
+
+    def inputs(cols):
+        gen = torch.Generator("cuda").manual_seed(cols)
+        x, dy = (torch.randn(rows, cols, device="cuda", generator=gen).bfloat16() for _ in range(2))
+        return dy, x, None, torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda"), torch.empty_like(x)
+
+    def calls(args, stream, until):
+        n = 0
+        while time.monotonic() < until and not failed:
+            try:
+                for _ in range(50):
+                    xt.xp_layernorm_backward(*args, stream=stream)
+            except xt.XpError as e:
+                failed.append(str(e))
+            stream.synchronize()
+            n += 50
+        made.append(n)
+
+    for backs in ((6144, 8192, 7168, 8192), (12000, 16384, 12288, 16384)):
+        all_args, streams = [inputs(c) for c in backs], [torch.cuda.Stream() for _ in backs]
+        torch.cuda.synchronize()
+        until = time.monotonic() + 3.0
+        threads = [threading.Thread(target=calls, args=(a, s, until)) for a, s in zip(all_args, streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed, failed[0]
+        for a in all_args:
+            alone = torch.empty_like(a[-1])
+            xt.xp_layernorm_backward(*a[:-1], alone)
+            assert torch.equal(alone, a[-1])
+    assert len(made) == 8 and min(made) > 0
