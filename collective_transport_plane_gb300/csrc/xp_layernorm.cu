@@ -890,15 +890,15 @@ __global__ void __launch_bounds__(32 * kPartWarps) ln_parts_kernel(const float* 
 // ---------------------------------------------------------------- launches
 
 int sm_count() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1) {
+  static PerDevice known;
+  return known.get([](int dev) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
-      v = 152;
+      n = 152;
     }
-    return v;
-  }();
-  return n;
+    return n;
+  });
 }
 
 size_t div_up(size_t a, size_t b) { return (a + b - 1) / b; }
@@ -906,10 +906,10 @@ int threads_for(size_t elems, int e) { return elems ? 32 * (int)div_up(elems, (s
 
 // A row's CTAs: enough that a slice has `most` columns at most, and more where
 // the rows are too few for the GPU's SMs, as long as a slice keeps 2048.
-int cluster_for(size_t rows, size_t cols, size_t most) {
+int cluster_for(size_t rows, size_t cols, size_t most, size_t sms) {
   int c = (int)div_up(cols, most);
   if (c > kMaxCluster8) c = kMaxCluster8;
-  while (2 * c <= kMaxCluster8 && rows * c < (size_t)sm_count() && cols / (2 * c) >= 2048) c *= 2;
+  while (2 * c <= kMaxCluster8 && rows * c < sms && cols / (2 * c) >= 2048) c *= 2;
   return c;
 }
 
@@ -949,18 +949,19 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 // moved in 4-byte words and was units in shared memory), 20046 x 3877 75.
 template <typename T, bool NARROW>
 cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
+  const size_t sms = sm_count();
   if constexpr (!NARROW) {
-    if (p.cols <= 128 && p.rows >= 64 * (size_t)sm_count()) return forward_e<T, NARROW, 8, 4, kHalf, 128>(p, 16, 1, st);
+    if (p.cols <= 128 && p.rows >= 64 * sms) return forward_e<T, NARROW, 8, 4, kHalf, 128>(p, 16, 1, st);
   }
   if (p.cols <= 256) {
-    if (p.rows >= 32 * (size_t)sm_count()) return forward_e<T, NARROW, 8, 4, kWarp, 128>(p, 32, 1, st);
+    if (p.rows >= 32 * sms) return forward_e<T, NARROW, 8, 4, kWarp, 128>(p, 32, 1, st);
     return forward_e<T, NARROW, 8, 1, kWarp, 128>(p, 32, 1, st);
   }
   constexpr size_t kOneCta = sizeof(T) == 2 ? 65536 : 32768;
-  int c = cluster_for(p.rows, p.cols, 16384);
-  if (p.cols <= kOneCta && p.rows >= (size_t)sm_count()) c = 1;
+  int c = cluster_for(p.rows, p.cols, 16384, sms);
+  if (p.cols <= kOneCta && p.rows >= sms) c = 1;
   const size_t slice = div_up(p.cols, c);
-  const bool few = p.rows * c <= 2 * (size_t)sm_count() && slice <= 4096;
+  const bool few = p.rows * c <= 2 * sms && slice <= 4096;
   if (c > 1) {
     if (few) return forward_e<T, NARROW, 8, 1, kCluster, 512>(p, threads_for(slice, 8), c, st);
     return forward_e<T, NARROW, 32, 1, kCluster, 512>(p, threads_for(slice, 32), c, st);
@@ -972,7 +973,7 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
     if (p.cols <= 1792) return forward_e<T, NARROW, 64, 1, kWarp, 128>(p, 32, 1, st);
     if (p.cols > 2048 && p.cols <= 2 * 32 * 40) return forward_e<T, NARROW, 40, 1, kCta, 512>(p, 64, 1, st);
     if (p.cols > 4096 && p.cols <= 4 * 32 * 40) return forward_e<T, NARROW, 40, 1, kCta, 512>(p, 128, 1, st);
-    if (p.cols > 4096 && p.cols <= 16384 && p.rows >= 4 * (size_t)sm_count()) return forward_e<T, NARROW, 64, 1, kCta, 512>(p, threads_for(slice, 64), 1, st);
+    if (p.cols > 4096 && p.cols <= 16384 && p.rows >= 4 * sms) return forward_e<T, NARROW, 64, 1, kCta, 512>(p, threads_for(slice, 64), 1, st);
   }
   if (p.cols <= 16384) return forward_e<T, NARROW, 32, 1, kCta, 512>(p, threads_for(slice, 32), 1, st);
   return forward_e<T, NARROW, sizeof(T) == 2 ? 64 : 32, 1, kCta, 1024>(p, threads_for(slice, sizeof(T) == 2 ? 64 : 32), 1, st);
@@ -992,21 +993,18 @@ cudaError_t forward(NormRowsParams& p, cudaStream_t st) {
 //   NARROW's layout 9973 x 1031 takes 29 us with 2 rows, 32 with 4 (the code
 //   of a turn outgrows the instruction cache) and 35 with 1.
 int resident_clusters(int csize);
-struct BackwardShape {
-  int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, NARROW: 2), else 1
-  unsigned nparts;
-};
 BackwardShape backward_shape(size_t rows, size_t cols) {
+  const size_t sms = sm_count();
   BackwardShape s;
-  s.csize = cols <= 512 ? 1 : cluster_for(rows, cols, 512 * 16);
+  s.csize = cols <= 512 ? 1 : cluster_for(rows, cols, 512 * 16, sms);
   const size_t slice = div_up(cols, s.csize);
   s.e = slice <= 256 ? 8 : slice <= 8192 ? 16 : 32;
   s.threads = cols <= 128 ? 16 : threads_for(slice, s.e);
   s.groups = s.csize > 1 ? 1 : 512 / s.threads;
   if (s.threads > 32 && s.groups > 15) s.groups = 15;   // named barriers
-  while (s.groups > 1 && div_up(rows, s.groups) < (size_t)sm_count()) s.groups /= 2;   // few rows: an SM each
+  while (s.groups > 1 && div_up(rows, s.groups) < sms) s.groups /= 2;   // few rows: an SM each
   if (s.threads == 16 && s.groups == 1) s.threads = 32;   // a whole warp
-  const size_t most = (size_t)resident_clusters(s.csize);
+  const size_t most = s.csize == 1 ? sms : (size_t)resident_clusters(s.csize);
   s.many = s.e <= 16 && rows >= 8 * s.groups * most;   // two turns for everyone at least
   const size_t want = div_up(rows, (size_t)s.groups);
   s.nparts = (unsigned)(want < most ? want : most);
@@ -1018,27 +1016,26 @@ BackwardShape backward_shape(size_t rows, size_t cols) {
 // suggest, as a cluster lies within one GPC (of 152 SMs' worth of 5-CTA clusters, a second
 // wave of a few doubles the time).
 int resident_clusters(int csize) {
-  static int known[kMaxCluster8 + 1] = {};
-  if (csize == 1) return sm_count();
-  if (known[csize] > 0) return known[csize];
-  const auto kernel = ln_backward_kernel<bf16, false, 16, 1, kCluster>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(csize);
-  cfg.blockDim = dim3(512);
-  cfg.dynamicSmemBytes = 200 * 1024;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = csize;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (allow_dynamic_smem(kernel) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    n = sm_count() / csize;
-  }
-  return known[csize] = n;
+  static PerDevice known[kMaxCluster8 + 1];
+  return known[csize].get([csize](int) {
+    const auto kernel = ln_backward_kernel<bf16, false, 16, 1, kCluster>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(csize);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 200 * 1024;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = csize;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_dynamic_smem(kernel) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = sm_count() / csize;
+    }
+    return n;
+  });
 }
 
 template <typename T, bool NARROW, int E, int R, int MODE>
@@ -1099,14 +1096,10 @@ cudaError_t launch_ln_forward(NormRowsParams& p, int dtype, cudaStream_t st) {
   return wide ? forward<bf16, false>(p, st) : forward<bf16, true>(p, st);
 }
 
-cudaError_t ln_backward_parts(size_t rows, size_t cols, unsigned* nparts) {
-  *nparts = rows && cols ? backward_shape(rows, cols).nparts : 0;
-  return cudaSuccess;
-}
+BackwardShape ln_backward_shape(size_t rows, size_t cols) { return backward_shape(rows, cols); }
 
-cudaError_t launch_ln_backward(NormRowsParams& p, int dtype, cudaStream_t st) {
+cudaError_t launch_ln_backward(NormRowsParams& p, const BackwardShape& s, int dtype, cudaStream_t st) {
   const size_t es = dtype == XP_F32 ? 4 : 2;
-  const BackwardShape s = backward_shape(p.rows, p.cols);
   const bool wide = wide_rows(p.x, p.x_stride, p.cols, es) && wide_rows(p.dy, p.dy_stride, p.cols, es) && wide_rows(p.out, p.out_stride, p.cols, es) && wide_w(p.gamma);
   cudaError_t e;
   if (dtype == XP_F32)

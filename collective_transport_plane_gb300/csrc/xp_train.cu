@@ -195,6 +195,8 @@ xp_status check_sizes(size_t rows, size_t cols, int dtype, int wdtype) {
   return XP_OK;
 }
 
+size_t workspace_bytes_of(const xp::BackwardShape& s, size_t cols) { return (size_t)s.nparts * 2 * cols * sizeof(float); }
+
 }  // namespace
 
 extern "C" {
@@ -374,9 +376,7 @@ xp_status xp_layernorm_forward(const void* x, size_t x_stride, const void* gamma
 xp_status xp_layernorm_workspace(size_t rows, size_t cols, size_t* bytes) {
   if (!bytes) return fail(XP_ERR_INVALID, "bytes is NULL");
   if (cols > XP_LAYERNORM_MAX_COLS || rows > XP_LAYERNORM_MAX_ROWS) return fail(XP_ERR_INVALID, "rows %zu or cols %zu too large", rows, cols);
-  unsigned parts = 0;
-  XP_CUDA(xp::ln_backward_parts(rows, cols, &parts));
-  *bytes = (size_t)parts * 2 * cols * sizeof(float);
+  *bytes = rows && cols ? workspace_bytes_of(xp::ln_backward_shape(rows, cols), cols) : 0;
   return XP_OK;
 }
 
@@ -404,10 +404,10 @@ xp_status xp_layernorm_backward(const void* dy, size_t dy_stride, const void* x,
   const Span sdy = span_of(dy, dy_stride, rows, cols, es), sx = span_of(x, x_stride, rows, cols, es);
   const Span sdx = span_of(dx, dx_stride, rows, cols, es);
   if (overlap(sdx, sx) || (overlap(sdx, sdy) && !same(sdx, sdy))) return fail(XP_ERR_INVALID, "dx overlaps x or dy");
-  size_t need = 0;
+  const xp::BackwardShape shape = xp::ln_backward_shape(rows, cols);
   if (dgamma) {
-    if ((s = xp_layernorm_workspace(rows, cols, &need)) != XP_OK) return s;
-    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    const size_t need = workspace_bytes_of(shape, cols);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
       return fail(XP_ERR_INVALID, "workspace of %zu bytes (NULL, or not 16-byte aligned, or below the %zu needed)", workspace_bytes, need);
   }
   xp::NormRowsParams p = {};
@@ -427,7 +427,7 @@ xp_status xp_layernorm_backward(const void* dy, size_t dy_stride, const void* x,
   p.cols = (unsigned)cols;
   p.gamma_bf16 = wdtype == XP_BF16;
   p.accumulate = accumulate;
-  XP_CUDA(xp::launch_ln_backward(p, dtype, stream));
+  XP_CUDA(xp::launch_ln_backward(p, shape, dtype, stream));
   return XP_OK;
 }
 

@@ -4,12 +4,36 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "xp_train.h"
 
 namespace xp {
+
+// A positive number that belongs to a device, asked for once: whoever comes
+// first on whatever thread, every call gets the same answer from then on, as a
+// workspace's size and the launch that fills it must.
+class PerDevice {
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices] = {};
+
+ public:
+  template <typename Ask>
+  int get(Ask ask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+      (void)cudaGetLastError();
+      dev = 0;
+    }
+    if (dev >= kDevices) return ask(dev);
+    int n = known_[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    const int asked = ask(dev);
+    return known_[dev].compare_exchange_strong(n, asked, std::memory_order_acq_rel) ? asked : n;
+  }
+};
 
 // One tensor of a group, in the group's device table.
 struct GroupTensor {
@@ -119,8 +143,13 @@ cudaError_t launch_set_step(GroupState* s, unsigned long long step, double beta1
 cudaError_t launch_decode(const DecodeParams& p, int out_dtype, cudaStream_t st);
 
 cudaError_t launch_ln_forward(NormRowsParams& p, int dtype, cudaStream_t st);
-// Writes the number of partial rows to *nparts; workspace holds nparts * 2 * cols floats.
-cudaError_t ln_backward_parts(size_t rows, size_t cols, unsigned* nparts);
-cudaError_t launch_ln_backward(NormRowsParams& p, int dtype, cudaStream_t st);
+// How a backward pass over so many rows (1 at least) is laid out: asked for
+// once per call, for the workspace (nparts * 2 * cols floats) and the launch.
+struct BackwardShape {
+  int e, many, threads, groups, csize;   // many: 4 rows a turn (fp32, unaligned: 2), else 1
+  unsigned nparts;                       // partial sums per column
+};
+BackwardShape ln_backward_shape(size_t rows, size_t cols);
+cudaError_t launch_ln_backward(NormRowsParams& p, const BackwardShape& s, int dtype, cudaStream_t st);
 
 }  // namespace xp

@@ -3,6 +3,7 @@ and launches nothing."""
 import ctypes
 import os
 import re
+import shutil
 import subprocess
 import sys
 
@@ -158,3 +159,29 @@ def test_rows_that_share_bytes_are_refused(between):
     assert xt._lib.xp_layernorm_backward(at * 2, stride, at, stride, None, at * 3, at * 4, at + 4 * between, stride, None, None, 8, 40,
                                          xt.XP_F32, xt.XP_F32, 0, None, 0, None) == 1
     assert b"overlap" in xt._lib.xp_last_error()
+
+
+@pytest.fixture(scope="module")
+def fake_runtime(tmp_path_factory):
+    from collective_transport_plane_gb300 import build
+    build.build()
+    exe = str(tmp_path_factory.mktemp("fake") / "fake_runtime")
+    objects = [os.path.join(build.BUILD, name) for name in ("xp_train.o", "xp_adamw.o", "xp_layernorm.o")]
+    if not all(map(os.path.exists, objects)):
+        build.build(force=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(shutil.which(build.nvcc()))), "include")
+    done = subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", cuda, "-I", build.INCLUDE, os.path.join(ROOT, "tests", "fake_runtime.cpp"),
+                           *objects, "-o", exe], capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr[-2000:]
+    return lambda what: [[int(n) for n in line.split()] for line in subprocess.run([exe, what], capture_output=True, text=True, check=True).stdout.splitlines()]
+
+
+def test_workspaces_are_the_current_devices(fake_runtime):
+    # a part for each SM, and in clusters of two for each cluster that fits (here a quarter of the SMs)
+    assert fake_runtime("devices") == [[152, 38], [76, 19], [10, 2], [76, 19], [152, 38]]
+
+
+def test_threads_agree_on_a_workspace(fake_runtime):
+    for _ in range(5):
+        for got in fake_runtime("threads"):
+            assert len(set(got)) == 1 and len(got) == 17 and got[0] > 0
