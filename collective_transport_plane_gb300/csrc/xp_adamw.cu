@@ -220,9 +220,9 @@ __device__ __forceinline__ unsigned step_key(unsigned seed, unsigned step) { ret
 // branches of the functions' own: Markstein's iterations (P. W. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor", IBM Journal of Research and Development 34, 1990), in which
-// fused multiply-adds give exact remainders.  Correctly rounded where nothing
-// over- or underflows, as the callers see to (every significand of a square
-// root, and 5e10 random quotients, equal __fsqrt_rn's and __fdiv_rn's).
+// fused multiply-adds give exact remainders.  Correctly rounded where neither
+// results nor remainders leave fp32's normal range, as the caller sees to.  (A
+// remainder is a multiple of 2^-46 of its numerator at least.)
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float approximate_rsqrt(float x) {
   float r;
@@ -352,13 +352,21 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
   const unsigned turns = (u.n + kTurn - 1) / kTurn;
   float alpha = 0.f, rs = 0.f;
   unsigned key = 0;
+  unsigned top_v = 0, least_m = 0;   // patterns between which root2 and quotient2 serve (8-bit states)
   auto coefficients = [&](unsigned turn) {   // after the first turn's loads are on their way
     if (turn) return;
     __syncthreads();
     if (S8 && threadIdx.x == 0) count_in();
     alpha = lr * s_coef[0];
     rs = s_coef[1];
-    if (S8) key = step_key(prm.seed, s_step);
+    if (S8) {
+      key = step_key(prm.seed, s_step);
+      // with v up to 2^40 a denominator is between 2^-50 and `most`; numerators of 2^-100 and more have exact
+      // remainders, and of 2^-120 `most` and more normal quotients
+      const float most = 0x1p20f * rs + prm.eps;
+      top_v = most <= 0x1p100f && fabsf(alpha) <= 0x1p20f ? 167u << 23 : 0u;
+      least_m = alpha != 0.f ? 2u * __float_as_uint(fmaxf(0x1p-100f, 0x1p-120f * most) / fabsf(alpha)) : 0u;
+    }
   };
   if (turns == 0) coefficients(0);
   unsigned turn = 0;
@@ -398,15 +406,17 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
         m[k] = add2(mul2(m[k], prm.beta1), mul2(gi, prm.one_minus_beta1));
         v[k] = add2(mul2(v[k], prm.beta2), mul2(mul2(gi, prm.one_minus_beta2), gi));
       }
-      unsigned tm = 0, tv = 0, lv = 0xffffffffu;   // largest magnitudes, smallest v
+      unsigned tm = 0, tv = 0, lv = 0xffffffffu, lm = 0xffffffffu;   // largest magnitudes, smallest v, smallest m but 0 (less 1)
 #pragma unroll
       for (int k = 0; k < kVec / 2; ++k) {
-        tm = max(max(tm, __float_as_uint(m[k].x) & 0x7fffffffu), __float_as_uint(m[k].y) & 0x7fffffffu);
+        const unsigned mx = __float_as_uint(m[k].x) * 2u, my = __float_as_uint(m[k].y) * 2u;   // without their signs
+        tm = max(max(tm, mx), my);
+        lm = __viaddmin_u32(my, 0xffffffffu, __viaddmin_u32(mx, 0xffffffffu, lm));
         tv = max(max(tv, __float_as_uint(v[k].x)), __float_as_uint(v[k].y));
         lv = min(min(lv, __float_as_uint(v[k].x)), __float_as_uint(v[k].y));
       }
-      // v in [2^-100, 2^100] and m up to 2^100: roots, denominators and remainders are in range
-      const bool in_range = lv >= 27u << 23 && tv <= 227u << 23 && tm <= 227u << 23 && fabsf(alpha) <= 1e6f;
+      // v in [2^-100, 2^40], m up to 2^50 and above least_m or 0: roots, quotients and remainders are in range
+      const bool in_range = lv >= 27u << 23 && tv <= top_v && tm <= 177u << 24 && lm >= least_m;
       auto weights = [&](auto root, auto quotient) {
 #pragma unroll
         for (int k = 0; k < kVec / 2; ++k) {
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(kStepThreads + kBooksThreads<S8>, 3) adamw_ker
                 [](float2 a, float2 d) { return make_float2(__fdiv_rn(a.x, d.x), __fdiv_rn(a.y, d.y)); });
       store_vec(place.param, p);
       if (place.copy) store_vec(place.copy, p);
-      unsigned top = (tm >> 23) << 16 | (tv >> 23 & 0xffu);
+      unsigned top = (tm >> 24) << 16 | (tv >> 23 & 0xffu);
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int em = (int)(top >> 16), ev = (int)(top & 0xffffu);

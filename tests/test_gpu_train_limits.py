@@ -253,3 +253,50 @@ def test_calls_of_several_threads(xt):
             xt.xp_layernorm_backward(*a[:-1], alone)
             assert torch.equal(alone, a[-1])
     assert len(made) == 8 and min(made) > 0
+
+
+def _states8_step(torch, xt, n, seed, p, g, m, v, lr, eps, beta2=0.999, step=41):
+    """The weights that one step with 8-bit states makes of fp32 arrays, and what the same program in fp32 does."""
+    half = np.full(n, 1 << 15)
+    (cm, sm), (cv, sv) = train.encode(m, half, True), train.encode(v, half, False)
+    t = [torch.from_numpy(a).cuda() for a in (p, g, cm, sm, cv, sv)]
+    group = xt.xp_group_create([t[0]], [t[1]], [t[2]], [t[4]], m_scales=[t[3]], v_scales=[t[5]], seed=seed, step=step, eps=eps, beta2=beta2)
+    xt.xp_adamw_step(group, lr)
+    xt.xp_group_destroy(group)
+    m, v = train.decode(cm, sm, True).astype(np.float32), train.decode(cv, sv, False).astype(np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        return t[0].cpu().numpy(), train.adamw(p, g, m, v, step + 1, lr, 0.0, eps=eps, beta2=beta2)[0]
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-8, 1.0, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("m_power", [-130, -115, -100, -90, -60, 0, 45, 60, 110])
+@pytest.mark.parametrize("v_power", [-110, -95, -60, -20, 0, 35, 45, 90, 110])
+def test_steps_of_8_bit_states_at_any_magnitude(xt, m_power, v_power, eps):
+    # the weights are 0, so that every bit of the quotient shows: the fp32 program's, also where the quotient, its
+    # remainder or its denominator is near the ends of fp32's range
+    torch = torch_cuda()
+    n = 1 << 14
+    rng = np.random.default_rng(100000 + 200 * m_power + v_power)
+    g = (rng.standard_normal(n) * 2.0 ** min(m_power, 62)).astype(np.float32)
+    g[rng.random(n) < 0.1] = 0
+    m = (rng.standard_normal(n) * 2.0 ** (m_power + rng.integers(-3, 4, n))).astype(np.float32)
+    m[rng.random(n) < 0.1] = 0
+    v = ((rng.random(n) + 0.125) * 2.0 ** (v_power + rng.integers(-3, 4, n))).astype(np.float32)
+    for lr in (1e-3, 0.5, 0.0):
+        got, want = _states8_step(torch, xt, n, 5, np.zeros(n, np.float32), g, m, v, lr, eps)
+        assert np.array_equal(got, want, equal_nan=True), (lr, int((got != want).sum()))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_quotients_and_roots_of_8_bit_states(xt, seed):
+    # 4 million pairs with random significands and magnitudes, as ordinary training has them and beyond
+    torch = torch_cuda()
+    n = 1 << 22
+    rng = np.random.default_rng(seed)
+    spread = (6, 20, 40, 60)[seed]
+    g = (rng.standard_normal(n) * 2.0 ** rng.uniform(-spread, spread / 4, n)).astype(np.float32)
+    m = (rng.standard_normal(n) * 2.0 ** rng.uniform(-spread, spread / 4, n)).astype(np.float32)
+    v = (rng.random(n) * 2.0 ** rng.uniform(-spread, spread / 4, n) + 1e-30).astype(np.float32)
+    for p in (np.zeros(n, np.float32), rng.standard_normal(n).astype(np.float32)):
+        got, want = _states8_step(torch, xt, n, 5, p, g, m, v, 3e-4, 1e-8)
+        assert np.array_equal(got, want), int((got != want).sum())
