@@ -300,3 +300,27 @@ def test_quotients_and_roots_of_8_bit_states(xt, seed):
     for p in (np.zeros(n, np.float32), rng.standard_normal(n).astype(np.float32)):
         got, want = _states8_step(torch, xt, n, 5, p, g, m, v, 3e-4, 1e-8)
         assert np.array_equal(got, want), int((got != want).sum())
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols,pad", [(20000, 256, 0), (20000, 512, 0), (10000, 1024, 0), (9973, 1031, 6), (40000, 95, 0), (40000, 96, 0), (40000, 96, 1), (9729, 8, 0),
+                                           (30001, 64, 0), (3000, 2080, 0), (2999, 4097, 0), (1300, 8192, 0), (700, 12000, 0), (611, 12001, 0), (400, 40001, 0),
+                                           (170, 66000, 0), (153, 300, 0), (7, 5000, 0)])
+def test_weight_gradients_add_every_row_once(xt, rows, cols, pad, name):
+    # small whole numbers, mean 0 and rstd 1: every product and sum is exact (at most 32 * 40000 < 2^24), in whatever order,
+    # so a row left out or taken twice, in any of the layouts, turns or tails, shows in the column's last bit
+    torch = torch_cuda()
+    dtype, _ = _types(torch, name)
+    rng = np.random.default_rng(rows + cols)
+    x, dy = (_matrix(torch, rng.integers(-k, k + 1, (rows, cols)).astype(np.float64), dtype, pad) for k in (4, 8))
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    gamma, dx = torch.ones(cols, dtype=dtype, device="cuda"), torch.empty_like(x)
+    start = torch.from_numpy(rng.integers(-9, 10, (2, cols)).astype(np.float32)).cuda()
+    dgamma, dbeta = start[0].clone(), start[1].clone()
+    work = torch.full((xt.xp_layernorm_workspace(rows, cols),), 255, dtype=torch.uint8, device="cuda")
+    want = (dy.double() * x.double()).sum(0).float(), dy.double().sum(0).float()
+    xt.xp_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, work)
+    assert torch.equal(dgamma, want[0]) and torch.equal(dbeta, want[1])
+    dgamma, dbeta = start[0].clone(), start[1].clone()
+    xt.xp_layernorm_backward(dy, x, None, mean, rstd, dx, dgamma, dbeta, work, accumulate=True)
+    assert torch.equal(dgamma, want[0] + start[0]) and torch.equal(dbeta, want[1] + start[1])
