@@ -65,7 +65,7 @@ _forward, _backward, _norm, _step, _decode = (_lib.xp_layernorm_forward, _lib.xp
 _DTYPES = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16, "torch.uint8": XP_U8}
 _types = {}   # torch dtype -> xp_dtype, filled as types are met
 _REPORT_BYTES = ctypes.sizeof(xp_grad_report)
-_gradients = {}   # group -> (its tensors' lengths, their gradients' xp_dtype)
+_gradients = {}   # group -> (its tensors' lengths, their gradients' type)
 
 
 def _dtype(t) -> int:
@@ -178,7 +178,7 @@ def xp_group_create(params, grads, m=None, v=None, *, m_scales=None, v_scales=No
     table = (xp_tensor * max(n, 1))(*[xp_tensor(*row) for row in rows])
     out = ctypes.c_void_p()
     _check(_lib.xp_group_create(ctypes.byref(cfg), n, table, ctypes.byref(out)), "xp_group_create")
-    _gradients[out.value] = counts, cfg.grad_dtype
+    _gradients[out.value] = counts, grads[0].dtype
     return out.value
 
 
@@ -194,7 +194,10 @@ def xp_group_set_grads(group: int, grads, stream=None) -> None:
     counts, dtype = _gradients[group]
     if len(grads) != len(counts):
         raise ValueError(f"{len(grads)} gradients for {len(counts)} tensors")
-    ptrs = (ctypes.c_void_p * len(counts))(*[_vector(t, n, f"grad {i}", dtype) for i, (t, n) in enumerate(zip(grads, counts))])
+    if not all([t.numel() == n and t.dtype == dtype and t.is_contiguous() for t, n in zip(grads, counts)]):
+        for i, (t, n) in enumerate(zip(grads, counts)):
+            _vector(t, n, f"grad {i}", _types[dtype])
+    ptrs = (ctypes.c_void_p * len(counts))(*[t.data_ptr() for t in grads])
     _check(_lib.xp_group_set_grads(group, ptrs, _stream(stream)), "xp_group_set_grads")
 
 
