@@ -539,22 +539,40 @@ __device__ __forceinline__ F warp_sum(F x) {
   return x;
 }
 
-// The squares of all of a thread's elements, added in fp64: for warps whose sum
-// went out of range.  Not inlined, and after the loop over the units: kept in
-// that loop it cost registers (2^27 fp32: 85 us, 80 so).
+// A warp's squares with sums in fp64 beyond eight elements, where its fp32 sum
+// of unit `bad` became an infinity.  (Not a NaN: squares give that only where
+// an element is one.)  If an element's own square is infinite there, that is the
+// answer; else all units are added up again.  Not inlined, and after the loop
+// over the units: what the call needs there cost the loop registers (2^27 fp32:
+// 85 us, 80 so).
 template <typename G>
-__device__ __noinline__ double squares64(const NormParams& prm) {
+__device__ __noinline__ double squares64(const NormParams& prm, unsigned bad) {
   double sum = 0.0;
-  for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) {
+  bool infinite = false;
+  auto add_unit = [&](unsigned k) {
     const GroupUnit u = prm.units[prm.nunits - 1 - k];
     const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
     for (unsigned at = threadIdx.x * kVec; at < u.n; at += kNormThreads * kVec) {
-      float f[kVec];
+      float f[kVec], eight = 0.f;
       load_some(grad + u.start + at, (int)min((unsigned)kVec, u.n - at), vec_ok(grad), f);
-      for (int i = 0; i < kVec; ++i) sum += (double)(f[i] * f[i]);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) eight += f[i] * f[i];
+      if (isfinite(eight)) {
+        sum += (double)eight;
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        infinite |= isinf(f[i] * f[i]);
+        sum += (double)(f[i] * f[i]);
+      }
     }
-  }
-  return sum;
+  };
+  add_unit(bad);
+  if (__any_sync(0xffffffffu, infinite)) return (double)__int_as_float(0x7f800000);
+  sum = 0.0;
+  for (unsigned k = blockIdx.x; k < prm.nunits; k += gridDim.x) add_unit(k);
+  return warp_sum(sum);
 }
 
 // Each CTA adds up its units' squares and leaves one fp64 sum; the CTA that
@@ -567,6 +585,10 @@ template <typename G>
 __global__ void __launch_bounds__(kNormThreads, 5) grad_norm_kernel(const __grid_constant__ NormParams prm) {
   __shared__ double s_sum[kNormThreads / 32];
   __shared__ bool s_last;
+  // Where a unit whose sum became an infinity is noted: fp32 has no register to
+  // spare (2^27: 82 us in one, 80 so), bf16 has (44.5 us, 47 in shared memory).
+  constexpr bool kBadShared = sizeof(G) == 4;
+  __shared__ unsigned s_bad[kBadShared ? kNormThreads / 32 : 1];
   constexpr unsigned kTurn = kNormThreads * kVec;
   constexpr int kDeep = sizeof(G) == 2 ? 4 : 2;   // loads of a thread in flight, 64 bytes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -576,6 +598,7 @@ __global__ void __launch_bounds__(kNormThreads, 5) grad_norm_kernel(const __grid
   let_successor_start();
   const G* grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
   double sum = 0.0;
+  unsigned bad = 0;
   while (true) {
     const G* g = grad + u.start + threadIdx.x * kVec;
     const unsigned n = u.n, after = k + gridDim.x;
@@ -608,11 +631,18 @@ __global__ void __launch_bounds__(kNormThreads, 5) grad_norm_kernel(const __grid
     }
     if (more) grad = static_cast<const G*>(prm.tensors[u.tensor].grad);
     const float w = warp_sum(((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
-    if (lane == 0) sum += (double)w;
+    if (lane == 0) {
+      sum += (double)w;
+      if (kBadShared && isinf(w)) s_bad[warp] = k;
+    }
+    if (!kBadShared && isinf(w)) bad = k;
     if (!more) break;
     k = after;
   }
-  if (__any_sync(0xffffffffu, !isfinite(sum))) sum = warp_sum(squares64<G>(prm));
+  if (__any_sync(0xffffffffu, isinf(sum))) {
+    __syncwarp();
+    sum = squares64<G>(prm, kBadShared ? s_bad[warp] : bad);
+  }
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {

@@ -155,8 +155,10 @@ xp_status xp_group_get_step(xp_group* g, uint64_t* step, xp_stream_t stream);
  * the norm over all of them.  Squares are fp32: a gradient element beyond
  * 1.8e19 in magnitude overflows its square, and reads as not finite; one below
  * 1e-19 loses precision in it, and counts as 0 below 2e-23.  They are added in
- * fp32 within a warp's part of 2048 to 8192 elements and in fp64 beyond (all in
- * fp64 where fp32 overflows), in an order that the lengths alone decide. */
+ * fp32 within a warp's part of 2048 to 8192 elements and in fp64 beyond (in fp64
+ * beyond eight elements where fp32 overflows), in an order that the lengths
+ * alone decide.  sumsq is a NaN where a gradient is one, an infinity where one
+ * overflows its square or is infinite, and finite otherwise. */
 xp_status xp_grad_norm(xp_group* g, float grad_scale, float max_norm, int accumulate, xp_grad_report* report,
                        xp_stream_t stream);
 

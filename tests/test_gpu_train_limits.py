@@ -196,6 +196,32 @@ def test_norm_of_finite_gradients_up_to_the_limit(xt, grad, n, largest, lead):
     xt.xp_group_destroy(group)
 
 
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [100, 5000, 9_000_001])
+def test_norm_names_what_is_not_finite(xt, grad, n):
+    # infinities give an infinite norm, a NaN anywhere a NaN, beside ordinary elements or ones whose squares only add up
+    # to an infinity in fp32
+    torch = torch_cuda()
+    t = torch.ones(n, device="cuda").to(_types(torch, grad)[0])
+    group, report = xt.xp_group_create(None, [t]), torch.zeros(8, device="cuda")
+    inf, nan = float("inf"), float("nan")
+    for fill in (1.0, 1.7e19):
+        for where, want in (({}, None), ({0: inf}, inf), ({n - 1: -inf}, inf), ({n // 2: inf, n // 3: inf}, inf), ({n - 1: nan}, nan),
+                            ({0: inf, n - 1: nan}, nan), ({0: nan, 1: inf}, nan), ({k: inf for k in range(0, n, max(1, n // 50))}, inf)):
+            t.fill_(fill)
+            for k, value in where.items():
+                t[k] = value
+            xt.xp_grad_norm(group, report, max_norm=1.0)
+            norm = report[2].item()
+            assert report.view(torch.int32)[4].item() == (want is not None)
+            if want is None:
+                exact = t[0].double().item() * n ** 0.5
+                assert abs(norm - exact) <= 12 * U * exact
+            else:
+                assert norm == want or norm != norm and want != want
+    xt.xp_group_destroy(group)
+
+
 def test_reading_the_step_count_leaves_a_capture_as_it_is(xt):
     torch = torch_cuda()
     g = Group(torch, xt, [100])
