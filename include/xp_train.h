@@ -44,8 +44,9 @@ extern "C" {
  * apart (>= cols); gamma and beta are `wdtype` (XP_F32 or XP_BF16), cols
  * each; either may be NULL (1 and 0).  mean and rstd (fp32, rows each) may be
  * NULL where no backward pass follows.  Statistics are fp32, over the row's
- * own values (two sums: the second about the mean); y is rounded once.  y may
- * be x itself when the strides are equal.  rows == 0 is a no-op. */
+ * own values (two sums: the second about the mean; their terms have to stay
+ * below 3.4e38, which deviations of 1e16 do in the longest rows); y is rounded
+ * once.  y may be x itself when the strides are equal.  rows == 0 is a no-op. */
 xp_status xp_layernorm_forward(const void* x, size_t x_stride, const void* gamma, const void* beta, void* y,
                                size_t y_stride, float* mean, float* rstd, size_t rows, size_t cols, float eps,
                                xp_dtype dtype, xp_dtype wdtype, xp_stream_t stream);
@@ -63,8 +64,9 @@ xp_status xp_layernorm_workspace(size_t rows, size_t cols, size_t* bytes);
  * zeroes them otherwise).  dx may be dy itself when the strides are equal.
  * `workspace` holds the rows' partial sums (16-byte aligned; its bytes are
  * checked against xp_layernorm_workspace); it is not needed, and may be NULL,
- * where dgamma is NULL.  Sums are fp32 in an order that depends on the sizes
- * alone, so equal calls give equal bits. */
+ * where dgamma is NULL.  Sums are fp32, in an order that depends on the sizes,
+ * the type, the device, and whether rows and weights begin and end at multiples
+ * of 16 bytes: equal calls on buffers alike in that give equal bits. */
 xp_status xp_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size_t x_stride, const void* gamma,
                                 const float* mean, const float* rstd, void* dx, size_t dx_stride, float* dgamma,
                                 float* dbeta, size_t rows, size_t cols, xp_dtype dtype, xp_dtype wdtype,
@@ -72,6 +74,10 @@ xp_status xp_layernorm_backward(const void* dy, size_t dy_stride, const void* x,
 
 /* ------------------------------------------- groups of tensors and AdamW */
 
+/* A group has one step count and one set of partial sums: calls on it follow
+ * one another, on one stream or on streams that wait for each other.  Different
+ * groups, and layer norm calls with workspaces of their own, may run at the same
+ * time, and be made by different threads. */
 typedef struct xp_group xp_group;   /* opaque, owned by the library */
 
 /* One tensor of a group: device pointers, owned by the caller, valid until
@@ -110,9 +116,11 @@ typedef struct {
  * a sign bit (K = 119).  Rounding to a code is stochastic: 20 bits (a 16-bit
  * hash h of the seed, the step and the element's position, as 16 h + 8) are
  * added to the fp32 pattern before it is cut, so a state's expected value is
- * kept although one step changes v by less than a code.  A v of 2^-129 or
- * more never rounds to 0.  The position of element i of tensor k is i + 32 times the
- * blocks of tensors 0 .. k - 1. */
+ * kept although one step changes v by less than a code.  That holds from code 1
+ * up, 2^-15 (m) and 2^-31 (v) of the block's power of two: below it an m becomes
+ * 0 or code 1, and a v code 1, unless the v is below 2^-129 and the code stands
+ * for 0.  The position of element i of tensor k is i + 32 times the blocks of
+ * tensors 0 .. k - 1. */
 #define XP_STATE8_BLOCK 32
 
 /* The norm's outcome, in device memory (16-byte aligned). */
