@@ -941,7 +941,7 @@ cudaError_t forward_e(NormRowsParams& p, int threads, int csize, cudaStream_t st
 // 50 us, 63 with 32; 8192: 45 and 46; 4000 x 20000: 58 and 90; 4096 itself 46.5
 // and 45) unless the rows are few (310 x 8193: 8.5 us, 6.8 with 32).  40 where that makes
 // two or four full warps of what were three or five (30000 x 2400: 50 us, 56 with 32;
-// 13000 x 5120: 45, 46 with 64).  Warps of 40 and 64 skip the units of which
+// against 64: 3000 x 5120 13.2 and 14.5, 13000 x 5120 44.5 and 45.5, 13000 x 4609 unaligned 56 and 61).  Warps of 40 and 64 skip the units of which
 // they have no column (60000 x 1056: 46 us, 54 without); with 32 that cost more
 // than it gave (8000 x 8160: 48 us, 46 without).  2000 x 40032 takes 86 us (125
 // in a cluster of 3).
