@@ -90,7 +90,7 @@ def decode(code, scale, signed):
     n = len(code)
     c = _blocks(code.astype(np.int64))
     mag = c % 128 if signed else c
-    at = mag + 8 * scale.astype(np.int64)[:, None] - (119 if signed else 247)
+    at = np.maximum(mag + 8 * scale.astype(np.int64)[:, None] - (119 if signed else 247), 0)   # below the least pattern: 0
     with np.errstate(over="ignore"):
         x = np.where(mag == 0, 0.0, np.ldexp(1 + (at % 8) / 8, at // 8 - 127))
     x = np.where(at < 8, at * 2.0 ** -129 * (mag > 0), x)        # patterns without an exponent are subnormal numbers

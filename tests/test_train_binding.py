@@ -1,5 +1,5 @@
-"""What the binding of the training operators refuses before a call, on the CPU, against a library that records its calls
-and launches nothing."""
+"""The training operators' host side, on the CPU: what the binding refuses before a call, against a library that records
+its calls and launches nothing; the library's own rules, refusals and launches, against a runtime that runs nothing."""
 import ctypes
 import os
 import re
@@ -185,3 +185,18 @@ def test_threads_agree_on_a_workspace(fake_runtime):
     for _ in range(5):
         for got in fake_runtime("threads"):
             assert len(set(got)) == 1 and len(got) == 17 and got[0] > 0
+
+
+def test_codes_below_the_least_pattern_stand_for_0():
+    # codes of blocks of small scales whose patterns would be negative, and the code of pattern 0 that a v below 2^-129 takes
+    import numpy as np
+
+    from oracle import train
+    for signed, k in ((True, 119), (False, 247)):
+        for e in range(0, 40):
+            codes = np.arange(128, dtype=np.uint8)
+            got = train.decode(codes, np.full(4, e, np.uint8), signed)
+            bits = np.where(codes == 0, 0, np.maximum(codes.astype(np.int64) + 8 * e - k, 0)) << 20
+            assert np.array_equal(got, bits.astype(np.uint32).view(np.float32).astype(np.float64))
+    c, e = train.encode(np.array([2.0 ** -140, 2.0 ** -129, 2.0 ** -100], np.float32), np.zeros(3, np.int64), False)
+    assert c[0] == 247 - 8 * e[0].astype(int) and train.decode(c, e, False).tolist() == [0.0, 2.0 ** -129, 2.0 ** -100]
