@@ -4,6 +4,7 @@
 //   fake_runtime devices   parts of a backward pass on devices of 152, 76 and 10 SMs, in turn
 //   fake_runtime threads   the same size asked for by 16 threads at once, while the runtime's
 //                          answer changes from call to call
+//   fake_runtime launches  the largest of what layer norm launches ask for over a sweep of sizes
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -19,6 +20,9 @@ constexpr int kSms[] = {152, 76, 10};
 thread_local int current = 0;
 std::atomic<int> asked{0};
 bool changing = false;
+struct {
+  size_t launches = 0, smem = 0, threads = 0, cluster = 0, broken = 0;
+} seen;
 }  // namespace
 
 namespace xp {
@@ -38,7 +42,18 @@ cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunch
 cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 const char* cudaGetErrorString(cudaError_t) { return ""; }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t*, const void*, void**) { return cudaSuccess; }
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void*, void**) {
+  size_t cluster = 1;
+  for (unsigned i = 0; i < c->numAttrs; ++i)
+    if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
+  const size_t threads = (size_t)c->blockDim.x * c->blockDim.y * c->blockDim.z;
+  ++seen.launches;
+  if (c->dynamicSmemBytes > seen.smem) seen.smem = c->dynamicSmemBytes;
+  if (threads > seen.threads) seen.threads = threads;
+  if (cluster > seen.cluster) seen.cluster = cluster;
+  seen.broken += c->gridDim.x == 0 || threads % 32 != 0 || c->gridDim.x % cluster != 0;
+  return cudaSuccess;
+}
 cudaError_t cudaMalloc(void** p, size_t) { return *p = nullptr, cudaErrorMemoryAllocation; }
 cudaError_t cudaFree(void*) { return cudaSuccess; }
 cudaError_t cudaMemcpyAsync(void*, const void*, size_t, cudaMemcpyKind, cudaStream_t) { return cudaSuccess; }
@@ -69,6 +84,25 @@ int main(int argc, char** argv) {
       current = d;
       printf("%zu %zu\n", parts(1000000, 1024), parts(1000000, 12000));   // CTAs; clusters of two
     }
+    return 0;
+  }
+  if (argc > 1 && !strcmp(argv[1], "launches")) {
+    char* const at = reinterpret_cast<char*>((size_t)1 << 40);   // nothing reads it
+    const size_t apart = (size_t)1 << 44;
+    for (size_t cols = 1; cols <= XP_LAYERNORM_MAX_COLS; cols += 1 + cols / 37)
+      for (size_t width : {cols, (cols + 7) / 8 * 8})
+        for (size_t rows = 1; rows <= ((size_t)1 << 20); rows += 1 + rows / 3)
+          for (xp_dtype type : {XP_F32, XP_BF16})
+            for (size_t off : {0, 4}) {
+              if (width > XP_LAYERNORM_MAX_COLS) continue;
+              float* const v = reinterpret_cast<float*>(at + 4 * apart);
+              const size_t room = (size_t)1 << 40;
+              if (xp_layernorm_forward(at + off, width, v, v, at + apart, width, v, v, rows, width, 1e-5f, type, XP_F32, nullptr) != XP_OK ||
+                  xp_layernorm_backward(at + off, width, at + 2 * apart, width, v, v, v, at + apart, width, v, v, rows, width, type, XP_F32, 0,
+                                        at + 5 * apart, room, nullptr) != XP_OK)
+                ++seen.broken;
+            }
+    printf("%zu %zu %zu %zu %zu\n", seen.launches, seen.smem, seen.threads, seen.cluster, seen.broken);
     return 0;
   }
   changing = true;

@@ -350,3 +350,60 @@ def test_weight_gradients_add_every_row_once(xt, rows, cols, pad, name):
     dgamma, dbeta = start[0].clone(), start[1].clone()
     xt.xp_layernorm_backward(dy, x, None, mean, rstd, dx, dgamma, dbeta, work, accumulate=True)
     assert torch.equal(dgamma, want[0] + start[0]) and torch.equal(dbeta, want[1] + start[1])
+
+
+@pytest.mark.parametrize("lead", [0, 1])
+@pytest.mark.parametrize("m_power", [-149, -130, -115, -100, -60, 0, 60, 110, 126])
+def test_states_at_every_magnitude(xt, m_power, lead):
+    # 8-bit states: weights, codes and scales of a step, in whole turns and at the end, are the fp32 program's, and so are
+    # weights and states in fp32; subnormal numbers and blocks of zeros among them
+    torch = torch_cuda()
+    n, step, lr = 4096 + 77, 9, 1e-3
+    half = np.full(n, 1 << 15)
+
+    def dev(a):
+        buf = torch.zeros(len(a) + lead, dtype=torch.from_numpy(a).dtype, device="cuda")
+        buf[lead:] = torch.from_numpy(a)
+        return buf[lead:]
+
+    hashes = train.rounding_bits(77, step + 1, range(n))
+    for v_power in (-149, -130, -120, -110, -95, -60, 0, 60, 110, 126):
+        rng = np.random.default_rng(100000 + 200 * m_power + v_power)
+        g = (rng.standard_normal(n) * 2.0 ** min(m_power - 2, 55) * (rng.random(n) < 0.7)).astype(np.float32)
+        m = (np.clip(rng.standard_normal(n) * 2.0 ** (m_power + rng.integers(-12, 1, n)), -1.5e38, 1.5e38) * (rng.random(n) < 0.8)).astype(np.float32)
+        v = (np.clip(rng.random(n) * 2.0 ** (v_power + rng.integers(-12, 1, n)), 0, 1.5e38) * (rng.random(n) < 0.9)).astype(np.float32)
+        p = rng.standard_normal(n).astype(np.float32)
+        (cm, sm), (cv, sv) = train.encode(m, half, True), train.encode(v, half, False)
+        t = [dev(a) for a in (p, g, cm, cv, sm, sv)]
+        m_out, v_out = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        xt.xp_state8_decode(t[2], t[4], t[3], t[5], m_out, v_out)
+        m, v = train.decode(cm, sm, True).astype(np.float32), train.decode(cv, sv, False).astype(np.float32)
+        assert np.array_equal(m_out.cpu().numpy(), m) and np.array_equal(v_out.cpu().numpy(), v)
+        with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
+            want = train.adamw(p, g, m, v, step + 1, lr, 0.0)
+        assert np.isfinite(want[1]).all() and np.isfinite(want[2]).all()
+        group = xt.xp_group_create([t[0]], [t[1]], [t[2]], [t[3]], m_scales=[t[4]], v_scales=[t[5]], seed=77, step=step)
+        xt.xp_adamw_step(group, lr)
+        xt.xp_group_destroy(group)
+        codes = [*train.encode(want[1], hashes[0], True), *train.encode(want[2], hashes[1], False)]
+        for got, ref in zip((t[0], t[2], t[4], t[3], t[5]), (want[0], *codes)):
+            assert np.array_equal(got.cpu().numpy(), ref), v_power
+        t = [dev(a) for a in (p, g, m, v)]
+        group = xt.xp_group_create([t[0]], [t[1]], [t[2]], [t[3]], step=step)
+        xt.xp_adamw_step(group, lr)
+        xt.xp_group_destroy(group)
+        for got, ref in zip((t[0], t[2], t[3]), want):
+            assert np.array_equal(got.cpu().numpy(), ref), v_power
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_every_code_under_every_scale(xt, out):
+    torch = torch_cuda()
+    codes, scales = np.tile(np.arange(256, dtype=np.uint8), 256), np.repeat(np.arange(256, dtype=np.uint8), 8)
+    c, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    got = [torch.empty(len(codes), dtype=_types(torch, out)[0], device="cuda") for _ in range(2)]
+    xt.xp_state8_decode(c, s, c, s, *got)
+    for values, signed in zip(got, (True, False)):
+        with np.errstate(over="ignore"):
+            want = train.decode(codes, scales, signed).astype(np.float32).astype(np.float64)
+        assert np.array_equal(_f64(values), want, equal_nan=True)

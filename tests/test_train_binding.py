@@ -200,3 +200,10 @@ def test_codes_below_the_least_pattern_stand_for_0():
             assert np.array_equal(got, bits.astype(np.uint32).view(np.float32).astype(np.float64))
     c, e = train.encode(np.array([2.0 ** -140, 2.0 ** -129, 2.0 ** -100], np.float32), np.zeros(3, np.int64), False)
     assert c[0] == 247 - 8 * e[0].astype(int) and train.decode(c, e, False).tolist() == [0.0, 2.0 ** -129, 2.0 ** -100]
+
+
+def test_every_launch_is_within_the_devices_limits(fake_runtime):
+    # layer norm of 1 to 131072 columns in 1 to 2^20 rows, both types, aligned and not: dynamic shared memory, threads, CTAs
+    # of a cluster, and CTAs that are no whole number of clusters
+    (launches, smem, threads, cluster, broken), = fake_runtime("launches")
+    assert launches > 100000 and smem <= 224 * 1024 and threads <= 1024 and cluster <= 8 and broken == 0
