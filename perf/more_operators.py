@@ -113,9 +113,6 @@ def prepare(case, seed):
             s[name + "_scales"].copy_(scales)
         s["c"] = torch.empty(m, n, dtype=TYPES[case["out"]], device="cuda")
         s["c"].copy_(normal(m, n) * 0.1)
-        if own:
-            from collective_transport_plane_gb300 import xp_model
-            s["work"] = torch.empty(xp_model.xp_matmul8_workspace(m, n, k), dtype=torch.uint8, device="cuda")
         return s
     dt = TYPES[case["type"]]
     if op in ("distill_fwd", "distill_bwd"):
@@ -208,8 +205,7 @@ def _own(s):
     from collective_transport_plane_gb300 import xp_model
     op = s["op"]
     if op == "product":
-        xp_model.xp_matmul8(s["a"], s["a_scales"], s["b"], s["b_scales"], s["c"], b_block_rows=s["b_block_rows"], accumulate=s["add"],
-                            workspace=s["work"])
+        xp_model.xp_matmul8(s["a"], s["a_scales"], s["b"], s["b_scales"], s["c"], b_block_rows=s["b_block_rows"], accumulate=s["add"])
         return {"c": s["c"]}
     if op == "distill_fwd":
         xp_model.xp_distill_forward(s["logits"], s["ids"], s["teacher"], s["loss"], s["lse"], s["temperature"])
