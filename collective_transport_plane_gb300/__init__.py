@@ -1,7 +1,8 @@
 """GB300-native FIFO data plane of a collective transport (SIMPLE, LL, zero
 copy, receiver-driven credit, host-placed FIFO, virtual ring allreduce)
 behind the C ABI in include/xp.h, and the training operators around the
-allreduce behind include/xp_train.h.  `xp` and `xp_train` are the ctypes
+allreduce behind include/xp_train.h, and the operators of a layer in 8 bits
+behind include/xp_model.h.  `xp`, `xp_train` and `xp_model` are the ctypes
 bindings; `build` compiles libxp.so.
 
 The binding is imported on first use, so `build` can run before libxp.so
@@ -11,7 +12,7 @@ import importlib
 
 
 def __getattr__(name):
-    if name in ("xp", "xp_train", "build"):
+    if name in ("xp", "xp_train", "xp_model", "build"):
         return importlib.import_module(f".{name}", __name__)
     xp = importlib.import_module(".xp", __name__)
     try:

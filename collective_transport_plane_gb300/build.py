@@ -13,8 +13,10 @@ LIB = os.path.join(PKG, "libxp.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["xp_api.cu", "xp_p2p.cu", "xp_p2p_tma.cu", "xp_ll.cu", "xp_ll128.cu", "xp_ring.cu", "xp_ring_tma.cu",
-           "xp_noalloc.cu", "xp_proxy.cu", "xp_train.cu", "xp_adamw.cu", "xp_layernorm.cu"]
-HEADERS = ["xp_internal.h", "xp_device.cuh", "xp_proxy.h", "xp_train_internal.h", "xp_train_device.cuh"]
+           "xp_noalloc.cu", "xp_proxy.cu", "xp_train.cu", "xp_adamw.cu", "xp_layernorm.cu",
+           "xp_model.cu", "xp_block8.cu", "xp_matmul8.cu", "xp_rmsnorm.cu", "xp_distill.cu"]
+HEADERS = ["xp_internal.h", "xp_device.cuh", "xp_proxy.h", "xp_train_internal.h", "xp_train_device.cuh", "xp_checks.h",
+           "xp_model_internal.h", "xp_code8.cuh", "xp_tcgen05.cuh"]
 
 # --fmad=false and the default -ftz=false keep the ring's fp32 adds plain IEEE
 # round-to-nearest-even additions (the reductions must match the oracle bit
@@ -40,7 +42,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    deps += [os.path.join(INCLUDE, "xp.h"), os.path.join(INCLUDE, "xp_train.h"), __file__]
+    deps += [os.path.join(INCLUDE, h) for h in ("xp.h", "xp_train.h", "xp_model.h")] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -1,0 +1,455 @@
+// The root-mean-square norm with the residual's addition and an output in 8
+// bits, and its backward pass (include/xp_model.h).
+//
+// Both directions read and write every element once and compute little on it:
+// HBM bounds them.  A row's threads keep it in registers between its sum and
+// its outputs (rows of more than 2048 units of 16 bytes, 8192 columns backward,
+// are read twice).  Blocks of 128 columns lie in one warp's units, so a block's scale is
+// a maximum over lanes.
+#include <algorithm>
+
+#include "xp_code8.cuh"
+#include "xp_model_internal.h"
+#include "xp_train_device.cuh"
+
+namespace xp {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+typedef unsigned long long u64;
+
+// ---- units: what a thread takes at a time.  WIDE: 16 bytes side by side.  In
+// rows that do not allow it (lengths, strides or addresses that are no multiple
+// of 16 bytes) a warp's lanes take neighbouring elements, 128 columns at a time.
+template <typename T, bool WIDE>
+constexpr int kUnit = WIDE ? 16 / (int)sizeof(T) : 4;
+
+// A row's thread, of `threads`: the first column of its unit k, and what its
+// unit's elements are apart.
+template <typename T, bool WIDE>
+__device__ __forceinline__ unsigned column(unsigned tid, unsigned threads, unsigned k) {
+  if constexpr (WIDE) return (tid + k * threads) * kUnit<T, WIDE>;
+  return ((tid >> 5) + k * (threads >> 5)) * 128 + (tid & 31);
+}
+template <bool WIDE>
+constexpr unsigned kApart = WIDE ? 1 : 32;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float v, float& x) { x = v; }
+__device__ __forceinline__ void from_f(float v, bf16& x) { x = __float2bfloat16_rn(v); }
+template <typename T>
+__device__ __forceinline__ float rounded(float v) {
+  T x;
+  from_f(v, x);
+  return to_f(x);
+}
+
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+
+// A unit whose first column is c, of a row of `cols`; zeros past its end.
+template <typename T, bool WIDE, int V>
+__device__ __forceinline__ void load(const T* row, unsigned c, unsigned cols, float (&f)[V]) {
+  if constexpr (WIDE) {
+    const uint4 q = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+    const unsigned w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = c + 32 * i < cols ? to_f(row[c + 32 * i]) : 0.f;
+  }
+}
+template <typename T, bool WIDE, int V>
+__device__ __forceinline__ void store(T* row, unsigned c, unsigned cols, const float (&f)[V]) {
+  if constexpr (WIDE) {
+    if (c >= cols) return;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(row + c) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + 32 * i < cols) from_f(f[i], row[c + 32 * i]);
+  }
+}
+// gamma's unit; ones where there is none (fp32 or bf16, its own alignment in `g`)
+template <bool WIDE, int V>
+__device__ __forceinline__ void load_gamma(const void* gamma, bool is_bf16, unsigned c, unsigned cols, float (&f)[V]) {
+  if (!gamma) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 1.f;
+  } else if (!WIDE) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      f[i] = c + 32 * i < cols ? is_bf16 ? to_f(static_cast<const bf16*>(gamma)[c + 32 * i]) : static_cast<const float*>(gamma)[c + 32 * i] : 0.f;
+  } else if (c >= cols) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 0.f;
+  } else if (is_bf16) {
+    const bf16* g = static_cast<const bf16*>(gamma) + c;
+    const uint2 a = *reinterpret_cast<const uint2*>(g);
+    const uint2 b = V == 8 ? *reinterpret_cast<const uint2*>(g + V - 4) : a;
+    const unsigned w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(gamma) + c);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 q = g[i];
+      f[4 * i] = q.x, f[4 * i + 1] = q.y, f[4 * i + 2] = q.z, f[4 * i + 3] = q.w;
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The sum over a row's threads (whole warps), the same in each; every thread of
+// the CTA calls it.  words: one per warp, two buffers in turn where it is
+// called more than once.
+__device__ __forceinline__ float row_sum(float v, float* words, unsigned threads) {
+  v = warp_sum(v);
+  if (threads == 32) return v;
+  const unsigned warp = threadIdx.x >> 5, n = threads >> 5, first = warp / n * n;
+  if ((threadIdx.x & 31) == 0) words[warp] = v;
+  __syncthreads();
+  v = 0.f;
+  for (unsigned i = 0; i < n; ++i) v += words[first + i];
+  return v;
+}
+
+// A unit's codes, and its block's scale by the lane that has its first columns.
+template <typename T, bool WIDE, int V>
+__device__ __forceinline__ void store8(const RmsForwardParams& p, u64 row, bool there, unsigned c, const float (&y)[V]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) top = max(top, abs_bits(y[i]));
+  constexpr int kBlockLanes = WIDE ? 128 / V : 32;
+#pragma unroll
+  for (int o = kBlockLanes / 2; o > 0; o /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (!there || c >= p.cols) return;
+  const unsigned e = scale_of(top);
+  const float inverse = inverse_of(e);
+  if ((threadIdx.x & (kBlockLanes - 1)) == 0) p.y8_scales[row * p.y8_scales_stride + c / 128] = (uint8_t)e;
+  uint8_t* out = p.y8 + row * p.y8_stride + c;
+  const unsigned lo = codes4(y[0], y[1], y[2], y[3], inverse, e);
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 32 * i < p.cols) out[32 * i] = (uint8_t)(lo >> 8 * i);
+  } else if constexpr (V == 8) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, codes4(y[V - 4], y[V - 3], y[V - 2], y[V - 1], inverse, e));
+  } else {
+    *reinterpret_cast<unsigned*>(out) = lo;
+  }
+}
+
+// NU units of a row per thread at once; LONG: rows of more, read twice.
+template <typename T, bool WIDE, int NU, bool LONG>
+__global__ void __launch_bounds__(LONG ? 1024 : 512) forward_kernel(const RmsForwardParams p) {
+  constexpr int V = kUnit<T, WIDE>;
+  __shared__ float words[32];
+  wait_for_predecessors();
+  let_successor_start();
+  const unsigned threads = p.threads, group = threadIdx.x / threads, tid = threadIdx.x - group * threads;
+  const u64 row = (u64)blockIdx.x * (blockDim.x / threads) + group;
+  const bool there = row < p.rows;
+  const unsigned cols = there ? p.cols : 0, turn = threads * NU * V;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  const T* r = static_cast<const T*>(p.residual) + row * p.residual_stride;
+  T* added = static_cast<T*>(p.added) + row * p.added_stride;
+  T* y = static_cast<T*>(p.y) + row * p.y_stride;
+
+  float h[NU][V], sum = 0.f;
+  for (unsigned from = 0; from < (LONG ? p.cols : 1); from += turn) {
+#pragma unroll
+    for (int k = 0; k < NU; ++k) load<T, WIDE>(x, from + column<T, WIDE>(tid, threads, k), cols, h[k]);
+    if (p.residual) {
+      float b[NU][V];
+#pragma unroll
+      for (int k = 0; k < NU; ++k) load<T, WIDE>(r, from + column<T, WIDE>(tid, threads, k), cols, b[k]);
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[k][i] = rounded<T>(h[k][i] + b[k][i]);
+        if (LONG) store<T, WIDE>(added, from + column<T, WIDE>(tid, threads, k), cols, h[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum = fmaf(h[k][i], h[k][i], sum);
+  }
+  sum = row_sum(sum, words, threads);
+  const float rstd = 1.f / sqrtf(sum / (float)p.cols + p.eps);
+  if (p.rstd && tid == 0 && there) p.rstd[row] = rstd;
+  for (unsigned from = 0; from < (LONG ? p.cols : 1); from += turn) {
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const unsigned c = from + column<T, WIDE>(tid, threads, k);
+      if (LONG)
+        load<T, WIDE>(p.residual ? added : x, c, cols, h[k]);
+      else if (p.residual)
+        store<T, WIDE>(added, c, cols, h[k]);
+      float g[V];
+      load_gamma<WIDE>(p.gamma, p.gamma_bf16, c, cols, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * rstd * g[i];
+      if (p.y) store<T, WIDE>(y, c, cols, h[k]);
+      if (p.y8) store8<T, WIDE>(p, row, there, c, h[k]);
+    }
+  }
+}
+
+// A group of threads keeps its columns through all its rows and adds their part
+// of dgamma up in registers; the CTA's groups leave one row of partial sums.
+template <typename T, bool WIDE, int NU>
+__global__ void __launch_bounds__(512) backward_kernel(const RmsBackwardParams p) {
+  constexpr int V = kUnit<T, WIDE>;
+  __shared__ float words[2][32];
+  extern __shared__ float parts[];
+  wait_for_predecessors();
+  let_successor_start();
+  const unsigned threads = p.threads, groups = blockDim.x / threads, group = threadIdx.x / threads, tid = threadIdx.x - group * threads;
+  float acc[NU][V], g[NU][V];
+#pragma unroll
+  for (int k = 0; k < NU; ++k) {
+    load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g[k]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+  }
+  const float inv_cols = 1.f / (float)p.cols;
+  int buf = 0;
+  for (u64 first = (u64)blockIdx.x * groups; first < p.rows; first += (u64)gridDim.x * groups, buf ^= 1) {
+    const u64 row = first + group;
+    const bool there = row < p.rows;
+    const unsigned cols = there ? p.cols : 0;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+    const T* x = static_cast<const T*>(p.h) + row * p.h_stride;
+    const float rstd = there ? p.rstd[row] : 0.f;
+    float d[NU][V], h[NU][V], e[NU][V], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const unsigned c = column<T, WIDE>(tid, threads, k);
+      load<T, WIDE>(dy, c, cols, d[k]);
+      load<T, WIDE>(x, c, cols, h[k]);
+      if (p.dadded) load<T, WIDE>(static_cast<const T*>(p.dadded) + row * p.dadded_stride, c, cols, e[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[k][i] *= rstd;
+        acc[k][i] = fmaf(d[k][i], h[k][i], acc[k][i]);
+        d[k][i] *= g[k][i];
+        sum = fmaf(d[k][i], h[k][i], sum);
+      }
+    sum = row_sum(sum, words[buf], threads) * inv_cols;
+    T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        d[k][i] = fmaf(-h[k][i], sum, d[k][i]) * rstd;
+        if (p.dadded) d[k][i] += e[k][i];
+      }
+      store<T, WIDE>(dx, column<T, WIDE>(tid, threads, k), cols, d[k]);
+    }
+  }
+  if (!p.partial) return;
+  float* mine = p.partial + (u64)blockIdx.x * p.cols;
+  if (groups > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) parts[(group * NU * V + k * V + i) * threads + tid] = acc[k][i];
+    __syncthreads();
+    if (group) return;
+    for (unsigned j = 1; j < groups; ++j)
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[k][i] += parts[(j * NU * V + k * V + i) * threads + tid];
+  }
+#pragma unroll
+  for (int k = 0; k < NU; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const unsigned c = column<T, WIDE>(tid, threads, k) + kApart<WIDE> * i;
+      if (c < p.cols) mine[c] = acc[k][i];
+    }
+}
+
+// Long rows, first launch: sum(a * xhat) / cols of each row.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(1024) long_sums_kernel(const RmsBackwardParams p) {
+  constexpr int V = kUnit<T, WIDE>;
+  __shared__ float words[32];
+  wait_for_predecessors();
+  let_successor_start();
+  const u64 row = blockIdx.x;
+  const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+  const T* x = static_cast<const T*>(p.h) + row * p.h_stride;
+  const float rstd = p.rstd[row];
+  float sum = 0.f;
+  for (unsigned from = 0; from < p.cols; from += blockDim.x * V) {
+    const unsigned c = from + column<T, WIDE>(threadIdx.x, blockDim.x, 0);
+    float d[V], h[V], g[V];
+    load<T, WIDE>(dy, c, p.cols, d);
+    load<T, WIDE>(x, c, p.cols, h);
+    load_gamma<WIDE>(p.gamma, p.gamma_bf16, c, p.cols, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum = fmaf(d[i] * g[i], h[i] * rstd, sum);
+  }
+  sum = row_sum(sum, words, blockDim.x);
+  if (threadIdx.x == 0) p.row_sums[row] = sum / (float)p.cols;
+}
+// Second launch: a CTA takes a slice of the columns through every gridDim.y-th row.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) long_rows_kernel(const RmsBackwardParams p) {
+  constexpr int V = kUnit<T, WIDE>;
+  wait_for_predecessors();
+  let_successor_start();
+  const unsigned c = blockIdx.x * blockDim.x * V + column<T, WIDE>(threadIdx.x, blockDim.x, 0);
+  float acc[V], g[V];
+  load_gamma<WIDE>(p.gamma, p.gamma_bf16, c, p.cols, g);
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 2
+  for (u64 row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const float rstd = p.rstd[row], sum = p.row_sums[row];
+    float d[V], h[V], e[V];
+    load<T, WIDE>(static_cast<const T*>(p.dy) + row * p.dy_stride, c, p.cols, d);
+    load<T, WIDE>(static_cast<const T*>(p.h) + row * p.h_stride, c, p.cols, h);
+    if (p.dadded) load<T, WIDE>(static_cast<const T*>(p.dadded) + row * p.dadded_stride, c, p.cols, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      h[i] *= rstd;
+      acc[i] = fmaf(d[i], h[i], acc[i]);
+      d[i] = fmaf(-h[i], sum, d[i] * g[i]) * rstd;
+      if (p.dadded) d[i] += e[i];
+    }
+    store<T, WIDE>(static_cast<T*>(p.dx) + row * p.dx_stride, c, p.cols, d);
+  }
+  if (!p.partial) return;
+  float* mine = p.partial + (u64)blockIdx.y * p.cols;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c + kApart<WIDE> * i < p.cols) mine[c + kApart<WIDE> * i] = acc[i];
+}
+
+// dgamma from the partial sums: 32 columns per CTA, a warp takes every 32nd row of them.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const RmsBackwardParams p) {
+  __shared__ float words[32][33];
+  wait_for_predecessors();
+  let_successor_start();
+  const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < p.cols) {
+#pragma unroll 4
+    for (unsigned j = warp; j < p.nparts; j += 32) v += p.partial[(u64)j * p.cols + c];
+  }
+  words[warp][lane] = v;
+  __syncthreads();
+  v = warp_sum(words[lane][warp]);
+  const unsigned out = blockIdx.x * 32 + warp;
+  if (lane == 0 && out < p.cols) p.dgamma[out] = p.accumulate ? p.dgamma[out] + v : v;
+}
+
+unsigned round32(u64 n) { return (unsigned)((n + 31) / 32 * 32); }
+
+template <typename T, bool WIDE>
+cudaError_t forward(RmsForwardParams& p, cudaStream_t st) {
+  constexpr int V = kUnit<T, WIDE>;
+  const unsigned units = WIDE ? (p.cols + V - 1) / V : (p.cols + 127) / 128 * 32;
+  if (units > 4 * 512) {
+    p.threads = 1024;
+    return launch_dependent(forward_kernel<T, WIDE, 2, true>, dim3((unsigned)p.rows), 1024, 0, 1, st, p);
+  }
+  const unsigned nu = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
+  p.threads = round32((units + nu - 1) / nu);
+  const unsigned groups = p.threads >= 256 ? 1 : 256 / p.threads;
+  const dim3 grid((unsigned)((p.rows + groups - 1) / groups));
+  const int block = (int)(groups * p.threads);
+  switch (nu) {
+    case 1: return launch_dependent(forward_kernel<T, WIDE, 1, false>, grid, block, 0, 1, st, p);
+    case 2: return launch_dependent(forward_kernel<T, WIDE, 2, false>, grid, block, 0, 1, st, p);
+    default: return launch_dependent(forward_kernel<T, WIDE, 4, false>, grid, block, 0, 1, st, p);
+  }
+}
+
+template <typename T, bool WIDE, int NU>
+cudaError_t backward_rows(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream_t st) {
+  const unsigned groups = s.groups;
+  const size_t smem = groups > 1 ? (size_t)groups * s.threads * NU * kUnit<T, WIDE> * sizeof(float) : 0;
+  return launch_dependent(backward_kernel<T, WIDE, NU>, dim3(s.nparts), (int)(groups * s.threads), smem, 1, st, p);
+}
+
+template <typename T, bool WIDE>
+cudaError_t backward(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream_t st) {
+  constexpr int V = kUnit<T, WIDE>;
+  p.threads = s.threads;
+  p.nparts = s.nparts;
+  cudaError_t e;
+  if (s.is_long) {
+    e = launch_dependent(long_sums_kernel<T, WIDE>, dim3((unsigned)p.rows), 1024, 0, 1, st, p);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(long_rows_kernel<T, WIDE>, dim3((p.cols + 256 * V - 1) / (256 * V), s.nparts), 256, 0, 1, st, p);
+  } else {
+    constexpr int kMost = V == 8 ? 2 : 4;
+    e = s.nu == 1 ? backward_rows<T, WIDE, 1>(p, s, st) : s.nu == 2 ? backward_rows<T, WIDE, 2>(p, s, st) : backward_rows<T, WIDE, kMost>(p, s, st);
+  }
+  if (e != cudaSuccess || !p.dgamma) return e;
+  return launch_dependent(sum_parts_kernel, dim3((p.cols + 31) / 32), 1024, 0, 1, st, p);
+}
+
+}  // namespace
+
+RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wide, int sms) {
+  const unsigned v = wide && dtype == XP_BF16 ? 8 : 4;
+  const unsigned units = wide ? (unsigned)((cols + v - 1) / v) : (unsigned)((cols + 127) / 128 * 32);
+  RmsBackwardShape s = {};
+  s.nu = units <= 256 ? 1 : units <= 1024 || v == 8 ? 2 : 4;
+  s.threads = round32((units + s.nu - 1) / s.nu);
+  s.is_long = s.threads > 512;
+  if (s.is_long) {
+    const size_t slices = (cols + 256 * v - 1) / (256 * v), most = (8 * (size_t)sms + slices - 1) / slices;
+    s.nparts = (unsigned)std::min<size_t>(rows, std::max<size_t>(1, most));
+    return s;
+  }
+  s.groups = s.threads >= 256 ? 1 : 256 / s.threads;
+  const unsigned per_sm = std::max(1u, 1024 / (s.groups * s.threads));
+  s.nparts = (unsigned)std::min<size_t>((rows + s.groups - 1) / s.groups, (size_t)sms * per_sm);
+  return s;
+}
+
+cudaError_t launch_rms_forward(RmsForwardParams& p, int dtype, bool wide, cudaStream_t st) {
+  if (dtype == XP_F32) return wide ? forward<float, true>(p, st) : forward<float, false>(p, st);
+  return wide ? forward<bf16, true>(p, st) : forward<bf16, false>(p, st);
+}
+
+cudaError_t launch_rms_backward(RmsBackwardParams& p, const RmsBackwardShape& s, int dtype, bool wide, cudaStream_t st) {
+  if (dtype == XP_F32) return wide ? backward<float, true>(p, s, st) : backward<float, false>(p, s, st);
+  return wide ? backward<bf16, true>(p, s, st) : backward<bf16, false>(p, s, st);
+}
+
+}  // namespace xp

@@ -3,17 +3,12 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <new>
 #include <vector>
 
+#include "xp_checks.h"
 #include "xp_train_internal.h"
-
-namespace xp {
-void set_last_error(const char* msg);
-}
 
 struct xp_group {
   int device = 0;
@@ -31,29 +26,8 @@ struct xp_group {
 
 namespace {
 
-xp_status fail(xp_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  try {
-    xp::set_last_error(buf);
-  } catch (...) {   // no memory for the message
-  }
-  return s;
-}
+using namespace xp::checks;
 
-#define XP_CUDA(call)                                                                     \
-  do {                                                                                    \
-    cudaError_t e_ = (call);                                                              \
-    if (e_ != cudaSuccess) return fail(XP_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
-
-bool is_float_type(int dt) { return dt == XP_F32 || dt == XP_BF16; }
-size_t size_of(int dt) { return dt == XP_F32 ? 4 : dt == XP_BF16 ? 2 : 1; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 bool step_ok(uint64_t step) { return step <= XP_GROUP_MAX_STEP; }
 
 // Elements of a unit.  Small groups are cut finer, so that their elements
@@ -159,34 +133,6 @@ xp_status create(const xp_group_config& cfg, int ntensors, const xp_tensor* tens
   XP_CUDA(e2);
   return XP_OK;
 }
-
-xp_status check_rows(const char* what, const void* p, size_t stride, size_t rows, size_t cols, int dtype) {
-  if (!p) return fail(XP_ERR_INVALID, "%s is NULL", what);
-  if (stride < cols && rows > 1) return fail(XP_ERR_INVALID, "%s: rows %zu elements apart overlap (%zu columns)", what, stride, cols);
-  if (stride > ((size_t)1 << 40)) return fail(XP_ERR_INVALID, "%s: rows %zu elements apart", what, stride);
-  if (!aligned(p, size_of(dtype))) return fail(XP_ERR_INVALID, "%s is not aligned to its element", what);
-  return XP_OK;
-}
-
-// Where a matrix of `rows` rows lies.
-struct Span {
-  uintptr_t lo, hi;
-  size_t rows, width, pitch;   // bytes of a row, and from one row to the next
-};
-Span span_of(const void* p, size_t stride, size_t rows, size_t cols, size_t es) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + ((rows - 1) * stride + cols) * es, rows, cols * es, stride * es};
-}
-// Whether two matrices of the same size share bytes.  At equal strides rows may
-// lie between rows, as side-by-side columns of one buffer do: b's rows begin at
-// the same place between two of a's.  At different strides that is not followed up.
-bool overlap(const Span& a, const Span& b) {
-  if (a.hi <= b.lo || b.hi <= a.lo) return false;
-  if (a.rows == 1 || a.pitch != b.pitch) return true;
-  const size_t at = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
-  return at < a.width || a.pitch - at < a.width;
-}
-bool same(const Span& a, const Span& b) { return a.lo == b.lo && (a.rows == 1 || a.pitch == b.pitch); }
 
 xp_status check_sizes(size_t rows, size_t cols, int dtype, int wdtype) {
   if (!is_float_type(dtype) || !is_float_type(wdtype)) return fail(XP_ERR_INVALID, "dtype %d / %d is neither XP_F32 nor XP_BF16", dtype, wdtype);
