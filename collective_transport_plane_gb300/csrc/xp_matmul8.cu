@@ -9,12 +9,15 @@
 // Few rows of A take few columns, and the same kernel reads a weight at the
 // memory's rate for one token.
 //
-// A CTA works on tiles of 128 x `bn`, one after another: one thread copies
-// boxes of 128 columns into a ring of stages, one issues the products, a warp
-// brings scales for four blocks at a time, and four warps store the last tile's
-// sums while the next one's are made.  Where tiles are few, the CTAs of a
-// cluster share one: each sums a part of the columns, and they add their sums up
-// through shared memory, in the order of their ranks.
+// One warp copies boxes of 128 columns into a ring of stages, one issues the
+// products, two bring scales for four blocks at a time, and sixteen keep the tile's sums in registers: TMEM's are added to them after each 32
+// blocks, since the tensor core's own additions round towards zero and would be
+// off by a few 2^-24 for each thousand columns.  While they are stored the next
+// tile's products run.  Large products are made by pairs of CTAs, 256 rows of B
+// at a time, half of A's rows in each's shared memory, which then has to deliver
+// 256 bytes for what a CTA alone reads 384 for.  Where tiles are few, the CTAs of
+// a cluster share one: each sums a part of the columns, and they add their sums
+// up through shared memory, in the order of their ranks.
 #include "xp_model_internal.h"
 #include "xp_tcgen05.cuh"
 #include "xp_train_device.cuh"
@@ -24,17 +27,24 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kRows = 128;                        // of B in a tile
+constexpr int kScaleWarps = 2;                    // beside one that copies, one for the products
+constexpr int kFirstStoreWarp = 2 + kScaleWarps;
+constexpr int kStoreWarps = 16;
+constexpr int kThreads = 32 * (kFirstStoreWarp + kStoreWarps);
+constexpr int kRows = 128;                        // of B in a CTA's tile
 constexpr unsigned kBoxCols = 128;                // a block's codes: 128 bytes
 constexpr unsigned kRowsBytes = kRows * kBoxCols;
 constexpr int kMaxStages = 12;
-constexpr unsigned kScaleSlots = 4;               // of four blocks' scales each, at most
+constexpr unsigned kScaleSlots = 4;               // of four blocks' scales each
 constexpr unsigned kScaleBytes = 512 + 2 * 512;
 constexpr unsigned kSharedBytes = 212 * 1024;     // stages and scales
 constexpr unsigned kTmemColumns = 512;
+constexpr unsigned kChunk = 32;                   // blocks between two readings of TMEM's sums
+constexpr unsigned kMaxSplit = 8;
 
-__device__ unsigned stalled_ctas;
+static_assert(kScaleSlots == 2 * kScaleWarps, "a slot's phases are all waited for by the one warp that fills it");
+
+__device__ unsigned stalled_warps;
 
 struct Bars {
   u64 full[kMaxStages], empty[kMaxStages];
@@ -65,55 +75,48 @@ __device__ __forceinline__ uint4 scale_line(const uint8_t* scales, u64 pitch, in
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ float load_remote(unsigned smem, unsigned rank) {
-  unsigned r;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+__device__ __forceinline__ float4 load_remote(unsigned smem, unsigned rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(tc::in_cta(smem, rank)) : "memory");
   return v;
 }
 
-// The first n of N elements of C, a row apart from the next; what is there is read before anything is written.
+// The first n of N elements of C, `step` apart; what is there is read before anything is written.
 template <int N>
-__device__ __forceinline__ void put(const Matmul8Params& p, u64 at, unsigned n, const float (&v)[N]) {
+__device__ __forceinline__ void put(const Matmul8Params& p, u64 at, u64 step, unsigned n, const float (&v)[N]) {
   if (p.out_bf16) {
     __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.c) + at;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) c[i * p.c_stride] = __float2bfloat16_rn(v[i]);
+      if (i < n) c[i * step] = __float2bfloat16_rn(v[i]);
     return;
   }
   float* c = static_cast<float*>(p.c) + at;
   float old[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) old[i] = p.accumulate && i < n ? c[i * p.c_stride] : 0.f;
+  for (int i = 0; i < N; ++i) old[i] = p.accumulate && i < n ? c[i * step] : 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (i < n) c[i * p.c_stride] = p.accumulate ? old[i] + v[i] : v[i];
+    if (i < n) c[i * step] = p.accumulate ? old[i] + v[i] : v[i];
 }
 
+// CTAS: of a pair (2), or alone or in a cluster that shares a tile (1).
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_constant__ Matmul8Params p) {
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ unsigned tmem_at;
   const unsigned base = (tc::smem_of(raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned stages = p.stages, bn = p.bn, stage_bytes = kRowsBytes + bn * kBoxCols;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const unsigned stages = p.stages, bn = p.bn, q_box = bn / CTAS, stage_bytes = kRowsBytes + q_box * kBoxCols;
   const unsigned scales_at = base + stages * stage_bytes;
   const unsigned full = tc::smem_of(bars.full), empty = tc::smem_of(bars.empty);
   const unsigned scales_full = tc::smem_of(bars.scales_full), scales_empty = tc::smem_of(bars.scales_empty);
   const unsigned sums_full = tc::smem_of(bars.sums_full), sums_empty = tc::smem_of(bars.sums_empty);
   const unsigned drained = tc::smem_of(&bars.drained);
-  const unsigned nsums = p.nsums, nslots = p.slots, q_lines = (bn + 127) / 128, slot_columns = 4 + 4 * q_lines;
+  const unsigned nsums = p.nsums, q_lines = (bn + 127) / 128, slot_columns = 4 + 4 * q_lines;
+  const unsigned rank = CTAS == 2 || p.split > 1 ? tc::cluster_rank() : 0;
+  const bool leader = CTAS == 1 || rank == 0;   // of a pair: it issues the products, and keeps the barriers they wait for
 
   if (warp == 0 && lane == 0) {
     tc::prefetch_map(&p.p_map);
@@ -126,174 +129,257 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
     }
     tc::bar_init(drained, 1);
     for (unsigned i = 0; i < kScaleSlots; ++i) {
-      tc::bar_init(scales_full + 8 * i, 1);
+      tc::bar_init(scales_full + 8 * i, CTAS);
       tc::bar_init(scales_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(sums_full + 8 * i, 1);
-      tc::bar_init(sums_empty + 8 * i, 4);
+      tc::bar_init(sums_empty + 8 * i, CTAS * kStoreWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) tc::tmem_alloc(tc::smem_of(&tmem_at), kTmemColumns);
+  if (warp == 2) tc::tmem_alloc<CTAS>(tc::smem_of(&tmem_at), kTmemColumns);
   tc::fence_before();
   __syncthreads();
+  if (CTAS == 2) tc::cluster_meet();
   tc::fence_after();
-  const unsigned tmem = tmem_at;
+  const unsigned tmem = __shfl_sync(0xffffffffu, tmem_at, 0);   // the same for the warp, as the compiler then knows
   wait_for_predecessors();
   let_successor_start();
 
-  const unsigned rank = p.split > 1 ? cluster_rank() : 0;
-  const unsigned first_tile = blockIdx.x / p.split, tile_step = gridDim.x / p.split, ntiles = p.tiles_p * p.tiles_q;
-  const unsigned k0 = (unsigned)((u64)p.kblocks * rank / p.split), k1 = (unsigned)((u64)p.kblocks * (rank + 1) / p.split);
+  const unsigned sharers = CTAS * p.split;   // CTAs of a tile
+  const unsigned first_tile = blockIdx.x / sharers, tile_step = gridDim.x / sharers, ntiles = p.tiles_p * p.tiles_q;
+  const unsigned part = CTAS == 2 ? 0 : rank;
+  const unsigned k0 = (unsigned)((u64)p.kblocks * part / p.split), k1 = (unsigned)((u64)p.kblocks * (part + 1) / p.split);
+  const unsigned p_first = CTAS == 2 ? rank * kRows : 0, q_first = CTAS == 2 ? rank * q_box : 0;   // of the tile's rows, in this CTA
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      unsigned n = 0;   // boxes brought so far
-      for (unsigned t = first_tile; t < ntiles && ok; t += tile_step) {
-        unsigned tp, tq;
-        tile_at(p, t, tp, tq);
-        for (unsigned kb = k0; kb < k1; ++kb, ++n) {
-          const unsigned s = n % stages, at = base + s * stage_bytes;
-          if (n >= stages && !(ok = tc::bar_wait(empty + 8 * s, (n / stages - 1) & 1))) break;
-          tc::bar_expect(full + 8 * s, stage_bytes);
-          tc::load_box(at, &p.p_map, kb * kBoxCols, tp * kRows, full + 8 * s);
-          tc::load_box(at + kRowsBytes, &p.q_map, kb * kBoxCols, tq * bn, full + 8 * s);
-        }
-      }
-      if (!ok)   // what is in flight lands before the CTA goes
-        for (unsigned i = n >= stages ? n - stages : 0; i < n; ++i) tc::bar_wait(full + 8 * (i % stages), (i / stages) & 1);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      unsigned n = 0, groups = 0, tiles = 0;
-      for (unsigned t = first_tile; t < ntiles && ok; t += tile_step, ++tiles) {
-        const unsigned sums = tiles % nsums, turn = tiles / nsums, d = tmem + sums * bn;
-        if (turn > 0 && !(ok = tc::bar_wait(sums_empty + 8 * sums, (turn - 1) & 1))) break;
-        tc::fence_after();
-        unsigned slot = 0, scale_p = 0, scale_q = 0;
-        for (unsigned kb = k0; kb < k1; ++kb, ++n) {
-          const unsigned s = n % stages, at = base + s * stage_bytes;
-          if (!(ok = tc::bar_wait(full + 8 * s, (n / stages) & 1))) break;
-          if (kb == k0 || kb % 4 == 0) {   // the next four blocks' scales
-            slot = groups % nslots;
-            const unsigned from = scales_at + slot * kScaleBytes;
-            if (!(ok = tc::bar_wait(scales_full + 8 * slot, (groups / nslots) & 1))) break;
-            scale_p = tmem + nsums * bn + slot * slot_columns;
-            scale_q = scale_p + 4;
-            tc::fence_after();
-            tc::copy_scales(scale_p, tc::rows16(from));
-            for (unsigned i = 0; i < q_lines; ++i) tc::copy_scales(scale_q + 4 * i, tc::rows16(from + 512 + 512 * i));
-            ++groups;
-          }
-          tc::fence_after();
-          const unsigned shape = tc::scaled_shape(bn, kb % 4);
-          const u64 a = tc::rows128(at), b = tc::rows128(at + kRowsBytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc::mma_scaled(d, a + 2 * i, b + 2 * i, shape, scale_p, scale_q, kb != k0 || i > 0);
-          tc::commit_to(empty + 8 * s);
-          // a slot is free, here and in TMEM, when the last products that read it are done
-          if (kb + 1 == k1 || kb % 4 == 3) tc::commit_to(scales_empty + 8 * slot);
-        }
-        if (ok) tc::commit_to(sums_full + 8 * sums);
-      }
-      if (!ok) {   // what was issued ends before TMEM is given back
-        tc::commit_to(drained);
-        tc::bar_wait(drained, 0);
-      }
-    }
-  } else if (warp == 2) {
-    unsigned n = 0;
+    const unsigned full_at = CTAS == 2 ? tc::in_cta(full, 0) : full;
+    unsigned n = 0, s = 0, turn = 0;   // boxes brought so far; the stage of the next, and how often the ring went round
     for (unsigned t = first_tile; t < ntiles && ok; t += tile_step) {
       unsigned tp, tq;
       tile_at(p, t, tp, tq);
-      for (unsigned g = k0 / 4; g * 4 < k1 && k0 < k1; ++g, ++n) {
-        const unsigned slot = n % nslots, to = scales_at + slot * kScaleBytes + 16 * lane;
-        uint4 line[3];
-        line[0] = scale_line(p.p_scales, p.p_pitch, p.p_shift, tp * kRows, p.p_rows, g, lane);
+      const int row_p = tp * (CTAS * kRows) + p_first, row_q = tq * bn + q_first;
+      for (unsigned kb = k0; kb < k1; ++kb, ++n) {
+        if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(empty + 8 * s, (turn - 1) & 1)))) break;
+        if (tc::elected()) {
+          const unsigned at = base + s * stage_bytes;
+          if (leader) tc::bar_expect(full + 8 * s, CTAS * stage_bytes);
+          tc::load_box<CTAS>(at, &p.p_map, kb * kBoxCols, row_p, full_at + 8 * s);
+          tc::load_box<CTAS>(at + kRowsBytes, &p.q_map, kb * kBoxCols, row_q, full_at + 8 * s);
+        }
+        if (++s == stages) s = 0, ++turn;
+      }
+    }
+    if (!ok && leader)   // what is in flight lands before the CTA goes
+      for (unsigned i = n >= stages ? n - stages : 0; i < n; ++i) tc::bar_wait(full + 8 * (i % stages), (i / stages) & 1);
+  } else if (warp == 1) {
+    if (leader) {
+      unsigned s = 0, phase = 0, slot = 0, slot_phase = 0, sums = 0, turn = 0;
+      for (unsigned t = first_tile; t < ntiles && ok; t += tile_step) {
+        for (unsigned from = k0; from < k1 && ok; from += kChunk) {
+          const unsigned d = tmem + sums * bn, to = min(from + kChunk, k1);
+          if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(sums_empty + 8 * sums, (turn - 1) & 1)))) break;
+          for (unsigned kb = from; kb < to; ++kb) {
+            const unsigned at = base + s * stage_bytes, scale_p = tmem + nsums * bn + slot * slot_columns, scale_q = scale_p + 4;
+            const bool more = kb == k0 || kb % 4 == 0, last = kb + 1 == k1 || kb % 4 == 3;
+            ok = tc::bar_wait(full + 8 * s, phase) && (!more || tc::bar_wait(scales_full + 8 * slot, slot_phase));
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc::fence_after();
+            if (tc::elected()) {
+              if (more) {   // the next four blocks' scales
+                const unsigned in = scales_at + slot * kScaleBytes;
+                tc::copy_scales<CTAS>(scale_p, tc::rows16(in));
+                tc::copy_scales<CTAS>(scale_q, tc::rows16(in + 512));
+                if (q_lines > 1) tc::copy_scales<CTAS>(scale_q + 4, tc::rows16(in + 1024));
+              }
+              const unsigned shape = tc::scaled_shape<CTAS>(bn, kb % 4);
+              const u64 a = tc::rows128(at), b = tc::rows128(at + kRowsBytes);
 #pragma unroll
-        for (unsigned i = 0; i < 2; ++i)
-          if (i < q_lines) line[1 + i] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn + 128 * i, p.q_rows, g, lane);
-        if (n >= nslots && !(ok = __all_sync(0xffffffffu, tc::bar_wait(scales_empty + 8 * slot, (n / nslots - 1) & 1)))) break;
+              for (int i = 0; i < 4; ++i) tc::mma_scaled<CTAS>(d, a + 2 * i, b + 2 * i, shape, scale_p, scale_q, kb != from || i > 0);
+              tc::commit_to<CTAS>(empty + 8 * s);
+              // a slot is free, here and in TMEM, when the last products that read it are done
+              if (last) tc::commit_to<CTAS>(scales_empty + 8 * slot);
+              if (kb + 1 == to) tc::commit_to<CTAS>(sums_full + 8 * sums);
+            }
+            __syncwarp();
+            if (last && ++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
+            if (++s == stages) s = 0, phase ^= 1;
+          }
+          if (++sums == nsums) sums = 0, ++turn;
+        }
+      }
+      if (!ok) {   // what was issued ends before TMEM is given back
+        if (tc::elected()) tc::commit_to<CTAS>(drained);
+        tc::bar_wait(drained, 0);
+      }
+    }
+  } else if (warp < kFirstStoreWarp) {
+    // A warp brings two groups of four blocks' scales at a time: the fence between its loads and the tensor core's
+    // copies waits for all that the warp has on its way, and one group after another takes 2800 cycles each, longer
+    // than four blocks' products (8192 x 16384 x 4096: 364 us with one such warp, 335 with four groups on their way).
+    const unsigned scales_full_at = CTAS == 2 ? tc::in_cta(scales_full, 0) : scales_full;
+    const unsigned g0 = k0 / 4, per_tile = k0 < k1 ? (k1 + 3) / 4 - g0 : 0;
+    const unsigned mine = first_tile < ntiles ? (ntiles - first_tile + tile_step - 1) / tile_step * per_tile : 0;
+    unsigned at = 2 * (warp - 2), tile = first_tile;   // the group within its tile
+    for (unsigned n = 2 * (warp - 2); n < mine && ok; n += 2 * kScaleWarps) {
+      uint4 line[2][3];
+#pragma unroll
+      for (unsigned u = 0; u < 2; ++u, ++at) {
+        while (at >= per_tile) at -= per_tile, tile += tile_step;
+        if (n + u >= mine) break;
+        unsigned tp, tq;
+        tile_at(p, tile, tp, tq);
+        line[u][0] = scale_line(p.p_scales, p.p_pitch, p.p_shift, tp * (CTAS * kRows) + p_first, p.p_rows, g0 + at, lane);
+        line[u][1] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn, p.q_rows, g0 + at, lane);
+        if (q_lines > 1) line[u][2] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn + 128, p.q_rows, g0 + at, lane);
+      }
+      at += 2 * (kScaleWarps - 1);
+#pragma unroll
+      for (unsigned u = 0; u < 2; ++u) {
+        const unsigned slot = (n + u) % kScaleSlots, to = scales_at + slot * kScaleBytes + 16 * lane;
+        if (n + u >= mine) break;
+        if (n + u >= kScaleSlots && !(ok = __all_sync(0xffffffffu, tc::bar_wait(scales_empty + 8 * slot, ((n + u) / kScaleSlots - 1) & 1)))) break;
 #pragma unroll
         for (unsigned i = 0; i < 3; ++i)
           if (i <= q_lines)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512 * i), "r"(line[i].x), "r"(line[i].y), "r"(line[i].z), "r"(line[i].w) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(scales_full + 8 * slot);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512 * i), "r"(line[u][i].x), "r"(line[u][i].y), "r"(line[u][i].z), "r"(line[u][i].w) : "memory");
       }
+      if (!ok) break;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane < 2 && n + lane < mine) tc::bar_arrive_cluster(scales_full_at + 8 * ((n + lane) % kScaleSlots));
     }
-  } else if (warp >= 4) {
-    const unsigned row = 32 * (warp - 4) + lane;
-    unsigned tiles = 0;
-    for (unsigned t = first_tile; t < ntiles; t += tile_step, ++tiles) {
+  } else {
+    // a warp has 32 rows of B, and every fourth 16 of A's
+    const unsigned quarter = warp & 3, first = 16 * ((warp - kFirstStoreWarp) >> 2), row = 32 * quarter + lane;
+    const unsigned sums_empty_at = CTAS == 2 ? tc::in_cta(sums_empty, 0) : sums_empty;
+    unsigned sums = 0, phase = 0;
+    for (unsigned t = first_tile; t < ntiles; t += tile_step) {
+      float v[4][16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
+      for (unsigned from = k0; from < k1; from += kChunk) {
+        ok = ok && __all_sync(0xffffffffu, tc::bar_wait(sums_full + 8 * sums, phase));
+        tc::fence_after();
+        // (columns past bn are read too, within TMEM's 512, and not used)
+        const unsigned at = tmem + sums * bn + first + ((32 * quarter) << 16);
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          if (64 * j + first >= bn) break;
+          float f[2][16];
+          tc::tmem_load16(at + 64 * j, f[0]);
+          tc::tmem_load16(at + 64 * j + 64, f[1]);
+          tc::tmem_wait();
+          tc::landed(f[0]);
+          tc::landed(f[1]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[j][i] += f[0][i], v[j + 1][i] += f[1][i];
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive_relaxed(sums_empty_at + 8 * sums);
+        if (++sums == nsums) sums = 0, phase ^= 1;
+      }
+      if (!ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[j][i] = __int_as_float(0x7fffffff);
+      }
       unsigned tp, tq;
       tile_at(p, t, tp, tq);
-      const unsigned sums = tiles % nsums, turn = tiles / nsums, n = tp * kRows + row, m0 = tq * bn;
-      const bool none = k0 == k1;
-      ok = ok && (none || __all_sync(0xffffffffu, tc::bar_wait(sums_full + 8 * sums, turn & 1)));
-      tc::fence_after();
-      const unsigned there = n < p.p_rows ? p.q_rows - m0 : 0;
-      for (unsigned j = 0; j < bn; j += 16) {
-        float v[16];
-        if (ok && !none) {
-          tc::tmem_load16(tmem + sums * bn + j + ((32u * (warp - 4)) << 16), v);
-        } else {
+      const unsigned n = tp * (CTAS * kRows) + p_first + row, m0 = tq * bn;
+      const unsigned there = n < p.p_rows ? min(bn, p.q_rows - m0) : 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = none ? 0.f : __int_as_float(0x7fffffff);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const unsigned c = 64 * j + first;
         if (p.split == 1) {
-          put<16>(p, (u64)(m0 + j) * p.c_stride + n, j < there ? there - j : 0, v);
-        } else {
+          if (c < there) put<16>(p, (u64)(m0 + c) * p.c_stride + n, p.c_stride, there - c, v[j]);
+        } else if (c < bn) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((j + i) * kRows + row) * 4), "f"(v[i]) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + i) * kRows + row) * 4), "f"(v[j][i]) : "memory");
         }
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(sums_empty + 8 * sums);
     }
   }
-  if (!ok && lane == 0) atomicAdd(&stalled_ctas, 1u);
+  if (!ok && lane == 0) atomicAdd(&stalled_warps, 1u);
   __syncwarp();
-  if (p.split > 1) {
-    cluster_meet();
+  if (CTAS == 1 && p.split > 1) {
+    tc::cluster_meet();
     unsigned tp, tq;
     tile_at(p, first_tile, tp, tq);
-    const unsigned row = threadIdx.x % kRows, n = tp * kRows + row;
-    for (unsigned j = rank + p.split * (threadIdx.x / kRows); j < bn && tq * bn + j < p.q_rows; j += p.split * (kThreads / kRows)) {
-      float v[1] = {0.f};
-      for (unsigned r = 0; r < p.split; ++r) v[0] += load_remote(base + (j * kRows + row) * 4, r);
-      put<1>(p, (u64)(tq * bn + j) * p.c_stride + n, n < p.p_rows, v);
+    // a thread adds up four of the 128 rows of B at one of A's, which go to the CTAs in turn
+    const unsigned row = 4 * lane, n = tp * kRows + row;
+    for (unsigned j = rank + p.split * warp; j < bn && tq * bn + j < p.q_rows; j += p.split * (kThreads / 32)) {
+      float4 part[kMaxSplit];
+#pragma unroll
+      for (unsigned r = 0; r < kMaxSplit; ++r)
+        if (r < p.split) part[r] = load_remote(base + (j * kRows + row) * 4, r);
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (unsigned r = 0; r < kMaxSplit; ++r)
+        if (r < p.split) v[0] += part[r].x, v[1] += part[r].y, v[2] += part[r].z, v[3] += part[r].w;
+      if (n < p.p_rows) put<4>(p, (u64)(tq * bn + j) * p.c_stride + n, 1, p.p_rows - n, v);
     }
-    cluster_meet();
   }
   tc::fence_before();
-  __syncthreads();
+  if (CTAS == 2 || p.split > 1)
+    tc::cluster_meet();   // nobody reads or signals this CTA's shared memory any more
+  else
+    __syncthreads();
   if (warp == 2) {
     tc::fence_after();
-    tc::tmem_free(tmem, kTmemColumns);
+    tc::tmem_free<CTAS>(tmem, kTmemColumns);
   }
+}
+
+int pair_count(int sms) {
+  static PerDevice known;
+  return known.get([sms](int) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSharedBytes;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_dynamic_smem(matmul8_kernel<2>) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, matmul8_kernel<2>, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = sms > 1 ? sms / 2 : 1;
+    }
+    return n;
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_matmul8(Matmul8Params& p, int sms, cudaStream_t st) {
-  const unsigned stage = kRowsBytes + p.bn * kBoxCols;
+  const unsigned stage = kRowsBytes + p.bn / p.ctas * kBoxCols;
   p.stages = (kSharedBytes - 1024 - kScaleSlots * kScaleBytes) / stage;
   if (p.stages > (unsigned)kMaxStages) p.stages = kMaxStages;
-  // two tiles' sums at a time where they fit beside two slots of scales
+  // two chunks' sums at a time where they fit beside the scales
   const unsigned slot = 4 + 4 * ((p.bn + 127) / 128);
-  p.nsums = 2 * (p.bn + slot) <= kTmemColumns ? 2 : 1;
-  p.slots = p.nsums * p.bn + kScaleSlots * slot <= kTmemColumns ? kScaleSlots : 2;
+  p.nsums = 2 * p.bn + kScaleSlots * slot <= kTmemColumns ? 2 : 1;
   const unsigned tiles = p.tiles_p * p.tiles_q;
+  // (a CTA has its SM to itself, so clusters do not hold up the kernel that drains before them: 310 us with programmatic
+  // dependence and 324 without at 8192 x 16384 x 4096, 8.7 and 9.6 for one row of 4096 x 4096)
+  if (p.ctas == 2) {
+    const unsigned pairs = (unsigned)pair_count(sms);
+    return launch_clusters(matmul8_kernel<2>, dim3(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSharedBytes, 2, true, st, p);
+  }
   const unsigned grid = p.split > 1 ? tiles * p.split : tiles < (unsigned)sms ? tiles : (unsigned)sms;
-  return launch_dependent(matmul8_kernel, dim3(grid), kThreads, kSharedBytes, (int)p.split, st, p);
+  return launch_clusters(matmul8_kernel<1>, dim3(grid), kThreads, kSharedBytes, (int)p.split, true, st, p);
 }
 
-cudaError_t matmul8_stalls(unsigned* n) { return cudaMemcpyFromSymbol(n, stalled_ctas, sizeof *n); }
+cudaError_t matmul8_stalls(unsigned* n) { return cudaMemcpyFromSymbol(n, stalled_warps, sizeof *n); }
 
 }  // namespace xp

@@ -90,21 +90,35 @@ bool map_codes(CUtensorMap* map, const uint8_t* codes, size_t stride, size_t row
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is cut: tiles of 128 of b's rows and bn of a's, and the CTAs that share one.
+// How a product is cut: tiles of 128 of b's rows (256 for a pair of CTAs) and
+// bn of a's, and the CTAs that share one.  The least of a model in ns, fitted to
+// times of all choices at 16 sizes (N = K = 4096: 64 rows 9.1 us as 4 CTAs a
+// tile, 12.5 as one, 10.2 in pairs; 512 rows 12.6 in pairs of 128, 14.8 alone;
+// 4096 rows 42.7 in pairs of 224, 46.7 of 256, which have room in TMEM for one
+// tile's sums only, 52.3 alone): a block's copies and products, which a pair
+// shares, what a tile's last sums take, and what CTAs that share a tile add.
 void cut_product(size_t m, size_t n, size_t kblocks, unsigned sms, xp::Matmul8Params& p) {
-  p.tiles_p = (unsigned)ceil_div(n, 128);
-  p.bn = (unsigned)std::min<size_t>(256, round_up(m, 16));
-  if (m > 256) {
-    // the least time of all waves; a tile's copies cost as much as 64 more of its rows
-    size_t best = ~(size_t)0;
-    for (unsigned bn = 64; bn <= 256; bn += 16) {
-      const size_t waves = ceil_div(ceil_div(m, bn) * p.tiles_p, sms), cost = waves * (bn + 64);
-      if (cost <= best) best = cost, p.bn = bn;
+  static const unsigned widths[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
+  size_t least = ~(size_t)0;
+  for (unsigned ctas = 1; ctas <= 2; ++ctas) {
+    const unsigned whole = (unsigned)std::min<size_t>(256, round_up(m, 16 * ctas));
+    const size_t tiles_p = ceil_div(n, 128 * ctas), units = std::max(1u, sms / ctas);
+    for (unsigned width : widths) {
+      const unsigned bn = std::min(width, whole);
+      if (bn % (16 * ctas)) continue;
+      const size_t tiles = tiles_p * ceil_div(m, bn), waves = ceil_div(tiles, units);
+      const size_t block = ctas == 2 ? std::max(150u, 90u + bn * 9 / 10) : 150u + bn * 23 / 20;
+      for (unsigned split = 1; split <= (ctas == 2 ? 1 : 8); split *= 2) {
+        // (clusters of 8 find room for 64 CTAs: with 128 they came one after another)
+        if (split > 1 && (split > kblocks || tiles * split > (split == 8 ? std::min(64u, sms) : sms))) break;
+        const size_t cost = waves * (ceil_div(kblocks, split) * block + (bn > 224 ? 1000 : 0)) + 5500 + 4 * bn + (split > 1 ? 1300 + 11 * bn : 0);
+        if (cost < least) least = cost, p.ctas = ctas, p.bn = bn, p.split = split;
+      }
+      if (bn == whole) break;
     }
   }
+  p.tiles_p = (unsigned)ceil_div(n, 128 * p.ctas);
   p.tiles_q = (unsigned)ceil_div(m, p.bn);
-  const size_t tiles = (size_t)p.tiles_p * p.tiles_q;
-  p.split = (unsigned)std::max<size_t>(1, std::min<size_t>({8, sms / tiles, kblocks / 2}));
 }
 
 // A backward pass's workspace, whatever its type and alignment: long rows' sums, and rows of partial sums.
@@ -236,7 +250,7 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
   const int sms = sm_count();
   cut_product(m, n, kblocks, (unsigned)sms, p);
   if ((size_t)p.tiles_p * p.tiles_q > 0x7fffffff) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", m, n);
-  if (!map_codes(&p.p_map, b, b_stride, n, k, 128) || !map_codes(&p.q_map, a, a_stride, m, k, p.bn))
+  if (!map_codes(&p.p_map, b, b_stride, n, k, 128) || !map_codes(&p.q_map, a, a_stride, m, k, p.bn / p.ctas))
     return fail(XP_ERR_CUDA, "cuTensorMapEncodeTiled refuses %zu x %zu or %zu x %zu codes", m, k, n, k);
   p.p_scales = b_scales;
   p.q_scales = a_scales;

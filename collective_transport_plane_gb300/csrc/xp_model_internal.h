@@ -19,8 +19,8 @@ struct Matmul8Params {
   int p_shift, q_shift;                  // 7: a row of scales serves 128 rows
   unsigned p_rows, q_rows;               // C's columns and rows
   unsigned kblocks;
-  unsigned bn, split;                    // rows of A in a tile; CTAs that share one
-  unsigned stages, nsums, slots;
+  unsigned bn, ctas, split;              // rows of A in a tile; CTAs of a pair, or that share the columns of a tile
+  unsigned stages, nsums;
   unsigned tiles_p, tiles_q;
   void* c;
   unsigned long long c_stride;           // elements

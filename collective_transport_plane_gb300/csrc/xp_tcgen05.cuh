@@ -11,6 +11,16 @@ namespace tc {
 
 __device__ __forceinline__ unsigned smem_of(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
 
+// One lane of a converged warp, the same each time.  (Code that the warp walks
+// through together with an elected lane's instructions in between keeps its
+// values in uniform registers, which the tensor core's instructions take: a
+// product's block of 128 columns took 800 cycles to issue from a lane's own loop.)
+__device__ __forceinline__ bool elected() {
+  unsigned p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- mbarriers, all waits with a limit
 __device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -23,7 +33,7 @@ __device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {
 }
 __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
   unsigned ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.u32 %0, 1, 0, p;\n}"
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
@@ -45,34 +55,77 @@ __device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity) {
 }
 __device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity) { return bar_try(bar, parity) || bar_wait_long(bar, parity); }
 
+// ---- the CTAs of a cluster
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Where a CTA's shared memory address lies in the cluster's.
+__device__ __forceinline__ unsigned in_cta(unsigned smem, unsigned rank) {
+  unsigned r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(unsigned bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One that publishes nothing in memory, and waits for no store before it.
+__device__ __forceinline__ void bar_arrive_relaxed(unsigned bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ---- tiled copies into shared memory
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
-// the box of `m` whose first element is column x of row y
+// The box of `m` whose first element is column x of row y.  CTAS 2: the barrier may be the other CTA's of a pair.
+template <int CTAS>
 __device__ __forceinline__ void load_box(unsigned smem, const CUtensorMap* m, int x, int y, unsigned bar) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-               ::"r"(smem), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-// ---- TMEM: 128 lanes of 512 columns of 32 bits; an address is lane << 16 | column
+// ---- TMEM: 128 lanes of 512 columns of 32 bits; an address is lane << 16 | column.
+// CTAS 2: a warp of each CTA of a pair takes part.
+template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(unsigned result_smem, unsigned columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(result_smem), "r"(columns) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  if constexpr (CTAS == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(result_smem), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(result_smem), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
 }
+template <int CTAS>
 __device__ __forceinline__ void tmem_free(unsigned at, unsigned columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+  if constexpr (CTAS == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
-// 16 columns of the warp's 32 lanes, a lane's into its own registers
+// 16 columns of the warp's 32 lanes, a lane's into its own registers: there
+// after tmem_wait() and landed() of them.
 __device__ __forceinline__ void tmem_load16(unsigned at, float (&v)[16]) {
-  unsigned u[16];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
-                 "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+                 "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
                : "r"(at) : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// No use of the registers moves before this.
+__device__ __forceinline__ void landed(float (&v)[16]) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+               "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -87,25 +140,43 @@ __device__ __forceinline__ unsigned long long rows128(unsigned smem) {
 __device__ __forceinline__ unsigned long long rows16(unsigned smem) {
   return (unsigned long long)(smem >> 4 & 0x3fff) | 8ull << 32 | 1ull << 46;
 }
-// 32 rows of 16 bytes to 4 columns, the same for each 32 lanes.
+// 32 rows of 16 bytes to 4 columns, the same for each 32 lanes.  CTAS 2: in
+// both CTAs of a pair, each from its own shared memory.
+template <int CTAS>
 __device__ __forceinline__ void copy_scales(unsigned tmem, unsigned long long rows) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(rows) : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(rows) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(rows) : "memory");
 }
 // d = [d +] a b^T over 32 columns of codes (e4m3), each row's 32 columns times
-// the power of two that its scale byte says.
+// the power of two that its scale byte says.  CTAS 2: 256 rows of a, half of
+// them in each CTA's shared memory and TMEM, and half of b's rows in each's.
+template <int CTAS>
 __device__ __forceinline__ void mma_scaled(unsigned d, unsigned long long a, unsigned long long b, unsigned shape, unsigned scale_a,
                                            unsigned scale_b, bool add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-               ::"r"(d), "l"(a), "l"(b), "r"(shape), "r"(scale_a), "r"(scale_b), "r"((unsigned)add) : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(shape), "r"(scale_a), "r"(scale_b), "r"((unsigned)add) : "memory");
+  else
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+                 "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(shape), "r"(scale_a), "r"(scale_b), "r"((unsigned)add) : "memory");
 }
-// 128 x n products of e4m3 codes; `byte` of its columns' words is the scale.
+// CTAS 128 x n products of e4m3 codes; `byte` of its columns' words is the scale.
+template <int CTAS>
 __device__ __forceinline__ unsigned scaled_shape(unsigned n, unsigned byte) {
-  return byte << 4 | (n >> 3) << 17 | 1u << 23 | (128u >> 4) << 24 | byte << 29;
+  return byte << 4 | (n >> 3) << 17 | 1u << 23 | (CTAS * 128u >> 4) << 24 | byte << 29;
 }
-// The mbarrier's phase counts this thread's products and copies so far as one arrival.
+// The mbarrier's phase counts this thread's products and copies so far as one
+// arrival (CTAS 2: the barriers at this place in both CTAs).
+template <int CTAS>
 __device__ __forceinline__ void commit_to(unsigned bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((unsigned short)3) : "memory");
 }
 
 }  // namespace tc

@@ -26,14 +26,11 @@ cudaError_t allow_dynamic_smem(void (*kernel)(Params...)) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamicSmem);
 }
 
-// One launch, with programmatic dependence on the work before it (a stream of
-// small steps: 8.3 us each without, 4.0 with it); csize > 1: in clusters of
-// that many CTAs, and without it, as clusters placed beside a kernel that
-// drains held each other up (layer norm backward 2000 x 40032: 169 us with it,
-// 116 without).
+// One launch in clusters of csize CTAs; dependent: with programmatic dependence
+// on the work before it.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, size_t smem, int csize, cudaStream_t st,
-                             Args... args) {
+cudaError_t launch_clusters(void (*kernel)(Params...), dim3 grid, int block, size_t smem, int csize, bool dependent, cudaStream_t st,
+                            Args... args) {
   if (smem > 40 * 1024) {   // with what the kernel takes statically, more than the 48 KiB every kernel may have
     const cudaError_t e = allow_dynamic_smem(kernel);
     if (e != cudaSuccess) return e;
@@ -44,14 +41,31 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, si
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = csize;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = csize > 1 ? at + 1 : at;
-  cfg.numAttrs = 1;
+  unsigned n = 0;
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (csize > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = csize;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+// One launch, with programmatic dependence on the work before it (a stream of
+// small steps: 8.3 us each without, 4.0 with it); csize > 1: in clusters of
+// that many CTAs, and without it, as clusters placed beside a kernel that
+// drains held each other up (layer norm backward 2000 x 40032: 169 us with it,
+// 116 without).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, size_t smem, int csize, cudaStream_t st,
+                             Args... args) {
+  return launch_clusters(kernel, grid, block, smem, csize, csize == 1, st, args...);
 }
 
 }  // namespace xp
