@@ -14,29 +14,68 @@ namespace {
 typedef __nv_bfloat16 bf16;
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTurns = 128 / (4 * kWarps);   // a warp takes 4 rows at a time
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 
-// n of 4 neighbouring elements; zeros behind them
+// Four neighbouring elements as they are stored: registers decide how many CTAs an SM has.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, bool aligned, float (&f)[4]) {
+struct Four;
+template <>
+struct Four<float> {
+  float4 q;
+  __device__ __forceinline__ void load(const float* p) { q = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void set(const float (&f)[4]) { q = make_float4(f[0], f[1], f[2], f[3]); }
+  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w; }
+  // Largest magnitudes, of each of the four columns or of all: as bits, NaN above all.
+  struct Tops {
+    unsigned t[4] = {0, 0, 0, 0};
+  };
+  __device__ __forceinline__ void raise(Tops& m) const {
+    m.t[0] = max(m.t[0], abs_bits(q.x)), m.t[1] = max(m.t[1], abs_bits(q.y));
+    m.t[2] = max(m.t[2], abs_bits(q.z)), m.t[3] = max(m.t[3], abs_bits(q.w));
+  }
+  static __device__ __forceinline__ uint4 tops(const Tops& m) { return make_uint4(m.t[0], m.t[1], m.t[2], m.t[3]); }
+  __device__ __forceinline__ unsigned top() const { return max(max(abs_bits(q.x), abs_bits(q.y)), max(abs_bits(q.z), abs_bits(q.w))); }
+};
+template <>
+struct Four<bf16> {
+  uint2 q;
+  __device__ __forceinline__ void load(const bf16* p) { q = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void set(const float (&f)[4]) {   // exact: these were bf16
+    q.x = __float_as_uint(f[0]) >> 16 | (__float_as_uint(f[1]) & 0xffff0000u);
+    q.y = __float_as_uint(f[2]) >> 16 | (__float_as_uint(f[3]) & 0xffff0000u);
+  }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(q.x << 16), f[1] = __uint_as_float(q.x & 0xffff0000u);
+    f[2] = __uint_as_float(q.y << 16), f[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+  struct Tops {   // two columns' bits in a word: magnitudes order like 16-bit numbers
+    unsigned t[2] = {0, 0};
+  };
+  __device__ __forceinline__ void raise(Tops& m) const { m.t[0] = __vmaxu2(m.t[0], q.x & 0x7fff7fffu), m.t[1] = __vmaxu2(m.t[1], q.y & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint4 tops(const Tops& m) { return make_uint4(m.t[0] << 16, m.t[0] & 0xffff0000u, m.t[1] << 16, m.t[1] & 0xffff0000u); }
+  __device__ __forceinline__ unsigned top() const {
+    const unsigned m = __vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
+  }
+};
+// n of them; zeros behind
+template <typename T>
+__device__ __forceinline__ Four<T> load4(const T* p, int n, bool aligned) {
+  Four<T> four;
   if (n >= 4 && aligned) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p);
-      f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      f[0] = __uint_as_float(q.x << 16), f[1] = __uint_as_float(q.x & 0xffff0000u);
-      f[2] = __uint_as_float(q.y << 16), f[3] = __uint_as_float(q.y & 0xffff0000u);
-    }
+    four.load(p);
   } else {
+    float f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
+    four.set(f);
   }
+  return four;
 }
 __device__ __forceinline__ void store4(uint8_t* p, unsigned codes, int n, bool aligned) {
   if (n >= 4 && aligned) {
@@ -48,42 +87,44 @@ __device__ __forceinline__ void store4(uint8_t* p, unsigned codes, int n, bool a
   }
 }
 
-// Rows of the tile: warp w has 4 w .. 4 w + 3 of each 32 (turn), lane l the
+// Rows of the tile: warp w has 4 w .. 4 w + 3 of each 64 (turn), lane l the
 // columns 4 l .. 4 l + 3.  So four rows' codes of a column are one word of the
 // transposed tile, whose word (column, rows / 4) is kept at the place that
 // column / 4 turns: a warp's words lie in 32 banks when it writes those of a
 // row and when it reads those of a column.
-template <typename T, bool TILE>
-__global__ void __launch_bounds__(kThreads) encode_kernel(const Encode8Params p) {
-  __shared__ unsigned words[128 * 32];
-  __shared__ unsigned tops[kWarps][128];
-  wait_for_predecessors();
-  let_successor_start();
+// WHOLE: all of the tile is there, and its rows and columns are aligned.
+template <typename T, bool TILE, bool WHOLE>
+__device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&words)[128 * 32], unsigned (&tops)[kWarps][128], unsigned tile_r,
+                                            unsigned tile_c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned tile_r = blockIdx.x / p.tiles_c, tile_c = blockIdx.x - tile_r * p.tiles_c;
   const unsigned r0 = tile_r * 128, c0 = tile_c * 128 + 4 * lane;
-  const int n = (int)min(4u, p.cols > c0 ? p.cols - c0 : 0u);
-  const T* x = static_cast<const T*>(p.x) + (u64)r0 * p.x_stride + c0;
-  float f[kTurns][4][4];
+  const int n = WHOLE ? 4 : (int)min(4u, p.cols > c0 ? p.cols - c0 : 0u);
+  // this warp's rows of turn 0; a turn's are kWarps * 4 rows further
+  const unsigned mine = 4 * warp, next = 4 * kWarps;
+  const T* x = static_cast<const T*>(p.x) + (u64)(r0 + mine) * p.x_stride + c0;
+  Four<T> four[kTurns][4];
 #pragma unroll
-  for (int t = 0; t < kTurns; ++t)
+  for (int t = 0; t < kTurns; ++t, x += next * p.x_stride) {
+    const T* at = x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned r = 32 * t + 4 * warp + i;
-      load4(x + r * p.x_stride, r0 + r < p.rows ? n : 0, p.x_aligned, f[t][i]);
+    for (int i = 0; i < 4; ++i, at += p.x_stride) {
+      if (WHOLE)
+        four[t][i].load(at);
+      else
+        four[t][i] = load4(at, r0 + mine + next * t + i < p.rows ? n : 0, p.x_aligned);
     }
+  }
 
   unsigned tile_e = 0;
   if (TILE || p.codes_t) {
-    unsigned top[4] = {0, 0, 0, 0};
+    typename Four<T>::Tops most_of;
 #pragma unroll
     for (int t = 0; t < kTurns; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = max(top[c], abs_bits(f[t][i][c]));
+      for (int i = 0; i < 4; ++i) four[t][i].raise(most_of);
+    const uint4 top = Four<T>::tops(most_of);
     if constexpr (TILE) {
-      const unsigned all = __reduce_max_sync(0xffffffffu, max(max(top[0], top[1]), max(top[2], top[3])));
+      const unsigned all = __reduce_max_sync(0xffffffffu, max(max(top.x, top.y), max(top.z, top.w)));
       if (lane == 0) tops[warp][0] = all;
       __syncthreads();
       unsigned most = 0;
@@ -95,101 +136,171 @@ __global__ void __launch_bounds__(kThreads) encode_kernel(const Encode8Params p)
         if (p.codes_t) p.scales_t[tile_c * p.scales_t_stride + tile_r] = (uint8_t)tile_e;
       }
     } else {
-      *reinterpret_cast<uint4*>(&tops[warp][4 * lane]) = make_uint4(top[0], top[1], top[2], top[3]);
+      *reinterpret_cast<uint4*>(&tops[warp][4 * lane]) = top;
+      __syncthreads();
+      if (threadIdx.x < 128) {   // a column's scale by one thread; its inverse goes into the first warp's row
+        unsigned most = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) most = max(most, tops[w][threadIdx.x]);
+        const unsigned e = scale_of(most), col = tile_c * 128 + threadIdx.x;
+        tops[0][threadIdx.x] = __float_as_uint(inverse_of(e));
+        if (WHOLE || col < p.cols) p.scales_t[(u64)col * p.scales_t_stride + tile_r] = (uint8_t)e;
+      }
       __syncthreads();
     }
   }
 
+  const float tile_inverse = inverse_of(tile_e);
   if (p.codes) {
-    uint8_t* codes = p.codes + (u64)r0 * p.codes_stride + c0;
+    uint8_t* codes = p.codes + (u64)(r0 + mine) * p.codes_stride + c0;
+    uint8_t* scales = p.scales + (u64)(r0 + mine) * p.scales_stride + tile_c;
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t)
+    for (int t = 0; t < kTurns; ++t, codes += next * p.codes_stride, scales += next * p.scales_stride) {
+      unsigned e[4];
+      if constexpr (!TILE) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned r = 32 * t + 4 * warp + i;
-        const float(&v)[4] = f[t][i];
-        unsigned e = tile_e;
-        if constexpr (!TILE) {
-          e = scale_of(__reduce_max_sync(0xffffffffu, max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])))));
-          if (lane == 0 && r0 + r < p.rows) p.scales[(u64)(r0 + r) * p.scales_stride + tile_c] = (uint8_t)e;
-        }
-        store4(codes + r * p.codes_stride, codes4(v[0], v[1], v[2], v[3], inverse_of(e), e), r0 + r < p.rows ? n : 0, p.codes_aligned);
+        for (int i = 0; i < 4; ++i) e[i] = scale_of(__reduce_max_sync(0xffffffffu, four[t][i].top()));
+        // four rows' scales by four lanes
+        const unsigned m = lane == 0 ? e[0] : lane == 1 ? e[1] : lane == 2 ? e[2] : e[3];
+        if (lane < 4 && (WHOLE || r0 + mine + next * t + lane < p.rows)) scales[lane * p.scales_stride] = (uint8_t)m;
       }
+      uint8_t* at = codes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i, at += p.codes_stride) {
+        float f[4];
+        four[t][i].get(f);
+        const unsigned c = codes4(f[0], f[1], f[2], f[3], TILE ? tile_inverse : inverse_of(e[i]));
+        if (WHOLE)
+          *reinterpret_cast<unsigned*>(at) = c;
+        else
+          store4(at, c, r0 + mine + next * t + i < p.rows ? n : 0, p.codes_aligned);
+      }
+    }
   }
   if (!p.codes_t) return;
 
+  float inverse[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    unsigned e = tile_e;
-    if constexpr (!TILE) {
-      unsigned most = 0;
+  for (int c = 0; c < 4; ++c) inverse[c] = TILE ? tile_inverse : __uint_as_float(tops[0][4 * lane + c]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) most = max(most, tops[w][4 * lane + c]);
-      e = scale_of(most);
-      if (warp == 0 && c < n) p.scales_t[(u64)(c0 + c) * p.scales_t_stride + tile_r] = (uint8_t)e;
-    }
-    const float inverse = inverse_of(e);
+  for (int t = 0; t < kTurns; ++t) {
+    float f[4][4];
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t)
-      words[(4 * lane + c) * 32 + ((kWarps * t + warp) ^ lane)] = codes4(f[t][0][c], f[t][1][c], f[t][2][c], f[t][3][c], inverse, e);
+    for (int i = 0; i < 4; ++i) four[t][i].get(f[i]);
+    unsigned* to = words + 128 * lane + ((kWarps * t + warp) ^ lane);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) to[32 * c] = codes4(f[0][c], f[1][c], f[2][c], f[3][c], inverse[c]);
   }
   __syncthreads();
-  const unsigned row = r0 + 4 * lane;
-  const int nr = (int)min(4u, p.rows > row ? p.rows - row : 0u);
+  const unsigned row = r0 + 4 * lane, first = warp * (128 / kWarps);
+  const int nr = WHOLE ? 4 : (int)min(4u, p.rows > row ? p.rows - row : 0u);
+  uint8_t* out = p.codes_t + (u64)(tile_c * 128 + first) * p.codes_t_stride + row;
 #pragma unroll
-  for (int j = 0; j < 128 / kWarps; ++j) {
-    const unsigned c = warp * (128 / kWarps) + j, col = tile_c * 128 + c;
-    if (col < p.cols) store4(p.codes_t + (u64)col * p.codes_t_stride + row, words[c * 32 + (lane ^ (c >> 2))], nr, p.codes_t_aligned);
+  for (int j = 0; j < 128 / kWarps; ++j, out += p.codes_t_stride) {
+    const unsigned c = first + j, word = words[c * 32 + (lane ^ (c >> 2))];
+    if (WHOLE)
+      *reinterpret_cast<unsigned*>(out) = word;
+    else if (tile_c * 128 + c < p.cols)
+      store4(out, word, nr, p.codes_t_aligned);
   }
 }
 
-// 16 codes per thread; a row's threads side by side.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const Decode8Params p) {
+// (16384 x 4096 bf16, both forms: 80 us with addresses and edges worked out for
+// every row, at 0.7 instructions per clock and scheduler, 30 for each element.)
+template <typename T, bool TILE>
+__global__ void __launch_bounds__(kThreads, 2) encode_kernel(const Encode8Params p) {
+  __shared__ unsigned words[128 * 32];
+  __shared__ __align__(16) unsigned tops[kWarps][128];
   wait_for_predecessors();
   let_successor_start();
-  const unsigned per_row = (p.cols + 15) / 16;
-  const u64 at = (u64)blockIdx.x * kThreads + threadIdx.x;
-  if (at >= (u64)per_row * p.rows) return;
-  const unsigned row = (unsigned)(at / per_row), c = ((unsigned)(at - (u64)row * per_row)) * 16;
-  const int n = (int)min(16u, p.cols - c);
-  const uint8_t* from = p.codes + (u64)row * p.codes_stride + c;
-  T* out = static_cast<T*>(p.out) + (u64)row * p.out_stride + c;
-  const float scale = power_of(p.scales[(u64)(row >> p.shift) * p.scales_stride + c / 128]);
-  if (n == 16 && p.aligned) {
-    const uint4 q = *reinterpret_cast<const uint4*>(from);
-    const unsigned w[4] = {q.x, q.y, q.z, q.w};
-    float v[16];
+  const unsigned tile_r = blockIdx.x / p.tiles_c, tile_c = blockIdx.x - tile_r * p.tiles_c;
+  if (p.all_aligned && (tile_r + 1) * 128 <= p.rows && (tile_c + 1) * 128 <= p.cols)
+    encode_tile<T, TILE, true>(p, words, tops, tile_r, tile_c);
+  else
+    encode_tile<T, TILE, false>(p, words, tops, tile_r, tile_c);
+}
+
+// A warp has a piece of 1024 columns of a row.  Where rows are aligned its lanes
+// take the codes of 16 bytes of output each, side by side (each lane 16 codes, in
+// two stores of every other 16 bytes: 36 us for 16384 x 4096 to bf16), else every
+// 32nd column.
+constexpr int kDecodeThreads = 256;
+constexpr unsigned kPiece = 1024;
+
+template <typename T>
+__global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const Decode8Params p) {
+  wait_for_predecessors();
+  let_successor_start();
+  const int lane = threadIdx.x & 31;
+  const unsigned per_row = (p.cols + kPiece - 1) / kPiece;
+  const u64 piece = (u64)blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
+  if (piece >= (u64)per_row * p.rows) return;
+  const u64 row = piece / per_row;
+  const unsigned from = (unsigned)(piece - row * per_row) * kPiece;
+  const uint8_t* codes = p.codes + row * p.codes_stride;
+  const uint8_t* scales = p.scales + (row >> p.shift) * p.scales_stride;
+  T* out = static_cast<T*>(p.out) + row * p.out_stride;
+  constexpr int E = 16 / (int)sizeof(T), N = kPiece / 32 / E;
+  if (p.aligned && p.cols % E == 0) {
+    unsigned w[N][E / 4];
+    float scale[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = values2((unsigned short)(w[i / 2] >> 16 * (i & 1)));
-      v[2 * i] = f.x * scale;
-      v[2 * i + 1] = f.y * scale;
+    for (int k = 0; k < N; ++k) {
+      const unsigned c = from + (32 * k + lane) * E;
+      if (c >= p.cols) break;
+      scale[k] = power_of(scales[c / 128]);
+      if constexpr (E == 8) {
+        const uint2 q = *reinterpret_cast<const uint2*>(codes + c);
+        w[k][0] = q.x, w[k][1] = q.y;
+      } else {
+        w[k][0] = *reinterpret_cast<const unsigned*>(codes + c);
+      }
     }
-    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
+    for (int k = 0; k < N; ++k) {
+      const unsigned c = from + (32 * k + lane) * E;
+      if (c >= p.cols) break;
+      float v[E];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 f = values2((unsigned short)(w[k][i / 2] >> 16 * (i & 1)));
+        v[2 * i] = f.x * scale[k], v[2 * i + 1] = f.y * scale[k];
+      }
+      if constexpr (E == 8) {
         unsigned u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
           u[j] = *reinterpret_cast<const unsigned*>(&h);
         }
-        reinterpret_cast<uint4*>(out)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+        *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
       }
     }
     return;
   }
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float v = values2(from[i]).x * scale;
-    if constexpr (sizeof(T) == 4)
-      out[i] = v;
-    else
-      out[i] = __float2bfloat16_rn(v);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const unsigned c0 = from + 512 * half + lane;
+    uint8_t code[16], e[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const unsigned c = c0 + 32 * i;
+      code[i] = c < p.cols ? codes[c] : 0;
+      if (i % 4 == 0) e[i / 4] = c < p.cols ? scales[c / 128] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const unsigned c = c0 + 32 * i;
+      const float v = values2(code[i]).x * power_of(e[i / 4]);
+      if (c < p.cols) {
+        if constexpr (sizeof(T) == 4)
+          out[c] = v;
+        else
+          out[c] = __float2bfloat16_rn(v);
+      }
+    }
   }
 }
 
@@ -203,8 +314,9 @@ cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, cu
 }
 
 cudaError_t launch_decode8(const Decode8Params& p, int dtype, cudaStream_t st) {
-  const u64 n = (u64)((p.cols + 15) / 16) * p.rows;
-  return launch_dependent(dtype == XP_F32 ? decode_kernel<float> : decode_kernel<bf16>, dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, 1, st, p);
+  const u64 pieces = (u64)((p.cols + kPiece - 1) / kPiece) * p.rows, per_cta = kDecodeThreads / 32;
+  return launch_dependent(dtype == XP_F32 ? decode_kernel<float> : decode_kernel<bf16>, dim3((unsigned)((pieces + per_cta - 1) / per_cta)), kDecodeThreads,
+                          0, 1, st, p);
 }
 
 }  // namespace xp

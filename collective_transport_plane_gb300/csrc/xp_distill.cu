@@ -61,6 +61,43 @@ __device__ __forceinline__ unsigned head_of(const T* row, unsigned n) {
   return min(n, (unsigned)((16u - (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / (unsigned)sizeof(T));
 }
 
+// ---- a row's units on their way into shared memory: two at a time per thread
+// (a batch), into places of its own, three batches ahead of the one in work.
+constexpr int kBatch = 2, kBatches = 4;
+struct Ring {
+  unsigned smem, n, threads;   // this thread's first place; whole batches that it has
+  const uint4* from;
+  __device__ __forceinline__ Ring(const uint8_t* raw, unsigned top, const uint4* body, unsigned units) {
+    threads = blockDim.x;
+    smem = (unsigned)__cvta_generic_to_shared(raw) + 12 * ((top + 3) & ~3u) + 16 * threadIdx.x;
+    from = body + threadIdx.x;
+    const unsigned each = units > threadIdx.x ? (units - threadIdx.x - 1) / threads + 1 : 0;
+    n = each / kBatch;
+  }
+  __device__ __forceinline__ unsigned place(unsigned b, int i) const { return smem + 16 * threads * (b % kBatches * kBatch + i); }
+  __device__ __forceinline__ void bring(unsigned b) const {
+    if (b < n) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(b, i)), "l"(from + (u64)(b * kBatch + i) * threads) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void begin() const {
+#pragma unroll
+    for (int b = 0; b + 1 < kBatches; ++b) bring(b);
+  }
+  __device__ __forceinline__ void next(unsigned b, uint4 (&q)[kBatch]) const {   // batch b, and one more on its way
+    bring(b + kBatches - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBatches - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w) : "r"(place(b, i)) : "memory");
+  }
+  // nothing lands after this
+  __device__ __forceinline__ void end() const { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+};
+
 // The CTA's maximum and sum, the same in every thread.  (A NaN is a sum's to
 // carry on: fmaxf leaves it out.)
 __device__ __forceinline__ float cta_max(float v, float* words) {
@@ -96,7 +133,8 @@ __device__ __forceinline__ Entries entries_in(uint8_t* raw, unsigned top) {
 }
 
 // Brings them.  False, the same for the CTA, if the row has none.  max_u: the
-// largest of this thread's.
+// largest of this thread's.  (The threads' first loads of the row's logits are on
+// their way meanwhile: 8192 x 32000 bf16 forward 117 us without.)
 template <typename T>
 __device__ __forceinline__ bool bring_entries(const DistillParams& p, u64 row, const T* logits, const Entries& e, float inv_t, float& max_u) {
   max_u = -INFINITY;
@@ -116,41 +154,108 @@ __device__ __forceinline__ bool bring_entries(const DistillParams& p, u64 row, c
   return __syncthreads_or(any);
 }
 
-// A thread's share of a row: the running maximum m and the sum s of
-// 2^((z - m) c).  m is the largest z met, or -infinity, where s is 0.
+// A thread's share of a row: the running maximum m of z and the sum s of
+// 2^((z - m) c).  (Differences first: z c and m c by themselves overflow where a
+// mask is the type's lowest value.)  m is -infinity and s 0 while nothing above
+// -infinity was met; differences are from 0 then.
 struct Running {
   float m, s;
 };
-template <int N>
-__device__ __forceinline__ void take(Running& r, const float (&f)[N], float c) {
-  float top = f[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
+__device__ __forceinline__ float from(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ void raise_to(Running& r, float top, float c) {
   if (top > r.m) {
-    r.s *= pow2((r.m - top) * c);   // 2^-infinity: 0
+    r.s *= pow2((r.m - top) * c);   // 2^-infinity is 0
     r.m = top;
   }
-  // nothing but -infinity (or NaN, which goes on) so far: no difference from it is formed
-  const float m = r.m == -INFINITY ? 0.f : r.m;
-  float s = 0.f;
+}
+// Two sums at once: packed additions, half the instructions.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %4};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b));
+  return d;
+}
+// N units of 16 bytes
+template <typename T, int N>
+__device__ __forceinline__ void take(Running& r, const uint4 (&q)[N], float c) {
+  float top = -INFINITY;
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) s += pow2((f[i] - m) * c);
-  r.s += s;
+    for (int i = 0; i < N; ++i) {
+      float f[4];
+      unpack<T>(q[i], f);
+      top = fmaxf(top, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+    }
+  } else {   // pairs as they are
+    __nv_bfloat162 most = *reinterpret_cast<const __nv_bfloat162*>(&q[0].x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most = __hmax2(most, *reinterpret_cast<const __nv_bfloat162*>(&w[j]));
+    }
+    top = fmaxf(__low2float(most), __high2float(most));
+  }
+  raise_to(r, top, c);
+  const float low = -from(r.m);
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f[kUnit<T>];
+    unpack<T>(q[i], f);
+#pragma unroll
+    for (int j = 0; j < kUnit<T>; j += 2) {
+      const float2 x = mul2(add2(make_float2(f[j], f[j + 1]), make_float2(low, low)), c);
+      s = add2(s, make_float2(pow2(x.x), pow2(x.y)));
+    }
+  }
+  r.s += s.x + s.y;
+}
+// What two threads, or warps, have, as one: the same for both.
+__device__ __forceinline__ Running joined(const Running& a, float m, float s, float c) {
+  const float most = fmaxf(a.m, m), low = from(most);
+  return {most, a.s * pow2((a.m - low) * c) + s * pow2((m - low) * c)};
+}
+__device__ __forceinline__ Running warp_joined(Running r, float c) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) r = joined(r, __shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o), c);
+  return r;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(1024) forward_kernel(const DistillParams p) {
-  constexpr int V = kUnit<T>, kAtOnce = 4;
-  extern __shared__ uint8_t raw[];
-  __shared__ float words[32];
+  constexpr int V = kUnit<T>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ Running words[32];
   wait_for_predecessors();
   let_successor_start();
   const Entries e = entries_in(raw, p.top);
   const u64 row = blockIdx.x;
   const T* z = static_cast<const T*>(p.logits) + row * p.logits_stride;
   const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
+  const unsigned head = head_of(z, p.vocab), units = (p.vocab - head) / V, tail = head + units * V, n = blockDim.x;
+  const uint4* body = reinterpret_cast<const uint4*>(z + head);
+  const Ring ring(raw, p.top, body, units);
+  ring.begin();
   float max_u;
   if (!bring_entries(p, row, z, e, inv_t, max_u)) {
+    ring.end();
     if (threadIdx.x == 0) {
       p.loss[row] = 0.f;
       if (p.lse) p.lse[row] = 0.f;
@@ -158,48 +263,47 @@ __global__ void __launch_bounds__(1024) forward_kernel(const DistillParams p) {
     return;
   }
   Running r = {-INFINITY, 0.f};
-  const unsigned head = head_of(z, p.vocab), units = (p.vocab - head) / V, tail = head + units * V;
-  const uint4* body = reinterpret_cast<const uint4*>(z + head);
-  unsigned k = threadIdx.x;
-  for (; k + (kAtOnce - 1) * blockDim.x < units; k += kAtOnce * blockDim.x) {
-    uint4 q[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) q[i] = body[k + i * blockDim.x];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      float f[V];
-      unpack<T>(q[i], f);
-      take<V>(r, f, c);
-    }
+  for (unsigned b = 0; b < ring.n; ++b) {
+    uint4 q[kBatch];
+    ring.next(b, q);
+    take<T>(r, q, c);
   }
-  for (; k < units; k += blockDim.x) {
-    float f[V];
-    unpack<T>(body[k], f);
-    take<V>(r, f, c);
+  for (unsigned k = threadIdx.x + ring.n * kBatch * n; k < units; k += n) {
+    const uint4 one[1] = {body[k]};
+    take<T>(r, one, c);
   }
   // the row's ends: fewer elements than threads
   if (threadIdx.x < head || tail + threadIdx.x - head < p.vocab) {
-    const float f[1] = {to_f(z[threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head])};
-    take<1>(r, f, c);
+    const float f = to_f(z[threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head]);
+    raise_to(r, f, c);
+    r.s += pow2((f - from(r.m)) * c);
   }
-  const float m = cta_max(r.m, words), m0 = m == -INFINITY ? 0.f : m;
-  const float s = cta_sum(r.m == -INFINITY ? r.s : r.s * pow2((r.m - m0) * c), words);
-  const float lse = m * inv_t + logf(s);
-
-  const float top_u = cta_max(max_u, words);
+  r = warp_joined(r, c);
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = r;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  // the first warp: all warps' sums, then the few entries
+  const unsigned nw = blockDim.x >> 5, lane = threadIdx.x;
+  r = lane < nw ? words[lane] : Running{-INFINITY, 0.f};
+  r = warp_joined(r, c);
+  const float lse = r.m * inv_t + logf(r.s);
+  float top_u = -INFINITY;
+  for (unsigned j = lane; j < p.top; j += 32)
+    if (e.id[j] >= 0) top_u = fmaxf(top_u, e.u[j]);
+  top_u = warp_max(top_u);
   float w = 0.f;
-  for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x)
+  for (unsigned j = lane; j < p.top; j += 32)
     if (e.id[j] >= 0) w += pow2((e.u[j] - top_u) * kLog2e);
-  w = cta_sum(w, words);
+  w = warp_sum(w);
   const float log_w = logf(w);
   float loss = 0.f;
-  for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x) {
+  for (unsigned j = lane; j < p.top; j += 32) {
     if (e.id[j] < 0) continue;
     const float d = e.u[j] - top_u, prob = pow2(d * kLog2e) / w;
     if (!(prob == 0.f)) loss += prob * ((d - log_w) - (e.z[j] * inv_t - lse));
   }
-  loss = cta_sum(loss, words);
-  if (threadIdx.x == 0) {
+  loss = warp_sum(loss);
+  if (lane == 0) {
     p.loss[row] = loss * p.temperature * p.temperature;
     if (p.lse) p.lse[row] = lse;
   }
@@ -207,8 +311,8 @@ __global__ void __launch_bounds__(1024) forward_kernel(const DistillParams p) {
 
 template <typename T>
 __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
-  constexpr int V = kUnit<T>, kAtOnce = 4;
-  extern __shared__ uint8_t raw[];
+  constexpr int V = kUnit<T>;
+  extern __shared__ __align__(16) uint8_t raw[];
   __shared__ float words[32];
   wait_for_predecessors();
   let_successor_start();
@@ -216,40 +320,36 @@ __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
   const u64 row = blockIdx.x;
   const T* z = static_cast<const T*>(p.logits) + row * p.logits_stride;
   T* out = static_cast<T*>(p.dlogits) + row * p.dlogits_stride;
-  const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
+  const float inv_t = 1.f / p.temperature;
+  const unsigned head = head_of(out, p.vocab), units = (p.vocab - head) / V, tail = head + units * V, n = blockDim.x;
+  const bool alike = head_of(z, p.vocab) == head;   // z has the same phase
+  const uint4* body = reinterpret_cast<const uint4*>(z + head);
+  uint4* to = reinterpret_cast<uint4*>(out + head);
+  const Ring ring(raw, p.top, body, alike ? units : 0);
+  ring.begin();
   float max_u;
   const bool any = bring_entries(p, row, z, e, inv_t, max_u);
-  const float lse = any ? p.lse[row] : 0.f, scale = any ? p.dloss[row] * p.temperature : 0.f, lse2 = lse * kLog2e;
-  // q = 2^(z c - lse2); rows without entries do not look at z
-  auto q_of = [&](float v) { return pow2(fmaf(v, c, -lse2)); };
-  const unsigned head = head_of(out, p.vocab), units = (p.vocab - head) / V, tail = head + units * V;
-  const bool alike = head_of(z, p.vocab) == head;   // z has the same phase
-  uint4* to = reinterpret_cast<uint4*>(out + head);
+  const float lse = any ? p.lse[row] : 0.f, scale = any ? p.dloss[row] * p.temperature : 0.f;
+  // q = e^(z / T - lse); rows without entries do not look at z
+  auto q_of = [&](float v) { return pow2(fmaf(v, inv_t, -lse) * kLog2e); };
+  auto gradient = [&](uint4 unit) {
+    float f[V];
+    unpack<T>(unit, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = q_of(f[j]) * scale;
+    return pack<T>(f);
+  };
   if (!any) {
-    for (unsigned k = threadIdx.x; k < units; k += blockDim.x) to[k] = make_uint4(0, 0, 0, 0);
+    ring.end();
+    for (unsigned k = threadIdx.x; k < units; k += n) to[k] = make_uint4(0, 0, 0, 0);
   } else if (alike) {
-    const uint4* body = reinterpret_cast<const uint4*>(z + head);
-    unsigned k = threadIdx.x;
-    for (; k + (kAtOnce - 1) * blockDim.x < units; k += kAtOnce * blockDim.x) {
-      uint4 q[kAtOnce];
+    for (unsigned b = 0; b < ring.n; ++b) {
+      uint4 q[kBatch];
+      ring.next(b, q);
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) q[i] = body[k + i * blockDim.x];
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        float f[V];
-        unpack<T>(q[i], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = q_of(f[j]) * scale;
-        to[k + i * blockDim.x] = pack<T>(f);
-      }
+      for (int i = 0; i < kBatch; ++i) to[threadIdx.x + (b * kBatch + i) * n] = gradient(q[i]);
     }
-    for (; k < units; k += blockDim.x) {
-      float f[V];
-      unpack<T>(body[k], f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = q_of(f[j]) * scale;
-      to[k] = pack<T>(f);
-    }
+    for (unsigned k = threadIdx.x + ring.n * kBatch * n; k < units; k += n) to[k] = gradient(body[k]);
   } else {
     for (unsigned k = threadIdx.x; k < units * V; k += blockDim.x) from_f(q_of(to_f(z[head + k])) * scale, out[head + k]);
   }
@@ -283,17 +383,17 @@ int threads_for(const DistillParams& p, int unit, int sms) {
   while (n < most && n * 4 < units) n *= 2;
   return (int)n;
 }
-size_t smem_for(const DistillParams& p) { return (size_t)3 * ((p.top + 3) & ~3u) * 4; }
+size_t smem_for(const DistillParams& p, int threads) { return (size_t)12 * ((p.top + 3) & ~3u) + (size_t)16 * kBatch * kBatches * threads; }
 
 }  // namespace
 
 cudaError_t launch_distill_forward(const DistillParams& p, int dtype, int sms, cudaStream_t st) {
-  if (dtype == XP_F32) return launch_dependent(forward_kernel<float>, dim3(p.rows), threads_for(p, 4, sms), smem_for(p), 1, st, p);
-  return launch_dependent(forward_kernel<bf16>, dim3(p.rows), threads_for(p, 8, sms), smem_for(p), 1, st, p);
+  const int threads = threads_for(p, dtype == XP_F32 ? 4 : 8, sms);
+  return launch_dependent(dtype == XP_F32 ? forward_kernel<float> : forward_kernel<bf16>, dim3(p.rows), threads, smem_for(p, threads), 1, st, p);
 }
 cudaError_t launch_distill_backward(const DistillParams& p, int dtype, int sms, cudaStream_t st) {
-  if (dtype == XP_F32) return launch_dependent(backward_kernel<float>, dim3(p.rows), threads_for(p, 4, sms), smem_for(p), 1, st, p);
-  return launch_dependent(backward_kernel<bf16>, dim3(p.rows), threads_for(p, 8, sms), smem_for(p), 1, st, p);
+  const int threads = threads_for(p, dtype == XP_F32 ? 4 : 8, sms);
+  return launch_dependent(dtype == XP_F32 ? backward_kernel<float> : backward_kernel<bf16>, dim3(p.rows), threads, smem_for(p, threads), 1, st, p);
 }
 
 }  // namespace xp

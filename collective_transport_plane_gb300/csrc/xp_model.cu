@@ -187,6 +187,7 @@ xp_status xp_block8_encode(const void* x, size_t x_stride, size_t rows, size_t c
   p.x_aligned = rows_aligned(x, x_stride, rows, es, 4 * es);
   p.codes_aligned = rows_aligned(codes, codes_stride, rows, 1, 4);
   p.codes_t_aligned = rows_aligned(codes_t, codes_t_stride, cols, 1, 4);
+  p.all_aligned = p.x_aligned && (!codes || p.codes_aligned) && (!codes_t || p.codes_t_aligned);
   XP_CUDA(xp::launch_encode8(p, dtype, block_rows, stream));
   return XP_OK;
 }
@@ -203,7 +204,7 @@ xp_status xp_block8_decode(const uint8_t* codes, size_t codes_stride, const uint
   const Span read[2] = {span8(codes, codes_stride, rows, cols), span_scales(scales, scales_stride, rows, cols, block_rows)};
   const Span written[1] = {span_of(out, out_stride, rows, cols, es)};
   if (any_overlap(written, 1, read, 2)) return fail(XP_ERR_INVALID, "codes, scales and out overlap");
-  if (ceil_div(cols, 16) * rows > (size_t)0x7fffffff * 256) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", rows, cols);
+  if (ceil_div(ceil_div(cols, 1024) * rows, 8) > 0x7fffffff) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", rows, cols);
   xp::Decode8Params p = {};
   p.codes = codes;
   p.scales = scales;
@@ -214,7 +215,7 @@ xp_status xp_block8_decode(const uint8_t* codes, size_t codes_stride, const uint
   p.rows = (unsigned)rows;
   p.cols = (unsigned)cols;
   p.shift = shift_of(block_rows);
-  p.aligned = rows_aligned(codes, codes_stride, rows, 1, 16) && rows_aligned(out, out_stride, rows, es, 16);
+  p.aligned = rows_aligned(codes, codes_stride, rows, 1, 8) && rows_aligned(out, out_stride, rows, es, 16);
   XP_CUDA(xp::launch_decode8(p, dtype, stream));
   return XP_OK;
 }

@@ -37,7 +37,7 @@ struct Encode8Params {
   uint8_t* scales_t;
   unsigned long long x_stride, codes_stride, scales_stride, codes_t_stride, scales_t_stride;
   unsigned rows, cols, tiles_c;
-  int x_aligned, codes_aligned, codes_t_aligned;   // four elements are one access
+  int x_aligned, codes_aligned, codes_t_aligned, all_aligned;   // four elements are one access
 };
 cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, cudaStream_t st);
 
@@ -47,7 +47,7 @@ struct Decode8Params {
   void* out;
   unsigned long long codes_stride, scales_stride, out_stride;
   unsigned rows, cols;
-  int shift, aligned;                    // 16 elements are whole accesses
+  int shift, aligned;                    // 16 bytes of output are one access, and so are their codes
 };
 cudaError_t launch_decode8(const Decode8Params& p, int dtype, cudaStream_t st);
 
@@ -82,12 +82,13 @@ struct RmsBackwardParams {
   unsigned long long dy_stride, h_stride, dadded_stride, dx_stride;
   unsigned long long rows;
   unsigned cols, threads, nparts;
+  int stages;                            // rows in flight per group, and one in work
   int gamma_bf16, accumulate;
 };
 // How a backward pass is cut: threads of a row with nu units each, rows of a
 // CTA at a time, and CTAs (slices of rows, where they are long).
 struct RmsBackwardShape {
-  unsigned nu, threads, groups, nparts;
+  unsigned nu, threads, groups, per_sm, nparts;
   bool is_long;
 };
 RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wide, int sms);

@@ -150,13 +150,13 @@ __device__ __forceinline__ void store8(const RmsForwardParams& p, u64 row, bool 
   const float inverse = inverse_of(e);
   if ((threadIdx.x & (kBlockLanes - 1)) == 0) p.y8_scales[row * p.y8_scales_stride + c / 128] = (uint8_t)e;
   uint8_t* out = p.y8 + row * p.y8_stride + c;
-  const unsigned lo = codes4(y[0], y[1], y[2], y[3], inverse, e);
+  const unsigned lo = codes4(y[0], y[1], y[2], y[3], inverse);
   if constexpr (!WIDE) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (c + 32 * i < p.cols) out[32 * i] = (uint8_t)(lo >> 8 * i);
   } else if constexpr (V == 8) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(lo, codes4(y[V - 4], y[V - 3], y[V - 2], y[V - 1], inverse, e));
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, codes4(y[V - 4], y[V - 3], y[V - 2], y[V - 1], inverse));
   } else {
     *reinterpret_cast<unsigned*>(out) = lo;
   }
@@ -219,64 +219,158 @@ __global__ void __launch_bounds__(LONG ? 1024 : 512) forward_kernel(const RmsFor
   }
 }
 
+// ---- backward: 16 bytes on their way into shared memory (`there` false: zeros)
+__device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_made() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n groups of this thread's copies have landed
+__device__ __forceinline__ void wait_copies(int n) {
+  if (n == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_landed(unsigned smem, float (&f)[V]) {
+  unsigned w[4];
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(smem) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(w[i]);
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
 // A group of threads keeps its columns through all its rows and adds their part
 // of dgamma up in registers; the CTA's groups leave one row of partial sums.
-template <typename T, bool WIDE, int NU>
-__global__ void __launch_bounds__(512) backward_kernel(const RmsBackwardParams p) {
+// WIDE: the rows of the next turns are on their way into shared memory, each
+// thread's units into places of its own, while this turn's are in work
+// (16384 x 5120 bf16 with dadded: 240 us without, 107 with it, 0.93 of the copy
+// rate).  Registers are bounded so that two CTAs or more are there to fill each
+// other's waits for their rows' sums (one of 121 registers: 133 us).  Narrow rows
+// come by plain loads, many CTAs at a time: with four-byte copies ahead
+// 4099 x 1031 fp32 took 21 us, without 14.
+template <typename T, bool WIDE, int NU, bool LARGE>
+__global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE> == 16 ? 1 : 2) backward_kernel(const RmsBackwardParams p) {
   constexpr int V = kUnit<T, WIDE>;
-  __shared__ float words[2][32];
-  extern __shared__ float parts[];
+  __shared__ float words[2][16];
+  extern __shared__ __align__(16) uint8_t raw[];
   wait_for_predecessors();
   let_successor_start();
   const unsigned threads = p.threads, groups = blockDim.x / threads, group = threadIdx.x / threads, tid = threadIdx.x - group * threads;
-  float acc[NU][V], g[NU][V];
+  const unsigned ring = (unsigned)__cvta_generic_to_shared(raw) + threadIdx.x * 16, unit_bytes = blockDim.x * 16, stage_bytes = 3 * NU * unit_bytes;
+  const u64 step = (u64)gridDim.x * groups;
+  u64 row = (u64)blockIdx.x * groups + group;
+  auto bring = [&](u64 r, unsigned at) {   // row r's units into the stage at `at`
+    if constexpr (WIDE) {
+      const bool there = r < p.rows;
 #pragma unroll
-  for (int k = 0; k < NU; ++k) {
-    load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g[k]);
+      for (int k = 0; k < NU; ++k) {
+        const unsigned c = column<T, WIDE>(tid, threads, k);
+        const bool mine = there && c < p.cols;
+        copy_async16(at + k * unit_bytes, static_cast<const T*>(p.dy) + (mine ? r * p.dy_stride + c : 0), mine);
+        copy_async16(at + (NU + k) * unit_bytes, static_cast<const T*>(p.h) + (mine ? r * p.h_stride + c : 0), mine);
+        if (p.dadded) copy_async16(at + (2 * NU + k) * unit_bytes, static_cast<const T*>(p.dadded) + (mine ? r * p.dadded_stride + c : 0), mine);
+      }
+      copies_made();
+    }
+  };
+  float acc[NU][V];
+#pragma unroll
+  for (int k = 0; k < NU; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+  float gamma[NU][V];
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int k = 0; k < NU; ++k) load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, gamma[k]);
   }
+  for (int s = 0; s + 1 < p.stages; ++s) bring(row + s * step, ring + s * stage_bytes);
   const float inv_cols = 1.f / (float)p.cols;
-  int buf = 0;
-  for (u64 first = (u64)blockIdx.x * groups; first < p.rows; first += (u64)gridDim.x * groups, buf ^= 1) {
-    const u64 row = first + group;
+  float rstd = row < p.rows ? p.rstd[row] : 0.f;
+  int buf = 0, stage = 0;
+  for (u64 first = (u64)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 1) {
     const bool there = row < p.rows;
     const unsigned cols = there ? p.cols : 0;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
-    const T* x = static_cast<const T*>(p.h) + row * p.h_stride;
-    const float rstd = there ? p.rstd[row] : 0.f;
-    float d[NU][V], h[NU][V], e[NU][V], sum = 0.f;
+    const float next_rstd = row + step < p.rows ? p.rstd[row + step] : 0.f;
+    float sum = 0.f;
+    const unsigned at = ring + stage * stage_bytes;
+    float d[WIDE ? 1 : NU][V], h[WIDE ? 1 : NU][V];   // (WIDE rows are read from shared memory once more instead)
+    if constexpr (WIDE) {
+      const int ahead = p.stages - 1, into = stage == 0 ? ahead : stage - 1;
+      bring(row + ahead * step, ring + into * stage_bytes);
+      wait_copies(ahead);
+      stage = stage == ahead ? 0 : stage + 1;
+    } else {
 #pragma unroll
-    for (int k = 0; k < NU; ++k) {
-      const unsigned c = column<T, WIDE>(tid, threads, k);
-      load<T, WIDE>(dy, c, cols, d[k]);
-      load<T, WIDE>(x, c, cols, h[k]);
-      if (p.dadded) load<T, WIDE>(static_cast<const T*>(p.dadded) + row * p.dadded_stride, c, cols, e[k]);
+      for (int k = 0; k < NU; ++k) {
+        const unsigned c = column<T, WIDE>(tid, threads, k);
+        load<T, WIDE>(static_cast<const T*>(p.dy) + row * p.dy_stride, c, cols, d[k]);
+        load<T, WIDE>(static_cast<const T*>(p.h) + row * p.h_stride, c, cols, h[k]);
+      }
     }
 #pragma unroll
-    for (int k = 0; k < NU; ++k)
+    for (int k = 0; k < NU; ++k) {
+      constexpr int kEach = WIDE ? 0 : 1;
+      float(&x)[V] = h[k * kEach], (&y)[V] = d[k * kEach], g[V];
+      if constexpr (WIDE) {
+        load_landed<T>(at + k * unit_bytes, y);
+        load_landed<T>(at + (NU + k) * unit_bytes, x);
+      }
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = gamma[k][i];
+      } else {
+        load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        h[k][i] *= rstd;
-        acc[k][i] = fmaf(d[k][i], h[k][i], acc[k][i]);
-        d[k][i] *= g[k][i];
-        sum = fmaf(d[k][i], h[k][i], sum);
+        x[i] *= rstd;
+        acc[k][i] = fmaf(y[i], x[i], acc[k][i]);
+        y[i] *= g[i];
+        sum = fmaf(y[i], x[i], sum);
       }
+    }
     sum = row_sum(sum, words[buf], threads) * inv_cols;
     T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      constexpr int kEach = WIDE ? 0 : 1;
+      const unsigned c = column<T, WIDE>(tid, threads, k);
+      float(&x)[V] = h[k * kEach], (&y)[V] = d[k * kEach], e[V];
+      if constexpr (WIDE) {
+        load_landed<T>(at + k * unit_bytes, y);
+        load_landed<T>(at + (NU + k) * unit_bytes, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] *= rstd, y[i] *= gamma[k][i];
+      }
+      if (p.dadded) {
+        if constexpr (WIDE)
+          load_landed<T>(at + (2 * NU + k) * unit_bytes, e);
+        else
+          load<T, WIDE>(static_cast<const T*>(p.dadded) + row * p.dadded_stride, c, cols, e);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        d[k][i] = fmaf(-h[k][i], sum, d[k][i]) * rstd;
-        if (p.dadded) d[k][i] += e[k][i];
+        y[i] = fmaf(-x[i], sum, y[i]) * rstd;
+        if (p.dadded) y[i] += e[i];
       }
-      store<T, WIDE>(dx, column<T, WIDE>(tid, threads, k), cols, d[k]);
+      store<T, WIDE>(dx, c, cols, y);
     }
+    rstd = next_rstd;
   }
+  if (WIDE) wait_copies(0);
   if (!p.partial) return;
   float* mine = p.partial + (u64)blockIdx.x * p.cols;
   if (groups > 1) {
+    float* parts = reinterpret_cast<float*>(raw);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < NU; ++k)
@@ -357,21 +451,24 @@ __global__ void __launch_bounds__(256) long_rows_kernel(const RmsBackwardParams 
     if (c + kApart<WIDE> * i < p.cols) mine[c + kApart<WIDE> * i] = acc[i];
 }
 
-// dgamma from the partial sums: 32 columns per CTA, a warp takes every 32nd row of them.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const RmsBackwardParams p) {
-  __shared__ float words[32][33];
+// dgamma from the partial sums: 16 columns (two sectors of a row of them) per
+// CTA, every 32nd row by the same 16 threads.
+constexpr int kSumCols = 16, kSumRows = 32;
+__global__ void __launch_bounds__(kSumCols * kSumRows) sum_parts_kernel(const RmsBackwardParams p) {
+  __shared__ float words[kSumRows][kSumCols + 1];
   wait_for_predecessors();
   let_successor_start();
-  const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+  const unsigned at = threadIdx.x / kSumCols, i = threadIdx.x % kSumCols, c = blockIdx.x * kSumCols + i;
   float v = 0.f;
   if (c < p.cols) {
-#pragma unroll 4
-    for (unsigned j = warp; j < p.nparts; j += 32) v += p.partial[(u64)j * p.cols + c];
+#pragma unroll 8
+    for (unsigned j = at; j < p.nparts; j += kSumRows) v += p.partial[(u64)j * p.cols + c];
   }
-  words[warp][lane] = v;
+  words[at][i] = v;
   __syncthreads();
-  v = warp_sum(words[lane][warp]);
-  const unsigned out = blockIdx.x * 32 + warp;
+  const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = warp_sum(words[lane][warp]);   // 16 warps, 32 rows
+  const unsigned out = blockIdx.x * kSumCols + warp;
   if (lane == 0 && out < p.cols) p.dgamma[out] = p.accumulate ? p.dgamma[out] + v : v;
 }
 
@@ -399,9 +496,13 @@ cudaError_t forward(RmsForwardParams& p, cudaStream_t st) {
 
 template <typename T, bool WIDE, int NU>
 cudaError_t backward_rows(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream_t st) {
-  const unsigned groups = s.groups;
-  const size_t smem = groups > 1 ? (size_t)groups * s.threads * NU * kUnit<T, WIDE> * sizeof(float) : 0;
-  return launch_dependent(backward_kernel<T, WIDE, NU>, dim3(s.nparts), (int)(groups * s.threads), smem, 1, st, p);
+  const unsigned block = s.groups * s.threads, stage = 3 * NU * 16 * block;
+  // as many rows ahead as the SM's CTAs have room for, three at most
+  p.stages = WIDE ? std::min(4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage)))) : 1;
+  size_t smem = WIDE ? (size_t)p.stages * stage : 0;
+  if (s.groups > 1) smem = std::max<size_t>(smem, (size_t)block * NU * kUnit<T, WIDE> * sizeof(float));
+  const auto kernel = block > 384 ? backward_kernel<T, WIDE, NU, true> : backward_kernel<T, WIDE, NU, !WIDE>;
+  return launch_dependent(kernel, dim3(s.nparts), (int)block, smem, 1, st, p);
 }
 
 template <typename T, bool WIDE>
@@ -419,7 +520,7 @@ cudaError_t backward(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream
     e = s.nu == 1 ? backward_rows<T, WIDE, 1>(p, s, st) : s.nu == 2 ? backward_rows<T, WIDE, 2>(p, s, st) : backward_rows<T, WIDE, kMost>(p, s, st);
   }
   if (e != cudaSuccess || !p.dgamma) return e;
-  return launch_dependent(sum_parts_kernel, dim3((p.cols + 31) / 32), 1024, 0, 1, st, p);
+  return launch_dependent(sum_parts_kernel, dim3((p.cols + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, 1, st, p);
 }
 
 }  // namespace
@@ -437,8 +538,12 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
     return s;
   }
   s.groups = s.threads >= 256 ? 1 : 256 / s.threads;
-  const unsigned per_sm = std::max(1u, 1024 / (s.groups * s.threads));
-  s.nparts = (unsigned)std::min<size_t>((rows + s.groups - 1) / s.groups, (size_t)sms * per_sm);
+  const unsigned block = s.groups * s.threads;
+  // by their registers: 80 a thread in CTAs of up to 384 threads, 128 in larger ones that keep 16 columns' sums, else 64
+  s.per_sm = 65536 / (block * (block <= 384 && wide ? 80 : s.nu * v == 16 ? 128 : 64));
+  if (wide) s.per_sm = std::min(s.per_sm, 216 * 1024 / (2 * 3 * s.nu * 16 * block));   // two rows each in shared memory
+  s.per_sm = std::max(1u, s.per_sm);
+  s.nparts = (unsigned)std::min<size_t>((rows + s.groups - 1) / s.groups, (size_t)sms * s.per_sm);
   return s;
 }
 

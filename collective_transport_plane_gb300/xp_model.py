@@ -41,6 +41,10 @@ for _name, _args in {
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = ctypes.c_int
 
+_encode, _decode, _matmul, _forward, _backward, _distill, _distill_back = (
+    _lib.xp_block8_encode, _lib.xp_block8_decode, _lib.xp_matmul8, _lib.xp_rmsnorm_forward, _lib.xp_rmsnorm_backward, _lib.xp_distill_forward,
+    _lib.xp_distill_backward)
+
 _FLOATS = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16}
 _BYTES = ("torch.uint8", "torch.float8_e4m3fn", "torch.float8_e8m0fnu")
 _types = {}   # torch dtype -> xp_dtype (XP_U8: codes and scales), filled as types are met
@@ -56,51 +60,68 @@ def _dtype(t) -> int:
     return found
 
 
-def _current_device() -> int:
+def _device_of(t) -> int:
+    """The current device, as torch says; 0 where the tensors are not torch's."""
+    global _device_of
     torch = sys.modules.get("torch")
-    return torch.cuda.current_device() if torch is not None else 0
+    if torch is None:
+        return 0
+    if not hasattr(torch._C, "_cuda_getDevice"):
+        return torch.cuda.current_device()
+    _device_of = lambda _: torch._C._cuda_getDevice()  # noqa: E731
+    return _device_of(t)
 
 
-def _on_device(*tensors):
-    """Refuses tensors that are not on the current device."""
-    at = {t.get_device() for t in tensors if t is not None}
-    if len(at) > 1 or at and (min(at) < 0 or at != {_current_device()}):
-        raise ValueError(f"tensors on devices {sorted(at)}, not all on the current one (-1: the host)")
+def _refuse_devices(tensors, current):
+    at = sorted({t.get_device() for t in tensors if t is not None})
+    raise ValueError(f"tensors on devices {at}, not all on the current one, {current} (-1: the host)")
 
 
-def _matrix(t, rows, cols, what, dtype):
-    """(address, stride) of a rows x cols matrix whose columns are side by side (None: none)."""
-    if t is None:
-        return None, 0
-    if t.shape != (rows, cols) or (_types.get(t.dtype) or _dtype(t)) != dtype:
-        raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not ({rows}, {cols}) of its type")
+def _refuse_matrix(t, shape, what, dtype):
+    if t.shape != shape or _dtype(t) != dtype:
+        raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of its type")
+    raise ValueError(f"{what}'s columns are {t.stride()[1]} elements apart")
+
+
+def _matrix(t, shape, what, dtype, device):
+    """(address, stride) of a matrix of a shape and type whose columns are side by side."""
     stride, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{what}'s columns are {step} elements apart")
+    if t.shape != shape or (step != 1 and shape[1] > 1) or (_types.get(t.dtype) or _dtype(t)) != dtype:
+        _refuse_matrix(t, shape, what, dtype)
+    if t.get_device() != device:
+        _refuse_devices((t,), device)
     return t.data_ptr(), stride
 
 
-def _vector(t, n, what, dtype):
+def _vector(t, n, what, dtype, device):
     """The address of n contiguous elements (None: none)."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_contiguous() or _dtype(t) != dtype:
+    if t.numel() != n or not t.is_contiguous() or (_types.get(t.dtype) or _dtype(t)) != dtype:
         raise ValueError(f"{what} is not {n} contiguous elements of its type")
+    if t.get_device() != device:
+        _refuse_devices((t,), device)
     return t.data_ptr()
 
 
-def _block8(codes, scales, rows, cols, block_rows, what):
+def _block8(codes, scales, shape, block_rows, what, device):
     """(codes, stride, scales, stride) of a matrix in 8 bits; both or neither."""
-    if (codes is None) != (scales is None):
-        raise ValueError(f"{what} without its scales, or scales without codes")
-    if block_rows not in (1, XP_BLOCK8):
-        raise ValueError(f"{what}: blocks of {block_rows} rows, neither 1 nor 128")
-    return (*_matrix(codes, rows, cols, what, XP_U8),
-            *_matrix(scales, -(-rows // block_rows), -(-cols // XP_BLOCK8), f"{what}'s scales", XP_U8))
+    if codes is None or scales is None:
+        if codes is not scales:
+            raise ValueError(f"{what} without its scales, or scales without codes")
+        return None, 0, None, 0
+    rows, cols = shape
+    if block_rows != 1:
+        if block_rows != XP_BLOCK8:
+            raise ValueError(f"{what}: blocks of {block_rows} rows, neither 1 nor 128")
+        rows = (rows + 127) // 128
+    p, s = _matrix(codes, shape, what, XP_U8, device)
+    ps, ss = _matrix(scales, (rows, (cols + 127) // 128), "scales", XP_U8, device)
+    return p, s, ps, ss
 
 
 def _float(t, what):
-    dt = _dtype(t)
+    dt = _types.get(t.dtype) or _dtype(t)
     if dt == XP_U8:
         raise ValueError(f"{what} is {t.dtype}")
     return dt
@@ -113,30 +134,38 @@ def _check(st: int, where: str):
 
 def xp_block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, block_rows: int = 1, stream=None) -> None:
     """x (rows x cols) in 8 bits into codes and scales, and its transpose into codes_t and scales_t; either pair may be None."""
-    rows, cols = x.shape
-    dt = _float(x, "x")
-    _on_device(x, codes, scales, codes_t, scales_t)
-    _check(_lib.xp_block8_encode(*_matrix(x, rows, cols, "x", dt), rows, cols, dt, block_rows, *_block8(codes, scales, rows, cols, block_rows, "codes"),
-                                 *_block8(codes_t, scales_t, cols, rows, block_rows, "codes_t"), _stream(stream)), "xp_block8_encode")
+    shape, dt, dev = x.shape, _float(x, "x"), _device_of(x)
+    rows, cols = shape
+    px, sx = _matrix(x, shape, "x", dt, dev)
+    pc, sc, ps, ss = _block8(codes, scales, shape, block_rows, "codes", dev)
+    pct, sct, pst, sst = _block8(codes_t, scales_t, (cols, rows), block_rows, "codes_t", dev)
+    st = _encode(px, sx, rows, cols, dt, block_rows, pc, sc, ps, ss, pct, sct, pst, sst, stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_block8_encode")
 
 
 def xp_block8_decode(codes, scales, out, block_rows: int = 1, stream=None) -> None:
     """The values that a matrix in 8 bits stands for, into out."""
-    rows, cols = out.shape
-    dt = _float(out, "out")
-    _on_device(codes, scales, out)
-    _check(_lib.xp_block8_decode(*_block8(codes, scales, rows, cols, block_rows, "codes"), rows, cols, block_rows, *_matrix(out, rows, cols, "out", dt), dt,
-                                 _stream(stream)), "xp_block8_decode")
+    shape, dt, dev = out.shape, _float(out, "out"), _device_of(out)
+    rows, cols = shape
+    po, so = _matrix(out, shape, "out", dt, dev)
+    pc, sc, ps, ss = _block8(codes, scales, shape, block_rows, "codes", dev)
+    st = _decode(pc, sc, ps, ss, rows, cols, block_rows, po, so, dt, stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_block8_decode")
 
 
 def xp_matmul8(a, a_scales, b, b_scales, c, a_block_rows: int = 1, b_block_rows: int = 1, accumulate: bool = False, stream=None) -> None:
     """c = a b^T (accumulate: c + a b^T) of a (m x k) and b (n x k) in 8 bits."""
-    (m, k), n, dt = a.shape, b.shape[0], _float(c, "c")
-    _on_device(a, a_scales, b, b_scales, c)
-    pa, sa, psa, ssa = _block8(a, a_scales, m, k, a_block_rows, "a")
-    pb, sb, psb, ssb = _block8(b, b_scales, n, k, b_block_rows, "b")
-    _check(_lib.xp_matmul8(pa, sa, psa, ssa, a_block_rows, pb, sb, psb, ssb, b_block_rows, *_matrix(c, m, n, "c", dt), m, n, k, dt,
-                           1 if accumulate else 0, _stream(stream)), "xp_matmul8")
+    shape, dt, dev = a.shape, _float(c, "c"), _device_of(c)
+    (m, k), n = shape, b.shape[0]
+    pa, sa, psa, ssa = _block8(a, a_scales, shape, a_block_rows, "a", dev)
+    pb, sb, psb, ssb = _block8(b, b_scales, (n, k), b_block_rows, "b", dev)
+    pc, sc = _matrix(c, (m, n), "c", dt, dev)
+    st = _matmul(pa, sa, psa, ssa, a_block_rows, pb, sb, psb, ssb, b_block_rows, pc, sc, m, n, k, dt, 1 if accumulate else 0,
+                 stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_matmul8")
 
 
 def xp_matmul8_status() -> int:
@@ -149,14 +178,18 @@ def xp_matmul8_status() -> int:
 
 def xp_rmsnorm_forward(x, gamma, y=None, residual=None, added=None, rstd=None, y8=None, y8_scales=None, eps: float = 1e-5, stream=None) -> None:
     """The root-mean-square norm of x, or of x + residual (stored in added), into y, and in 8 bits into y8."""
-    rows, cols = x.shape
-    dt = _float(x, "x")
+    shape, dt, dev = x.shape, _float(x, "x"), _device_of(x)
+    rows, cols = shape
     wdt = dt if gamma is None else _float(gamma, "gamma")
-    _on_device(x, gamma, y, residual, added, rstd, y8, y8_scales)
-    _check(_lib.xp_rmsnorm_forward(*_matrix(x, rows, cols, "x", dt), *_matrix(residual, rows, cols, "residual", dt), _vector(gamma, cols, "gamma", wdt),
-                                   *_matrix(added, rows, cols, "added", dt), *_matrix(y, rows, cols, "y", dt),
-                                   *_block8(y8, y8_scales, rows, cols, 1, "y8"), _vector(rstd, rows, "rstd", XP_F32), rows, cols, eps, dt, wdt,
-                                   _stream(stream)), "xp_rmsnorm_forward")
+    px, sx = _matrix(x, shape, "x", dt, dev)
+    pr, sr = (None, 0) if residual is None else _matrix(residual, shape, "residual", dt, dev)
+    pa, sa = (None, 0) if added is None else _matrix(added, shape, "added", dt, dev)
+    py, sy = (None, 0) if y is None else _matrix(y, shape, "y", dt, dev)
+    p8, s8, p8s, s8s = _block8(y8, y8_scales, shape, 1, "y8", dev)
+    st = _forward(px, sx, pr, sr, _vector(gamma, cols, "gamma", wdt, dev), pa, sa, py, sy, p8, s8, p8s, s8s,
+                  _vector(rstd, rows, "rstd", XP_F32, dev), rows, cols, eps, dt, wdt, stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_rmsnorm_forward")
 
 
 def xp_rmsnorm_workspace(rows: int, cols: int) -> int:
@@ -167,45 +200,59 @@ def xp_rmsnorm_workspace(rows: int, cols: int) -> int:
 
 def xp_rmsnorm_backward(dy, h, gamma, rstd, dx, dgamma=None, workspace=None, dadded=None, accumulate: bool = False, stream=None) -> None:
     """dx (+ dadded), and over the rows dgamma, from dy, the norm's input h and the forward pass's rstd."""
-    rows, cols = h.shape
-    dt = _float(h, "h")
+    shape, dt, dev = h.shape, _float(h, "h"), _device_of(h)
+    rows, cols = shape
     wdt = dt if gamma is None else _float(gamma, "gamma")
-    _on_device(dy, h, gamma, rstd, dx, dgamma, workspace, dadded)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace is not contiguous")
-    work, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    _check(_lib.xp_rmsnorm_backward(*_matrix(dy, rows, cols, "dy", dt), *_matrix(h, rows, cols, "h", dt), _vector(gamma, cols, "gamma", wdt),
-                                    _vector(rstd, rows, "rstd", XP_F32), *_matrix(dadded, rows, cols, "dadded", dt),
-                                    *_matrix(dx, rows, cols, "dx", dt), _vector(dgamma, cols, "dgamma", XP_F32), rows, cols, dt, wdt,
-                                    1 if accumulate else 0, work, nbytes, _stream(stream)), "xp_rmsnorm_backward")
+    work, nbytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace is not contiguous")
+        if workspace.get_device() != dev:
+            _refuse_devices((workspace,), dev)
+        work, nbytes = workspace.data_ptr(), workspace.nbytes
+    pdy, sdy = _matrix(dy, shape, "dy", dt, dev)
+    ph, sh = _matrix(h, shape, "h", dt, dev)
+    pa, sa = (None, 0) if dadded is None else _matrix(dadded, shape, "dadded", dt, dev)
+    pdx, sdx = _matrix(dx, shape, "dx", dt, dev)
+    st = _backward(pdy, sdy, ph, sh, _vector(gamma, cols, "gamma", wdt, dev), _vector(rstd, rows, "rstd", XP_F32, dev), pa, sa, pdx, sdx,
+                   _vector(dgamma, cols, "dgamma", XP_F32, dev), rows, cols, dt, wdt, 1 if accumulate else 0, work, nbytes,
+                   stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_rmsnorm_backward")
 
 
-def _top(ids, teacher, rows):
+def _top(ids, teacher, rows, dev):
     """(ids, teacher, entries per row), both rows x top side by side."""
-    top = ids.shape[1]
-    if ids.shape != (rows, top) or str(ids.dtype) != "torch.int32" or not ids.is_contiguous():
-        raise ValueError(f"ids is {tuple(ids.shape)} of {ids.dtype}, not {rows} contiguous rows of torch.int32")
-    if teacher.shape != (rows, top):
-        raise ValueError(f"teacher is {tuple(teacher.shape)}, not {(rows, top)}")
-    return ids.data_ptr(), _vector(teacher, rows * top, "teacher", XP_F32), top
+    shape = ids.shape
+    if shape[0] != rows or str(ids.dtype) != "torch.int32" or not ids.is_contiguous():
+        raise ValueError(f"ids is {tuple(shape)} of {ids.dtype}, not {rows} contiguous rows of torch.int32")
+    if teacher.shape != shape:
+        raise ValueError(f"teacher is {tuple(teacher.shape)}, not {tuple(shape)}")
+    if ids.get_device() != dev:
+        _refuse_devices((ids,), dev)
+    return ids.data_ptr(), _vector(teacher, rows * shape[1], "teacher", XP_F32, dev), shape[1]
 
 
 def xp_distill_forward(logits, ids, teacher, loss, lse=None, temperature: float = 1.0, stream=None) -> None:
     """Each row's loss against the teacher's logits (rows x top, fp32) at ids (int32), and the row's log-sum-exp."""
-    rows, vocab = logits.shape
-    dt = _float(logits, "logits")
-    _on_device(logits, ids, teacher, loss, lse)
-    pi, pt, top = _top(ids, teacher, rows)
-    _check(_lib.xp_distill_forward(*_matrix(logits, rows, vocab, "logits", dt), pi, pt, rows, vocab, top, temperature,
-                                   _vector(loss, rows, "loss", XP_F32), _vector(lse, rows, "lse", XP_F32), dt, _stream(stream)), "xp_distill_forward")
+    shape, dt, dev = logits.shape, _float(logits, "logits"), _device_of(logits)
+    rows, vocab = shape
+    pi, pt, top = _top(ids, teacher, rows, dev)
+    pz, sz = _matrix(logits, shape, "logits", dt, dev)
+    st = _distill(pz, sz, pi, pt, rows, vocab, top, temperature, _vector(loss, rows, "loss", XP_F32, dev), _vector(lse, rows, "lse", XP_F32, dev), dt,
+                  stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_distill_forward")
 
 
 def xp_distill_backward(logits, ids, teacher, lse, dloss, dlogits, temperature: float = 1.0, stream=None) -> None:
     """dlogits from dloss (one per row) and the forward pass's lse; dlogits may be logits."""
-    rows, vocab = logits.shape
-    dt = _float(logits, "logits")
-    _on_device(logits, ids, teacher, lse, dloss, dlogits)
-    pi, pt, top = _top(ids, teacher, rows)
-    _check(_lib.xp_distill_backward(*_matrix(logits, rows, vocab, "logits", dt), pi, pt, _vector(lse, rows, "lse", XP_F32),
-                                    _vector(dloss, rows, "dloss", XP_F32), rows, vocab, top, temperature,
-                                    *_matrix(dlogits, rows, vocab, "dlogits", dt), dt, _stream(stream)), "xp_distill_backward")
+    shape, dt, dev = logits.shape, _float(logits, "logits"), _device_of(logits)
+    rows, vocab = shape
+    pi, pt, top = _top(ids, teacher, rows, dev)
+    pz, sz = _matrix(logits, shape, "logits", dt, dev)
+    pd, sd = _matrix(dlogits, shape, "dlogits", dt, dev)
+    st = _distill_back(pz, sz, pi, pt, _vector(lse, rows, "lse", XP_F32, dev), _vector(dloss, rows, "dloss", XP_F32, dev), rows, vocab, top,
+                       temperature, pd, sd, dt, stream if stream is None else _stream(stream))
+    if st:
+        xp._check(st, "xp_distill_backward")

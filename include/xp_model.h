@@ -135,10 +135,11 @@ xp_status xp_rmsnorm_backward(const void* dy, size_t dy_stride, const void* h, s
  * An entry whose id is not in [0, vocab) (-1, say) names no token and counts
  * for nothing; so does one whose t is -infinity.  An id may come more than
  * once: its entries each add to it.  A row without entries has loss 0 and lse
- * 0, and its logits are not read.  z is `dtype` (XP_F32 or XP_BF16), ids int32,
+ * 0, whatever its logits.  z is `dtype` (XP_F32 or XP_BF16), ids int32,
  * t fp32, rows x top each, side by side; loss and lse fp32, lse may be NULL
  * where no backward pass follows.  (One entry is the cross entropy of a
- * label.)  Sums are fp32. */
+ * label.)  Sums are fp32; logits over T that count have to be below 3e38 (masks of
+ * the type's lowest value need not be). */
 xp_status xp_distill_forward(const void* logits, size_t logits_stride, const int32_t* ids, const float* teacher,
                              size_t rows, size_t vocab, size_t top, float temperature, float* loss, float* lse,
                              xp_dtype dtype, xp_stream_t stream);

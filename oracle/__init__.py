@@ -28,7 +28,7 @@ arithmetic rounded to fp32, against int64 sums for int32, against the
 fp64 sum within the standard error bound, and the pages' printed sizes and
 ring-neighbour example (tests/golden/).
 """
-from . import train
+from . import model, train
 from .fifo import (CEFifo, CEProxy, CEReceiver, CESender, Deadlock, LL128Fifo, LL128LaneFifo, LL128LaneReceiver,
                    LL128LaneSender, LL128Receiver, LL128Sender, LLFifo, LLReceiver, LLSender, PostedChannel, PostedReceiver, PostedSender,
                    ProtocolViolation, SimpleFifo, SimpleReceiver, SimpleSender, System, ZeroCopyChannel,
@@ -48,5 +48,5 @@ __all__ = [
     "PostedChannel", "PostedSender", "PostedReceiver", "posted_transfer",
     "CEFifo", "CESender", "CEProxy", "CEReceiver", "ce_transfer",
     "LL128Fifo", "LL128Sender", "LL128Receiver", "ll128_flag", "ll128_transfer",
-    "LL128LaneFifo", "LL128LaneSender", "LL128LaneReceiver", "train",
+    "LL128LaneFifo", "LL128LaneSender", "LL128LaneReceiver", "train", "model",
 ]
