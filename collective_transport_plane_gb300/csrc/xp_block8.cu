@@ -53,13 +53,17 @@ struct Four<bf16> {
     f[0] = __uint_as_float(q.x << 16), f[1] = __uint_as_float(q.x & 0xffff0000u);
     f[2] = __uint_as_float(q.y << 16), f[3] = __uint_as_float(q.y & 0xffff0000u);
   }
-  struct Tops {   // two columns' bits in a word: magnitudes order like 16-bit numbers
+  struct Tops {   // two columns' in a word; NaN above all
     unsigned t[2] = {0, 0};
   };
-  __device__ __forceinline__ void raise(Tops& m) const { m.t[0] = __vmaxu2(m.t[0], q.x & 0x7fff7fffu), m.t[1] = __vmaxu2(m.t[1], q.y & 0x7fff7fffu); }
+  static __device__ __forceinline__ unsigned larger(unsigned m, unsigned w) {
+    const __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    return *reinterpret_cast<const unsigned*>(&a);
+  }
+  __device__ __forceinline__ void raise(Tops& m) const { m.t[0] = larger(m.t[0], q.x), m.t[1] = larger(m.t[1], q.y); }
   static __device__ __forceinline__ uint4 tops(const Tops& m) { return make_uint4(m.t[0] << 16, m.t[0] & 0xffff0000u, m.t[1] << 16, m.t[1] & 0xffff0000u); }
   __device__ __forceinline__ unsigned top() const {
-    const unsigned m = __vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu);
+    const unsigned m = larger(q.x & 0x7fff7fffu, q.y);
     return max(m << 16, m & 0xffff0000u);
   }
 };
@@ -92,10 +96,29 @@ __device__ __forceinline__ void store4(uint8_t* p, unsigned codes, int n, bool a
 // transposed tile, whose word (column, rows / 4) is kept at the place that
 // column / 4 turns: a warp's words lie in 32 banks when it writes those of a
 // row and when it reads those of a column.
-// WHOLE: all of the tile is there, and its rows and columns are aligned.
-template <typename T, bool TILE, bool WHOLE>
-__device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&words)[128 * 32], unsigned (&tops)[kWarps][128], unsigned tile_r,
-                                            unsigned tile_c) {
+// A thread's 4 elements of each of its rows on their way into shared memory, into places of its own.
+template <typename T>
+__device__ __forceinline__ unsigned place_of(const uint8_t* ahead, int t, int i) {
+  return (unsigned)__cvta_generic_to_shared(ahead) + (unsigned)((t * 4 + i) * kThreads + threadIdx.x) * 4 * (unsigned)sizeof(T);
+}
+template <typename T>
+__device__ __forceinline__ void bring_tile(const Encode8Params& p, const uint8_t* ahead, unsigned tile_r, unsigned tile_c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = static_cast<const T*>(p.x) + (u64)(tile_r * 128 + 4 * warp) * p.x_stride + tile_c * 128 + 4 * lane;
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t, x += 4 * kWarps * p.x_stride) {
+    const T* at = x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, at += p.x_stride)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(place_of<T>(ahead, t, i)), "l"(at), "n"(4 * (int)sizeof(T)) : "memory");
+  }
+}
+
+// WHOLE: all of the tile is there, and its rows and columns are aligned; its
+// elements came ahead.  taken: called when they are in registers.
+template <typename T, bool TILE, bool WHOLE, typename Taken>
+__device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&words)[128 * 32], unsigned (&tops)[kWarps][128], const uint8_t* ahead,
+                                            unsigned tile_r, unsigned tile_c, Taken taken) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned r0 = tile_r * 128, c0 = tile_c * 128 + 4 * lane;
   const int n = WHOLE ? 4 : (int)min(4u, p.cols > c0 ? p.cols - c0 : 0u);
@@ -109,11 +132,13 @@ __device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&w
 #pragma unroll
     for (int i = 0; i < 4; ++i, at += p.x_stride) {
       if (WHOLE)
-        four[t][i].load(at);
+        four[t][i].load(reinterpret_cast<const T*>(ahead) + 4 * ((t * 4 + i) * kThreads + threadIdx.x));
       else
         four[t][i] = load4(at, r0 + mine + next * t + i < p.rows ? n : 0, p.x_aligned);
     }
   }
+
+  taken();
 
   unsigned tile_e = 0;
   if (TILE || p.codes_t) {
@@ -177,7 +202,7 @@ __device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&w
       }
     }
   }
-  if (!p.codes_t) return;
+  if (!p.codes_t) return;   // the same for the CTA
 
   float inverse[4];
 #pragma unroll
@@ -205,19 +230,38 @@ __device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&w
   }
 }
 
-// (16384 x 4096 bf16, both forms: 80 us with addresses and edges worked out for
-// every row, at 0.7 instructions per clock and scheduler, 30 for each element.)
+// CTAs take tiles one after another, the next one's elements on their way
+// meanwhile.  (16384 x 4096 bf16, both forms: 80 us with addresses and edges
+// worked out for every row, at 30 instructions for each element; 58 without,
+// a tile per CTA and nothing on its way while codes are made.)
 template <typename T, bool TILE>
 __global__ void __launch_bounds__(kThreads, 2) encode_kernel(const Encode8Params p) {
-  __shared__ unsigned words[128 * 32];
-  __shared__ __align__(16) unsigned tops[kWarps][128];
+  extern __shared__ __align__(16) uint8_t raw[];
+  auto& words = *reinterpret_cast<unsigned(*)[128 * 32]>(raw);
+  auto& tops = *reinterpret_cast<unsigned(*)[kWarps][128]>(raw + sizeof words);
+  const uint8_t* ahead = raw + sizeof words + sizeof tops;
   wait_for_predecessors();
   let_successor_start();
-  const unsigned tile_r = blockIdx.x / p.tiles_c, tile_c = blockIdx.x - tile_r * p.tiles_c;
-  if (p.all_aligned && (tile_r + 1) * 128 <= p.rows && (tile_c + 1) * 128 <= p.cols)
-    encode_tile<T, TILE, true>(p, words, tops, tile_r, tile_c);
-  else
-    encode_tile<T, TILE, false>(p, words, tops, tile_r, tile_c);
+  auto whole = [&](unsigned tile, unsigned& r, unsigned& c) {
+    r = tile / p.tiles_c;
+    c = tile - r * p.tiles_c;
+    return p.all_aligned && (r + 1) * 128 <= p.rows && (c + 1) * 128 <= p.cols;
+  };
+  unsigned r, c;
+  if (whole(blockIdx.x, r, c)) bring_tile<T>(p, ahead, r, c);
+  for (unsigned tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const bool now = whole(tile, r, c);
+    const auto next = [&] {
+      unsigned nr, nc;
+      if (tile + gridDim.x < p.tiles && whole(tile + gridDim.x, nr, nc)) bring_tile<T>(p, ahead, nr, nc);
+    };
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (now)
+      encode_tile<T, TILE, true>(p, words, tops, ahead, r, c, next);
+    else
+      encode_tile<T, TILE, false>(p, words, tops, ahead, r, c, next);
+    __syncthreads();   // words and tops are free
+  }
 }
 
 // A warp has a piece of 1024 columns of a row.  Where rows are aligned its lanes
@@ -306,11 +350,11 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const Decode8Par
 
 }  // namespace
 
-cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, cudaStream_t st) {
-  const u64 tiles = (u64)p.tiles_c * ((p.rows + 127) / 128);
+cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, int sms, cudaStream_t st) {
   const auto kernel = dtype == XP_F32 ? (block_rows == 1 ? encode_kernel<float, false> : encode_kernel<float, true>)
                                       : (block_rows == 1 ? encode_kernel<bf16, false> : encode_kernel<bf16, true>);
-  return launch_dependent(kernel, dim3((unsigned)tiles), kThreads, 0, 1, st, p);
+  const size_t smem = sizeof(unsigned) * (128 * 32 + kWarps * 128) + (size_t)128 * 128 * (dtype == XP_F32 ? 4 : 2);
+  return launch_dependent(kernel, dim3(p.tiles < 2u * sms ? p.tiles : 2u * sms), kThreads, smem, 1, st, p);
 }
 
 cudaError_t launch_decode8(const Decode8Params& p, int dtype, cudaStream_t st) {

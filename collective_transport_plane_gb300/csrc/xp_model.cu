@@ -184,11 +184,12 @@ xp_status xp_block8_encode(const void* x, size_t x_stride, size_t rows, size_t c
   p.rows = (unsigned)rows;
   p.cols = (unsigned)cols;
   p.tiles_c = (unsigned)tiles_c;
+  p.tiles = (unsigned)(tiles_c * ceil_div(rows, 128));
   p.x_aligned = rows_aligned(x, x_stride, rows, es, 4 * es);
   p.codes_aligned = rows_aligned(codes, codes_stride, rows, 1, 4);
   p.codes_t_aligned = rows_aligned(codes_t, codes_t_stride, cols, 1, 4);
   p.all_aligned = p.x_aligned && (!codes || p.codes_aligned) && (!codes_t || p.codes_t_aligned);
-  XP_CUDA(xp::launch_encode8(p, dtype, block_rows, stream));
+  XP_CUDA(xp::launch_encode8(p, dtype, block_rows, sm_count(), stream));
   return XP_OK;
 }
 

@@ -36,10 +36,10 @@ struct Encode8Params {
   uint8_t* codes_t;
   uint8_t* scales_t;
   unsigned long long x_stride, codes_stride, scales_stride, codes_t_stride, scales_t_stride;
-  unsigned rows, cols, tiles_c;
+  unsigned rows, cols, tiles_c, tiles;
   int x_aligned, codes_aligned, codes_t_aligned, all_aligned;   // four elements are one access
 };
-cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, cudaStream_t st);
+cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, int sms, cudaStream_t st);
 
 struct Decode8Params {
   const uint8_t* codes;

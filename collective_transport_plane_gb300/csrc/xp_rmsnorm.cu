@@ -539,8 +539,10 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
   }
   s.groups = s.threads >= 256 ? 1 : 256 / s.threads;
   const unsigned block = s.groups * s.threads;
-  // by their registers: 80 a thread in CTAs of up to 384 threads, 128 in larger ones that keep 16 columns' sums, else 64
-  s.per_sm = 65536 / (block * (block <= 384 && wide ? 80 : s.nu * v == 16 ? 128 : 64));
+  // by their registers, of which a quarter of the SM gives each of its warps a whole number: 80 a thread in CTAs of up
+  // to 384 threads, 128 in larger ones that keep 16 columns' sums, else 64
+  const unsigned regs = block <= 384 && wide ? 80 : s.nu * v == 16 ? 128 : 64;
+  s.per_sm = 4 * (512 / regs) / (block / 32);
   if (wide) s.per_sm = std::min(s.per_sm, 216 * 1024 / (2 * 3 * s.nu * 16 * block));   // two rows each in shared memory
   s.per_sm = std::max(1u, s.per_sm);
   s.nparts = (unsigned)std::min<size_t>((rows + s.groups - 1) / s.groups, (size_t)sms * s.per_sm);
