@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
           for (unsigned kb = from; kb < to; ++kb) {
             const unsigned at = base + s * stage_bytes, scale_p = tmem + nsums * bn + slot * slot_columns, scale_q = scale_p + 4;
             const bool more = kb == k0 || kb % 4 == 0, last = kb + 1 == k1 || kb % 4 == 3;
-            ok = tc::bar_wait(full + 8 * s, phase) && (!more || tc::bar_wait(scales_full + 8 * slot, slot_phase));
+            ok = tc::bar_wait(full + 8 * s, phase) && (!more || tc::bar_wait<CTAS == 2>(scales_full + 8 * slot, slot_phase));
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc::fence_after();
             if (tc::elected()) {

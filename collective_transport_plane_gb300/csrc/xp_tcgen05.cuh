@@ -25,16 +25,19 @@ __device__ __forceinline__ bool elected() {
 __device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(unsigned bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// CLUSTER: what the arriving threads of other CTAs wrote before is seen.
+template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
   unsigned ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  if constexpr (CLUSTER)
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
 // A wait gives up after two seconds of the GPU's clock (no wait here is for
@@ -45,15 +48,19 @@ __device__ __forceinline__ unsigned long long clock_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+template <bool CLUSTER>
 __device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity) {
   const unsigned long long start = clock_ns();
   do {
     for (int i = 0; i < 64; ++i)
-      if (bar_try(bar, parity)) return true;
+      if (bar_try<CLUSTER>(bar, parity)) return true;
   } while (clock_ns() - start < kLimitNs);
   return false;
 }
-__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity) { return bar_try(bar, parity) || bar_wait_long(bar, parity); }
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity) {
+  return bar_try<CLUSTER>(bar, parity) || bar_wait_long<CLUSTER>(bar, parity);
+}
 
 // ---- the CTAs of a cluster
 __device__ __forceinline__ unsigned cluster_rank() {
