@@ -50,7 +50,9 @@ extern "C" {
  * holds an infinity or a NaN (its codes are 0x7f then).  The scales of a matrix
  * of rows x cols are ceil(rows / block_rows) x ceil(cols / 128) bytes.
  * For xp_matmul8 codes begin at, and their rows are, multiples of 16 bytes
- * apart, scales 4 bytes; what lies between rows does not matter. */
+ * apart, scales 4 bytes; what lies between rows does not matter.  (Rows of
+ * codes at multiples of 128 bytes are faster: a third less time with many rows
+ * and columns.) */
 #define XP_BLOCK8 128
 
 /* Encode x (`dtype` XP_F32 or XP_BF16): x / 2^(E - 127) rounded to the nearest
