@@ -327,22 +327,24 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const Decode8Par
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const unsigned c0 = from + 512 * half + lane;
-    uint8_t code[16], e[4];
+    const int n = (int)p.cols - (int)c0;
+    const uint8_t* in = codes + c0;
+    T* to = out + c0;
+    uint8_t code[16];
+    float e[4];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const unsigned c = c0 + 32 * i;
-      code[i] = c < p.cols ? codes[c] : 0;
-      if (i % 4 == 0) e[i / 4] = c < p.cols ? scales[c / 128] : 0;
+      code[i] = 32 * i < n ? in[32 * i] : 0;
+      if (i % 4 == 0) e[i / 4] = 32 * i < n ? power_of(scales[c0 / 128 + i / 4]) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const unsigned c = c0 + 32 * i;
-      const float v = values2(code[i]).x * power_of(e[i / 4]);
-      if (c < p.cols) {
+      const float v = values2(code[i]).x * e[i / 4];
+      if (32 * i < n) {
         if constexpr (sizeof(T) == 4)
-          out[c] = v;
+          to[32 * i] = v;
         else
-          out[c] = __float2bfloat16_rn(v);
+          to[32 * i] = __float2bfloat16_rn(v);
       }
     }
   }

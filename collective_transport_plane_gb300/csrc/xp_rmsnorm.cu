@@ -66,8 +66,15 @@ __device__ __forceinline__ void load(const T* row, unsigned c, unsigned cols, fl
       }
     }
   } else {
+    const T* at = row + c;
+    const int n = (int)cols - (int)c;
+    if (n > 32 * (V - 1)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = c + 32 * i < cols ? to_f(row[c + 32 * i]) : 0.f;
+      for (int i = 0; i < V; ++i) f[i] = to_f(at[32 * i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = 32 * i < n ? to_f(at[32 * i]) : 0.f;
+    }
   }
 }
 template <typename T, bool WIDE, int V>
@@ -79,9 +86,16 @@ __device__ __forceinline__ void store(T* row, unsigned c, unsigned cols, const f
     else
       *reinterpret_cast<uint4*>(row + c) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   } else {
+    T* at = row + c;
+    const int n = (int)cols - (int)c;
+    if (n > 32 * (V - 1)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + 32 * i < cols) from_f(f[i], row[c + 32 * i]);
+      for (int i = 0; i < V; ++i) from_f(f[i], at[32 * i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (32 * i < n) from_f(f[i], at[32 * i]);
+    }
   }
 }
 // gamma's unit; ones where there is none (fp32 or bf16, its own alignment in `g`)
@@ -90,10 +104,11 @@ __device__ __forceinline__ void load_gamma(const void* gamma, bool is_bf16, unsi
   if (!gamma) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = 1.f;
-  } else if (!WIDE) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      f[i] = c + 32 * i < cols ? is_bf16 ? to_f(static_cast<const bf16*>(gamma)[c + 32 * i]) : static_cast<const float*>(gamma)[c + 32 * i] : 0.f;
+  } else if constexpr (!WIDE) {
+    if (is_bf16)
+      load<bf16, false>(static_cast<const bf16*>(gamma), c, cols, f);
+    else
+      load<float, false>(static_cast<const float*>(gamma), c, cols, f);
   } else if (c >= cols) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = 0.f;
@@ -152,9 +167,10 @@ __device__ __forceinline__ void store8(const RmsForwardParams& p, u64 row, bool 
   uint8_t* out = p.y8 + row * p.y8_stride + c;
   const unsigned lo = codes4(y[0], y[1], y[2], y[3], inverse);
   if constexpr (!WIDE) {
+    const int n = (int)p.cols - (int)c;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (c + 32 * i < p.cols) out[32 * i] = (uint8_t)(lo >> 8 * i);
+      if (32 * i < n) out[32 * i] = (uint8_t)(lo >> 8 * i);
   } else if constexpr (V == 8) {
     *reinterpret_cast<uint2*>(out) = make_uint2(lo, codes4(y[V - 4], y[V - 3], y[V - 2], y[V - 1], inverse));
   } else {
@@ -219,9 +235,9 @@ __global__ void __launch_bounds__(LONG ? 1024 : 512) forward_kernel(const RmsFor
   }
 }
 
-// ---- backward: 16 bytes on their way into shared memory (`there` false: zeros)
-__device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(there ? 16 : 0) : "memory");
+// ---- backward: 16 bytes on their way into shared memory, the first n of them (zeros after)
+__device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_made() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest n groups of this thread's copies have landed
@@ -248,15 +264,60 @@ __device__ __forceinline__ void load_landed(unsigned smem, float (&f)[V]) {
   }
 }
 
+// A narrow row's room in shared memory: as it lies in memory, from the 16-byte
+// piece in which it begins.
+template <typename T>
+__host__ __device__ constexpr unsigned room_of(unsigned cols) {
+  return (cols * (unsigned)sizeof(T) + 15u + 15u) / 16u * 16u;
+}
+// Its pieces on their way there, by the row's threads.  (The first piece of the
+// matrix's first row may begin before the matrix: its elements go one by one.)
+template <typename T>
+__device__ __forceinline__ void bring_row(unsigned smem, const void* matrix, u64 row, u64 stride, unsigned cols, unsigned tid, unsigned threads) {
+  const T* p = static_cast<const T*>(matrix) + row * stride;
+  const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u), bytes = shift + cols * (unsigned)sizeof(T);
+  const char* from = reinterpret_cast<const char*>(p) - shift;
+  for (unsigned at = 16 * tid; at < bytes; at += 16 * threads) {
+    if (at == 0 && row == 0 && shift) {
+      for (unsigned j = 0; j < cols && shift + j * sizeof(T) < 16; ++j) {
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + shift + 4 * j), "f"(p[j]) : "memory");
+        else
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(smem + shift + 2 * j), "h"(reinterpret_cast<const unsigned short*>(p)[j]) : "memory");
+      }
+    } else {
+      copy_async16(smem + at, from + at, (int)min(16u, bytes - at));
+    }
+  }
+}
+// A unit of it: four elements 32 columns apart, zeros past the row's end (where
+// nothing is read: a row's threads may have units behind its room).  at: its
+// first in shared memory; n columns are left from there.
+template <typename T>
+__device__ __forceinline__ void load_landed_narrow(unsigned at, int n, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = 0.f;
+    if (32 * i >= n) continue;
+    if constexpr (sizeof(T) == 4) {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[i]) : "r"(at + 128 * i) : "memory");
+    } else {
+      unsigned short v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at + 64 * i) : "memory");
+      f[i] = __uint_as_float((unsigned)v << 16);
+    }
+  }
+}
+
 // A group of threads keeps its columns through all its rows and adds their part
 // of dgamma up in registers; the CTA's groups leave one row of partial sums.
-// WIDE: the rows of the next turns are on their way into shared memory, each
-// thread's units into places of its own, while this turn's are in work
-// (16384 x 5120 bf16 with dadded: 240 us without, 107 with it, 0.93 of the copy
-// rate).  Registers are bounded so that two CTAs or more are there to fill each
-// other's waits for their rows' sums (one of 121 registers: 133 us).  Narrow rows
-// come by plain loads, many CTAs at a time: with four-byte copies ahead
-// 4099 x 1031 fp32 took 21 us, without 14.
+// The rows of the next turns are on their way into shared memory while this
+// turn's are in work (16384 x 5120 bf16 with dadded: 240 us without, 107 with it,
+// 0.93 of the copy rate).  WIDE: each thread's units into places of its own.
+// Narrow rows lie there as in memory, copied by other threads than read them (by
+// plain loads 12000 x 4097 bf16 took 543 us).  Registers are bounded so that two
+// CTAs or more are there to fill each other's waits for their rows' sums (one of
+// 121 registers: 133 us).
 template <typename T, bool WIDE, int NU, bool LARGE>
 __global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE> == 16 ? 1 : 2) backward_kernel(const RmsBackwardParams p) {
   constexpr int V = kUnit<T, WIDE>;
@@ -265,108 +326,95 @@ __global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE
   wait_for_predecessors();
   let_successor_start();
   const unsigned threads = p.threads, groups = blockDim.x / threads, group = threadIdx.x / threads, tid = threadIdx.x - group * threads;
-  const unsigned ring = (unsigned)__cvta_generic_to_shared(raw) + threadIdx.x * 16, unit_bytes = blockDim.x * 16, stage_bytes = 3 * NU * unit_bytes;
+  const unsigned room = room_of<T>(p.cols);                                 // narrow: of a row
+  const unsigned unit_bytes = blockDim.x * 16, stage_bytes = WIDE ? 3 * NU * unit_bytes : 3 * groups * room;
+  const unsigned ring = (unsigned)__cvta_generic_to_shared(raw) + (WIDE ? threadIdx.x * 16 : 3 * group * room);
   const u64 step = (u64)gridDim.x * groups;
   u64 row = (u64)blockIdx.x * groups + group;
-  auto bring = [&](u64 r, unsigned at) {   // row r's units into the stage at `at`
+  auto bring = [&](u64 r, unsigned at) {   // row r into the stage at `at`
+    const bool there = r < p.rows;
     if constexpr (WIDE) {
-      const bool there = r < p.rows;
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const unsigned c = column<T, WIDE>(tid, threads, k);
         const bool mine = there && c < p.cols;
-        copy_async16(at + k * unit_bytes, static_cast<const T*>(p.dy) + (mine ? r * p.dy_stride + c : 0), mine);
-        copy_async16(at + (NU + k) * unit_bytes, static_cast<const T*>(p.h) + (mine ? r * p.h_stride + c : 0), mine);
-        if (p.dadded) copy_async16(at + (2 * NU + k) * unit_bytes, static_cast<const T*>(p.dadded) + (mine ? r * p.dadded_stride + c : 0), mine);
+        copy_async16(at + k * unit_bytes, static_cast<const T*>(p.dy) + (mine ? r * p.dy_stride + c : 0), mine ? 16 : 0);
+        copy_async16(at + (NU + k) * unit_bytes, static_cast<const T*>(p.h) + (mine ? r * p.h_stride + c : 0), mine ? 16 : 0);
+        if (p.dadded) copy_async16(at + (2 * NU + k) * unit_bytes, static_cast<const T*>(p.dadded) + (mine ? r * p.dadded_stride + c : 0), mine ? 16 : 0);
       }
-      copies_made();
+    } else if (there) {
+      bring_row<T>(at, p.dy, r, p.dy_stride, p.cols, tid, threads);
+      bring_row<T>(at + room, p.h, r, p.h_stride, p.cols, tid, threads);
+      if (p.dadded) bring_row<T>(at + 2 * room, p.dadded, r, p.dadded_stride, p.cols, tid, threads);
+    }
+    copies_made();
+  };
+  // unit k of the row's dy (which 0), h (1) or dadded (2), in the stage at `at`
+  auto landed = [&](unsigned at, int which, int k, const void* matrix, u64 stride, unsigned cols, float (&f)[V]) {
+    if constexpr (WIDE) {
+      load_landed<T>(at + (which * NU + k) * unit_bytes, f);
+    } else {
+      const unsigned c = column<T, WIDE>(tid, threads, k);
+      const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(static_cast<const T*>(matrix) + row * stride) & 15u);
+      load_landed_narrow<T>(at + which * room + shift + c * (unsigned)sizeof(T), (int)cols - (int)c, f);
     }
   };
-  float acc[NU][V];
+  float acc[NU][V], gamma[NU][V];
 #pragma unroll
-  for (int k = 0; k < NU; ++k)
+  for (int k = 0; k < NU; ++k) {
+    load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, gamma[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
-  float gamma[NU][V];
-  if constexpr (WIDE) {
-#pragma unroll
-    for (int k = 0; k < NU; ++k) load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, gamma[k]);
   }
   for (int s = 0; s + 1 < p.stages; ++s) bring(row + s * step, ring + s * stage_bytes);
   const float inv_cols = 1.f / (float)p.cols;
   float rstd = row < p.rows ? p.rstd[row] : 0.f;
   int buf = 0, stage = 0;
+  const int ahead = p.stages - 1;
   for (u64 first = (u64)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 1) {
-    const bool there = row < p.rows;
-    const unsigned cols = there ? p.cols : 0;
+    const unsigned cols = row < p.rows ? p.cols : 0;
     const float next_rstd = row + step < p.rows ? p.rstd[row + step] : 0.f;
-    float sum = 0.f;
-    const unsigned at = ring + stage * stage_bytes;
-    float d[WIDE ? 1 : NU][V], h[WIDE ? 1 : NU][V];   // (WIDE rows are read from shared memory once more instead)
+    const unsigned at = ring + stage * stage_bytes, into = ring + (stage == 0 ? ahead : stage - 1) * stage_bytes;
     if constexpr (WIDE) {
-      const int ahead = p.stages - 1, into = stage == 0 ? ahead : stage - 1;
-      bring(row + ahead * step, ring + into * stage_bytes);
+      bring(row + ahead * step, into);
       wait_copies(ahead);
-      stage = stage == ahead ? 0 : stage + 1;
-    } else {
-#pragma unroll
-      for (int k = 0; k < NU; ++k) {
-        const unsigned c = column<T, WIDE>(tid, threads, k);
-        load<T, WIDE>(static_cast<const T*>(p.dy) + row * p.dy_stride, c, cols, d[k]);
-        load<T, WIDE>(static_cast<const T*>(p.h) + row * p.h_stride, c, cols, h[k]);
-      }
+    } else {   // what all threads copied is there, and nobody reads the stage that is filled next
+      wait_copies(ahead - 1);
+      __syncthreads();
+      bring(row + ahead * step, into);
     }
+    stage = stage == ahead ? 0 : stage + 1;
+    float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      constexpr int kEach = WIDE ? 0 : 1;
-      float(&x)[V] = h[k * kEach], (&y)[V] = d[k * kEach], g[V];
-      if constexpr (WIDE) {
-        load_landed<T>(at + k * unit_bytes, y);
-        load_landed<T>(at + (NU + k) * unit_bytes, x);
-      }
-      if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = gamma[k][i];
-      } else {
-        load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g);
-      }
+      float x[V], y[V];
+      landed(at, 0, k, p.dy, p.dy_stride, cols, y);
+      landed(at, 1, k, p.h, p.h_stride, cols, x);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         x[i] *= rstd;
         acc[k][i] = fmaf(y[i], x[i], acc[k][i]);
-        y[i] *= g[i];
-        sum = fmaf(y[i], x[i], sum);
+        sum = fmaf(y[i] * gamma[k][i], x[i], sum);
       }
     }
     sum = row_sum(sum, words[buf], threads) * inv_cols;
     T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
-    for (int k = 0; k < NU; ++k) {
-      constexpr int kEach = WIDE ? 0 : 1;
-      const unsigned c = column<T, WIDE>(tid, threads, k);
-      float(&x)[V] = h[k * kEach], (&y)[V] = d[k * kEach], e[V];
-      if constexpr (WIDE) {
-        load_landed<T>(at + k * unit_bytes, y);
-        load_landed<T>(at + (NU + k) * unit_bytes, x);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] *= rstd, y[i] *= gamma[k][i];
-      }
-      if (p.dadded) {
-        if constexpr (WIDE)
-          load_landed<T>(at + (2 * NU + k) * unit_bytes, e);
-        else
-          load<T, WIDE>(static_cast<const T*>(p.dadded) + row * p.dadded_stride, c, cols, e);
-      }
+    for (int k = 0; k < NU; ++k) {   // (read once more: registers for them would cost a CTA)
+      float x[V], y[V], e[V];
+      landed(at, 0, k, p.dy, p.dy_stride, cols, y);
+      landed(at, 1, k, p.h, p.h_stride, cols, x);
+      if (p.dadded) landed(at, 2, k, p.dadded, p.dadded_stride, cols, e);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        y[i] = fmaf(-x[i], sum, y[i]) * rstd;
+        y[i] = fmaf(-(x[i] * rstd), sum, y[i] * gamma[k][i]) * rstd;
         if (p.dadded) y[i] += e[i];
       }
-      store<T, WIDE>(dx, c, cols, y);
+      store<T, WIDE>(dx, column<T, WIDE>(tid, threads, k), cols, y);
     }
     rstd = next_rstd;
   }
-  if (WIDE) wait_copies(0);
+  wait_copies(0);
   if (!p.partial) return;
   float* mine = p.partial + (u64)blockIdx.x * p.cols;
   if (groups > 1) {
@@ -496,12 +544,12 @@ cudaError_t forward(RmsForwardParams& p, cudaStream_t st) {
 
 template <typename T, bool WIDE, int NU>
 cudaError_t backward_rows(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream_t st) {
-  const unsigned block = s.groups * s.threads, stage = 3 * NU * 16 * block;
+  const unsigned block = s.groups * s.threads, stage = WIDE ? 3 * NU * 16 * block : 3 * s.groups * room_of<T>(p.cols);
   // as many rows ahead as the SM's CTAs have room for, three at most
-  p.stages = WIDE ? std::min(4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage)))) : 1;
-  size_t smem = WIDE ? (size_t)p.stages * stage : 0;
+  p.stages = std::min(4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage))));
+  size_t smem = (size_t)p.stages * stage;
   if (s.groups > 1) smem = std::max<size_t>(smem, (size_t)block * NU * kUnit<T, WIDE> * sizeof(float));
-  const auto kernel = block > 384 ? backward_kernel<T, WIDE, NU, true> : backward_kernel<T, WIDE, NU, !WIDE>;
+  const auto kernel = block > 384 ? backward_kernel<T, WIDE, NU, true> : backward_kernel<T, WIDE, NU, false>;
   return launch_dependent(kernel, dim3(s.nparts), (int)block, smem, 1, st, p);
 }
 
@@ -541,9 +589,9 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
   const unsigned block = s.groups * s.threads;
   // by their registers, of which a quarter of the SM gives each of its warps a whole number: 80 a thread in CTAs of up
   // to 384 threads, 128 in larger ones that keep 16 columns' sums, else 64
-  const unsigned regs = block <= 384 && wide ? 80 : s.nu * v == 16 ? 128 : 64;
-  s.per_sm = 4 * (512 / regs) / (block / 32);
-  if (wide) s.per_sm = std::min(s.per_sm, 216 * 1024 / (2 * 3 * s.nu * 16 * block));   // two rows each in shared memory
+  const unsigned regs = block <= 384 ? 80 : s.nu * v == 16 ? 128 : 64;
+  const unsigned es = dtype == XP_F32 ? 4 : 2, stage = wide ? 3 * s.nu * 16 * block : 3 * s.groups * (es == 4 ? room_of<float>((unsigned)cols) : room_of<bf16>((unsigned)cols));
+  s.per_sm = std::min(4 * (512 / regs) / (block / 32), 216 * 1024 / (2 * stage));   // two rows each in shared memory
   s.per_sm = std::max(1u, s.per_sm);
   s.nparts = (unsigned)std::min<size_t>((rows + s.groups - 1) / s.groups, (size_t)sms * s.per_sm);
   return s;

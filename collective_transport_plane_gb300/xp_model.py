@@ -47,29 +47,32 @@ _encode, _decode, _matmul, _forward, _backward, _distill, _distill_back = (
 
 _FLOATS = {"torch.float32": XP_F32, "torch.bfloat16": XP_BF16}
 _BYTES = ("torch.uint8", "torch.float8_e4m3fn", "torch.float8_e8m0fnu")
-_types = {}   # torch dtype -> xp_dtype (XP_U8: codes and scales), filled as types are met
 
 
-def _dtype(t) -> int:
-    found = _types.get(t.dtype)
-    if found is None:
-        name = str(t.dtype)
+class _Types(dict):
+    """torch dtype -> xp_dtype (XP_U8: codes and scales), filled as types are met."""
+
+    def __missing__(self, dtype):
+        name = str(dtype)
         if name not in _FLOATS and name not in _BYTES:
-            raise ValueError(f"no xp_dtype for {t.dtype}")
-        found = _types[t.dtype] = _FLOATS.get(name, XP_U8)
-    return found
+            raise ValueError(f"no xp_dtype for {dtype}")
+        found = self[dtype] = _FLOATS.get(name, XP_U8)
+        return found
+
+
+_types = _Types()
+_current_device = None   # asks torch for it, once torch is there
 
 
 def _device_of(t) -> int:
     """The current device, as torch says; 0 where the tensors are not torch's."""
-    global _device_of
-    torch = sys.modules.get("torch")
-    if torch is None:
-        return 0
-    if not hasattr(torch._C, "_cuda_getDevice"):
-        return torch.cuda.current_device()
-    _device_of = lambda _: torch._C._cuda_getDevice()  # noqa: E731
-    return _device_of(t)
+    global _current_device
+    if _current_device is None:
+        torch = sys.modules.get("torch")
+        if torch is None:
+            return 0
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
 
 
 def _refuse_devices(tensors, current):
@@ -78,7 +81,7 @@ def _refuse_devices(tensors, current):
 
 
 def _refuse_matrix(t, shape, what, dtype):
-    if t.shape != shape or _dtype(t) != dtype:
+    if t.shape != shape or _types[t.dtype] != dtype:
         raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of its type")
     raise ValueError(f"{what}'s columns are {t.stride()[1]} elements apart")
 
@@ -86,7 +89,7 @@ def _refuse_matrix(t, shape, what, dtype):
 def _matrix(t, shape, what, dtype, device):
     """(address, stride) of a matrix of a shape and type whose columns are side by side."""
     stride, step = t.stride()
-    if t.shape != shape or (step != 1 and shape[1] > 1) or (_types.get(t.dtype) or _dtype(t)) != dtype:
+    if t.shape != shape or (step != 1 and shape[1] > 1) or _types[t.dtype] != dtype:
         _refuse_matrix(t, shape, what, dtype)
     if t.get_device() != device:
         _refuse_devices((t,), device)
@@ -97,7 +100,7 @@ def _vector(t, n, what, dtype, device):
     """The address of n contiguous elements (None: none)."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_contiguous() or (_types.get(t.dtype) or _dtype(t)) != dtype:
+    if t.numel() != n or not t.is_contiguous() or _types[t.dtype] != dtype:
         raise ValueError(f"{what} is not {n} contiguous elements of its type")
     if t.get_device() != device:
         _refuse_devices((t,), device)
@@ -121,7 +124,7 @@ def _block8(codes, scales, shape, block_rows, what, device):
 
 
 def _float(t, what):
-    dt = _types.get(t.dtype) or _dtype(t)
+    dt = _types[t.dtype]
     if dt == XP_U8:
         raise ValueError(f"{what} is {t.dtype}")
     return dt
