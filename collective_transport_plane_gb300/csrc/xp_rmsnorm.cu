@@ -3,9 +3,9 @@
 //
 // Both directions read and write every element once and compute little on it:
 // HBM bounds them.  A row's threads keep it in registers between its sum and
-// its outputs (rows of more than 2048 units of 16 bytes, 8192 columns backward,
-// are read twice).  Blocks of 128 columns lie in one warp's units, so a block's scale is
-// a maximum over lanes.
+// its outputs, or in shared memory, backward (rows of more than 16384 columns,
+// 8192 of fp32 or of unaligned rows, are read twice).  Blocks of 128 columns lie
+// in one warp's units, so a block's scale is a maximum over lanes.
 #include <algorithm>
 
 #include "xp_code8.cuh"
@@ -178,7 +178,10 @@ __device__ __forceinline__ void store8(const RmsForwardParams& p, u64 row, bool 
   }
 }
 
-// NU units of a row per thread at once; LONG: rows of more, read twice.
+// NU units of a row per thread at once; LONG: rows of more, read twice.  The sum
+// with the residual is rounded to the type it is stored in before its norm is
+// taken: the backward pass, which reads what was stored, is then that of the
+// very values the norm saw.
 template <typename T, bool WIDE, int NU, bool LONG>
 __global__ void __launch_bounds__(LONG ? 1024 : 512) forward_kernel(const RmsForwardParams p) {
   constexpr int V = kUnit<T, WIDE>;
@@ -319,7 +322,7 @@ __device__ __forceinline__ void load_landed_narrow(unsigned at, int n, float (&f
 // CTAs or more are there to fill each other's waits for their rows' sums (one of
 // 121 registers: 133 us).
 template <typename T, bool WIDE, int NU, bool LARGE>
-__global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE> == 16 ? 1 : 2) backward_kernel(const RmsBackwardParams p) {
+__global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE> >= 16 ? 1 : 2) backward_kernel(const RmsBackwardParams p) {
   constexpr int V = kUnit<T, WIDE>;
   __shared__ float words[2][16];
   extern __shared__ __align__(16) uint8_t raw[];
@@ -359,10 +362,11 @@ __global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE
       load_landed_narrow<T>(at + which * room + shift + c * (unsigned)sizeof(T), (int)cols - (int)c, f);
     }
   };
-  float acc[NU][V], gamma[NU][V];
+  constexpr bool kKeep = NU * V <= 16;   // gamma in registers; else it is read for each row
+  float acc[NU][V], gamma[kKeep ? NU : 1][V];
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
-    load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, gamma[k]);
+    if constexpr (kKeep) load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, gamma[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
   }
@@ -387,27 +391,29 @@ __global__ void __launch_bounds__(LARGE ? 512 : 384, LARGE && NU * kUnit<T, WIDE
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      float x[V], y[V];
+      float x[V], y[V], (&g)[V] = gamma[kKeep ? k : 0];
+      if constexpr (!kKeep) load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g);
       landed(at, 0, k, p.dy, p.dy_stride, cols, y);
       landed(at, 1, k, p.h, p.h_stride, cols, x);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         x[i] *= rstd;
         acc[k][i] = fmaf(y[i], x[i], acc[k][i]);
-        sum = fmaf(y[i] * gamma[k][i], x[i], sum);
+        sum = fmaf(y[i] * g[i], x[i], sum);
       }
     }
     sum = row_sum(sum, words[buf], threads) * inv_cols;
     T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {   // (read once more: registers for them would cost a CTA)
-      float x[V], y[V], e[V];
+      float x[V], y[V], e[V], (&g)[V] = gamma[kKeep ? k : 0];
+      if constexpr (!kKeep) load_gamma<WIDE>(p.gamma, p.gamma_bf16, column<T, WIDE>(tid, threads, k), p.cols, g);
       landed(at, 0, k, p.dy, p.dy_stride, cols, y);
       landed(at, 1, k, p.h, p.h_stride, cols, x);
       if (p.dadded) landed(at, 2, k, p.dadded, p.dadded_stride, cols, e);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        y[i] = fmaf(-(x[i] * rstd), sum, y[i] * gamma[k][i]) * rstd;
+        y[i] = fmaf(-(x[i] * rstd), sum, y[i] * g[i]) * rstd;
         if (p.dadded) y[i] += e[i];
       }
       store<T, WIDE>(dx, column<T, WIDE>(tid, threads, k), cols, y);
@@ -549,7 +555,8 @@ cudaError_t backward_rows(RmsBackwardParams& p, const RmsBackwardShape& s, cudaS
   p.stages = std::min(4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage))));
   size_t smem = (size_t)p.stages * stage;
   if (s.groups > 1) smem = std::max<size_t>(smem, (size_t)block * NU * kUnit<T, WIDE> * sizeof(float));
-  const auto kernel = block > 384 ? backward_kernel<T, WIDE, NU, true> : backward_kernel<T, WIDE, NU, false>;
+  constexpr bool kSmall = (!WIDE && NU <= 2) || NU * kUnit<T, WIDE> > 16;   // 64 registers do, or 128 are needed, in CTAs of any size
+  const auto kernel = block > 384 ? backward_kernel<T, WIDE, NU, true> : backward_kernel<T, WIDE, NU, kSmall>;
   return launch_dependent(kernel, dim3(s.nparts), (int)block, smem, 1, st, p);
 }
 
@@ -564,8 +571,7 @@ cudaError_t backward(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream
     if (e != cudaSuccess) return e;
     e = launch_dependent(long_rows_kernel<T, WIDE>, dim3((p.cols + 256 * V - 1) / (256 * V), s.nparts), 256, 0, 1, st, p);
   } else {
-    constexpr int kMost = V == 8 ? 2 : 4;
-    e = s.nu == 1 ? backward_rows<T, WIDE, 1>(p, s, st) : s.nu == 2 ? backward_rows<T, WIDE, 2>(p, s, st) : backward_rows<T, WIDE, kMost>(p, s, st);
+    e = s.nu == 1 ? backward_rows<T, WIDE, 1>(p, s, st) : s.nu == 2 ? backward_rows<T, WIDE, 2>(p, s, st) : backward_rows<T, WIDE, 4>(p, s, st);
   }
   if (e != cudaSuccess || !p.dgamma) return e;
   return launch_dependent(sum_parts_kernel, dim3((p.cols + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, 1, st, p);
@@ -577,7 +583,7 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
   const unsigned v = wide && dtype == XP_BF16 ? 8 : 4;
   const unsigned units = wide ? (unsigned)((cols + v - 1) / v) : (unsigned)((cols + 127) / 128 * 32);
   RmsBackwardShape s = {};
-  s.nu = units <= 256 ? 1 : units <= 1024 || v == 8 ? 2 : 4;
+  s.nu = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
   s.threads = round32((units + s.nu - 1) / s.nu);
   s.is_long = s.threads > 512;
   if (s.is_long) {
@@ -587,9 +593,9 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
   }
   s.groups = s.threads >= 256 ? 1 : 256 / s.threads;
   const unsigned block = s.groups * s.threads;
-  // by their registers, of which a quarter of the SM gives each of its warps a whole number: 80 a thread in CTAs of up
-  // to 384 threads, 128 in larger ones that keep 16 columns' sums, else 64
-  const unsigned regs = block <= 384 ? 80 : s.nu * v == 16 ? 128 : 64;
+  // by their registers, of which a quarter of the SM gives each of its warps a whole number: 128 a thread where it keeps
+  // 32 columns' sums, or 16 in CTAs of more than 384 threads, 80 in smaller ones, else 64
+  const unsigned regs = s.nu * v == 32 ? 128 : !wide && s.nu <= 2 ? 64 : block <= 384 ? 80 : s.nu * v == 16 ? 128 : 64;
   const unsigned es = dtype == XP_F32 ? 4 : 2, stage = wide ? 3 * s.nu * 16 * block : 3 * s.groups * (es == 4 ? room_of<float>((unsigned)cols) : room_of<bf16>((unsigned)cols));
   s.per_sm = std::min(4 * (512 / regs) / (block / 32), 216 * 1024 / (2 * stage));   // two rows each in shared memory
   s.per_sm = std::max(1u, s.per_sm);

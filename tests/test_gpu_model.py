@@ -465,7 +465,7 @@ def test_norm_backward(xm, rows, cols, name):
 
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols", [(5001, 96), (4999, 95), (2500, 1032), (1201, 4104), (601, 5120), (400, 6200), (330, 8200), (310, 8191), (700, 3001),
-                                       (620, 4097), (2400, 515), (3100, 33), (640, 6145)])
+                                       (620, 4097), (2400, 515), (3100, 33), (640, 6145), (330, 12000), (200, 16384), (160, 16392)])
 def test_norm_backward_many_rows(xm, rows, cols, name):
     torch = torch_cuda()
     _check_norm_backward(torch, xm, rows, cols, name, "f32")
