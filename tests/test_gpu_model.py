@@ -195,6 +195,11 @@ PRODUCTS = [(1, 1, 1), (1, 5, 16), (2, 128, 128), (3, 129, 127), (16, 128, 129),
             (513, 2049, 385), (700, 5000, 130), (1025, 4096, 256), (1500, 9000, 140), (2000, 700, 2001), (3001, 2050, 4100), (5000, 33, 700), (16, 9000, 33), (1, 20001, 257)]
 
 
+# Many rows, whose tiles pairs of CTAs and clusters of two pairs make, with each number of rows in a tile.
+PRODUCTS += [(2596, 138, 228), (6920, 1, 397), (7319, 131, 356), (3240, 6325, 50), (4489, 5617, 90), (6978, 8031, 20), (5886, 569, 903), (148, 1948, 257),
+             (943, 8118, 2134), (813, 6767, 2216), (6863, 7968, 155), (6141, 1386, 2404), (7532, 784, 2532), (8558, 270, 2730)]
+
+
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
 def test_products_of_whole_numbers_are_exact(xm, m, n, k):
     torch = torch_cuda()
