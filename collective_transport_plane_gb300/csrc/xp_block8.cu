@@ -5,6 +5,7 @@
 // that a block's scale is known before its codes, along rows and along columns
 // alike; the transposed codes go through shared memory.
 #include "xp_code8.cuh"
+#include "xp_fours.cuh"
 #include "xp_model_internal.h"
 #include "xp_train_device.cuh"
 
@@ -114,6 +115,12 @@ __device__ __forceinline__ void bring_tile(const Encode8Params& p, const uint8_t
   }
 }
 
+// The piece that holds column c of a row, or none.
+__device__ __forceinline__ uint2 piece_of(const Encode8Params& p, const bf16* from, unsigned row, int c) {
+  if (row >= p.rows) return make_uint2(0, 0);
+  return piece_at(from, c - ahead_of(from), (int)p.cols, pieces_inside(row * p.x_stride, (p.rows - 1 - row) * p.x_stride + p.cols, p.cols));
+}
+
 // WHOLE: all of the tile is there, and its rows and columns are aligned; its
 // elements came ahead.  taken: called when they are in registers.
 template <typename T, bool TILE, bool WHOLE, typename Taken>
@@ -126,15 +133,35 @@ __device__ __forceinline__ void encode_tile(const Encode8Params& p, unsigned (&w
   const unsigned mine = 4 * warp, next = 4 * kWarps;
   const T* x = static_cast<const T*>(p.x) + (u64)(r0 + mine) * p.x_stride + c0;
   Four<T> four[kTurns][4];
+  bool taken_by_pieces = false;
+  if constexpr (sizeof(T) == 2 && !WHOLE) {
+    // (element by element 12000 x 4097 took 81 us, 64 by pieces; short rows' ends cost more: 20000 x 333 10.9, 13.3 by pieces)
+    taken_by_pieces = !p.x_aligned && p.cols >= 512;
+    if (taken_by_pieces) {
 #pragma unroll
-  for (int t = 0; t < kTurns; ++t, x += next * p.x_stride) {
-    const T* at = x;
+      for (int t = 0; t < kTurns; ++t) {
+        const unsigned row = r0 + mine + next * t;
+        const T* from = x - c0 + next * t * p.x_stride;
+        uint2 q[4], more = make_uint2(0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i, at += p.x_stride) {
-      if (WHOLE)
-        four[t][i].load(reinterpret_cast<const T*>(ahead) + 4 * ((t * 4 + i) * kThreads + threadIdx.x));
-      else
-        four[t][i] = load4(at, r0 + mine + next * t + i < p.rows ? n : 0, p.x_aligned);
+        for (int i = 0; i < 4; ++i) q[i] = piece_of(p, from + i * p.x_stride, row + i, (int)c0);
+        if (lane < 4) more = piece_of(p, from + lane * p.x_stride, row + lane, (int)(tile_c * 128 + 128));   // behind the last lane's
+#pragma unroll
+        for (int i = 0; i < 4; ++i) four[t][i].q = join_pieces(q[i], more, i, ahead_of(from + i * p.x_stride), c0, row + i < p.rows ? p.cols : 0);
+      }
+    }
+  }
+  if (!taken_by_pieces) {
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t, x += next * p.x_stride) {
+      const T* at = x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i, at += p.x_stride) {
+        if (WHOLE)
+          four[t][i].load(reinterpret_cast<const T*>(ahead) + 4 * ((t * 4 + i) * kThreads + threadIdx.x));
+        else
+          four[t][i] = load4(at, r0 + mine + next * t + i < p.rows ? n : 0, p.x_aligned);
+      }
     }
   }
 
@@ -264,14 +291,13 @@ __global__ void __launch_bounds__(kThreads, 2) encode_kernel(const Encode8Params
   }
 }
 
-// A warp has a piece of 1024 columns of a row.  Where rows are aligned its lanes
+// A warp has a piece of a row.  Where rows are aligned its lanes
 // take the codes of 16 bytes of output each, side by side (each lane 16 codes, in
 // two stores of every other 16 bytes: 36 us for 16384 x 4096 to bf16), else every
 // 32nd column.
 constexpr int kDecodeThreads = 256;
-constexpr unsigned kPiece = 1024;
 
-template <typename T>
+template <typename T, unsigned kPiece>
 __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const Decode8Params p) {
   wait_for_predecessors();
   let_successor_start();
@@ -324,21 +350,22 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const Decode8Par
     }
     return;
   }
+  constexpr int M = kPiece >= 512 ? 16 : kPiece / 32;   // elements at a time
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const unsigned c0 = from + 512 * half + lane;
+  for (int part = 0; part < (int)kPiece / 32 / M; ++part) {
+    const unsigned c0 = from + 32 * M * part + lane;
     const int n = (int)p.cols - (int)c0;
     const uint8_t* in = codes + c0;
     T* to = out + c0;
-    uint8_t code[16];
-    float e[4];
+    uint8_t code[M];
+    float e[M / 4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < M; ++i) {
       code[i] = 32 * i < n ? in[32 * i] : 0;
       if (i % 4 == 0) e[i / 4] = 32 * i < n ? power_of(scales[c0 / 128 + i / 4]) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < M; ++i) {
       const float v = values2(code[i]).x * e[i / 4];
       if (32 * i < n) {
         if constexpr (sizeof(T) == 4)
@@ -359,10 +386,18 @@ cudaError_t launch_encode8(const Encode8Params& p, int dtype, int block_rows, in
   return launch_dependent(kernel, dim3(p.tiles < 2u * sms ? p.tiles : 2u * sms), kThreads, smem, 1, st, p);
 }
 
-cudaError_t launch_decode8(const Decode8Params& p, int dtype, cudaStream_t st) {
+template <typename T, unsigned kPiece>
+cudaError_t decode(const Decode8Params& p, cudaStream_t st) {
   const u64 pieces = (u64)((p.cols + kPiece - 1) / kPiece) * p.rows, per_cta = kDecodeThreads / 32;
-  return launch_dependent(dtype == XP_F32 ? decode_kernel<float> : decode_kernel<bf16>, dim3((unsigned)((pieces + per_cta - 1) / per_cta)), kDecodeThreads,
-                          0, 1, st, p);
+  return launch_dependent(decode_kernel<T, kPiece>, dim3((unsigned)((pieces + per_cta - 1) / per_cta)), kDecodeThreads, 0, 1, st, p);
+}
+
+// Short rows leave much of a long piece empty (to bf16, 256 columns a piece and 1024: 60000 x 65 9.7 and 27 us, 12000 x
+// 1031 11.7 and 14.0), but where rows are aligned a piece of 256 is one load for a lane (12000 x 1032 11.7 and 9.1).
+cudaError_t launch_decode8(const Decode8Params& p, int dtype, cudaStream_t st) {
+  const bool aligned = p.aligned && p.cols % (dtype == XP_F32 ? 4 : 8) == 0, few = p.cols <= (aligned ? 256 : 1280);
+  if (dtype == XP_F32) return few ? decode<float, 256>(p, st) : decode<float, 1024>(p, st);
+  return few ? decode<bf16, 256>(p, st) : decode<bf16, 1024>(p, st);
 }
 
 }  // namespace xp

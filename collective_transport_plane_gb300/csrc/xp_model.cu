@@ -217,7 +217,7 @@ xp_status xp_block8_decode(const uint8_t* codes, size_t codes_stride, const uint
   const Span read[2] = {span8(codes, codes_stride, rows, cols), span_scales(scales, scales_stride, rows, cols, block_rows)};
   const Span written[1] = {span_of(out, out_stride, rows, cols, es)};
   if (any_overlap(written, 1, read, 2)) return fail(XP_ERR_INVALID, "codes, scales and out overlap");
-  if (ceil_div(ceil_div(cols, 1024) * rows, 8) > 0x7fffffff) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", rows, cols);
+  if (ceil_div(ceil_div(cols, 256) * rows, 8) > 0x7fffffff) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", rows, cols);
   xp::Decode8Params p = {};
   p.codes = codes;
   p.scales = scales;

@@ -273,15 +273,15 @@ template <typename T>
 __host__ __device__ constexpr unsigned room_of(unsigned cols) {
   return (cols * (unsigned)sizeof(T) + 15u + 15u) / 16u * 16u;
 }
-// Its pieces on their way there, by the row's threads.  (The first piece of the
-// matrix's first row may begin before the matrix: its elements go one by one.)
+// Its pieces on their way there, by the row's threads.  (A first piece that
+// begins before the matrix: its elements go one by one.)
 template <typename T>
 __device__ __forceinline__ void bring_row(unsigned smem, const void* matrix, u64 row, u64 stride, unsigned cols, unsigned tid, unsigned threads) {
   const T* p = static_cast<const T*>(matrix) + row * stride;
   const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u), bytes = shift + cols * (unsigned)sizeof(T);
   const char* from = reinterpret_cast<const char*>(p) - shift;
   for (unsigned at = 16 * tid; at < bytes; at += 16 * threads) {
-    if (at == 0 && row == 0 && shift) {
+    if (at == 0 && row * stride * sizeof(T) < shift) {
       for (unsigned j = 0; j < cols && shift + j * sizeof(T) < 16; ++j) {
         if constexpr (sizeof(T) == 4)
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + shift + 4 * j), "f"(p[j]) : "memory");

@@ -113,6 +113,16 @@ def test_encode_strides_and_alignment(xm, rows, cols, pad, offset, step):
         _check_encode(torch, xm, x, 128, out_step=step)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 513), (2, 512), (5, 515), (130, 640), (131, 1031), (3, 2049)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (0, 2), (0, 3), (1, 0), (2, 1), (3, 3), (4, 2)])
+def test_encode_rows_that_begin_anywhere(xm, rows, cols, pad, offset):
+    # NaN lies around the matrix and between its rows
+    torch = torch_cuda()
+    x, _ = _matrix(torch, rows, cols, torch.bfloat16, pad, offset, values=_spread(rows, cols, 11))
+    _check_encode(torch, xm, x, 1)
+    _check_encode(torch, xm, x, 128, "plain")
+
+
 def test_encode_where_it_is_decided(xm):
     # largest magnitudes at, below and above 448 times every power of two; elements at the middles between codes
     torch = torch_cuda()
@@ -168,6 +178,11 @@ def test_decode_shapes(xm, rows, cols, pad, offset, block_rows):
         assert np.array_equal(_f64(out), want, equal_nan=True)
         if pad:
             assert (buf[offset:offset + rows * (cols + pad)].view(rows, -1)[:, cols:] == 5).all()
+
+
+@pytest.mark.parametrize("rows,cols,pad,offset", [(100, 64, 0, 0), (100, 65, 0, 0), (20, 256, 8, 0), (20, 257, 0, 0), (9, 264, 0, 0), (9, 1279, 1, 0), (9, 1280, 1, 1), (9, 1281, 0, 3), (9, 1280, 0, 0)])
+def test_decode_short_rows(xm, rows, cols, pad, offset):
+    test_decode_shapes(xm, rows, cols, pad, offset, 1)
 
 
 # ---------------------------------------------------------------- products
