@@ -536,9 +536,12 @@ cudaError_t forward(RmsForwardParams& p, cudaStream_t st) {
     p.threads = 1024;
     return launch_dependent(forward_kernel<T, WIDE, 2, true>, dim3((unsigned)p.rows), 1024, 0, 1, st, p);
   }
-  const unsigned nu = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
+  // Two units a thread where a row has more than a warp's, so that a row's own steps are shared by more elements, and four
+  // in long rows (bf16, with the residual: 16384 x 2048 47 us by two and 63 by one, 6000 x 8192 69 by four and 73 by two;
+  // unaligned rows 98 by two and 116 by four at 16384 x 2049).
+  const unsigned nu = units <= 32 ? 1 : units <= (WIDE ? 512 : 1024) ? 2 : 4;
   p.threads = round32((units + nu - 1) / nu);
-  const unsigned groups = p.threads >= 256 ? 1 : 256 / p.threads;
+  const unsigned groups = p.threads >= 128 ? 1 : 128 / p.threads;
   const dim3 grid((unsigned)((p.rows + groups - 1) / groups));
   const int block = (int)(groups * p.threads);
   switch (nu) {
@@ -583,7 +586,10 @@ RmsBackwardShape rms_backward_shape(size_t rows, size_t cols, int dtype, bool wi
   const unsigned v = wide && dtype == XP_BF16 ? 8 : 4;
   const unsigned units = wide ? (unsigned)((cols + v - 1) / v) : (unsigned)((cols + 127) / 128 * 32);
   RmsBackwardShape s = {};
-  s.nu = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
+  // More than one unit a thread where a row has more than a warp's: 16384 x 2048 bf16 47 us by two and 54 by one, 60000 x 512
+  // 41, 48 and by four 74; unaligned rows 60000 x 257 bf16 67 by four, 79 by two and 98 by one, 16384 x 2049 101 by four and
+  // 108 by two, but 4099 x 1031 fp32 18 by two and 20 by four.
+  s.nu = units <= 32 ? 1 : !wide && (units <= 128 || dtype == XP_BF16) ? 4 : units <= 1024 ? 2 : 4;
   s.threads = round32((units + s.nu - 1) / s.nu);
   s.is_long = s.threads > 512;
   if (s.is_long) {
