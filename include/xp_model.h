@@ -51,7 +51,7 @@ extern "C" {
  * of rows x cols are ceil(rows / block_rows) x ceil(cols / 128) bytes.
  * For xp_matmul8 codes begin at, and their rows are, multiples of 16 bytes
  * apart, scales 4 bytes; what lies between rows does not matter.  (Rows of
- * codes at multiples of 128 bytes are faster: a third less time with many rows
+ * codes at multiples of 128 bytes are faster: a tenth less time with many rows
  * and columns.) */
 #define XP_BLOCK8 128
 
@@ -85,7 +85,9 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
 
 /* Waits for the device.  XP_ERR_TIMEOUT if a product on the current device
  * ever gave up a wait between its own warps (after two seconds; the tiles of
- * that call are NaN from there on), else XP_OK. */
+ * that call are NaN from there on), else XP_OK.  Not while a stream of the
+ * device is being captured: like any call that waits for a device, it would
+ * end the capture. */
 xp_status xp_matmul8_status(void);
 
 /* ------------------------------------------------- root-mean-square norm */
