@@ -4,6 +4,10 @@ bit, products of whole numbers exactly, everything else within bounds that follo
 U = 2^-24 is fp32's rounding error, a power of 2 is off by at most 2^-22 relatively (two units in the last place of the
 hardware's approximation).  A sum of n terms that is made in a chain of c additions and a tree above it is off by at most
 (c + tree) U times the sum of magnitudes."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -12,6 +16,7 @@ from tests.gpu_util import torch_cuda
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = 2.0 ** -24
 POW = 2.0 ** -22
 
@@ -789,6 +794,45 @@ def test_steps_in_graphs_and_on_streams(xm):
         torch.cuda.synchronize()
         for s, w in zip(layers, want):
             assert all(torch.equal(a, b) for a, b in zip(s.outputs(), w))
+
+
+def test_products_at_once_and_first_called_in_a_capture(xm):
+    # clusters of two pairs, pairs, CTAs that share a tile: a process's first products are captured, and replayed at once
+    code = """
+import sys
+sys.path.insert(0, %r)
+import torch
+from collective_transport_plane_gb300 import xp_model as xm
+sizes, calls = [(801, 6595, 2148), (4186, 1320, 1666), (2000, 700, 2001), (1, 4096, 4096)], []
+for i, (m, n, k) in enumerate(sizes):
+    g = torch.Generator().manual_seed(i)
+    pitch, kb = (k + 15) // 16 * 16, (k + 127) // 128
+    codes = [(torch.randint(0, 2, (r, pitch), generator=g) * 0x38).to(torch.uint8).cuda()[:, :k] for r in (m, n)]      # 0 or 1
+    scales = [torch.full((r, (kb + 3) // 4 * 4), 127, dtype=torch.uint8, device="cuda")[:, :kb] for r in (m, n)]
+    want = (codes[0].double() / 0x38) @ (codes[1].double() / 0x38).t()
+    calls.append((codes, scales, want.float(), torch.zeros(m, n, device="cuda")))
+torch.cuda.synchronize()
+graphs = []
+for (a, b), (sa, sb), want, c in calls:
+    graphs.append((torch.cuda.CUDAGraph(), torch.cuda.Stream()))
+    with torch.cuda.graph(graphs[-1][0], stream=graphs[-1][1]):
+        xm.xp_matmul8(a, sa, b, sb, c, stream=graphs[-1][1])
+for _ in range(5):
+    for *_, c in calls:
+        c.fill_(-1)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, want) for *_, want, c in calls)
+assert xm.xp_matmul8_status() == 0
+print("equal")
+""" % ROOT
+    torch_cuda()
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip().endswith("equal"), done.stderr[-2000:]
 
 
 def test_calls_of_threads(xm):
