@@ -368,13 +368,20 @@ __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
   for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x) {
     const int id = e.id[j];
     if (id < 0) continue;
-    float prob = 0.f;   // of all entries that name the token, in their order
+    // Mostly one entry names a token.  (Its p among the comparisons, where each lane meets itself at another step: 13558 x
+    // 3001 bf16 with 115 entries 91 us, 57 so.)
+    int named = 0;
     for (unsigned i = 0; i < p.top; i += 4) {
       const int4 four = *reinterpret_cast<const int4*>(e.id + i);
-      const int other[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll
-      for (unsigned k = 0; k < 4; ++k)
-        if (other[k] == id) prob += pow2((e.u[i + k] - top_u) * kLog2e) / w;
+      named += (four.x == id) + (four.y == id) + (four.z == id) + (four.w == id);
+    }
+    float prob = 0.f;
+    if (named == 1) {
+      prob = pow2((e.u[j] - top_u) * kLog2e) / w;
+    } else {   // of all entries that name it, in their order
+#pragma unroll 1
+      for (unsigned i = 0; i < p.top; ++i)
+        if (e.id[i] == id) prob += pow2((e.u[i] - top_u) * kLog2e) / w;
     }
     from_f((q_of(e.z[j]) - prob) * scale, out[id]);
   }
