@@ -611,6 +611,13 @@ def test_distill_strides_alignment_and_in_place(xm, pad, offset, in_place):
         _check_distill(torch, xm, 200, 777, 9, name, 1.0, pad, offset, in_place)
 
 
+@pytest.mark.parametrize("vocab,top,pad,offset", [(1, 1, 0, 0), (40, 3, 1, 1), (512, 20, 0, 0), (1000, 64, 3, 5), (1024, 7, 0, 0)])
+def test_distill_many_short_rows(xm, vocab, top, pad, offset):
+    torch = torch_cuda()
+    for name in ("f32", "bf16"):
+        _check_distill(torch, xm, 5003, vocab, top, name, 1.0, pad, offset, pad > 0)
+
+
 def test_distill_large_logits(xm):
     torch = torch_cuda()
     for spread in (30.0, 300.0):
