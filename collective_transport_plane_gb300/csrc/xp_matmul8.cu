@@ -16,14 +16,11 @@
 // 2^-24 for each thousand columns.  While they are stored the next tile's products
 // run.  Large products are made by pairs of CTAs, 256 rows of B at a time, half of
 // A's rows in each's shared memory, which then has to deliver 256 bytes for what a
-// CTA alone reads 384 for.  The largest are made by two pairs of a cluster, which
-// have the same rows of A beside neighbouring rows of B: each CTA copies a quarter
-// of A's for itself and the other pair, a quarter less from L2 in all (4096 x 5120
-// x 16001, rows 16016 bytes apart: 237 us, and 272 by pairs; 2176 x 1305 x 9221
-// 27.7 and 31.7; 8192 x 16384 x 4096 316 and 319, and 346 and 360 in long runs,
-// where the power cap holds).  Where tiles are few, the CTAs of a cluster share
-// one: each sums a part of the columns, and they add their sums up through shared
-// memory, in the order of their ranks.
+// CTA alone reads 384 for.  Where tiles are few, the CTAs of a cluster share one:
+// each sums a part of the columns, and they add their sums up through shared
+// memory, in the order of their ranks.  (A copy lands in the CTA that asks for it
+// alone: no load here names several CTAs, so that operands may lie in any memory
+// that the device reaches.)
 #include <algorithm>
 
 #include "xp_model_internal.h"
@@ -108,10 +105,8 @@ __device__ __forceinline__ void put(const Matmul8Params& p, u64 at, u64 step, un
     if (i < n) c[i * step] = p.accumulate ? old[i] + v[i] : v[i];
 }
 
-// CTAS: of a pair (2), or alone or in a cluster that shares a tile (1).  PAIRS:
-// two pairs of a cluster have the same rows of A beside neighbouring rows of B,
-// and each CTA copies a quarter of A's to one of either pair.
-template <int CTAS, int PAIRS>
+// CTAS: of a pair (2), or alone or in a cluster that shares a tile (1).
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_constant__ Matmul8Params p) {
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
@@ -126,9 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   const unsigned drained = tc::smem_of(&bars.drained);
   const unsigned nsums = p.nsums, q_lines = (bn + 127) / 128, slot_columns = 4 + 4 * q_lines;
   const unsigned rank = CTAS == 2 || p.split > 1 ? tc::cluster_rank() : 0;
-  const unsigned half = CTAS == 2 ? rank & 1 : 0, pair = CTAS == 2 ? rank >> 1 : 0, leader_rank = rank & ~1u;
-  const bool leader = half == 0;   // of a pair: it issues the products, and keeps the barriers they wait for
-  const unsigned short pair_mask = (unsigned short)(3u << leader_rank);
+  const bool leader = CTAS == 1 || rank == 0;   // of a pair: it issues the products, and keeps the barriers they wait for
 
   if (warp == 0 && lane == 0) {
     tc::prefetch_map(&p.p_map);
@@ -137,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   if (warp == 1 && lane == 0) {
     for (unsigned i = 0; i < stages; ++i) {
       tc::bar_init(full + 8 * i, 1);
-      tc::bar_init(empty + 8 * i, PAIRS);
+      tc::bar_init(empty + 8 * i, 1);
     }
     tc::bar_init(drained, 1);
     for (unsigned i = 0; i < kScaleSlots; ++i) {
@@ -159,17 +152,16 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   wait_for_predecessors();
   let_successor_start();
 
-  const unsigned sharers = CTAS * PAIRS * p.split;   // CTAs of a tile, or of two pairs' tiles
+  const unsigned sharers = CTAS * p.split;   // CTAs of a tile
   const unsigned first_tile = blockIdx.x / sharers, tile_step = gridDim.x / sharers, ntiles = p.tiles_p * p.tiles_q;
   const unsigned part = CTAS == 2 ? 0 : rank;
   const unsigned k0 = (unsigned)((u64)p.kblocks * part / p.split), k1 = (unsigned)((u64)p.kblocks * (part + 1) / p.split);
-  // of the tile's rows, in this CTA (tiles_p counts two pairs' rows of B at once)
-  constexpr unsigned kTileRows = CTAS * PAIRS * kRows;
-  const unsigned p_first = CTAS == 2 ? rank * kRows : 0, q_first = half * q_box;
+  constexpr unsigned kTileRows = CTAS * kRows;
+  const unsigned p_first = CTAS == 2 ? rank * kRows : 0, q_first = CTAS == 2 ? rank * q_box : 0;   // of the tile's rows, in this CTA
   bool ok = true;
 
   if (warp == 0) {
-    const unsigned full_at = CTAS == 2 ? tc::in_cta(full, leader_rank) : full, quarter = pair * (q_box / 2);
+    const unsigned full_at = CTAS == 2 ? tc::in_cta(full, 0) : full;
     unsigned n = 0, s = 0, turn = 0;   // boxes brought so far; the stage of the next, and how often the ring went round
     for (unsigned t = first_tile; t < ntiles && ok; t += tile_step) {
       unsigned tp, tq;
@@ -181,10 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
           const unsigned at = base + s * stage_bytes;
           if (leader) tc::bar_expect(full + 8 * s, CTAS * stage_bytes);
           tc::load_box<CTAS>(at, &p.p_map, kb * kBoxCols, row_p, full_at + 8 * s);
-          if constexpr (PAIRS == 2)
-            tc::load_box_to(at + kRowsBytes + quarter * kBoxCols, &p.q_map, kb * kBoxCols, row_q + quarter, full_at + 8 * s, (unsigned short)(5u << half));
-          else
-            tc::load_box<CTAS>(at + kRowsBytes, &p.q_map, kb * kBoxCols, row_q, full_at + 8 * s);
+          tc::load_box<CTAS>(at + kRowsBytes, &p.q_map, kb * kBoxCols, row_q, full_at + 8 * s);
         }
         if (++s == stages) s = 0, ++turn;
       }
@@ -215,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
               const u64 a = tc::rows128(at), b = tc::rows128(at + kRowsBytes);
 #pragma unroll
               for (int i = 0; i < 4; ++i) tc::mma_scaled<CTAS>(d, a + 2 * i, b + 2 * i, shape, scale_p, scale_q, kb != from || i > 0);
-              tc::commit_to<CTAS>(empty + 8 * s, PAIRS == 2 ? 15 : pair_mask);
+              tc::commit_to<CTAS>(empty + 8 * s);
               // a slot is free, here and in TMEM, when the last products that read it are done
-              if (last) tc::commit_to<CTAS>(scales_empty + 8 * slot, pair_mask);
-              if (kb + 1 == to) tc::commit_to<CTAS>(sums_full + 8 * sums, pair_mask);
+              if (last) tc::commit_to<CTAS>(scales_empty + 8 * slot);
+              if (kb + 1 == to) tc::commit_to<CTAS>(sums_full + 8 * sums);
             }
             __syncwarp();
             if (last && ++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
@@ -228,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
         }
       }
       if (!ok) {   // what was issued ends before TMEM is given back
-        if (tc::elected()) tc::commit_to<CTAS>(drained, pair_mask);
+        if (tc::elected()) tc::commit_to<CTAS>(drained);
         tc::bar_wait(drained, 0);
       }
     }
@@ -236,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
     // A warp brings two groups of four blocks' scales at a time: the fence between its loads and the tensor core's
     // copies waits for all that the warp has on its way, and one group after another takes 2800 cycles each, longer
     // than four blocks' products (8192 x 16384 x 4096: 364 us with one such warp, 335 with four groups on their way).
-    const unsigned scales_full_at = CTAS == 2 ? tc::in_cta(scales_full, leader_rank) : scales_full;
+    const unsigned scales_full_at = CTAS == 2 ? tc::in_cta(scales_full, 0) : scales_full;
     const unsigned g0 = k0 / 4, per_tile = k0 < k1 ? (k1 + 3) / 4 - g0 : 0;
     const unsigned mine = first_tile < ntiles ? (ntiles - first_tile + tile_step - 1) / tile_step * per_tile : 0;
     unsigned at = 2 * (warp - 2), tile = first_tile;   // the group within its tile
@@ -271,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   } else {
     // a warp has 32 rows of B, and every fourth 16 of A's
     const unsigned quarter = warp & 3, first = 16 * ((warp - kFirstStoreWarp) >> 2), row = 32 * quarter + lane;
-    const unsigned sums_empty_at = CTAS == 2 ? tc::in_cta(sums_empty, leader_rank) : sums_empty;
+    const unsigned sums_empty_at = CTAS == 2 ? tc::in_cta(sums_empty, 0) : sums_empty;
     unsigned sums = 0, phase = 0;
     for (unsigned t = first_tile; t < ntiles; t += tile_step) {
       float v[4][16];
@@ -355,25 +344,24 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   }
 }
 
-// Clusters of pairs that fit on the device at a time.
-template <int PAIRS>
-int cluster_count(int sms) {
+// Pairs of CTAs that fit on the device at a time.
+int pair_count(int sms) {
   static PerDevice known;
   return known.get([sms](int) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * PAIRS);
+    cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSharedBytes;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2 * PAIRS;
+    at.val.clusterDim.x = 2;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (allow_dynamic_smem(matmul8_kernel<2, PAIRS>) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, matmul8_kernel<2, PAIRS>, &cfg) != cudaSuccess || n < 1) {
+    if (allow_dynamic_smem(matmul8_kernel<2>) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, matmul8_kernel<2>, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
-      n = std::max(1, sms / (2 * PAIRS));
+      n = std::max(1, sms / 2);
     }
     return n;
   });
@@ -391,15 +379,11 @@ cudaError_t launch_matmul8(Matmul8Params& p, int sms, cudaStream_t st) {
   const unsigned tiles = p.tiles_p * p.tiles_q;
   // (a CTA has its SM to itself, so clusters do not hold up the kernel that drains before them: 310 us with programmatic
   // dependence and 324 without at 8192 x 16384 x 4096, 8.7 and 9.6 for one row of 4096 x 4096)
-  if (p.ctas == 2 && p.pairs == 2)
-    return launch_clusters(matmul8_kernel<2, 2>, dim3(4 * std::min(tiles, (unsigned)cluster_count<2>(sms))), kThreads, kSharedBytes, 4, true, st, p);
   if (p.ctas == 2)
-    return launch_clusters(matmul8_kernel<2, 1>, dim3(2 * std::min(tiles, (unsigned)cluster_count<1>(sms))), kThreads, kSharedBytes, 2, true, st, p);
+    return launch_clusters(matmul8_kernel<2>, dim3(2 * std::min(tiles, (unsigned)pair_count(sms))), kThreads, kSharedBytes, 2, true, st, p);
   const unsigned grid = p.split > 1 ? tiles * p.split : tiles < (unsigned)sms ? tiles : (unsigned)sms;
-  return launch_clusters(matmul8_kernel<1, 1>, dim3(grid), kThreads, kSharedBytes, (int)p.split, true, st, p);
+  return launch_clusters(matmul8_kernel<1>, dim3(grid), kThreads, kSharedBytes, (int)p.split, true, st, p);
 }
-
-int matmul8_quads(int sms) { return cluster_count<2>(sms); }
 
 cudaError_t matmul8_stalls(unsigned* n) { return cudaMemcpyFromSymbol(n, stalled_warps, sizeof *n); }
 

@@ -96,40 +96,34 @@ bool map_codes(CUtensorMap* map, const uint8_t* codes, size_t stride, size_t row
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is cut: tiles of 128 of b's rows (256 for a pair of CTAs, 512
-// for a cluster of two pairs) and bn of a's, and the CTAs that share one.  The
-// least of a model in ns, fitted to times of all choices at 27 sizes (N = K =
-// 4096: 64 rows 9.1 us as 4 CTAs a tile, 12.5 as one, 10.2 in pairs; 512 rows 12.8
-// in pairs of 128, 13.1 in two pairs, 14.8 alone; 4096 rows 45 in pairs of 224, 48
-// of 256, which have room in TMEM for one tile's sums only): a block's copies and
-// products, what a tile's last sums take, and what CTAs of a cluster add.  Two
-// pairs copy a quarter less, which counts most where blocks straddle L2's lines
-// (4096 x 5120 x 16001, rows 16016 bytes apart: 237 us, 272 in pairs; 2176 x 1305
-// x 9221 27.7 and 31.7), but leave some SMs without a cluster.
+// How a product is cut: tiles of 128 of b's rows (256 for a pair of CTAs) and bn
+// of a's, and the CTAs that share one.  The least of a model in ns, fitted to
+// times of all choices at 27 sizes (N = K = 4096: 64 rows 9.1 us as 4 CTAs a tile,
+// 12.5 as one, 10.2 in pairs; 512 rows 12.8 in pairs of 128, 14.8 alone; 4096 rows
+// 42 in pairs of 224, 46 of 256, which have room in TMEM for one tile's sums
+// only, 52 alone): a block's copies and products, which take longer where blocks straddle
+// L2's lines, what a tile's last sums take, and what CTAs that share a tile add.
 void cut_product(size_t m, size_t n, size_t kblocks, unsigned sms, bool lines, xp::Matmul8Params& p) {
   static const unsigned widths[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
   size_t least = ~(size_t)0;
-  for (unsigned ctas = 1; ctas <= 4; ctas *= 2) {   // of a cluster whose CTAs do not share a tile's columns
-    if (ctas == 4 && n <= 256) break;
-    const unsigned whole = (unsigned)std::min<size_t>(256, round_up(m, ctas == 1 ? 16 : 32));
-    const size_t tiles_p = ceil_div(n, 128 * ctas), units = ctas == 4 ? (size_t)xp::matmul8_quads((int)sms) : std::max(1u, sms / ctas);
+  for (unsigned ctas = 1; ctas <= 2; ++ctas) {
+    const unsigned whole = (unsigned)std::min<size_t>(256, round_up(m, 16 * ctas));
+    const size_t tiles_p = ceil_div(n, 128 * ctas), units = std::max(1u, sms / ctas);
     for (unsigned width : widths) {
       const unsigned bn = std::min(width, whole);
-      if (ctas > 1 && bn % 32) continue;
+      if (bn % (16 * ctas)) continue;
       const size_t tiles = tiles_p * ceil_div(m, bn), waves = ceil_div(tiles, units);
-      const size_t block = ctas == 1   ? 150u + bn * 23 / 20 + (lines ? 0 : bn * 9 / 10)
-                           : ctas == 2 ? std::max(150u, 120u + (lines ? bn : bn * 5 / 4))
-                                       : std::max(150u, (lines ? 110u : 150u) + bn * 9 / 10);
-      for (unsigned split = 1; split <= (ctas > 1 ? 1u : 8u); split *= 2) {
+      const size_t block = ctas == 1 ? 150u + bn * 23 / 20 + (lines ? 0 : bn * 9 / 10) : std::max(150u, 120u + (lines ? bn : bn * 5 / 4));
+      for (unsigned split = 1; split <= (ctas == 2 ? 1u : 8u); split *= 2) {
         // (clusters of 8 find room for 64 CTAs: with 128 they came one after another)
         if (split > 1 && (split > kblocks || tiles * split > (split == 8 ? std::min(64u, sms) : sms))) break;
-        const size_t cost = waves * (ceil_div(kblocks, split) * block + (bn > 224 ? 1000 : 0)) + 5500 + 4 * bn + (split > 1 ? 1200 + 11 * bn : 0) + (ctas == 4 ? 1300 : 0);
-        if (cost < least) least = cost, p.ctas = std::min(2u, ctas), p.pairs = ctas == 4 ? 2 : 1, p.bn = bn, p.split = split;
+        const size_t cost = waves * (ceil_div(kblocks, split) * block + (bn > 224 ? 1000 : 0)) + 5500 + 4 * bn + (split > 1 ? 1200 + 11 * bn : 0);
+        if (cost < least) least = cost, p.ctas = ctas, p.bn = bn, p.split = split;
       }
       if (bn == whole) break;
     }
   }
-  p.tiles_p = (unsigned)ceil_div(n, 128 * p.ctas * p.pairs);
+  p.tiles_p = (unsigned)ceil_div(n, 128 * p.ctas);
   p.tiles_q = (unsigned)ceil_div(m, p.bn);
 }
 
@@ -264,7 +258,7 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
   const int sms = sm_count();
   cut_product(m, n, kblocks, (unsigned)sms, on_lines(a, a_stride, m) && on_lines(b, b_stride, n), p);
   if ((size_t)p.tiles_p * p.tiles_q > 0x7fffffff) return fail(XP_ERR_INVALID, "%zu x %zu elements are too many", m, n);
-  if (!map_codes(&p.p_map, b, b_stride, n, k, 128) || !map_codes(&p.q_map, a, a_stride, m, k, p.bn / p.ctas / p.pairs))
+  if (!map_codes(&p.p_map, b, b_stride, n, k, 128) || !map_codes(&p.q_map, a, a_stride, m, k, p.bn / p.ctas))
     return fail(XP_ERR_CUDA, "cuTensorMapEncodeTiled refuses %zu x %zu or %zu x %zu codes", m, k, n, k);
   p.p_scales = b_scales;
   p.q_scales = a_scales;

@@ -19,7 +19,7 @@ struct Matmul8Params {
   int p_shift, q_shift;                  // 7: a row of scales serves 128 rows
   unsigned p_rows, q_rows;               // C's columns and rows
   unsigned kblocks;
-  unsigned bn, ctas, pairs, split;       // rows of A in a tile; CTAs of a pair; pairs of a cluster; CTAs that share the columns of a tile
+  unsigned bn, ctas, split;              // rows of A in a tile; CTAs of a pair; CTAs that share the columns of a tile
   unsigned stages, nsums;
   unsigned tiles_p, tiles_q;
   void* c;
@@ -27,7 +27,6 @@ struct Matmul8Params {
   int out_bf16, accumulate;
 };
 cudaError_t launch_matmul8(Matmul8Params& p, int sms, cudaStream_t st);
-int matmul8_quads(int sms);              // clusters of two pairs that fit at a time
 cudaError_t matmul8_stalls(unsigned* n);
 
 struct Encode8Params {

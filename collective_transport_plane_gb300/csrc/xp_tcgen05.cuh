@@ -101,12 +101,6 @@ __device__ __forceinline__ void load_box(unsigned smem, const CUtensorMap* m, in
                  ::"r"(smem), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-// A pair's box, to this place in each CTA of the mask; the barrier's place in each such CTA's pair's leader is signalled.
-__device__ __forceinline__ void load_box_to(unsigned smem, const CUtensorMap* m, int x, int y, unsigned bar, unsigned short mask) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;"
-               ::"r"(smem), "l"(m), "r"(x), "r"(y), "r"(bar), "h"(mask) : "memory");
-}
-
 // ---- TMEM: 128 lanes of 512 columns of 32 bits; an address is lane << 16 | column.
 // CTAS 2: a warp of each CTA of a pair takes part.
 template <int CTAS>
@@ -183,13 +177,13 @@ __device__ __forceinline__ unsigned scaled_shape(unsigned n, unsigned byte) {
   return byte << 4 | (n >> 3) << 17 | 1u << 23 | (CTAS * 128u >> 4) << 24 | byte << 29;
 }
 // The mbarrier's phase counts this thread's products and copies so far as one
-// arrival (CTAS 2: the barriers at this place in the CTAs of the mask).
+// arrival (CTAS 2: the barriers at this place in both CTAs).
 template <int CTAS>
-__device__ __forceinline__ void commit_to(unsigned bar, unsigned short mask = 3) {
+__device__ __forceinline__ void commit_to(unsigned bar) {
   if constexpr (CTAS == 1)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
   else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(mask) : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((unsigned short)3) : "memory");
 }
 
 }  // namespace tc
