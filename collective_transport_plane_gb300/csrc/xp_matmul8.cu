@@ -385,6 +385,10 @@ cudaError_t launch_matmul8(Matmul8Params& p, int sms, cudaStream_t st) {
   return launch_clusters(matmul8_kernel<1>, dim3(grid), kThreads, kSharedBytes, (int)p.split, true, st, p);
 }
 
-cudaError_t matmul8_stalls(unsigned* n) { return cudaMemcpyFromSymbol(n, stalled_warps, sizeof *n); }
+// (The copy by itself waits for the legacy default stream and those that wait for it, not for streams that do not.)
+cudaError_t matmul8_stalls(unsigned* n) {
+  const cudaError_t e = cudaDeviceSynchronize();
+  return e != cudaSuccess ? e : cudaMemcpyFromSymbol(n, stalled_warps, sizeof *n);
+}
 
 }  // namespace xp
