@@ -101,11 +101,21 @@ bool map_codes(CUtensorMap* map, const uint8_t* codes, size_t stride, size_t row
 // times of all choices at 27 sizes (N = K = 4096: 64 rows 9.1 us as 4 CTAs a tile,
 // 12.5 as one, 10.2 in pairs; 512 rows 12.8 in pairs of 128, 14.8 alone; 4096 rows
 // 42 in pairs of 224, 46 of 256, which have room in TMEM for one tile's sums
-// only, 52 alone): a block's copies and products, which take longer where blocks straddle
-// L2's lines, what a tile's last sums take, and what CTAs that share a tile add.
+// only, 52 alone): a block's copies and products, which take longer where blocks
+// straddle L2's lines, what a tile's last sums take, and what CTAs that share a
+// tile add.  Into how many parts the columns are cut decides the order of the
+// additions, so it is chosen as if rows lay on lines, wherever they lie: equal
+// products give equal bits in any layout.  (Choices for rows off lines by themselves
+// had other parts at 2% of sizes: 192 x 2048 x 4096 11.0 us, 9.8 so; 2024 x 435 x
+// 11067 21.9 and 19.3; 620 x 3028 x 12890 27.7 and 29.4.)
 void cut_product(size_t m, size_t n, size_t kblocks, unsigned sms, bool lines, xp::Matmul8Params& p) {
   static const unsigned widths[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
+  struct Cut {
+    size_t cost;
+    unsigned ctas, bn;
+  } cuts[4] = {{~(size_t)0, 0, 0}, {~(size_t)0, 0, 0}, {~(size_t)0, 0, 0}, {~(size_t)0, 0, 0}};   // the least for 1, 2, 4 and 8 parts
   size_t least = ~(size_t)0;
+  unsigned parts = 0;   // a power of 2
   for (unsigned ctas = 1; ctas <= 2; ++ctas) {
     const unsigned whole = (unsigned)std::min<size_t>(256, round_up(m, 16 * ctas));
     const size_t tiles_p = ceil_div(n, 128 * ctas), units = std::max(1u, sms / ctas);
@@ -113,16 +123,25 @@ void cut_product(size_t m, size_t n, size_t kblocks, unsigned sms, bool lines, x
       const unsigned bn = std::min(width, whole);
       if (bn % (16 * ctas)) continue;
       const size_t tiles = tiles_p * ceil_div(m, bn), waves = ceil_div(tiles, units);
-      const size_t block = ctas == 1 ? 150u + bn * 23 / 20 + (lines ? 0 : bn * 9 / 10) : std::max(150u, 120u + (lines ? bn : bn * 5 / 4));
-      for (unsigned split = 1; split <= (ctas == 2 ? 1u : 8u); split *= 2) {
+      const size_t on = ctas == 1 ? 150u + bn * 23 / 20 : std::max(150u, 120u + bn);
+      const size_t off = ctas == 1 ? on + bn * 9 / 10 : std::max(150u, 120u + bn * 5 / 4);
+      for (unsigned i = 0; i < (ctas == 2 ? 1u : 4u); ++i) {
+        const unsigned split = 1u << i;
         // (clusters of 8 find room for 64 CTAs: with 128 they came one after another)
         if (split > 1 && (split > kblocks || tiles * split > (split == 8 ? std::min(64u, sms) : sms))) break;
-        const size_t cost = waves * (ceil_div(kblocks, split) * block + (bn > 224 ? 1000 : 0)) + 5500 + 4 * bn + (split > 1 ? 1200 + 11 * bn : 0);
-        if (cost < least) least = cost, p.ctas = ctas, p.bn = bn, p.split = split;
+        const auto cost = [&](size_t block) {
+          return waves * (ceil_div(kblocks, split) * block + (bn > 224 ? 1000 : 0)) + 5500 + 4 * bn + (split > 1 ? 1200 + 11 * bn : 0);
+        };
+        if (cost(on) < least) least = cost(on), parts = i;
+        const size_t here = cost(lines ? on : off);
+        if (here < cuts[i].cost) cuts[i] = {here, ctas, bn};
       }
       if (bn == whole) break;
     }
   }
+  p.ctas = cuts[parts].ctas;
+  p.bn = cuts[parts].bn;
+  p.split = 1u << parts;
   p.tiles_p = (unsigned)ceil_div(n, 128 * p.ctas);
   p.tiles_q = (unsigned)ceil_div(m, p.bn);
 }

@@ -76,8 +76,9 @@ xp_status xp_block8_decode(const uint8_t* codes, size_t codes_stride, const uint
  * XP_F32 or XP_BF16 (accumulate: XP_F32), at any alignment of its element.
  * Products are exact and summed in fp32 by the tensor cores, rounded once to
  * c's type; the order of the additions depends on m, n, k, and the device
- * alone: equal calls give equal bits.  A block whose scale is 255 makes its
- * rows of a, or its columns of c, NaN.  k == 0 gives zeros, or leaves c. */
+ * alone: equal products give equal bits, wherever their rows lie.  A block whose
+ * scale is 255 makes its rows of a, or its columns of c, NaN.  k == 0 gives
+ * zeros, or leaves c. */
 xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales, size_t a_scales_stride, int a_block_rows,
                      const uint8_t* b, size_t b_stride, const uint8_t* b_scales, size_t b_scales_stride, int b_block_rows,
                      void* c, size_t c_stride, size_t m, size_t n, size_t k, xp_dtype c_dtype, int accumulate,

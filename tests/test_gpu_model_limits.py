@@ -54,3 +54,20 @@ def test_the_status_call_waits_for_every_stream(xm):
     assert xm.xp_matmul8_status() == xm.XP_OK
     assert behind.query()
     torch.cuda.synchronize()
+
+
+# Sizes of which one layout alone would be cut into parts of the columns differently than the other alone (with 152 SMs), and
+# of tiles by one CTA, by CTAs that share one and by pairs.
+@pytest.mark.parametrize("m,n,k", [(48, 1024, 4096), (192, 2048, 4096), (67, 511, 1588), (1, 2386, 1653), (391, 66, 6662), (762, 2152, 15524), (116, 9425, 10888),
+                                   (2024, 435, 11067), (620, 3028, 12890), (1, 4096, 4096), (3000, 2000, 1000), (200, 300, 128)])
+def test_equal_products_give_equal_bits_in_any_layout(xm, m, n, k):
+    torch = torch_cuda()
+    a, sa = _any_codes(torch, m, k, 1, m)
+    b, sb = _any_codes(torch, n, k, 1, n)
+    sa, sb = _apart(torch, sa, 4), _apart(torch, sb, 4)
+    want = None
+    for step_a, off_a, step_b, off_b in ((128, 0, 128, 0), (16, 0, 16, 0), (128, 0, 16, 0), (16, 0, 128, 0), (128, 16, 128, 64)):
+        c = torch.empty(m, n, device="cuda")
+        xm.xp_matmul8(_apart(torch, a, step_a, off_a), sa, _apart(torch, b, step_b, off_b), sb, c)
+        want = c if want is None else want
+        assert torch.equal(c, want), (step_a, off_a, step_b, off_b, int((c != want).sum()))
