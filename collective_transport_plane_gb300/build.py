@@ -16,7 +16,7 @@ SOURCES = ["xp_api.cu", "xp_p2p.cu", "xp_p2p_tma.cu", "xp_ll.cu", "xp_ll128.cu",
            "xp_noalloc.cu", "xp_proxy.cu", "xp_train.cu", "xp_adamw.cu", "xp_layernorm.cu",
            "xp_model.cu", "xp_block8.cu", "xp_matmul8.cu", "xp_rmsnorm.cu", "xp_distill.cu"]
 HEADERS = ["xp_internal.h", "xp_device.cuh", "xp_proxy.h", "xp_train_internal.h", "xp_train_device.cuh", "xp_checks.h",
-           "xp_model_internal.h", "xp_code8.cuh", "xp_fours.cuh", "xp_tcgen05.cuh"]
+           "xp_model_internal.h", "xp_scales.h", "xp_code8.cuh", "xp_fours.cuh", "xp_tcgen05.cuh"]
 
 # --fmad=false and the default -ftz=false keep the ring's fp32 adds plain IEEE
 # round-to-nearest-even additions (the reductions must match the oracle bit

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "xp_model_internal.h"
+#include "xp_scales.h"
 #include "xp_tcgen05.cuh"
 #include "xp_train_device.cuh"
 
@@ -70,12 +71,13 @@ __device__ __forceinline__ void tile_at(const Matmul8Params& p, unsigned t, unsi
 // The words of four blocks' scales that lane l's line holds, of the 128 rows
 // from row0: rows l, l + 32, l + 64 and l + 96.  Rows that are not there get 2^0.
 __device__ __forceinline__ uint4 scale_line(const uint8_t* scales, u64 pitch, int shift, unsigned row0, unsigned rows, unsigned group,
-                                            int lane) {
+                                            unsigned blocks, int lane) {
+  const unsigned last = (rows - 1) >> shift;
   unsigned w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const unsigned row = row0 + lane + 32 * i;
-    w[i] = row < rows ? *reinterpret_cast<const unsigned*>(scales + (u64)(row >> shift) * pitch + 4ull * group) : 0x7f7f7f7fu;
+    w[i] = row < rows ? scale_word(scales + (u64)(row >> shift) * pitch, group, blocks, row >> shift == last) : 0x7f7f7f7fu;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -237,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
         if (n + u >= mine) break;
         unsigned tp, tq;
         tile_at(p, tile, tp, tq);
-        line[u][0] = scale_line(p.p_scales, p.p_pitch, p.p_shift, tp * kTileRows + p_first, p.p_rows, g0 + at, lane);
-        line[u][1] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn, p.q_rows, g0 + at, lane);
-        if (q_lines > 1) line[u][2] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn + 128, p.q_rows, g0 + at, lane);
+        line[u][0] = scale_line(p.p_scales, p.p_pitch, p.p_shift, tp * kTileRows + p_first, p.p_rows, g0 + at, p.kblocks, lane);
+        line[u][1] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn, p.q_rows, g0 + at, p.kblocks, lane);
+        if (q_lines > 1) line[u][2] = scale_line(p.q_scales, p.q_pitch, p.q_shift, tq * bn + 128, p.q_rows, g0 + at, p.kblocks, lane);
       }
       at += 2 * (kScaleWarps - 1);
 #pragma unroll

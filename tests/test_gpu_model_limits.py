@@ -71,3 +71,25 @@ def test_equal_products_give_equal_bits_in_any_layout(xm, m, n, k):
         xm.xp_matmul8(_apart(torch, a, step_a, off_a), sa, _apart(torch, b, step_b, off_b), sb, c)
         want = c if want is None else want
         assert torch.equal(c, want), (step_a, off_a, step_b, off_b, int((c != want).sum()))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 5, 128), (1, 128, 100), (3, 200, 300), (2, 129, 640), (300, 1000, 900), (600, 3000, 1300)])
+def test_scales_of_exactly_their_size(xm, m, n, k):
+    # rows of scales a multiple of four apart, the last one ending with its buffer; NaN scales behind every row and the buffer
+    torch = torch_cuda()
+    a, sa = _any_codes(torch, m, k, 1, m)
+    b, sb = _any_codes(torch, n, k, 128, n)
+
+    def exact(s):
+        rows, cols = s.shape
+        pitch = _ceil(cols, 4) * 4
+        buf = torch.full(((rows - 1) * pitch + cols + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        view = torch.as_strided(buf, (rows, cols), (pitch, 1))
+        view.copy_(s)
+        return view
+
+    a, b = _apart(torch, a, 16), _apart(torch, b, 16)
+    c, want = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    xm.xp_matmul8(a, exact(sa), b, exact(sb), c, b_block_rows=128)
+    xm.xp_matmul8(a, _apart(torch, sa, 4), b, _apart(torch, sb, 4), want, b_block_rows=128)
+    assert torch.equal(c, want) and torch.isfinite(c).all()
