@@ -318,6 +318,7 @@ xp_status record_done(Common& c, cudaStream_t st) {
 namespace xp {
 // Sets the message xp_last_error() returns on this thread.
 void set_last_error(const char* msg) { g_err = msg; }
+unsigned long long spin_timeout_ns() { return g_timeout_ns.load(); }
 }  // namespace xp
 
 struct xp_fifo {

@@ -21,6 +21,12 @@
 // memory, in the order of their ranks.  (A copy lands in the CTA that asks for it
 // alone: no load here names several CTAs, so that operands may lie in any memory
 // that the device reaches.)
+//
+// Every wait has a limit.  A warp that gives one up does its part no more: it
+// arrives at no barrier again, so no other warp is told what is not so, and those
+// that it keeps waiting give up in their turn.  Sums that were not read become NaN
+// in C.  Before the CTA ends, its own copies and products have ended too, however far its
+// warps and those of its pair have come.
 #include <algorithm>
 
 #include "xp_model_internal.h"
@@ -47,6 +53,7 @@ constexpr unsigned kSharedBytes = 212 * 1024;     // stages and scales
 constexpr unsigned kTmemColumns = 512;
 constexpr unsigned kChunk = 32;                   // blocks between two readings of TMEM's sums
 constexpr unsigned kMaxSplit = 8;
+constexpr u64 kDrainNs = 2000000000ull;           // a limit for what is on its way when a wait was given up
 
 static_assert(kScaleSlots == 2 * kScaleWarps, "a slot's phases are all waited for by the one warp that fills it");
 
@@ -107,12 +114,40 @@ __device__ __forceinline__ void put(const Matmul8Params& p, u64 at, u64 step, un
     if (i < n) c[i * step] = p.accumulate ? old[i] + v[i] : v[i];
 }
 
+// What a CTA, or a pair, still has on its way when a wait was given up and its
+// warps are through; boxes: how many each CTA asked for.  (A function that calls
+// none, as inlined, or with calls of its own, it cost the kernel registers: 8.6 us
+// for one row of 4096 x 4096, 7.3 so.)
+template <int CTAS>
+__device__ __noinline__ void end_copies_and_products(Bars& bars, const unsigned* boxes, unsigned stages, unsigned stage_bytes) {
+  const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (CTAS == 2 && tc::cluster_rank() != 0) return;   // the leader has the barriers
+  if (warp == 0 && lane == 0) {
+    // each stage's last box, which one CTA of a pair alone may have asked for
+    const unsigned mine = boxes[0], other = boxes[CTAS - 1], n = max(mine, other);
+    for (unsigned i = n >= stages ? n - stages : 0; i < n; ++i) {
+      const unsigned bar = tc::smem_of(bars.full + i % stages);
+      if (i >= other) tc::bar_uncount(bar, stage_bytes);
+      if (i >= mine) tc::bar_expect(bar, stage_bytes);
+      tc::bar_wait_here(bar, (i / stages) & 1, kDrainNs);
+    }
+  }
+  if (warp == 1) {   // which issued the products
+    if (tc::elected()) tc::commit_to<CTAS>(tc::smem_of(&bars.drained));
+    tc::bar_wait_here(tc::smem_of(&bars.drained), 0, kDrainNs);
+    tc::fence_before();
+  }
+  __syncwarp();
+}
+
 // CTAS: of a pair (2), or alone or in a cluster that shares a tile (1).
 template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_constant__ Matmul8Params p) {
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ unsigned tmem_at;
+  __shared__ unsigned gave_up;          // a warp of this CTA, or of its pair
+  __shared__ unsigned boxes[CTAS];      // that were asked for, by each CTA of a pair: in the leader's
   const unsigned base = (tc::smem_of(raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const unsigned stages = p.stages, bn = p.bn, q_box = bn / CTAS, stage_bytes = kRowsBytes + q_box * kBoxCols;
@@ -120,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
   const unsigned full = tc::smem_of(bars.full), empty = tc::smem_of(bars.empty);
   const unsigned scales_full = tc::smem_of(bars.scales_full), scales_empty = tc::smem_of(bars.scales_empty);
   const unsigned sums_full = tc::smem_of(bars.sums_full), sums_empty = tc::smem_of(bars.sums_empty);
-  const unsigned drained = tc::smem_of(&bars.drained);
   const unsigned nsums = p.nsums, q_lines = (bn + 127) / 128, slot_columns = 4 + 4 * q_lines;
   const unsigned rank = CTAS == 2 || p.split > 1 ? tc::cluster_rank() : 0;
   const bool leader = CTAS == 1 || rank == 0;   // of a pair: it issues the products, and keeps the barriers they wait for
@@ -130,11 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
     tc::prefetch_map(&p.q_map);
   }
   if (warp == 1 && lane == 0) {
+    gave_up = 0;
     for (unsigned i = 0; i < stages; ++i) {
       tc::bar_init(full + 8 * i, 1);
       tc::bar_init(empty + 8 * i, 1);
     }
-    tc::bar_init(drained, 1);
+    tc::bar_init(tc::smem_of(&bars.drained), 1);
     for (unsigned i = 0; i < kScaleSlots; ++i) {
       tc::bar_init(scales_full + 8 * i, CTAS);
       tc::bar_init(scales_empty + 8 * i, 1);
@@ -170,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
       tile_at(p, t, tp, tq);
       const int row_p = tp * kTileRows + p_first, row_q = tq * bn + q_first;
       for (unsigned kb = k0; kb < k1; ++kb, ++n) {
-        if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(empty + 8 * s, (turn - 1) & 1)))) break;
+        if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(empty + 8 * s, (turn - 1) & 1, p.limit_ns)))) break;
         if (tc::elected()) {
           const unsigned at = base + s * stage_bytes;
           if (leader) tc::bar_expect(full + 8 * s, CTAS * stage_bytes);
@@ -180,19 +215,23 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
         if (++s == stages) s = 0, ++turn;
       }
     }
-    if (!ok && leader)   // what is in flight lands before the CTA goes
-      for (unsigned i = n >= stages ? n - stages : 0; i < n; ++i) tc::bar_wait(full + 8 * (i % stages), (i / stages) & 1);
+    if (lane == 0) {
+      if constexpr (CTAS == 2)
+        tc::store_in_cta(tc::smem_of(boxes + rank), 0, n);
+      else
+        boxes[0] = n;
+    }
   } else if (warp == 1) {
     if (leader) {
       unsigned s = 0, phase = 0, slot = 0, slot_phase = 0, sums = 0, turn = 0;
       for (unsigned t = first_tile; t < ntiles && ok; t += tile_step) {
         for (unsigned from = k0; from < k1 && ok; from += kChunk) {
           const unsigned d = tmem + sums * bn, to = min(from + kChunk, k1);
-          if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(sums_empty + 8 * sums, (turn - 1) & 1)))) break;
+          if (turn > 0 && !(ok = __all_sync(0xffffffffu, tc::bar_wait(sums_empty + 8 * sums, (turn - 1) & 1, p.limit_ns)))) break;
           for (unsigned kb = from; kb < to; ++kb) {
             const unsigned at = base + s * stage_bytes, scale_p = tmem + nsums * bn + slot * slot_columns, scale_q = scale_p + 4;
             const bool more = kb == k0 || kb % 4 == 0, last = kb + 1 == k1 || kb % 4 == 3;
-            ok = tc::bar_wait(full + 8 * s, phase) && (!more || tc::bar_wait<CTAS == 2>(scales_full + 8 * slot, slot_phase));
+            ok = tc::bar_wait(full + 8 * s, phase, p.limit_ns) && (!more || tc::bar_wait<CTAS == 2>(scales_full + 8 * slot, slot_phase, p.limit_ns));
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc::fence_after();
             if (tc::elected()) {
@@ -217,10 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
           }
           if (++sums == nsums) sums = 0, ++turn;
         }
-      }
-      if (!ok) {   // what was issued ends before TMEM is given back
-        if (tc::elected()) tc::commit_to<CTAS>(drained);
-        tc::bar_wait(drained, 0);
       }
     }
   } else if (warp < kFirstStoreWarp) {
@@ -248,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
       for (unsigned u = 0; u < 2; ++u) {
         const unsigned slot = (n + u) % kScaleSlots, to = scales_at + slot * kScaleBytes + 16 * lane;
         if (n + u >= mine) break;
-        if (n + u >= kScaleSlots && !(ok = __all_sync(0xffffffffu, tc::bar_wait(scales_empty + 8 * slot, ((n + u) / kScaleSlots - 1) & 1)))) break;
+        if (n + u >= kScaleSlots && !(ok = __all_sync(0xffffffffu, tc::bar_wait(scales_empty + 8 * slot, ((n + u) / kScaleSlots - 1) & 1, p.limit_ns)))) break;
 #pragma unroll
         for (unsigned i = 0; i < 3; ++i)
           if (i <= q_lines)
@@ -271,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
       for (unsigned from = k0; from < k1; from += kChunk) {
-        ok = ok && __all_sync(0xffffffffu, tc::bar_wait(sums_full + 8 * sums, phase));
+        if (!ok || !(ok = __all_sync(0xffffffffu, tc::bar_wait(sums_full + 8 * sums, phase, p.limit_ns)))) break;
         tc::fence_after();
         // (columns past bn are read too, within TMEM's 512, and not used)
         const unsigned at = tmem + sums * bn + first + ((32 * quarter) << 16);
@@ -307,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
         const unsigned c = 64 * j + first;
         if (p.split == 1) {
           if (c < there) put<16>(p, (u64)(m0 + c) * p.c_stride + n, p.c_stride, there - c, v[j]);
-        } else if (c < bn) {
+        } else if (c < bn && ok) {   // (else boxes may still land there)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + i) * kRows + row) * 4), "f"(v[j][i]) : "memory");
@@ -315,7 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
       }
     }
   }
-  if (!ok && lane == 0) atomicAdd(&stalled_warps, 1u);
+  if (!ok && lane == 0) {
+    atomicAdd(&stalled_warps, 1u);
+    gave_up = 1;
+    if constexpr (CTAS == 2) tc::store_in_cta(tc::smem_of(&gave_up), rank ^ 1, 1);
+  }
   __syncwarp();
   if (CTAS == 1 && p.split > 1) {
     tc::cluster_meet();
@@ -323,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
     tile_at(p, first_tile, tp, tq);
     // a thread adds up four of the 128 rows of B at one of A's, which go to the CTAs in turn
     const unsigned row = 4 * lane, n = tp * kRows + row;
+    const unsigned missing = lane < p.split ? tc::load_in_cta(tc::smem_of(&gave_up), lane) : 0;
     for (unsigned j = rank + p.split * warp; j < bn && tq * bn + j < p.q_rows; j += p.split * (kThreads / 32)) {
       float4 part[kMaxSplit];
 #pragma unroll
@@ -332,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
 #pragma unroll
       for (unsigned r = 0; r < kMaxSplit; ++r)
         if (r < p.split) v[0] += part[r].x, v[1] += part[r].y, v[2] += part[r].z, v[3] += part[r].w;
+      if (__any_sync(0xffffffffu, missing)) v[0] = v[1] = v[2] = v[3] = __int_as_float(0x7fffffff);
       if (n < p.p_rows) put<4>(p, (u64)(tq * bn + j) * p.c_stride + n, 1, p.p_rows - n, v);
     }
   }
@@ -340,6 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul8_kernel(const __grid_const
     tc::cluster_meet();   // nobody reads or signals this CTA's shared memory any more
   else
     __syncthreads();
+  if (gave_up) {   // in both CTAs of a pair
+    end_copies_and_products<CTAS>(bars, boxes, p.stages, kRowsBytes + p.bn / CTAS * kBoxCols);
+    if (CTAS == 2)
+      tc::cluster_meet();
+    else
+      __syncthreads();
+  }
   if (warp == 2) {
     tc::fence_after();
     tc::tmem_free<CTAS>(tmem, kTmemColumns);

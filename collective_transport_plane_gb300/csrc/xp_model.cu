@@ -292,6 +292,7 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
   p.c_stride = c_stride;
   p.out_bf16 = c_dtype == XP_BF16;
   p.accumulate = accumulate != 0;
+  p.limit_ns = xp::spin_timeout_ns();
   XP_CUDA(xp::launch_matmul8(p, sms, stream));
   return XP_OK;
 }

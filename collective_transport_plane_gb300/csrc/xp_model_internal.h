@@ -11,6 +11,8 @@
 
 namespace xp {
 
+unsigned long long spin_timeout_ns();     // xp_set_spin_timeout_ns's
+
 struct Matmul8Params {
   CUtensorMap p_map, q_map;              // B's and A's codes
   const uint8_t* p_scales;
@@ -25,6 +27,7 @@ struct Matmul8Params {
   void* c;
   unsigned long long c_stride;           // elements
   int out_bf16, accumulate;
+  unsigned long long limit_ns;           // after which a warp gives up a wait for another
 };
 cudaError_t launch_matmul8(Matmul8Params& p, int sms, cudaStream_t st);
 cudaError_t matmul8_stalls(unsigned* n);

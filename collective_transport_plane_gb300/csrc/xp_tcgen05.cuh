@@ -28,6 +28,10 @@ __device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
 __device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// What a copy that was never asked for would have counted.
+__device__ __forceinline__ void bar_uncount(unsigned bar, unsigned bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // CLUSTER: what the arriving threads of other CTAs wrote before is seen.
 template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
@@ -40,26 +44,34 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// A wait gives up after two seconds of the GPU's clock (no wait here is for
-// another kernel, and the longest loop of products takes milliseconds).
-constexpr unsigned long long kLimitNs = 2000000000ull;
+// A wait gives up after `limit` ns of the GPU's clock, which it looks at after 64
+// tries of up to 4 us each, or after each where the limit is below a millisecond.
+// (No wait here is for another kernel, and the longest loop of products takes
+// milliseconds.)
 __device__ __forceinline__ unsigned long long clock_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
 template <bool CLUSTER>
-__device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity) {
+__device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity, unsigned long long limit) {
   const unsigned long long start = clock_ns();
+  const int tries = limit < 1000000 ? 1 : 64;
   do {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < tries; ++i)
       if (bar_try<CLUSTER>(bar, parity)) return true;
-  } while (clock_ns() - start < kLimitNs);
+  } while (clock_ns() - start < limit);
   return false;
 }
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity) {
-  return bar_try<CLUSTER>(bar, parity) || bar_wait_long<CLUSTER>(bar, parity);
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, unsigned long long limit) {
+  return bar_try<CLUSTER>(bar, parity) || bar_wait_long<CLUSTER>(bar, parity, limit);
+}
+
+// The same without a call, for a function that is called itself.
+__device__ __forceinline__ void bar_wait_here(unsigned bar, unsigned parity, unsigned long long limit) {
+  for (const unsigned long long start = clock_ns(); !bar_try<false>(bar, parity) && clock_ns() - start < limit;) {
+  }
 }
 
 // ---- the CTAs of a cluster
@@ -77,6 +89,14 @@ __device__ __forceinline__ unsigned in_cta(unsigned smem, unsigned rank) {
   unsigned r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
   return r;
+}
+__device__ __forceinline__ void store_in_cta(unsigned smem, unsigned rank, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_in_cta(unsigned smem, unsigned rank) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_cta(smem, rank)) : "memory");
+  return v;
 }
 __device__ __forceinline__ void bar_arrive_cluster(unsigned bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");

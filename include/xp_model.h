@@ -85,8 +85,8 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
                      xp_stream_t stream);
 
 /* Waits for the device.  XP_ERR_TIMEOUT if a product on the current device
- * ever gave up a wait between its own warps (after two seconds; the tiles of
- * that call are NaN from there on), else XP_OK.  Not while a stream of the
+ * ever gave up a wait between its own warps (after the spin timeout of xp.h, two
+ * seconds; what it had not summed by then is NaN), else XP_OK.  Not while a stream of the
  * device is being captured: like any call that waits for a device, it would
  * end the capture. */
 xp_status xp_matmul8_status(void);

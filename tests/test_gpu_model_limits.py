@@ -1,10 +1,16 @@
 """The operators of a layer in 8 bits at the limits of what their header promises: what a call waits for, and which
 arguments equal calls may differ in."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 from tests.gpu_util import torch_cuda
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -93,3 +99,54 @@ def test_scales_of_exactly_their_size(xm, m, n, k):
     xm.xp_matmul8(a, exact(sa), b, exact(sb), c, b_block_rows=128)
     xm.xp_matmul8(a, _apart(torch, sa, 4), b, _apart(torch, sb, 4), want, b_block_rows=128)
     assert torch.equal(c, want) and torch.isfinite(c).all()
+
+
+# One CTA for a tile (one tile each, and several), CTAs that share a tile, pairs (one chunk of 4096 columns, and four).
+GIVEN_UP = {"alone": (9000, 300, 16384), "alone, tile after tile": (20000, 600, 8192), "shared": (762, 2152, 15524), "pairs": (4096, 4096, 4096),
+            "pairs, chunk after chunk": (2000, 4096, 16384)}
+
+
+@pytest.mark.parametrize("form", list(GIVEN_UP))
+def test_waits_that_are_given_up(xm, form):
+    # With a limit of 1 us every warp that waits for a tile's first sums, 10 us and more of copies and products, gives up after a
+    # try or two (4 us each), and all others in their turn.  C is NaN, the status says so, and copies, products and TMEM are
+    # left in order: the next call with the usual limit is right, and so is one of another form.  In a process of its own,
+    # whose status stays what it is.
+    code = """
+import sys
+sys.path.insert(0, %r)
+import torch
+from collective_transport_plane_gb300 import xp, xp_model as xm
+from tests.test_gpu_model_limits import GIVEN_UP, _any_codes
+calls = []
+for m, n, k in (GIVEN_UP[%r], (1, 4096, 4096)):
+    (a, sa), (b, sb) = _any_codes(torch, m, k, 1, m), _any_codes(torch, n, k, 128, n)
+    pitch = -(-k // 16) * 16
+    a, b = (torch.nn.functional.pad(t, (0, pitch - k))[:, :k] for t in (a, b))
+    sa, sb = (torch.nn.functional.pad(t, (0, -t.shape[1] %% 4))[:, :t.shape[1]] for t in (sa, sb))
+    calls.append((a, sa, b, sb, torch.zeros(m, n, device="cuda")))
+want = []
+for call in calls:
+    xm.xp_matmul8(*call, b_block_rows=128)
+    want.append(call[-1].clone())
+assert xm.xp_matmul8_status() == xm.XP_OK
+for _ in range(3):
+    for c in calls:
+        c[-1].zero_()
+    xp.xp_set_spin_timeout_ns(1000)
+    xm.xp_matmul8(*calls[0], b_block_rows=128)
+    assert xm.xp_matmul8_status() == xp.XP_ERR_TIMEOUT
+    assert torch.isnan(calls[0][-1]).all(), int(torch.isnan(calls[0][-1]).sum())
+    xp.xp_set_spin_timeout_ns(2_000_000_000)
+    for call, w in zip(calls, want):
+        xm.xp_matmul8(*call, b_block_rows=128)
+        torch.cuda.synchronize()
+        assert torch.equal(call[-1], w)
+    xm.xp_matmul8(*calls[0], b_block_rows=128, accumulate=True)
+    torch.cuda.synchronize()
+    assert torch.equal(calls[0][-1], want[0] + want[0])
+print("in order")
+""" % (ROOT, form)
+    torch_cuda()
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0 and done.stdout.strip().endswith("in order"), done.stdout + done.stderr[-2000:]
