@@ -243,7 +243,7 @@ __device__ __forceinline__ void copy_async16(unsigned smem, const void* gmem, in
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_made() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest n groups of this thread's copies have landed
+// all but the newest n groups of this thread's copies have landed, for n up to 2
 __device__ __forceinline__ void wait_copies(int n) {
   if (n == 0)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -554,8 +554,9 @@ cudaError_t forward(RmsForwardParams& p, cudaStream_t st) {
 template <typename T, bool WIDE, int NU>
 cudaError_t backward_rows(RmsBackwardParams& p, const RmsBackwardShape& s, cudaStream_t st) {
   const unsigned block = s.groups * s.threads, stage = WIDE ? 3 * NU * 16 * block : 3 * s.groups * room_of<T>(p.cols);
-  // as many rows ahead as the SM's CTAs have room for, three at most
-  p.stages = std::min(4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage))));
+  // As many rows ahead as the SM's CTAs have room for: two at most where units are wide (16384 x 8192 bf16 with dadded 176 us,
+  // 180 by three; 60000 x 256 24.3 and 25.8), else three, the first of which has to be there a turn early.
+  p.stages = std::min(WIDE ? 3 : 4, std::max(2, (int)(200 * 1024 / (s.per_sm * stage))));
   size_t smem = (size_t)p.stages * stage;
   if (s.groups > 1) smem = std::max<size_t>(smem, (size_t)block * NU * kUnit<T, WIDE> * sizeof(float));
   constexpr bool kSmall = (!WIDE && NU <= 2) || NU * kUnit<T, WIDE> > 16;   // 64 registers do, or 128 are needed, in CTAs of any size
