@@ -60,7 +60,19 @@ class _Types(dict):
         return found
 
 
+class _Bytes(dict):
+    """torch dtype -> XP_U8 for bytes and for one type of 8 bits, else -1, filled as types are met."""
+
+    def __init__(self, own):
+        self.own = own
+
+    def __missing__(self, dtype):
+        found = self[dtype] = XP_U8 if str(dtype) in ("torch.uint8", self.own) else -1
+        return found
+
+
 _types = _Types()
+_codes, _scales = _Bytes("torch.float8_e4m3fn"), _Bytes("torch.float8_e8m0fnu")
 _current_device = None   # asks torch for it, once torch is there
 
 
@@ -80,17 +92,17 @@ def _refuse_devices(tensors, current):
     raise ValueError(f"tensors on devices {at}, not all on the current one, {current} (-1: the host)")
 
 
-def _refuse_matrix(t, shape, what, dtype):
-    if t.shape != shape or _types[t.dtype] != dtype:
+def _refuse_matrix(t, shape, what, dtype, types):
+    if t.shape != shape or types[t.dtype] != dtype:
         raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype}, not {tuple(shape)} of its type")
     raise ValueError(f"{what}'s columns are {t.stride()[1]} elements apart")
 
 
-def _matrix(t, shape, what, dtype, device):
+def _matrix(t, shape, what, dtype, device, types=_types):
     """(address, stride) of a matrix of a shape and type whose columns are side by side."""
     stride, step = t.stride()
-    if t.shape != shape or (step != 1 and shape[1] > 1) or _types[t.dtype] != dtype:
-        _refuse_matrix(t, shape, what, dtype)
+    if t.shape != shape or (step != 1 and shape[1] > 1) or types[t.dtype] != dtype:
+        _refuse_matrix(t, shape, what, dtype, types)
     if t.get_device() != device:
         _refuse_devices((t,), device)
     return t.data_ptr(), stride
@@ -118,8 +130,8 @@ def _block8(codes, scales, shape, block_rows, what, device):
         if block_rows != XP_BLOCK8:
             raise ValueError(f"{what}: blocks of {block_rows} rows, neither 1 nor 128")
         rows = (rows + 127) // 128
-    p, s = _matrix(codes, shape, what, XP_U8, device)
-    ps, ss = _matrix(scales, (rows, (cols + 127) // 128), "scales", XP_U8, device)
+    p, s = _matrix(codes, shape, what, XP_U8, device, _codes)
+    ps, ss = _matrix(scales, (rows, (cols + 127) // 128), "scales", XP_U8, device, _scales)
     return p, s, ps, ss
 
 
