@@ -124,7 +124,7 @@ __device__ __forceinline__ float cta_sum(float v, float* words) {
 // The row's entries, laid out in shared memory.
 struct Entries {
   int* id;       // -1: counts for nothing
-  float* u;      // t / T
+  float* t;
   float* z;      // the logit
 };
 __device__ __forceinline__ Entries entries_in(uint8_t* raw, unsigned top) {
@@ -132,12 +132,12 @@ __device__ __forceinline__ Entries entries_in(uint8_t* raw, unsigned top) {
   return {reinterpret_cast<int*>(raw), reinterpret_cast<float*>(raw) + room, reinterpret_cast<float*>(raw) + 2 * room};
 }
 
-// Brings them.  False, the same for the CTA, if the row has none.  max_u: the
+// Brings them.  False, the same for the CTA, if the row has none.  max_t: the
 // largest of this thread's.  (The threads' first loads of the row's logits are on
 // their way meanwhile: 8192 x 32000 bf16 forward 117 us without.)
 template <typename T>
-__device__ __forceinline__ bool bring_entries(const DistillParams& p, u64 row, const T* logits, const Entries& e, float inv_t, float& max_u) {
-  max_u = -INFINITY;
+__device__ __forceinline__ bool bring_entries(const DistillParams& p, u64 row, const T* logits, const Entries& e, float& max_t) {
+  max_t = -INFINITY;
   bool any = false;
   if (threadIdx.x < ((p.top + 3) & ~3u) - p.top) e.id[p.top + threadIdx.x] = -1;   // what fills the last four
   for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x) {
@@ -145,10 +145,10 @@ __device__ __forceinline__ bool bring_entries(const DistillParams& p, u64 row, c
     const float t = p.teacher[row * p.top + j];
     if ((unsigned)id >= p.vocab || t == -INFINITY) id = -1;
     e.id[j] = id;
-    e.u[j] = t * inv_t;
+    e.t[j] = t;
     if (id >= 0) {
       e.z[j] = to_f(logits[id]);
-      max_u = fmaxf(max_u, t * inv_t);
+      max_t = fmaxf(max_t, t);
       any = true;
     }
   }
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(1024) forward_kernel(const DistillParams p) {
   const uint4* body = reinterpret_cast<const uint4*>(z + head);
   const Ring ring(raw, p.top, body, units);
   ring.begin();
-  float max_u;
-  if (!bring_entries(p, row, z, e, inv_t, max_u)) {
+  float max_t;
+  if (!bring_entries(p, row, z, e, max_t)) {
     ring.end();
     if (threadIdx.x == 0) {
       p.loss[row] = 0.f;
@@ -288,20 +288,20 @@ __global__ void __launch_bounds__(1024) forward_kernel(const DistillParams p) {
   r = lane < nw ? words[lane] : Running{-INFINITY, 0.f};
   r = warp_joined(r, c);
   const float lse = r.m * inv_t + logf(r.s);
-  float top_u = -INFINITY;
+  float top_t = -INFINITY;
   for (unsigned j = lane; j < p.top; j += 32)
-    if (e.id[j] >= 0) top_u = fmaxf(top_u, e.u[j]);
-  top_u = warp_max(top_u);
-  float w = 0.f;
+    if (e.id[j] >= 0) top_t = fmaxf(top_t, e.t[j]);
+  top_t = warp_max(top_t);
+  float w = 0.f;   // (differences first, as for the row)
   for (unsigned j = lane; j < p.top; j += 32)
-    if (e.id[j] >= 0) w += pow2((e.u[j] - top_u) * kLog2e);
+    if (e.id[j] >= 0) w += pow2((e.t[j] - top_t) * c);
   w = warp_sum(w);
   const float log_w = logf(w);
   float loss = 0.f;
   for (unsigned j = lane; j < p.top; j += 32) {
     if (e.id[j] < 0) continue;
-    const float d = e.u[j] - top_u, prob = pow2(d * kLog2e) / w;
-    if (!(prob == 0.f)) loss += prob * ((d - log_w) - (e.z[j] * inv_t - lse));
+    const float d = e.t[j] - top_t, prob = pow2(d * c) / w;
+    if (!(prob == 0.f)) loss += prob * ((d * inv_t - log_w) - (e.z[j] * inv_t - lse));
   }
   loss = warp_sum(loss);
   if (lane == 0) {
@@ -321,15 +321,15 @@ __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
   const u64 row = blockIdx.x;
   const T* z = static_cast<const T*>(p.logits) + row * p.logits_stride;
   T* out = static_cast<T*>(p.dlogits) + row * p.dlogits_stride;
-  const float inv_t = 1.f / p.temperature;
+  const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
   const unsigned head = head_of(out, p.vocab), units = (p.vocab - head) / V, tail = head + units * V, n = blockDim.x;
   const bool alike = head_of(z, p.vocab) == head;   // z has the same phase
   const uint4* body = reinterpret_cast<const uint4*>(z + head);
   uint4* to = reinterpret_cast<uint4*>(out + head);
   const Ring ring(raw, p.top, body, alike ? units : 0);
   ring.begin();
-  float max_u;
-  const bool any = bring_entries(p, row, z, e, inv_t, max_u);
+  float max_t;
+  const bool any = bring_entries(p, row, z, e, max_t);
   const float lse = any ? p.lse[row] : 0.f, scale = any ? p.dloss[row] * p.temperature : 0.f;
   // q = e^(z / T - lse); rows without entries do not look at z
   auto q_of = [&](float v) { return pow2(fmaf(v, inv_t, -lse) * kLog2e); };
@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
   }
   if (!any) return;
   // the entries' own elements once more, with their p
-  const float top_u = cta_max(max_u, words);
+  const float top_t = cta_max(max_t, words);
   float w = 0.f;
   for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x)
-    if (e.id[j] >= 0) w += pow2((e.u[j] - top_u) * kLog2e);
+    if (e.id[j] >= 0) w += pow2((e.t[j] - top_t) * c);
   w = cta_sum(w, words);
   for (unsigned j = threadIdx.x; j < p.top; j += blockDim.x) {
     const int id = e.id[j];
@@ -377,11 +377,11 @@ __global__ void __launch_bounds__(1024) backward_kernel(const DistillParams p) {
     }
     float prob = 0.f;
     if (named == 1) {
-      prob = pow2((e.u[j] - top_u) * kLog2e) / w;
+      prob = pow2((e.t[j] - top_t) * c) / w;
     } else {   // of all entries that name it, in their order
 #pragma unroll 1
       for (unsigned i = 0; i < p.top; ++i)
-        if (e.id[i] == id) prob += pow2((e.u[i] - top_u) * kLog2e) / w;
+        if (e.id[i] == id) prob += pow2((e.t[i] - top_t) * c) / w;
     }
     from_f((q_of(e.z[j]) - prob) * scale, out[id]);
   }

@@ -144,7 +144,8 @@ xp_status xp_rmsnorm_backward(const void* dy, size_t dy_stride, const void* h, s
  * t fp32, rows x top each, side by side; loss and lse fp32, lse may be NULL
  * where no backward pass follows.  (One entry is the cross entropy of a
  * label.)  Sums are fp32; logits over T that count have to be below 3e38 (masks of
- * the type's lowest value need not be). */
+ * the type's lowest value need not be, nor the teacher's, even where they are all
+ * of a row's). */
 xp_status xp_distill_forward(const void* logits, size_t logits_stride, const int32_t* ids, const float* teacher,
                              size_t rows, size_t vocab, size_t top, float temperature, float* loss, float* lse,
                              xp_dtype dtype, xp_stream_t stream);

@@ -150,3 +150,24 @@ print("in order")
     torch_cuda()
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert done.returncode == 0 and done.stdout.strip().endswith("in order"), done.stdout + done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("temperature", [0.5, 0.7, 1.0, 2.0])
+@pytest.mark.parametrize("top,vocab", [(1, 50), (3, 50), (37, 3000)])
+def test_a_teacher_whose_entries_are_all_masked_alike(xm, temperature, top, vocab):
+    # logits that are all the type's lowest value say as much as logits that are all 0; one among others has no share
+    torch = torch_cuda()
+    z = torch.randn(4, vocab, generator=torch.Generator("cuda").manual_seed(top), device="cuda")
+    ids = torch.arange(top, dtype=torch.int32, device="cuda").expand(4, top).contiguous()
+    out = []
+    for value in (torch.finfo(torch.float32).min, 0.0):
+        t = torch.full((4, top), value, device="cuda")
+        t[3, 0] = 1.0
+        if value == 0.0:
+            t[3, 1:] = -float("inf")
+        loss, lse, d, g = torch.empty(4, device="cuda"), torch.empty(4, device="cuda"), torch.ones(4, device="cuda"), torch.empty_like(z)
+        xm.xp_distill_forward(z, ids, t, loss, lse, temperature)
+        xm.xp_distill_backward(z, ids, t, lse, d, g, temperature)
+        out.append((loss, lse, g))
+    for masked, plain in zip(*out):
+        assert torch.isfinite(plain).all() and torch.equal(masked, plain)
