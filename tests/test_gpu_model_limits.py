@@ -171,3 +171,19 @@ def test_a_teacher_whose_entries_are_all_masked_alike(xm, temperature, top, voca
         out.append((loss, lse, g))
     for masked, plain in zip(*out):
         assert torch.isfinite(plain).all() and torch.equal(masked, plain)
+
+
+@pytest.mark.parametrize("m,n,k", [(33, 32000, 512), (3, 128256, 260), (200, 160001, 128), (130, 300, 32000), (70, 256, 128256), (2, 200, 160001), (5, 130, 1 << 20)])
+def test_products_of_a_vocabulary(xm, m, n, k):
+    # a last layer's logits and their gradient.  Products are multiples of 1/4 of 4 at most, and a million of them below 2^24
+    # quarters: exact in any order
+    from tests.test_gpu_model import _values, _whole
+    torch = torch_cuda()
+    a, sa = _whole(torch, m, k, 1, m, 126, 128)
+    b, sb = _whole(torch, n, k, 128, n, 126, 128)
+    want = (_values(torch, a, sa, 1) @ _values(torch, b, sb, 128).t()).float()
+    c = torch.full((m, n), float("nan"), device="cuda")
+    xm.xp_matmul8(a, sa, b, sb, c, b_block_rows=128)
+    assert torch.equal(c, want)
+    xm.xp_matmul8(a, sa, b, sb, c, b_block_rows=128, accumulate=True)
+    assert torch.equal(c, 2 * want)
