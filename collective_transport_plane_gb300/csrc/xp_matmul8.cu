@@ -25,8 +25,8 @@
 // Every wait has a limit.  A warp that gives one up does its part no more: it
 // arrives at no barrier again, so no other warp is told what is not so, and those
 // that it keeps waiting give up in their turn.  Sums that were not read become NaN
-// in C.  Before the CTA ends, its own copies and products have ended too, however far its
-// warps and those of its pair have come.
+// in C.  Before the CTA ends, its own copies and products have ended too, however
+// far its warps and those of its pair have come.
 #include <algorithm>
 
 #include "xp_model_internal.h"

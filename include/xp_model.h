@@ -86,9 +86,9 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
 
 /* Waits for the device.  XP_ERR_TIMEOUT if a product on the current device
  * ever gave up a wait between its own warps (after the spin timeout of xp.h, two
- * seconds; what it had not summed by then is NaN), else XP_OK.  Not while a stream of the
- * device is being captured: like any call that waits for a device, it would
- * end the capture. */
+ * seconds; what it had not summed by then is NaN), else XP_OK.  (xp_abort does
+ * not stop a product.)  Not while a stream of the device is being captured: like
+ * any call that waits for a device, it would end the capture. */
 xp_status xp_matmul8_status(void);
 
 /* ------------------------------------------------- root-mean-square norm */
@@ -99,11 +99,11 @@ xp_status xp_matmul8_status(void);
  * x, residual, added and y are `dtype` (XP_F32 or XP_BF16), gamma `wdtype`
  * (NULL: 1).  y is rounded once.  y8 and y8_scales are y in 8 bits with
  * block_rows 1, encoded from its values before they are rounded to `dtype`.
- * y, y8 (with its scales) and rstd (fp32) may each be NULL; added may be NULL
- * where residual is, and must not be where it is not.  added may be x or
- * residual itself, and y may be x or residual itself where added is not the
- * same one, at equal strides.  Sums are fp32 (elements of 1e16 and
- * more overflow them).  rows == 0 is a no-op. */
+ * y, y8 (with its scales) and rstd (fp32) may each be NULL; added is NULL
+ * where residual is, and only there.  added may be x or residual itself, and y
+ * may be x or residual itself where added is not the same one, at equal strides.
+ * Sums are fp32 (elements of 1e16 and more overflow them).  rows == 0 is a
+ * no-op. */
 xp_status xp_rmsnorm_forward(const void* x, size_t x_stride, const void* residual, size_t residual_stride,
                              const void* gamma, void* added, size_t added_stride, void* y, size_t y_stride, uint8_t* y8,
                              size_t y8_stride, uint8_t* y8_scales, size_t y8_scales_stride, float* rstd, size_t rows,
