@@ -86,8 +86,8 @@ xp_status xp_matmul8(const uint8_t* a, size_t a_stride, const uint8_t* a_scales,
 
 /* Waits for the device.  XP_ERR_TIMEOUT if a product on the current device
  * ever gave up a wait between its own warps (after the spin timeout of xp.h, two
- * seconds; what it had not summed by then is NaN), else XP_OK.  (xp_abort does
- * not stop a product.)  Not while a stream of the device is being captured: like
+ * seconds, which has to be above 0.1 ms for them; what it had not summed by then
+ * is NaN), else XP_OK.  (xp_abort does not stop a product.)  Not while a stream of the device is being captured: like
  * any call that waits for a device, it would end the capture. */
 xp_status xp_matmul8_status(void);
 
